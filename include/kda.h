@@ -309,6 +309,113 @@ kda_status_t kda_epilogue(const void* o, const void* gate, const float* weight, 
                           const kda_problem_t* problem, void* stream);
 
 /*
+ * Softmax attention next to the recurrence, for the full-attention layers that a hybrid stack puts
+ * between its KDA layers ("Kimi K3" reading notes, section 7, "Scaling to 1M Tokens: NoPE and KDA
+ * Context Parallelism": such layers carry no position encoding, so a key enters a cache as it is).
+ * Query head h reads key head h / (num_heads / num_kv_heads):
+ *
+ *   z_ij = scale * (q_i . k_j)      j over the keys that row i sees
+ *   o_i  = sum_j exp(z_ij) v_j / sum_j exp(z_ij)      a row that sees no key gives zeros
+ *
+ * What a row does not see never reaches it: a NaN or an infinity in a hidden key or value leaves
+ * the row as it is.  Sums, maxima and normalisers are fp32.
+ */
+typedef struct {
+    int32_t num_seqs;      /* N                                                                 */
+    int64_t total_tokens;  /* tokens of q (prefill, decode) or of k and v (append), all sequences */
+    int32_t num_heads;     /* query heads, a multiple of num_kv_heads (unused by append)         */
+    int32_t num_kv_heads;  /* key and value heads                                                */
+    int32_t head_dim;      /* channels of q, k, v and out: 32, 64 or 128                         */
+    kda_dtype_t io_dtype;  /* dtype of q, k, v and out                                           */
+    float scale;           /* > 0, finite; 1 / sqrt(head_dim) is usual (unused by append)        */
+    int64_t q_stride;      /* elements from one token of q to the next; 0: num_heads * head_dim  */
+    int64_t k_stride;      /* the same for k; 0: num_kv_heads * head_dim                         */
+    int64_t v_stride;      /* the same for v; 0: num_kv_heads * head_dim                         */
+} kda_attention_t;
+
+/* What an 8-bit cache holds: e4m3 floating point (largest value 448) or integers in [-127, 127]. */
+typedef enum { KDA_CACHE_E4M3 = 0, KDA_CACHE_INT8 = 1 } kda_cache_dtype_t;
+
+/*
+ * A paged cache of 8-bit keys and values.  A page holds page_tokens consecutive tokens of one
+ * sequence; the value a code stands for is code * scale, with one scale for each page and head.
+ */
+typedef struct {
+    void* k;                    /* [num_pages, num_kv_heads, page_tokens, head_dim] codes (8 bits)  */
+    void* v;                    /* the same for the values                                         */
+    float* k_scale;             /* [num_pages, num_kv_heads] fp32                                  */
+    float* v_scale;             /* [num_pages, num_kv_heads] fp32                                  */
+    const int32_t* block_table; /* [num_seqs, max_pages]: page of tokens [i page_tokens, ...) of a
+                                   sequence; entries past a sequence's last page are not read      */
+    int32_t num_pages;
+    int32_t page_tokens;        /* 16, 32, 64 or 128                                               */
+    int32_t max_pages;          /* columns of block_table                                          */
+    kda_cache_dtype_t dtype;
+} kda_cache_t;
+
+/*
+ * Causal attention over whole prompts, packed ("Kimi K3" reading notes, section 7: the
+ * full-attention layers of the stack).  Row i of a sequence sees that sequence's keys 0 .. i.
+ *
+ *   q : [T_tot, num_heads, head_dim], k, v : [T_tot, num_kv_heads, head_dim], io dtype; tokens
+ *       q_stride, k_stride, v_stride elements apart (a multiple of 16 bytes, so that q, k and v can
+ *       be views of one projection), heads and channels packed.
+ *   cu_seqlens : as for kda_forward (device [N+1], or NULL for N equal lengths).  Offsets are not
+ *       validated on the device here: invalid offsets give unspecified outputs (never an access
+ *       outside the tensors).
+ *   out : [T_tot, num_heads, head_dim] io dtype, packed; must not overlap any input.
+ * num_heads / num_kv_heads is at most 128.  No workspace.  bf16 products accumulate in fp32 with
+ * the weights exp(z_ij - max) rounded to bf16; fp32 operands enter as sums of three bf16 parts
+ * (24 bits).
+ */
+kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, void* out,
+                                   const kda_attention_t* problem, void* stream);
+
+/*
+ * Appends the keys and values of new tokens to a paged 8-bit cache ("Kimi K3" reading notes,
+ * section 7: the stack's full-attention layers keep keys and values of every token).
+ *
+ *   k, v : [T_tot, num_kv_heads, head_dim] io dtype, strides as for kda_attention_prefill.
+ *   cu_seqlens : device [N+1] offsets of every sequence's new tokens, or NULL for T_tot / N each.
+ *   lengths : [N] int32 on the device, tokens of each sequence INCLUDING the new ones: the last
+ *       cu_seqlens[n+1] - cu_seqlens[n] positions of sequence n are written.
+ *   cache : host descriptor.  A page and head takes the scale 2^e with the smallest e >= -60 that
+ *       keeps its largest finite magnitude within the code's range (448 or 127); a page that already
+ *       holds tokens keeps its scale unless the new tokens need a larger one, and then its older
+ *       codes are rounded again to the new scale.  Codes are x / scale rounded to nearest, ties to
+ *       even; infinities take the largest code, NaN is NaN in e4m3 and 0 in int8.
+ *   check : device word of 4 bytes (256-byte aligned), or NULL.  A sequence whose length or page is out of range
+ *       is skipped (the page, for a page) and sets bit 0; the word is never cleared by this call and is
+ *       read with kda_workspace_status(check, 256, stream).
+ * A page must not belong to two sequences of one call.  k, v, lengths must not overlap the cache.
+ */
+kda_status_t kda_cache_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths,
+                              const kda_cache_t* cache, const kda_attention_t* problem, uint32_t* check, void* stream);
+
+/* Bytes of device workspace kda_attention_decode needs (0 if the descriptor is invalid). */
+size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem);
+
+/*
+ * The newest L tokens of each of N sequences attend to the paged 8-bit cache, which holds their
+ * keys and values already (kda_cache_append): one token per sequence, or a drafted window as in
+ * kda_decode_replay ("Kimi K3: architecture, derivations and a pinned-source audit", section 10.3).
+ * Token t of the window sees the first lengths[n] - L + t + 1 keys of its sequence.
+ *
+ *   q : [N*L, num_heads, head_dim] io dtype, token t of sequence n at row n*L + t, q_stride as for
+ *       kda_attention_prefill.
+ *   lengths : [N] int32 on the device, keys of each sequence in the cache, the window's included.
+ *   out : [N*L, num_heads, head_dim] io dtype, packed; must not overlap any argument.
+ *   problem : total_tokens = N*L with L >= 1.
+ *   workspace : kda_attention_decode_workspace_bytes(problem) bytes, 256-byte aligned, not shared
+ *       with a concurrently running call.
+ * A length outside [0, max_pages * page_tokens] counts as 0 and a page outside [0, num_pages) as
+ * not there; kda_workspace_status(workspace, ...) then reports KDA_ERR_DEVICE_CHECK.  Codes enter
+ * the products exactly; q and the weights enter as f16 (fp32 io: as sums of two f16 parts).
+ */
+kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const kda_cache_t* cache, void* out,
+                                  const kda_attention_t* problem, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kda_forward for callers that cannot allocate device memory: a library or plugin that runs
  * inside a host application which owns every device allocation (its own pool or arena) and gives
  * the plugin no allocator, or a latency-critical path that must not enter the driver's allocator.

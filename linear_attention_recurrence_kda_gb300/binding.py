@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -28,6 +28,9 @@ KDA_ERR_DEVICE_CHECK = 6
 KDA_F32 = 0
 KDA_BF16 = 1
 
+KDA_CACHE_E4M3 = 0
+KDA_CACHE_INT8 = 1
+
 G_MIN = -5.0
 
 # Every symbol include/kda.h declares.
@@ -35,7 +38,9 @@ EXPORTS = ("kda_forward_workspace_bytes", "kda_forward", "kda_decode_step", "kda
            "kda_status_string", "kda_profile_enable", "kda_profile_read", "kda_abi_version",
            "kda_forward_static_scratch", "kda_forward_plan", "kda_decode_replay", "kda_prologue",
            "kda_epilogue", "kda_static_scratch_status", "kda_backward_workspace_bytes", "kda_backward",
-           "kda_forward_summary_workspace_bytes", "kda_forward_summary", "kda_state_scan")
+           "kda_forward_summary_workspace_bytes", "kda_forward_summary", "kda_state_scan",
+           "kda_attention_prefill", "kda_cache_append", "kda_attention_decode_workspace_bytes",
+           "kda_attention_decode")
 
 # Size of the library's own scratch array used by kda_forward_static_scratch.
 KDA_STATIC_SCRATCH_BYTES = 8 << 20
@@ -57,6 +62,30 @@ class KdaProblem(ctypes.Structure):
 class KdaKernelTime(ctypes.Structure):
     """Mirror of kda_kernel_time_t."""
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
+
+
+class KdaAttention(ctypes.Structure):
+    """Mirror of kda_attention_t."""
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class KdaCache(ctypes.Structure):
+    """Mirror of kda_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class KvCache(NamedTuple):
+    """A paged 8-bit cache: codes [num_pages, num_kv_heads, page_tokens, head_dim] (float8_e4m3fn or
+    int8) and one fp32 scale for each page and head [num_pages, num_kv_heads]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
 
 
 class KdaError(RuntimeError):
@@ -116,6 +145,15 @@ def lib():
             L.kda_static_scratch_status.argtypes = [_vp]
             L.kda_forward_plan.restype = ctypes.c_int
             L.kda_forward_plan.argtypes = [P, ctypes.c_size_t, ctypes.POINTER(KdaPlan)]
+            PA, PC = ctypes.POINTER(KdaAttention), ctypes.POINTER(KdaCache)
+            L.kda_attention_prefill.restype = ctypes.c_int
+            L.kda_attention_prefill.argtypes = [_vp] * 5 + [PA, _vp]
+            L.kda_cache_append.restype = ctypes.c_int
+            L.kda_cache_append.argtypes = [_vp] * 4 + [PC, PA, _vp, _vp]
+            L.kda_attention_decode_workspace_bytes.restype = ctypes.c_size_t
+            L.kda_attention_decode_workspace_bytes.argtypes = [PA]
+            L.kda_attention_decode.restype = ctypes.c_int
+            L.kda_attention_decode.argtypes = [_vp, _vp, PC, _vp, PA, _vp, ctypes.c_size_t, _vp]
             L.kda_abi_version.restype = ctypes.c_uint32
             L.kda_abi_version.argtypes = []
             _lib = L
@@ -486,9 +524,163 @@ def kda_epilogue(o, gate, weight, eps: float = 1e-5, y=None, stream=None):
     return y
 
 
+_IO = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_CODES = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
+
+
+def _tokens(t, name, dtype, heads, d, device):
+    """Checks t [T, heads, d] with packed heads and channels; returns its stride between tokens."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, {heads}, {d})")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: heads and channels must be packed (strides {t.stride()})")
+    if t.shape[0] <= 1:
+        return heads * d
+    if t.stride(0) < heads * d:
+        raise ValueError(f"{name}: tokens overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _io_dtype(t, name):
+    if t.dtype not in _IO:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {tuple(_IO)}")
+    return _IO[t.dtype]
+
+
+def _cache(cache, block_table, N, hkv, d, device):
+    """The KdaCache descriptor of a KvCache and its block table."""
+    k, v, k_scale, v_scale = cache
+    if k.dtype not in _CODES:
+        raise TypeError(f"cache.k: dtype {k.dtype}, expected one of {tuple(_CODES)}")
+    if k.dim() != 4:
+        raise ValueError(f"cache.k: shape {tuple(k.shape)}, expected (pages, heads, page_tokens, head_dim)")
+    pages, _, page, _ = k.shape
+    _need(k, "cache.k", k.dtype, (pages, hkv, page, d), device)
+    _need(v, "cache.v", k.dtype, (pages, hkv, page, d), device)
+    _need(k_scale, "cache.k_scale", torch.float32, (pages, hkv), device)
+    _need(v_scale, "cache.v_scale", torch.float32, (pages, hkv), device)
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: shape {tuple(block_table.shape)}, expected (sequences, pages)")
+    cols = block_table.shape[1]
+    _need(block_table, "block_table", torch.int32, (N, cols), device)
+    return KdaCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), pages,
+                    page, cols, _CODES[k.dtype])
+
+
+def kda_cache_alloc(num_pages: int, page_tokens: int, num_kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,
+                    device="cuda") -> KvCache:
+    """An empty :class:`KvCache` (codes and scales zero)."""
+    codes = [torch.zeros((num_pages, num_kv_heads, page_tokens, head_dim), dtype=torch.uint8, device=device).view(dtype)
+             for _ in range(2)]
+    scales = [torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KvCache(*codes, *scales)
+
+
+def kda_attention_prefill(q, k, v, cu_seqlens=None, num_seqs: Optional[int] = None, scale: Optional[float] = None,
+                          out=None, stream=None):
+    """Causal attention over packed prompts with grouped heads (see include/kda.h): q [T, Hq, d],
+    k, v [T, Hkv, d] in bf16 or fp32, d in {32, 64, 128}; tokens may be strided (views of one
+    projection), heads and channels packed.  cu_seqlens [N+1] int32 on the device, or None
+    (``num_seqs`` equal lengths, default 1).  ``scale`` defaults to d ** -0.5.  Returns out
+    [T, Hq, d]."""
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    dev, dt = q.device, q.dtype
+    io = _io_dtype(q, "q")
+    qs, ks, vs = (_tokens(q, "q", dt, Hq, d, dev), _tokens(k, "k", dt, Hkv, d, dev), _tokens(v, "v", dt, Hkv, d, dev))
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k, v hold {T}, {k.shape[0]}, {v.shape[0]} tokens")
+    if cu_seqlens is not None:
+        N = cu_seqlens.shape[0] - 1
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+    else:
+        _need(out, "out", dt, (T, Hq, d), dev)
+    prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, ks, vs)
+    st = lib().kda_attention_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     None if cu_seqlens is None else cu_seqlens.data_ptr(), out.data_ptr(),
+                                     ctypes.byref(prob), _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attention_prefill")
+    return out
+
+
+def kda_cache_append(k, v, cache: KvCache, block_table, lengths, cu_seqlens=None, check=None, stream=None) -> None:
+    """Appends new tokens' keys and values to a paged 8-bit cache (see include/kda.h): k, v
+    [T, Hkv, d] (strides as for :func:`kda_attention_prefill`); block_table [N, pages] int32;
+    lengths [N] int32, tokens of each sequence with the new ones; cu_seqlens [N+1] int32 offsets of
+    every sequence's new tokens, or None for T / N each.  ``check``: a uint32 or int32 tensor of 64
+    elements, zeroed by the caller, that collects out-of-range lengths and pages (read it with
+    :func:`kda_workspace_status`)."""
+    T, Hkv, d = k.shape
+    dev, dt = k.device, k.dtype
+    io = _io_dtype(k, "k")
+    N = lengths.shape[0]
+    ks, vs = _tokens(k, "k", dt, Hkv, d, dev), _tokens(v, "v", dt, Hkv, d, dev)
+    if v.shape[0] != T:
+        raise ValueError(f"k, v hold {T}, {v.shape[0]} tokens")
+    _need(lengths, "lengths", torch.int32, (N,), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    if check is not None and (check.numel() * check.element_size() < 256 or not check.is_contiguous() or check.device != dev):
+        raise ValueError("check: 256 contiguous bytes on the inputs' device are needed")
+    c = _cache(cache, block_table, N, Hkv, d, dev)
+    prob = KdaAttention(N, T, Hkv, Hkv, d, io, 1.0, 0, ks, vs)
+    st = lib().kda_cache_append(k.data_ptr(), v.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                                lengths.data_ptr(), ctypes.byref(c), ctypes.byref(prob), _ptr(check), _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_cache_append")
+
+
+def kda_attention_decode_workspace_bytes(problem: KdaAttention) -> int:
+    return int(lib().kda_attention_decode_workspace_bytes(ctypes.byref(problem)))
+
+
+def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optional[float] = None, out=None,
+                         workspace=None, stream=None):
+    """The newest L tokens of each of N sequences attend to the cache, which holds their keys and
+    values already (see include/kda.h): q [N*L, Hq, d], token t of sequence n at row n*L + t;
+    block_table [N, pages] int32; lengths [N] int32, keys in the cache with the window's.  Token t
+    sees the first lengths[n] - L + t + 1 keys.  Returns out [N*L, Hq, d]."""
+    T, Hq, d = q.shape
+    N = lengths.shape[0]
+    Hkv = cache.k.shape[1] if cache.k.dim() == 4 else 0
+    dev, dt = q.device, q.dtype
+    io = _io_dtype(q, "q")
+    qs = _tokens(q, "q", dt, Hq, d, dev)
+    _need(lengths, "lengths", torch.int32, (N,), dev)
+    c = _cache(cache, block_table, N, Hkv, d, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+    else:
+        _need(out, "out", dt, (T, Hq, d), dev)
+    prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, 0, 0)
+    if workspace is None:
+        wsb = kda_attention_decode_workspace_bytes(prob)
+        if wsb == 0:
+            raise KdaError(KDA_ERR_INVALID_ARG, "kda_attention_decode_workspace_bytes")
+        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)  # not reused by the current stream before `stream` is done with it
+    st = lib().kda_attention_decode(q.data_ptr(), lengths.data_ptr(), ctypes.byref(c), out.data_ptr(),
+                                    ctypes.byref(prob), workspace.data_ptr(),
+                                    ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attention_decode")
+    return out
+
+
 def kda_workspace_status(workspace, stream=None) -> int:
     """Synchronise and return the device-side check status of a forward workspace."""
-    return int(lib().kda_workspace_status(_ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream(stream)))
+    return int(lib().kda_workspace_status(
+        _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream)))
 
 
 def kda_static_scratch_status(stream=None) -> int:

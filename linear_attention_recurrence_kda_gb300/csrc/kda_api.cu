@@ -9,33 +9,15 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "kda_checks.cuh"
 #include "kda_internal.cuh"
 
 using kda::ForwardLayout;
+using namespace kda::checks;
 
 namespace {
 
 bool supported_dim(int32_t d) { return d == 32 || d == 64 || d == 128; }
-
-size_t io_size(kda_dtype_t dt) { return dt == KDA_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + bytes};
-}
-
-bool overlaps(Range a, Range b)
-{
-    if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
 
 enum class Call { Forward, Decode, Replay };
 
@@ -59,25 +41,6 @@ kda_status_t check_descriptor(const kda_problem_t* p, Call call)
         if (p->total_tokens / p->num_seqs > 2147483647LL) return KDA_ERR_UNSUPPORTED;
     } else {
         if (p->max_seqlen < 0) return KDA_ERR_INVALID_ARG;
-    }
-    return KDA_OK;
-}
-
-// Device-accessible memory of the current device (or mapped pinned host memory).
-kda_status_t check_device_pointer(const void* p)
-{
-    if (p == nullptr) return KDA_OK;
-    cudaPointerAttributes attr;
-    cudaError_t e = cudaPointerGetAttributes(&attr, p);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return e == cudaErrorInvalidValue ? KDA_ERR_INVALID_ARG : KDA_ERR_CUDA;
-    }
-    if (attr.devicePointer == nullptr) return KDA_ERR_INVALID_ARG;
-    if (attr.type == cudaMemoryTypeDevice) {
-        int dev = -1;
-        if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-        if (attr.device != dev) return KDA_ERR_INVALID_ARG;
     }
     return KDA_OK;
 }

@@ -1,0 +1,69 @@
+// kda_attn.cuh -- arguments and launchers of the softmax-attention kernels (declared in kda.h):
+// prompts (kda_attn_prefill.cu, kda_attn_prefill_tc.cu), the 8-bit paged cache (kda_cache.cu) and
+// the tokens that read it (kda_attn_decode.cu).
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kMaxGroup = 128;  // query heads that may share a key head: a tile's rows
+
+struct AttnArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* cu;  // NULL: N equal lengths
+    void* out;
+    int64_t T;
+    int64_t qs, ks, vs;  // elements between tokens
+    int32_t N, Hq, Hkv, group, d;
+    float scale;
+};
+
+struct CacheArgs {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* table;
+    int32_t num_pages, page, max_pages;
+    kda_cache_dtype_t dtype;
+};
+
+struct AppendArgs {
+    const void* k;
+    const void* v;
+    const int32_t* cu;       // NULL: T / N new tokens each
+    const int32_t* lengths;  // with the new tokens
+    uint32_t* check;         // NULL, or a word whose kCheckBadSeqlens bit is set on a bad length or page
+    int64_t T, ks, vs;
+    int32_t N, Hkv, d;
+    CacheArgs c;
+};
+
+struct AttnDecodeArgs {
+    const void* q;
+    const int32_t* lengths;
+    void* out;
+    unsigned char* ws;
+    int64_t qs;
+    int32_t N, L, Hq, Hkv, group, d;
+    float scale;
+    CacheArgs c;
+};
+
+cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t s);
+cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
+size_t attn_decode_workspace_bytes(int rows, int d);
+
+// cuTensorMapEncodeTiled of the loaded driver, or NULL (kda_attn_api.cu).
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncode attn_tensor_map_encoder();
+
+}  // namespace kda

@@ -1,0 +1,803 @@
+// kda_attn_decode.cu -- the newest tokens of every sequence attend to the paged 8-bit cache
+// (kda_attention_decode).
+//
+// A unit is one sequence, one key head and up to 16 rows (query heads of the group x tokens of the
+// window); its keys come in tiles of 32.  The work is cut evenly: with W workers (warps) and all
+// units' tiles in one line, worker w takes tiles [w total / W, (w + 1) total / W), whatever the
+// lengths are.  A worker that holds all of a unit writes its output; otherwise it leaves (max, sum,
+// unnormalised output) in the workspace, and the combine kernel joins the pieces in order.
+//
+// Per tile a warp does, with m16n8k16 f16 products and fp32 accumulators,
+//   z = scale ks (Q K^T),  m' = max(m, max z),  p = 2^(z - m'),  O = O 2^(m - m') + p V,  l likewise
+// K and V codes become f16 exactly (e4m3 and int8 are subsets of f16).  A row of q is scaled by a
+// power of two so that its largest value lies in [2^14, 2^15): bf16 values are then exact in f16 down
+// to 2^-38 of the row's largest; fp32 values are split into two f16 parts (22 bits), as are their p.
+// V's scale goes into O's unit: O is held in units of `vu`, which follows the pages' scales.
+//
+// HBM bounds it (2 d bytes per key and head, and a group of query heads per byte is far below the
+// tensor cores' rate), so each warp keeps its own ring of tiles in flight by TMA with no barrier
+// between warps; the 128-byte swizzle frees ldmatrix of bank conflicts, and a 16-byte chunk of a
+// K row serves one k-step with q's channels permuted to match what ldmatrix hands each thread.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "kda_attn.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTile = 32;     // keys per tile
+constexpr int kRows = 16;     // rows of a unit
+constexpr int kWarps = 4;     // workers per CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 2;
+constexpr uint32_t kCopyTries = 1u << 17;  // of up to 20 us each
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int stages_of(int d) { return d == 128 ? 3 : d == 64 ? 6 : 8; }
+
+// Workspace: check word | per-CTA flags | records | (max, sum) of slots | outputs of slots.
+// Worker w owns slots 2 w (a unit begun by an earlier worker) and 2 w + 1 (begun here).
+struct Record {
+    int32_t n, h, rt, last;  // unit and the last worker that holds a piece of it; n < 0: none
+};
+
+struct DecodeLayout {
+    size_t flags, records, ml, o, total;
+};
+
+__host__ __device__ inline DecodeLayout decode_layout(int workers, int rows, int d)
+{
+    DecodeLayout L;
+    size_t at = 256;
+    L.flags = at;
+    at += ((size_t)workers / kWarps * 4 + 255) / 256 * 256;
+    L.records = at;
+    at += ((size_t)workers * sizeof(Record) + 255) / 256 * 256;
+    L.ml = at;
+    at += ((size_t)workers * 2 * rows * 8 + 255) / 256 * 256;
+    L.o = at;
+    at += (size_t)workers * 2 * rows * d * 4;
+    L.total = (at + 255) / 256 * 256;
+    return L;
+}
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// four codes (bytes of x, low first) to two pairs of f16
+template <bool kE4m3>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi)
+{
+    if constexpr (kE4m3) {
+        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
+        lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
+        hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+    } else {
+        // byte b ^ 0x80 = b + 128 under the exponent of 1024 is 1024 + 128 + b; 1152 comes off exactly
+        const uint32_t u = x ^ 0x80808080u;
+        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), g = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&g), off);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// the part of (lo, hi) that their f16 rounding `h` leaves
+__device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t h)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_f16(lo - f.x, hi - f.y);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t swizzle(uint32_t off)
+{
+    return off ^ (((off >> 7) & (D == 128 ? 7u : D == 64 ? 3u : 1u)) << 4);
+}
+
+// Tokens of sequence n that count: 0 where the length is out of range.
+__device__ __forceinline__ int length_of(const AttnDecodeArgs& a, int n, bool* bad = nullptr)
+{
+    const int len = a.lengths[n];
+    const bool ok = len >= 0 && (int64_t)len <= (int64_t)a.c.max_pages * a.c.page;
+    if (!ok && bad != nullptr) *bad = true;
+    return ok ? len : 0;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// A place in the line of tiles: unit (n, h, rt) and the tile i of its `tiles`.
+struct Cursor {
+    int n, h, rt, i, tiles, len;
+};
+
+__device__ __forceinline__ void next_tile(const AttnDecodeArgs& a, int row_tiles, Cursor& c)
+{
+    if (++c.i < c.tiles) return;
+    c.i = 0;
+    if (++c.rt < row_tiles) return;
+    c.rt = 0;
+    if (++c.h < a.Hkv) return;
+    c.h = 0;
+    do {
+        if (++c.n >= a.N) {
+            c.tiles = 0;
+            return;
+        }
+        c.len = length_of(a, c.n);
+        c.tiles = tiles_of(c.len);
+    } while (c.tiles == 0);
+}
+
+}  // namespace
+
+template <typename TIO, int D, bool kE4m3>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    kda_attn_decode_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps, const int rows_max)
+{
+    constexpr bool kSplit = sizeof(TIO) == 4;  // fp32: q and p as two f16 parts
+    constexpr int PARTS = kSplit ? 2 : 1;
+    constexpr int NCH = D / 16;                // 16-byte chunks of a row = k-steps of Q K^T
+    constexpr int S = stages_of(D);
+    constexpr uint32_t TB = kTile * D;         // bytes of a K (or V) tile
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int64_t prefix[kThreads + 1];
+    __shared__ alignas(8) uint64_t full[kWarps][S];
+    __shared__ int pages[kWarps][S][2];
+    __shared__ uint32_t flag;
+
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, cq = lane & 3;
+    unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* ring = smem + (size_t)w * S * 2 * TB;
+    const DecodeLayout L = decode_layout(gridDim.x * kWarps, rows_max, D);
+    const int rows_all = a.L * a.group;
+    const int row_tiles = (rows_all + kRows - 1) / kRows;
+    const int64_t per_tile = (int64_t)a.Hkv * row_tiles;
+
+    griddep_launch_dependents();
+    if (tid == 0) flag = 0u;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) tc::mbar_init(&full[w][i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // tiles before every run of `chunk` sequences
+    const int chunk = (a.N + kThreads - 1) / kThreads;
+    {
+        int64_t sum = 0;
+        bool bad = false;
+        for (int i = 0; i < chunk; ++i) {
+            const int n = tid * chunk + i;
+            if (n < a.N) sum += tiles_of(length_of(a, n, &bad));
+        }
+        int64_t x = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        prefix[tid + 1] = x;
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+        if (bad) atomicOr(&flag, kCheckBadSeqlens);
+        int64_t before = 0;
+        for (int i = 0; i < w; ++i) before += prefix[(i + 1) * 32];
+        __syncthreads();
+        prefix[tid + 1] = x + before;
+        __syncthreads();
+    }
+    // a sequence with nothing in the cache: rows of zeros
+    const int64_t tokrow = (int64_t)a.Hq * D;
+    for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+        if (length_of(a, n) == 0) {
+            TIO* o = static_cast<TIO*>(a.out) + (int64_t)n * a.L * tokrow;
+            for (int64_t i = tid; i < a.L * tokrow; i += kThreads) st_io(o, i, 0.f);
+        }
+    }
+    const int64_t total = prefix[kThreads] * per_tile;
+    const int64_t W = min((int64_t)gridDim.x * kWarps, total);
+    const int64_t worker = (int64_t)blockIdx.x * kWarps + w;
+    Record* rec = reinterpret_cast<Record*>(a.ws + L.records) + worker;
+    float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
+    float* po = reinterpret_cast<float*>(a.ws + L.o);
+    Record mine{-1, 0, 0, 0};
+    if (worker < W) {
+        const int64_t b0 = worker * total / W, b1 = (worker + 1) * total / W;
+        // the unit that holds tile b0: a run of sequences by bisection, then one by one
+        Cursor cc;
+        {
+            int lo = 0, hi = kThreads - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (prefix[mid] * per_tile <= b0) lo = mid;
+                else hi = mid - 1;
+            }
+            int64_t at = prefix[lo] * per_tile;
+            cc.n = lo * chunk;
+            for (;;) {
+                cc.len = length_of(a, cc.n);
+                cc.tiles = tiles_of(cc.len);
+                const int64_t here = cc.tiles * per_tile;
+                if (at + here > b0 || cc.n + 1 >= a.N) break;
+                at += here;
+                ++cc.n;
+            }
+            const int64_t rest = b0 - at;
+            const int64_t unit = rest / cc.tiles;
+            cc.i = (int)(rest - unit * cc.tiles);
+            cc.h = (int)(unit / row_tiles);
+            cc.rt = (int)(unit - (int64_t)cc.h * row_tiles);
+        }
+        Cursor ic = cc;
+        const int count = (int)(b1 - b0);
+        const int box = min(kTile, a.c.page);  // rows of one copy
+        bool gone = false;                     // a wait gave up
+
+        auto page_id = [&](const Cursor& c, int piece) -> int {
+            const int key = c.i * kTile + piece * box;
+            if (key >= c.len) return -1;
+            const int p = __ldg(a.c.table + (int64_t)c.n * a.c.max_pages + key / a.c.page);
+            return p;
+        };
+        int p0 = page_id(ic, 0), p1 = box < kTile ? page_id(ic, 1) : -1;
+        // the next tile of the issuing cursor into its stage
+        auto issue = [&](int it) {
+            const int st = it % S;
+            bool ok0 = p0 >= 0 && p0 < a.c.num_pages, ok1 = p1 >= 0 && p1 < a.c.num_pages;
+            const int key = ic.i * kTile;
+            if ((key < ic.len && !ok0) || (box < kTile && key + box < ic.len && !ok1)) {
+                if (lane == 0) atomicOr(&flag, kCheckBadSeqlens);
+            }
+            if (lane == 0) {
+                pages[w][st][0] = ok0 ? p0 : -1;
+                pages[w][st][1] = box < kTile ? (ok1 ? p1 : -1) : (ok0 ? p0 : -1);
+                const uint32_t bytes = (uint32_t)((ok0 ? 1 : 0) + (ok1 ? 1 : 0)) * 2u * box * D;
+                tc::mbar_arrive_expect_tx(&full[w][st], bytes);
+                unsigned char* kd = ring + (size_t)st * 2 * TB;
+                const int slot = key & (a.c.page - 1);
+                if (ok0) {
+                    tc::tma_load_3d(kd, &maps.k, 0, slot, p0 * a.Hkv + ic.h, &full[w][st]);
+                    tc::tma_load_3d(kd + TB, &maps.v, 0, slot, p0 * a.Hkv + ic.h, &full[w][st]);
+                }
+                if (ok1) {
+                    tc::tma_load_3d(kd + box * D, &maps.k, 0, 0, p1 * a.Hkv + ic.h, &full[w][st]);
+                    tc::tma_load_3d(kd + TB + box * D, &maps.v, 0, 0, p1 * a.Hkv + ic.h, &full[w][st]);
+                }
+            }
+            next_tile(a, row_tiles, ic);
+            if (it + 1 < count) {
+                p0 = page_id(ic, 0);
+                p1 = box < kTile ? page_id(ic, 1) : -1;
+            }
+        };
+        int issued = 0;
+        while (issued < count && issued < S) issue(issued++);
+
+        uint32_t qf[PARTS][NCH][4];
+        float O[NCH][2][4];
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f, vu = 0.f, vtop = 0.f;
+        int seen0 = 0, seen1 = 0;  // keys that this thread's two rows see
+        bool begun = false;
+        auto row_of = [&](int r, int& t, int& head) {
+            const int R = cc.rt * kRows + r;
+            t = R / a.group;
+            head = cc.h * a.group + (R - t * a.group);
+            return R < rows_all;
+        };
+        auto start_unit = [&]() {
+            float x[2][NCH][4];
+            float mx[2];
+            int seen[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                int t, head;
+                const bool ok = row_of(g + 8 * u, t, head);
+                seen[u] = ok ? cc.len - a.L + t + 1 : 0;
+                mx[u] = 0.f;
+                const TIO* q = static_cast<const TIO*>(a.q) + ((int64_t)cc.n * a.L + t) * a.qs + (int64_t)head * D + 4 * cq;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    if constexpr (kSplit) {
+                        const float4 v = ok ? *reinterpret_cast<const float4*>(q + 16 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[u][c][0] = v.x; x[u][c][1] = v.y; x[u][c][2] = v.z; x[u][c][3] = v.w;
+                    } else {
+                        const uint2 v = ok ? *reinterpret_cast<const uint2*>(q + 16 * c) : make_uint2(0u, 0u);
+                        x[u][c][0] = __uint_as_float(v.x << 16);
+                        x[u][c][1] = __uint_as_float(v.x & 0xffff0000u);
+                        x[u][c][2] = __uint_as_float(v.y << 16);
+                        x[u][c][3] = __uint_as_float(v.y & 0xffff0000u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[u] = fmaxf(mx[u], fabsf(x[u][c][e]));
+                }
+                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+            }
+            // a power of two brings the row's largest value to [2^14, 2^15)
+            float f[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                int e = (int)((__float_as_uint(mx[u]) >> 23) & 0xffu) - 127;
+                e = min(max(e, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e), exponents -113 .. 114
+                f[u] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][c][i] *= up;
+            }
+            f0 = f[0] * a.scale * kLog2e;
+            f1 = f[1] * a.scale * kLog2e;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                qf[0][c][0] = pack_f16(x[0][c][0], x[0][c][1]);
+                qf[0][c][1] = pack_f16(x[1][c][0], x[1][c][1]);
+                qf[0][c][2] = pack_f16(x[0][c][2], x[0][c][3]);
+                qf[0][c][3] = pack_f16(x[1][c][2], x[1][c][3]);
+                if constexpr (kSplit) {
+                    qf[PARTS - 1][c][0] = rest_f16(x[0][c][0], x[0][c][1], qf[0][c][0]);
+                    qf[PARTS - 1][c][1] = rest_f16(x[1][c][0], x[1][c][1], qf[0][c][1]);
+                    qf[PARTS - 1][c][2] = rest_f16(x[0][c][2], x[0][c][3], qf[0][c][2]);
+                    qf[PARTS - 1][c][3] = rest_f16(x[1][c][2], x[1][c][3], qf[0][c][3]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[c][u][i] = 0.f;
+            }
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
+            vu = vtop = 0.f;
+            seen0 = seen[0];
+            seen1 = seen[1];
+        };
+        // this segment's result: the output where the whole unit was here, else a piece
+        auto finish = [&](bool whole, int slot) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                int t, head;
+                const int r = g + 8 * u;
+                if (!row_of(r, t, head)) continue;
+                const float l = u ? l1 : l0;
+                const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
+                float* pd = po + ((int64_t)slot * rows_max + r) * D;
+                TIO* od = static_cast<TIO*>(a.out) + ((int64_t)cc.n * a.L + t) * tokrow + (int64_t)head * D;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    // channels 16 c + 4 cq + {0, 1, 2, 3}: even ones from the first product, odd from the second
+                    const float4 o = make_float4(O[c][0][2 * u] * mul, O[c][1][2 * u] * mul, O[c][0][2 * u + 1] * mul,
+                                                 O[c][1][2 * u + 1] * mul);
+                    if (!whole) {
+                        *reinterpret_cast<float4*>(pd + 16 * c + 4 * cq) = o;
+                    } else if constexpr (kSplit) {
+                        *reinterpret_cast<float4*>(od + 16 * c + 4 * cq) = o;
+                    } else {
+                        *reinterpret_cast<uint2*>(od + 16 * c + 4 * cq) =
+                            make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
+                    }
+                }
+                if (!whole && cq == 0) ml[(int64_t)slot * rows_max + r] = make_float2(u ? m1 : m0, l);
+            }
+        };
+
+        float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;
+        bool has0 = false, has1 = false;
+        auto load_scales = [&](int st, int h) {
+            const int q0 = pages[w][st][0], q1 = pages[w][st][1];
+            has0 = q0 >= 0;
+            has1 = q1 >= 0;
+            ks0 = has0 ? __ldg(a.c.k_scale + (int64_t)q0 * a.Hkv + h) : 0.f;
+            vs0 = has0 ? __ldg(a.c.v_scale + (int64_t)q0 * a.Hkv + h) : 0.f;
+            ks1 = q1 == q0 ? ks0 : has1 ? __ldg(a.c.k_scale + (int64_t)q1 * a.Hkv + h) : 0.f;
+            vs1 = q1 == q0 ? vs0 : has1 ? __ldg(a.c.v_scale + (int64_t)q1 * a.Hkv + h) : 0.f;
+        };
+        for (int it = 0; it < count && !gone; ++it) {
+            const int st = it % S;
+            if (!begun) {
+                start_unit();
+                begun = true;
+            }
+            __syncwarp();
+            load_scales(st, cc.h);
+            const bool arrived = tc::mbar_wait(&full[w][st], (uint32_t)(it / S) & 1u, kCopyTries);
+            if (!__all_sync(0xffffffffu, arrived)) {
+                gone = true;
+                break;
+            }
+            unsigned char* kt = ring + (size_t)st * 2 * TB;
+            unsigned char* vt = kt + TB;
+            const uint32_t ka = tc::smem_u32(kt), va = tc::smem_u32(vt);
+            const int key0 = cc.i * kTile;
+            // rows of the tile that hold no key of this sequence: V must not reach the product
+            const bool partial = key0 + kTile > cc.len || !has0 || !has1;
+            if (partial) {
+                for (int i = lane; i < (int)TB / 16; i += 32) {
+                    const int r = i * 16 / D;
+                    const bool dead = key0 + r >= cc.len || !(r < 16 ? has0 : has1);
+                    // the swizzle permutes 16-byte chunks within a row (or within the rows that share 128 bytes)
+                    if (dead) *reinterpret_cast<uint4*>(vt + swizzle<D>((uint32_t)i * 16)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+            }
+            // a key of the window is hidden from the window's earlier rows: a NaN in its value must
+            // not reach them, so it leaves the tile here and joins the rows that see it below
+            if (kE4m3 && a.L > 1 && key0 + kTile > cc.len - a.L + 1) {
+                const int from = max(0, cc.len - a.L + 1 - key0), to = min(kTile, cc.len - key0);
+                for (int r = from; r < to; ++r) {
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) {
+                        uint32_t* at = reinterpret_cast<uint32_t*>(vt + swizzle<D>((uint32_t)(r * D + 16 * c)) + 4 * cq);
+                        const uint32_t u = *at;
+                        const uint32_t nan = __vcmpeq4(u & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        if (nan != 0u) {
+                            // bytes 0, 2 belong to the even channels' product, 1, 3 to the odd one's
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((nan >> (8 * e)) & 1u) {
+                                    if (key0 + r < seen0) O[c][e & 1][e >> 1] = NAN;
+                                    if (key0 + r < seen1) O[c][e & 1][2 + (e >> 1)] = NAN;
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    for (int i = lane; i < D / 4; i += 32) {
+                        uint32_t* at = reinterpret_cast<uint32_t*>(vt + swizzle<D>((uint32_t)(r * D + (i / 4) * 16)) + 4 * (i & 3));
+                        *at &= ~__vcmpeq4(*at & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    }
+                    __syncwarp();
+                }
+                tc::fence_async_smem();
+            }
+
+            // z = q K^T over the four groups of eight keys
+            float z[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] = 0.f;
+            if constexpr (D >= 64) {
+#pragma unroll
+                for (int c = 0; c < NCH; c += 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t r[4];
+                        const int row = 8 * j + (lane & 7), ch = c + (lane >> 3);
+                        ldsm4(r, ka + swizzle<D>((uint32_t)(row * D + ch * 16)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t b0, b1;
+                            widen<kE4m3>(r[i], b0, b1);
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p) mma_f16(z[j], qf[p][c + i], b0, b1);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    uint32_t r[4];
+                    const int row = 8 * (j + (lane >> 4)) + (lane & 7), ch = (lane >> 3) & 1;
+                    ldsm4(r, ka + swizzle<D>((uint32_t)(row * D + ch * 16)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b0, b1;
+                        widen<kE4m3>(r[i], b0, b1);
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) mma_f16(z[j + (i >> 1)], qf[p][i & 1], b0, b1);
+                    }
+                }
+            }
+            // scores in base 2: z s, their maxima over the keys that are seen
+            float t0 = -INFINITY, t1 = -INFINITY;
+            const bool edge = partial || key0 + kTile > cc.len - a.L + 1;
+            uint32_t hid0 = 0u, hid1 = 0u;  // bit 2 j + e: key 8 j + 2 cq + e is hidden from the row
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = key0 + 8 * j + 2 * cq + e;
+                        const bool there = j < 2 ? has0 : has1;
+                        if (key >= seen0 || !there) hid0 |= 1u << (2 * j + e);
+                        if (key >= seen1 || !there) hid1 |= 1u << (2 * j + e);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float s0 = f0 * (j < 2 ? ks0 : ks1), s1 = f1 * (j < 2 ? ks0 : ks1);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!((hid0 >> (2 * j + e)) & 1u)) t0 = fmaxf(t0, z[j][e] * s0);
+                    if (!((hid1 >> (2 * j + e)) & 1u)) t1 = fmaxf(t1, z[j][2 + e] * s1);
+                }
+            }
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+            float a0 = ex2(m0 - u0), a1 = ex2(m1 - u1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+            // p = 2^(z s - m) with one rounding of the difference
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float s0 = f0 * (j < 2 ? ks0 : ks1), s1 = f1 * (j < 2 ? ks0 : ks1);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float y0 = ex2(fmaf(z[j][e], s0, -u0)), y1 = ex2(fmaf(z[j][2 + e], s1, -u1));
+                    z[j][e] = (hid0 >> (2 * j + e)) & 1u ? 0.f : y0;
+                    z[j][2 + e] = (hid1 >> (2 * j + e)) & 1u ? 0.f : y1;
+                }
+                l0 += z[j][0] + z[j][1];
+                l1 += z[j][2] + z[j][3];
+            }
+            // O += p V, sixteen keys (at most one page) at a time
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float vs = s == 0 ? vs0 : vs1;
+                const float mag = fabsf(vs);
+                // O's unit follows V's scale, from it to 64 times it, but never falls under 2^-40 of the
+                // largest scale met (what is in O would grow past fp32): a page that far below
+                // adds nothing that fp32 could hold
+                float ratio = 1.f;
+                if (!(mag <= vu && mag * 64.f >= vu) && mag > 0.f && mag < INFINITY) {
+                    vtop = fmaxf(vtop, mag);
+                    const float nu = fmaxf(mag, vtop * 9.094947e-13f);
+                    ratio = vu == 0.f ? 0.f : vu / nu;
+                    vu = nu;
+                }
+                const float b0 = a0 * ratio, b1 = a1 * ratio;
+                a0 = a1 = 1.f;
+                if (__any_sync(0xffffffffu, b0 != 1.f || b1 != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            O[c][u][0] *= b0;
+                            O[c][u][1] *= b0;
+                            O[c][u][2] *= b1;
+                            O[c][u][3] *= b1;
+                        }
+                }
+                const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs / vu;
+                uint32_t pf[PARTS][4];
+                float y[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[j][i] = z[2 * s + j][i] * pv;
+                pf[0][0] = pack_f16(y[0][0], y[0][1]);
+                pf[0][1] = pack_f16(y[0][2], y[0][3]);
+                pf[0][2] = pack_f16(y[1][0], y[1][1]);
+                pf[0][3] = pack_f16(y[1][2], y[1][3]);
+                if constexpr (kSplit) {
+                    pf[PARTS - 1][0] = rest_f16(y[0][0], y[0][1], pf[0][0]);
+                    pf[PARTS - 1][1] = rest_f16(y[0][2], y[0][3], pf[0][1]);
+                    pf[PARTS - 1][2] = rest_f16(y[1][0], y[1][1], pf[0][2]);
+                    pf[PARTS - 1][3] = rest_f16(y[1][2], y[1][3], pf[0][3]);
+                }
+#pragma unroll
+                for (int c = 0; c < NCH; c += 2) {
+                    uint32_t r[4];
+                    const int row = 16 * s + (lane & 15), ch = c + (lane >> 4);
+                    ldsm4t(r, va + swizzle<D>((uint32_t)(row * D + ch * 16)));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t e0, e1, o0, o1;
+                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x6420), e0, e1);
+                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x7531), o0, o1);
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {
+                            mma_f16(O[c + i][0], pf[p], e0, e1);
+                            mma_f16(O[c + i][1], pf[p], o0, o1);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (issued < count) issue(issued++);
+
+            const bool unit_end = cc.i + 1 == cc.tiles;
+            if (unit_end || it + 1 == count) {
+                const bool here = (int64_t)cc.i <= it;  // the unit's first tile was this worker's
+                if (here && unit_end) {
+                    finish(true, 0);
+                } else {
+                    finish(false, (int)(2 * worker + (here ? 1 : 0)));
+                    if (here) {
+                        const int64_t e = b0 + it + (cc.tiles - cc.i);  // past the unit's last tile
+                        mine = Record{cc.n, cc.h, cc.rt, (int32_t)((e * W + total - 1) / total - 1)};
+                    }
+                }
+                begun = false;
+            }
+            next_tile(a, row_tiles, cc);
+        }
+        if (gone) {
+            // copies still in flight land in shared memory that the CTA gives back: wait for them
+            for (int it = 0; it < issued; ++it) {
+                if (it + S >= issued) (void)tc::mbar_wait(&full[w][it % S], (uint32_t)(it / S) & 1u, kCopyTries);
+            }
+            if (lane == 0) atomicOr(&flag, kCheckTimeout);
+            mine.n = -1;
+        }
+    }
+    if (lane == 0) *rec = mine;
+    __syncthreads();
+    if (tid == 0) reinterpret_cast<uint32_t*>(a.ws + L.flags)[blockIdx.x] = flag;
+}
+
+// Joins a unit's pieces: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the workers that hold
+// one, in order.  CTA w looks after the unit that worker w left unfinished, if any; a warp takes a
+// row at a time, a lane D / 32 channels.
+template <typename TIO, int D>
+__global__ void __launch_bounds__(128) kda_attn_combine_kernel(const AttnDecodeArgs a, const int rows_max)
+{
+    constexpr int V = D / 32;
+    const int workers = gridDim.x;
+    const DecodeLayout L = decode_layout(workers, rows_max, D);
+    const int lane = threadIdx.x & 31;
+    griddep_wait();
+    if (blockIdx.x == 0) {
+        // the call's check word: every CTA's flags, so that nothing has to be cleared before the call
+        __shared__ uint32_t word;
+        if (threadIdx.x == 0) word = 0u;
+        __syncthreads();
+        uint32_t f = 0u;
+        const uint32_t* flags = reinterpret_cast<const uint32_t*>(a.ws + L.flags);
+        for (int i = threadIdx.x; i < workers / kWarps; i += blockDim.x) f |= flags[i];
+        if (f) atomicOr(&word, f);
+        __syncthreads();
+        if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(a.ws) = word;
+    }
+    const int w0 = blockIdx.x;
+    const Record rec = reinterpret_cast<const Record*>(a.ws + L.records)[w0];
+    if (rec.n < 0) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.ws + L.ml);
+    const float* po = reinterpret_cast<const float*>(a.ws + L.o);
+    const int pieces = rec.last - w0 + 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
+    for (int r = threadIdx.x >> 5; r < rows_max; r += blockDim.x / 32) {
+        const int R = rec.rt * kRows + r;
+        if (R >= a.L * a.group) break;
+        float m = -INFINITY;
+        for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float mu = m == -INFINITY ? 0.f : m;
+        float l = 0.f, o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < pieces; ++i) {
+            const float2 x = ml[slot(i) * rows_max + r];
+            const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
+            const float f = ex2(x.x - mu);
+            l += x.y * f;
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(p);
+                o[0] += y.x * f; o[1] += y.y * f; o[2] += y.z * f; o[3] += y.w * f;
+            } else if constexpr (V == 2) {
+                const float2 y = *reinterpret_cast<const float2*>(p);
+                o[0] += y.x * f; o[1] += y.y * f;
+            } else {
+                o[0] += *p * f;
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int t = R / a.group, head = rec.h * a.group + (R - t * a.group);
+        TIO* od = static_cast<TIO*>(a.out) + (((int64_t)rec.n * a.L + t) * a.Hq + head) * D + lane * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
+    }
+}
+
+namespace {
+
+bool encode_codes(CUtensorMap* m, const void* base, const AttnDecodeArgs& a)
+{
+    const TensorMapEncode enc = attn_tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.c.page, (cuuint64_t)a.c.num_pages * a.Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.d, (cuuint64_t)a.d * a.c.page};
+    const cuuint32_t box[3] = {(cuuint32_t)a.d, (cuuint32_t)(a.c.page < kTile ? a.c.page : kTile), 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUtensorMapSwizzle sw = a.d == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : a.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_32B;
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int decode_ctas() { return kCtasPerSm * sm_count_of_current_device(); }
+
+template <typename TIO, int D, bool kE4m3>
+cudaError_t launch_decode_d(const AttnDecodeArgs& a, cudaStream_t s)
+{
+    Maps maps;
+    if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
+    constexpr int smem = kWarps * stages_of(D) * 2 * kTile * D + 1024;
+    static_assert(kCtasPerSm * (smem + 4096) <= 232448, "the rings of an SM's CTAs fit");
+    auto kern = kda_attn_decode_kernel<TIO, D, kE4m3>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int rows = a.L * a.group < kRows ? a.L * a.group : kRows;
+    kern<<<decode_ctas(), kThreads, smem, s>>>(a, maps, rows);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kda_attn_combine_kernel<TIO, D>, dim3((unsigned)(decode_ctas() * kWarps)), dim3(128), 0, s, a, rows);
+}
+
+template <typename TIO, bool kE4m3>
+cudaError_t launch_decode_io(const AttnDecodeArgs& a, cudaStream_t s)
+{
+    if (a.d == 32) return launch_decode_d<TIO, 32, kE4m3>(a, s);
+    if (a.d == 64) return launch_decode_d<TIO, 64, kE4m3>(a, s);
+    return launch_decode_d<TIO, 128, kE4m3>(a, s);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace_bytes(int rows, int d) { return decode_layout(decode_ctas() * kWarps, rows, d).total; }
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s)
+{
+    const bool e4m3 = a.c.dtype == KDA_CACHE_E4M3;
+    if (dt == KDA_BF16) return e4m3 ? launch_decode_io<__nv_bfloat16, true>(a, s) : launch_decode_io<__nv_bfloat16, false>(a, s);
+    return e4m3 ? launch_decode_io<float, true>(a, s) : launch_decode_io<float, false>(a, s);
+}
+
+}  // namespace kda
