@@ -56,6 +56,7 @@ struct AttnDecodeArgs {
 };
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t s);
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16, d = 64 or 128
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
 size_t attn_decode_workspace_bytes(int rows, int d);

@@ -322,6 +322,7 @@ cudaError_t launch_io(const AttnArgs& a, cudaStream_t s)
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t s)
 {
+    if (dt == KDA_BF16 && a.d != 32) return launch_attn_prefill_tc(a, s);
     return dt == KDA_BF16 ? launch_io<__nv_bfloat16>(a, s) : launch_io<float>(a, s);
 }
 
