@@ -37,12 +37,13 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTries = 1u << 17;  // of up to 20 us each
 // warpgroups' registers after the split: 256 x 208 + 128 x 88 = 384 x 168, what the launch holds
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kInfoReaders = 8 + 3;  // softmax warps, products, copies, cleaner
 
 template <int D> struct Cfg {
     static constexpr int NB = D / 64;                        // 64-channel blocks of a row
     static constexpr uint32_t BLK = 128 * 128;               // bytes of a block: 128 rows of 128 bytes
     static constexpr uint32_t TILE = NB * BLK;
-    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
 };
 
@@ -50,12 +51,24 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-struct Shared {
-    uint64_t q_full, kv_full[8], kv_empty[8], z_full[2], p_full[2], o_full[2], drained;
-    uint64_t v_load[4], v_clean[4];  // V tile `edge` + e on barriers e % 4: the ring holds at most four
-    uint32_t tmem, dead;
-    int odd[3][128];
+struct TileInfo {
+    int64_t start;
+    int first, last, head, valid;
 };
+
+struct Shared {
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], z_full[2], p_full[2], o_full[2], drained;
+    uint64_t v_load[4], v_clean[4];  // V tiles with hidden keys, in turn: the ring holds at most four
+    uint64_t info_full[2], info_empty[2], answer_full, near_end;
+    alignas(16) uint64_t answer[2];
+    TileInfo info[2];
+    uint32_t tmem, dead, dirty[2];
+    uint32_t odd[2][3][128];  // by the tile's parity: first key with +inf, -inf, NaN in a channel
+};
+
+// What is noted in odd[]: the tile's turn (later turns are smaller, so that atomicMin prefers them)
+// and the key's distance from the first key that is looked at.
+__device__ __forceinline__ uint32_t odd_tag(uint32_t turn) { return 0x3fffffu - (turn & 0x3fffffu); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v)
 {
@@ -81,17 +94,48 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v)
         : "memory");
 }
 
-// V as the second operand, token-major (its channels contiguous): 64-channel blocks BLK apart, groups
-// of 8 tokens 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_v(uint32_t addr, uint32_t block)
+// Shared-memory operand descriptors, low words (the high word is the same for all): 128-byte swizzle.
+// Q and K, channels contiguous: groups of 8 rows 1024 bytes apart.  V, token-major: 64-channel blocks
+// `block` bytes apart, groups of 8 tokens 1024 bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_qk(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_v(uint32_t addr, uint32_t block) { return ((addr & 0x3FFFFu) >> 4) | ((block >> 4) << 16); }
+
+// The products are issued by one elected lane of a warp whose control flow and operands are uniform:
+// descriptors then stay in uniform registers.  (Issued from a branch that one lane takes, each
+// product cost about 57 cycles of moves into them, more than half of what it takes to execute.)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(block >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;  // SWIZZLE_128B
-    return d;
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// mbar_wait by a whole warp; true only where every lane's wait ended
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kTries));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -99,6 +143,35 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// The grid index of a CTA that has not started yet, which then never starts: this CTA does its work
+// (cluster launch control).  -1: none is left, and no further request is made.
+__device__ __forceinline__ int take_tile(uint64_t* answer, uint64_t* bar, uint32_t asked)
+{
+    tc::fence_async_smem();  // the last answer was read
+    tc::mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     tc::smem_u32(answer)),
+                 "r"(tc::smem_u32(bar))
+                 : "memory");
+    if (!tc::mbar_wait(bar, asked & 1u, kTries)) return -1;
+    const uint64_t lo = ((volatile uint64_t*)answer)[0], hi = ((volatile uint64_t*)answer)[1];
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tmov.b128 r, {%2, %3};\n\tmov.u32 %1, 0;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=&r"(x)
+        : "l"(lo), "l"(hi));
+    return got ? (int)x : -1;
 }
 
 __device__ __forceinline__ float f_of(uint32_t u) { return __uint_as_float(u); }
@@ -114,40 +187,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Shared sh;
     unsigned char* sq = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = sq + 2 * C::TILE;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const int tpt = kHalfRows / a.group;
 
-    // the longest rows of every sequence first
-    const int h = blockIdx.x % a.Hkv;
-    AttnTile t;
-    if (!attn_tile(a, slots - 1 - (int)(blockIdx.x / a.Hkv), 2 * tpt, t)) return;
-    // each half's tokens [first, last) and its number of key tiles
-    const int last0 = min(t.first + tpt, t.last);
-    const int n0 = (last0 + kKeys - 1) / kKeys;
-    const int n1 = t.last > t.first + tpt ? (t.last + kKeys - 1) / kKeys : 0;
-    const int n = max(n0, n1);
-    const int edge = (t.first + 1) / kKeys;  // tiles from here on are hidden in part from some row
-
     if (tid == 0) {
-        tc::mbar_init(&sh.q_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.q_full[i], 1);
+            tc::mbar_init(&sh.q_empty[i], 1);
+            tc::mbar_init(&sh.z_full[i], 1);
+            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.o_full[i], 1);
+            tc::mbar_init(&sh.info_full[i], 1);
+            tc::mbar_init(&sh.info_empty[i], kInfoReaders);
+        }
         for (int i = 0; i < C::STAGES; ++i) {
             tc::mbar_init(&sh.kv_full[i], 1);
             tc::mbar_init(&sh.kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.z_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], 128);
-            tc::mbar_init(&sh.o_full[i], 1);
-        }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&sh.v_load[i], 1);
-            tc::mbar_init(&sh.v_clean[i], 64);
+            tc::mbar_init(&sh.v_clean[i], 32);
         }
+        tc::mbar_init(&sh.answer_full, 1);
+        tc::mbar_init(&sh.near_end, 1);
         tc::mbar_init(&sh.drained, 1);
         sh.dead = 0u;
+        sh.dirty[0] = sh.dirty[1] = 0xffffffffu;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = tid; i < 3 * 128; i += kThreads) (&sh.odd[0][0])[i] = 0x7fffffff;
+    for (int i = tid; i < 2 * 3 * 128; i += kThreads) (&sh.odd[0][0][0])[i] = 0xffffffffu;
     if (w == 8) tc::tmem_alloc(&sh.tmem, 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -155,129 +224,223 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = sh.tmem;
     volatile uint32_t* dead = &sh.dead;
 
+    // A role's next tile: waits until the scheduler has published it.  False: there is none (or a
+    // wait gave up).  The role gives the slot back with done_tile.
+    struct Tile {
+        int64_t start;
+        int first, last, head, n0, n1, n, edge;
+    };
+    auto next_tile = [&](uint32_t turn, Tile& t) -> bool {
+        if (!warp_wait(&sh.info_full[turn & 1], (turn >> 1) & 1u)) {
+            *dead = 1u;
+            return false;
+        }
+        const TileInfo& i = sh.info[turn & 1];
+        if (!i.valid) return false;
+        t.start = i.start;
+        t.first = i.first;
+        t.last = i.last;
+        t.head = i.head;
+        // key tiles of each half's tokens, and the first tile that is hidden in part from some row
+        t.n0 = (min(t.first + tpt, t.last) + kKeys - 1) / kKeys;
+        t.n1 = t.last > t.first + tpt ? (t.last + kKeys - 1) / kKeys : 0;
+        t.n = max(t.n0, t.n1);
+        t.edge = (t.first + 1) / kKeys;
+        return true;
+    };
+    auto done_tile = [&](uint32_t turn) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.info_empty[turn & 1]);
+    };
+
     if (w >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (w == 9 && lane == 0) {
-            // ---- copies: Q, then K0 V0 K1 V1 ... through the ring
-            tc::mbar_arrive_expect_tx(&sh.q_full, 2u * C::NB * (uint32_t)(tpt * a.group) * 128u);
-            for (int hf = 0; hf < 2; ++hf)
-                for (int b = 0; b < C::NB; ++b)
-                    tc::tma_load_3d(sq + hf * C::TILE + b * C::BLK, &maps.q, 64 * b, h * a.group,
-                                    (int)(t.start + t.first + hf * tpt), &sh.q_full);
-            int it = 0;
-            for (; it < 2 * n && *dead == 0u; ++it) {
-                const int st = it % C::STAGES;
-                if (!tc::mbar_wait(&sh.kv_empty[st], ((uint32_t)(it / C::STAGES) & 1u) ^ 1u, kTries)) {
+        Tile t;
+        if (w == 9) {
+            // ---- copies: K0, Q, V0, K1, V1 ... through the ring, tile after tile
+            uint32_t it = 0, e = 0, qc[2] = {0, 0};
+            for (uint32_t turn = 0; next_tile(turn, t); ++turn) {
+                bool ok = true;
+                if (lane == 0) {
+                    for (int x = 0; x < 2 * t.n && ok; ++x, ++it) {
+                        if (x == 1) {
+                            for (int hf = 0; hf < 2 && ok; ++hf) {
+                                if (hf == 1 && t.n1 == 0) break;
+                                ok = tc::mbar_wait(&sh.q_empty[hf], (qc[hf] & 1u) ^ 1u, kTries) && *dead == 0u;
+                                if (!ok) break;
+                                ++qc[hf];
+                                tc::mbar_arrive_expect_tx(&sh.q_full[hf], C::NB * (uint32_t)(tpt * a.group) * 128u);
+                                for (int b = 0; b < C::NB; ++b)
+                                    tc::tma_load_3d(sq + hf * C::TILE + b * C::BLK, &maps.q, 64 * b, t.head * a.group,
+                                                    (int)(t.start + t.first + hf * tpt), &sh.q_full[hf]);
+                            }
+                            if (!ok) break;
+                        }
+                        const uint32_t st = it % C::STAGES;
+                        ok = tc::mbar_wait(&sh.kv_empty[st], ((it / C::STAGES) & 1u) ^ 1u, kTries) && *dead == 0u;
+                        if (!ok) break;
+                        // a V tile that is cleaned reports to the cleaner alone; its own barrier only turns over
+                        const bool clean = (x & 1) && (x >> 1) >= t.edge;
+                        uint64_t* bar = clean ? &sh.v_load[e & 3] : &sh.kv_full[st];
+                        if (clean) {
+                            tc::mbar_arrive(&sh.kv_full[st]);
+                            ++e;
+                        }
+                        tc::mbar_arrive_expect_tx(bar, C::TILE);
+                        for (int b = 0; b < C::NB; ++b)
+                            tc::tma_load_3d(ring + st * C::TILE + b * C::BLK, x & 1 ? &maps.v : &maps.k, 64 * b, t.head,
+                                            (int)(t.start + (x >> 1) * kKeys), bar);
+                    }
+                }
+                done_tile(turn);
+                if (!__all_sync(0xffffffffu, ok)) {
                     *dead = 1u;
                     break;
                 }
-                // a V tile that is cleaned reports to the cleaners alone; its own barrier only turns over
-                const int e = (it >> 1) - edge;
-                const bool clean = (it & 1) && e >= 0;
-                uint64_t* bar = clean ? &sh.v_load[e & 3] : &sh.kv_full[st];
-                if (clean) tc::mbar_arrive(&sh.kv_full[st]);
-                tc::mbar_arrive_expect_tx(bar, C::TILE);
-                for (int b = 0; b < C::NB; ++b)
-                    tc::tma_load_3d(ring + st * C::TILE + b * C::BLK, it & 1 ? &maps.v : &maps.k, 64 * b, h,
-                                    (int)(t.start + (it >> 1) * kKeys), bar);
             }
             // after a wait that gave up, what was issued still lands before the CTA ends
-            if (*dead) {
-                (void)tc::mbar_wait(&sh.q_full, 0, kTries);
-                for (int i = max(0, it - C::STAGES); i < it; ++i) {
-                    (void)tc::mbar_wait(&sh.kv_full[i % C::STAGES], (uint32_t)(i / C::STAGES) & 1u, kTries);
-                    const int e = (i >> 1) - edge;
-                    if ((i & 1) && e >= 0) (void)tc::mbar_wait(&sh.v_load[e & 3], (uint32_t)(e >> 2) & 1u, kTries);
-                }
+            if (lane == 0 && *dead) {
+                for (int hf = 0; hf < 2; ++hf)
+                    if (qc[hf] > 0) (void)tc::mbar_wait(&sh.q_full[hf], (qc[hf] - 1) & 1u, kTries);
+                for (uint32_t i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+                    (void)tc::mbar_wait(&sh.kv_full[i % C::STAGES], (i / C::STAGES) & 1u, kTries);
+                for (uint32_t i = e > 4 ? e - 4 : 0; i < e; ++i) (void)tc::mbar_wait(&sh.v_load[i & 3], (i >> 2) & 1u, kTries);
             }
-        } else if (w == 8 && lane == 0) {
-            // ---- products, in the order Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ...
+        } else if (w == 8) {
+            // ---- products, in the order Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ... tile after tile
             const uint32_t id_z = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, D) | (1u << 16);
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
-            auto full = [&](int it) {
-                const bool ok = tc::mbar_wait(&sh.kv_full[it % C::STAGES], (uint32_t)(it / C::STAGES) & 1u, kTries);
-                if (!ok) *dead = 1u;
-                return *dead == 0u;
-            };
-            auto issue_z = [&](int hf, int j) {
-                const uint32_t k = ra + ((2 * j) % C::STAGES) * C::TILE, q = qa + hf * C::TILE;
+            uint32_t base = 0, e = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+            bool ok = true;
+            auto full = [&](uint32_t it) { return warp_wait(&sh.kv_full[it % C::STAGES], (it / C::STAGES) & 1u); };
+            auto issue_z = [&](int hf, uint32_t it) {
+                const uint32_t k = ra + (it % C::STAGES) * C::TILE, q = qa + hf * C::TILE;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
                     const uint32_t off = (s >> 2) * C::BLK + (s & 3) * 32;
-                    tc::umma(tm + 128 * hf, tc::desc_sw128(q + off), tc::desc_sw128(k + off), id_z, s > 0);
+                    mma_ss(tm + 128 * hf, desc_qk(q + off), desc_qk(k + off), id_z, s > 0);
                 }
-                tc::umma_commit(&sh.z_full[hf]);
+                commit(&sh.z_full[hf]);
             };
-            auto issue_o = [&](int hf, int j) {
-                const uint32_t v = ra + ((2 * j + 1) % C::STAGES) * C::TILE;
+            auto issue_o = [&](int hf, uint32_t it, bool first) {
+                const uint32_t v = ra + (it % C::STAGES) * C::TILE;
 #pragma unroll
                 for (int s = 0; s < kKeys / 16; ++s)
-                    tc::umma_ts(tm + 256 + D * hf, tm + 128 * hf + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u),
-                                id_o, j > 0 || s > 0);
-                tc::umma_commit(&sh.o_full[hf]);
+                    mma_ts(tm + 256 + D * hf, tm + 128 * hf + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u), id_o,
+                           !first || s > 0);
             };
-            bool ok = tc::mbar_wait(&sh.q_full, 0, kTries) && full(0);
-            if (!ok) *dead = 1u;
-            if (ok) {
-                issue_z(0, 0);
-                if (n1 > 0) issue_z(1, 0);
-                tc::umma_commit(&sh.kv_empty[0]);
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                ok = full(2 * j + 1);
-                if (ok && j + 1 < n) ok = full(2 * j + 2);
-                if (ok && j >= edge && !tc::mbar_wait(&sh.v_clean[(j - edge) & 3], (uint32_t)((j - edge) >> 2) & 1u, kTries)) ok = false;
+            for (uint32_t turn = 0; ok && next_tile(turn, t); ++turn) {
+                ok = full(base);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int nh = hf ? n1 : n0;
-                    if (!ok || j >= nh) continue;
-                    if (!tc::mbar_wait(&sh.p_full[hf], (uint32_t)j & 1u, kTries) || *dead != 0u) {
-                        ok = false;
-                        continue;
-                    }
-                    tc::fence_after_sync();
-                    issue_o(hf, j);
-                    if (j + 1 < nh) issue_z(hf, j + 1);
+                    if (!ok || (hf == 1 && t.n1 == 0)) continue;
+                    ok = warp_wait(&sh.q_full[hf], qc[hf]++ & 1u);
+                    if (!ok) continue;
+                    issue_z(hf, base);
+                    if ((hf ? t.n1 : t.n0) == 1) commit(&sh.q_empty[hf]);
                 }
-                if (!ok) break;
-                tc::umma_commit(&sh.kv_empty[(2 * j + 1) % C::STAGES]);
-                if (j + 1 < n) tc::umma_commit(&sh.kv_empty[(2 * j + 2) % C::STAGES]);
+                if (ok) commit(&sh.kv_empty[base % C::STAGES]);
+                for (int j = 0; j < t.n && ok; ++j) {
+                    const uint32_t iv = base + 2 * j + 1;
+                    if (j == max(0, t.n - 2) && lane == 0) tc::mbar_arrive(&sh.near_end);
+                    ok = full(iv) && !__any_sync(0xffffffffu, *dead != 0u);
+                    if (ok && j + 1 < t.n) ok = full(iv + 1);
+                    if (ok && j >= t.edge) {
+                        ok = warp_wait(&sh.v_clean[e & 3], (e >> 2) & 1u);
+                        ++e;
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int nh = hf ? t.n1 : t.n0;
+                        if (!ok || j >= nh) continue;
+                        ok = warp_wait(&sh.p_full[hf], pc[hf]++ & 1u);
+                        if (!ok) continue;
+                        tc::fence_after_sync();
+                        issue_o(hf, iv, j == 0);
+                        if (j + 1 < nh) {
+                            issue_z(hf, iv + 1);  // its commit also covers O's product
+                            if (j + 2 == nh) commit(&sh.q_empty[hf]);
+                        } else {
+                            commit(&sh.o_full[hf]);
+                        }
+                    }
+                    if (!ok) break;
+                    commit(&sh.kv_empty[iv % C::STAGES]);
+                    if (j + 1 < t.n) commit(&sh.kv_empty[(iv + 1) % C::STAGES]);
+                }
+                base += 2 * t.n;
+                done_tile(turn);
             }
-            if (!ok) {
+            if (!ok || *dead != 0u) {
                 *dead = 1u;
-                tc::umma_commit(&sh.drained);  // products in flight end before tensor memory is given back
-                (void)tc::mbar_wait(&sh.drained, 0, kTries);
+                commit(&sh.drained);  // products in flight end before tensor memory is given back
+                (void)warp_wait(&sh.drained, 0);
             }
-        } else if (w >= 10) {
+        } else if (w == 10) {
             // ---- V tiles with hidden keys: infinities and NaN leave the tile
-            const int me = tid - 320;
-            for (int j = edge; j < n && *dead == 0u; ++j) {
-                const int it = 2 * j + 1, st = it % C::STAGES;
-                if (!tc::mbar_wait(&sh.v_load[(j - edge) & 3], (uint32_t)((j - edge) >> 2) & 1u, kTries)) {
+            uint32_t base = 0, e = 0;
+            for (uint32_t turn = 0; next_tile(turn, t); ++turn) {
+                bool ok = true;
+                for (int j = t.edge; j < t.n && ok; ++j, ++e) {
+                    ok = warp_wait(&sh.v_load[e & 3], (e >> 2) & 1u) && !__any_sync(0xffffffffu, *dead != 0u);
+                    if (!ok) break;
+                    unsigned char* v = ring + (base + 2 * j + 1) % C::STAGES * C::TILE;
+#pragma unroll 8
+                    for (int i = lane; i < (int)C::TILE / 16; i += 32) {
+                        uint4* at = reinterpret_cast<uint4*>(v + i * 16);
+                        const uint4 u = *at;
+                        auto odd2 = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
+                        if (odd2(u.x) || odd2(u.y) || odd2(u.z) || odd2(u.w)) {
+                            const int row = (i >> 3) & 127, key = j * kKeys + row;
+                            const int ch = (i >> 10) * 64 + (((i & 7) ^ (row & 7)) << 3);
+                            uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                            for (int c = 0; c < 8; ++c) {
+                                const uint32_t b = (x[c >> 1] >> (16 * (c & 1))) & 0xffffu;
+                                if ((b & 0x7f80u) != 0x7f80u) continue;
+                                if (key < t.last) {
+                                    sh.dirty[turn & 1] = odd_tag(turn);
+                                    atomicMin(&sh.odd[turn & 1][b & 0x7fu ? 2 : b >> 15][ch + c],
+                                              (odd_tag(turn) << 10) | (uint32_t)(key - t.edge * kKeys));
+                                }
+                                x[c >> 1] &= ~(0xffffu << (16 * (c & 1)));
+                            }
+                            *at = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                    tc::fence_async_smem();
+                    tc::mbar_arrive(&sh.v_clean[e & 3]);
+                }
+                base += 2 * t.n;
+                done_tile(turn);
+                if (!ok) {
                     *dead = 1u;
                     break;
                 }
-                unsigned char* v = ring + st * C::TILE;
-#pragma unroll 8
-                for (int i = me; i < (int)C::TILE / 16; i += 64) {
-                    uint4* at = reinterpret_cast<uint4*>(v + i * 16);
-                    const uint4 u = *at;
-                    auto odd2 = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
-                    if (odd2(u.x) || odd2(u.y) || odd2(u.z) || odd2(u.w)) {
-                        const int row = (i >> 3) & 127, key = j * kKeys + row;
-                        const int ch = (i >> 10) * 64 + (((i & 7) ^ (row & 7)) << 3);
-                        uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t b = (x[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                            if ((b & 0x7f80u) != 0x7f80u) continue;
-                            if (key < t.last) atomicMin(&sh.odd[b & 0x7fu ? 2 : b >> 15][ch + e], key);
-                            x[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-                        }
-                        *at = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        } else if (lane == 0) {
+            // ---- scheduler: this CTA's own tile, then tiles of CTAs that have not started yet
+            uint32_t asked = 0;
+            int idx = blockIdx.x;
+            for (uint32_t turn = 0;; ++turn) {
+                TileInfo f{};
+                for (;;) {
+                    AttnTile x;
+                    // the longest rows of every sequence first
+                    if (idx >= 0 && attn_tile(a, slots - 1 - idx / a.Hkv, 2 * tpt, x)) {
+                        f = TileInfo{x.start, x.first, x.last, idx % a.Hkv, 1};
+                        break;
                     }
+                    if (idx < 0) break;
+                    idx = take_tile(sh.answer, &sh.answer_full, asked++);
                 }
-                tc::fence_async_smem();
-                tc::mbar_arrive(&sh.v_clean[(j - edge) & 3]);
+                if (!tc::mbar_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u, kTries)) *dead = 1u;
+                if (*dead) f.valid = 0;
+                sh.info[turn & 1] = f;
+                tc::mbar_arrive(&sh.info_full[turn & 1]);
+                if (!f.valid) break;
+                // not before the tile is nearly done, so that tiles go to whoever is free
+                if (!tc::mbar_wait(&sh.near_end, turn & 1u, kTries)) *dead = 1u;
+                idx = *dead ? -1 : take_tile(sh.answer, &sh.answer_full, asked++);
             }
         }
         __syncwarp();
@@ -285,115 +448,129 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
         const int hf = w >> 2, r = tid & 127;
-        const int nh = hf ? n1 : n0;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
         const uint32_t zt = tm + 128 * hf + lanes, ot = tm + 256 + D * hf + lanes;
-        const int first = t.first + hf * tpt;
-        const int tok = first + r / a.group;
-        const int warp_first = first + (32 * (w & 3)) / a.group;
         const float cs = a.scale * 1.4426950408889634f;
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
-        bool gone = false;
-        for (int j = 0; j < nh; ++j) {
-            gone = !tc::mbar_wait(&sh.z_full[hf], (uint32_t)j & 1u, kTries) || *dead != 0u;
-            if (__any_sync(0xffffffffu, gone)) break;
-            tc::fence_after_sync();
-            uint32_t z[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
-            tc::tmem_wait_ld();
-            if (j * kKeys + kKeys - 1 > warp_first) {
-                const int seen = tok + 1 - j * kKeys;
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i >= seen) z[i] = 0xff800000u;
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 128; i += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(f_of(z[i + 2 * e]), f_of(z[i + 2 * e + 1])));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-            float alpha = 1.f;
-            if (j == 0) {
-                m = top;
-            } else if (top > m + 8.f) {
-                alpha = ex2(m - top);
-                m = top;
-            }
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                l2 = __fmul2_rn(l2, make_float2(alpha, alpha));
-                gone = !tc::mbar_wait(&sh.o_full[hf], (uint32_t)(j - 1) & 1u, kTries);
-                if (__any_sync(0xffffffffu, gone)) break;
+        const int rt = r / a.group, rh = r - rt * a.group;
+        const int wt = (32 * (w & 3)) / a.group;
+        uint32_t zc = 0, oc = 0;
+        Tile t;
+        for (uint32_t turn = 0; next_tile(turn, t); ++turn) {
+            const int nh = hf ? t.n1 : t.n0;
+            const int first = t.first + hf * tpt;
+            const int tok = first + rt;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            bool gone = false;
+            for (int j = 0; j < nh; ++j) {
+                gone = !warp_wait(&sh.z_full[hf], zc++ & 1u);
+                if (gone) break;
                 tc::fence_after_sync();
+                uint32_t z[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
+                tc::tmem_wait_ld();
+                if (j * kKeys + kKeys - 1 > first + wt) {
+                    const int seen = tok + 1 - j * kKeys;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= seen) z[i] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(f_of(z[2 * e]), f_of(z[2 * e + 1]));
+#pragma unroll
+                for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], f_of(z[i + 2 * e]), f_of(z[i + 2 * e + 1]));
+                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * cs;
+                float alpha = 1.f;
+                if (j == 0) {
+                    m = top;
+                } else if (top > m + 8.f) {
+                    alpha = ex2(m - top);
+                    m = top;
+                }
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // the products into O up to here ended with the scores that were waited for
+                    l2 = __fmul2_rn(l2, make_float2(alpha, alpha));
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(ot + 32 * c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f_of(o[i]) * alpha);
+                        tmem_st32(ot + 32 * c, o);
+                    }
+                }
+                const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-m, -m);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int e = 64 * q + 2 * i;
+                        const float2 x = __ffma2_rn(make_float2(f_of(z[e]), f_of(z[e + 1])), cs2, nm2);
+                        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                        sum[i & 1] = __fadd2_rn(sum[i & 1], y);
+                        p[i] = tc::pack_bf16(y.x, y.y);
+                    }
+                    tmem_st32(zt + 32 * q, p);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.p_full[hf]);
+                l2 = __fadd2_rn(l2, __fadd2_rn(sum[0], sum[1]));
+            }
+            if (nh > 0) {
+                if (!gone) gone = !warp_wait(&sh.o_full[hf], oc++ & 1u);
+                gone = __any_sync(0xffffffffu, gone || *dead != 0u);
+                if (gone) *dead = 1u;
+                tc::fence_after_sync();
+                const int rows = (min(first + tpt, t.last) - first) * a.group;
+                const float inv = gone ? NAN : 1.f / (l2.x + l2.y);  // a wait that gave up shows in the output
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                                     ((t.start + tok) * a.Hq + t.head * a.group + rh) * D;
+                const bool dirty = *(volatile uint32_t*)&sh.dirty[turn & 1] == odd_tag(turn);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(ot + 32 * c, o);
                     tc::tmem_wait_ld();
+                    uint32_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f_of(o[i]) * alpha);
-                    tmem_st32(ot + 32 * c, o);
-                }
-            }
-            const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-m, -m);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = 64 * q + 2 * i;
-                    const float2 x = __ffma2_rn(make_float2(f_of(z[e]), f_of(z[e + 1])), cs2, nm2);
-                    const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                    sum[i & 1] = __fadd2_rn(sum[i & 1], y);
-                    p[i] = tc::pack_bf16(y.x, y.y);
-                }
-                tmem_st32(zt + 32 * q, p);
-            }
-            l2 = __fadd2_rn(l2, __fadd2_rn(sum[0], sum[1]));
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(&sh.p_full[hf]);
-        }
-        if (nh > 0) {
-            if (!__any_sync(0xffffffffu, gone))
-                gone = !tc::mbar_wait(&sh.o_full[hf], (uint32_t)(nh - 1) & 1u, kTries) || *dead != 0u;
-            gone = __any_sync(0xffffffffu, gone);
-            if (gone) *dead = 1u;
-            tc::fence_after_sync();
-            const int rows = (min(first + tpt, t.last) - first) * a.group;
-            const float inv = gone ? NAN : 1.f / (l2.x + l2.y);  // a wait that gave up shows in the output
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                                 ((t.start + tok) * a.Hq + h * a.group + r % a.group) * D;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                if (!gone) {
-                    tmem_ld32(ot + 32 * c, o);
-                    tc::tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                uint32_t y[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float x[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int ch = 32 * c + 2 * i + e;
-                        x[e] = attn_odd(f_of(o[2 * i + e]) * inv, tok, sh.odd[0][ch], sh.odd[1][ch], sh.odd[2][ch]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 x = __fmul2_rn(make_float2(f_of(o[2 * i]), f_of(o[2 * i + 1])), make_float2(inv, inv));
+                        y[i] = tc::pack_bf16(x.x, x.y);
                     }
-                    y[i] = tc::pack_bf16(x[0], x[1]);
-                }
-                if (r < rows) {
+                    if (dirty) {
+                        auto at = [&](int kind, int ch) {
+                            const uint32_t e = sh.odd[turn & 1][kind][ch];
+                            return (e >> 10) == odd_tag(turn) ? t.edge * kKeys + (int)(e & 1023u) : 0x7fffffff;
+                        };
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                        for (int i = 0; i < 16; ++i) {
+                            float x[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int ch = 32 * c + 2 * i + e;
+                                x[e] = attn_odd(f_of(o[2 * i + e]) * inv, tok, at(0, ch), at(1, ch), at(2, ch));
+                            }
+                            y[i] = tc::pack_bf16(x[0], x[1]);
+                        }
+                    }
+                    if (r < rows) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
                 }
+                tc::fence_before_sync();
             }
+            done_tile(turn);
         }
     }
     tc::fence_before_sync();
