@@ -19,7 +19,6 @@
 // between warps; the 128-byte swizzle frees ldmatrix of bank conflicts, and a 16-byte chunk of a
 // K row serves one k-step with q's channels permuted to match what ldmatrix hands each thread.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "kda_attn.cuh"
 #include "kda_tc.cuh"
@@ -95,10 +94,9 @@ template <bool kE4m3>
 __device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi)
 {
     if constexpr (kE4m3) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
-        lo = (uint32_t)a.x | ((uint32_t)a.y << 16);
-        hi = (uint32_t)b.x | ((uint32_t)b.y << 16);
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(x));
     } else {
         // byte b ^ 0x80 = b + 128 under the exponent of 1024 is 1024 + 128 + b; 1152 comes off exactly
         const uint32_t u = x ^ 0x80808080u;
@@ -291,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (lane == 0) atomicOr(&flag, kCheckBadSeqlens);
             }
             if (lane == 0) {
-                pages[w][st][0] = ok0 ? p0 : -1;
-                pages[w][st][1] = box < kTile ? (ok1 ? p1 : -1) : (ok0 ? p0 : -1);
+                // the scales' places; a page serves the whole tile, or 16 keys of it
+                pages[w][st][0] = ok0 ? p0 * a.Hkv + ic.h : -1;
+                pages[w][st][1] = box < kTile ? (ok1 ? p1 * a.Hkv + ic.h : -1) : pages[w][st][0];
                 const uint32_t bytes = (uint32_t)((ok0 ? 1 : 0) + (ok1 ? 1 : 0)) * 2u * box * D;
                 tc::mbar_arrive_expect_tx(&full[w][st], bytes);
                 unsigned char* kd = ring + (size_t)st * 2 * TB;
@@ -426,25 +425,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         };
 
-        float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;
-        bool has0 = false, has1 = false;
-        auto load_scales = [&](int st, int h) {
-            const int q0 = pages[w][st][0], q1 = pages[w][st][1];
-            has0 = q0 >= 0;
-            has1 = q1 >= 0;
-            ks0 = has0 ? __ldg(a.c.k_scale + (int64_t)q0 * a.Hkv + h) : 0.f;
-            vs0 = has0 ? __ldg(a.c.v_scale + (int64_t)q0 * a.Hkv + h) : 0.f;
-            ks1 = q1 == q0 ? ks0 : has1 ? __ldg(a.c.k_scale + (int64_t)q1 * a.Hkv + h) : 0.f;
-            vs1 = q1 == q0 ? vs0 : has1 ? __ldg(a.c.v_scale + (int64_t)q1 * a.Hkv + h) : 0.f;
+        // a tile's scales are read while the tile before it is computed
+        struct Scales {
+            float k0, k1, v0, v1;
+            bool has0, has1;
         };
+        auto load_scales = [&](int st) {
+            const int q0 = pages[w][st][0], q1 = pages[w][st][1];
+            Scales x;
+            x.has0 = q0 >= 0;
+            x.has1 = q1 >= 0;
+            x.k0 = x.has0 ? __ldg(a.c.k_scale + q0) : 0.f;
+            x.v0 = x.has0 ? __ldg(a.c.v_scale + q0) : 0.f;
+            x.k1 = x.has1 ? __ldg(a.c.k_scale + q1) : 0.f;
+            x.v1 = x.has1 ? __ldg(a.c.v_scale + q1) : 0.f;
+            return x;
+        };
+        __syncwarp();
+        Scales next = load_scales(0);
         for (int it = 0; it < count && !gone; ++it) {
             const int st = it % S;
             if (!begun) {
                 start_unit();
                 begun = true;
             }
-            __syncwarp();
-            load_scales(st, cc.h);
+            const float ks0 = next.k0, ks1 = next.k1, vs0 = next.v0, vs1 = next.v1;
+            const bool has0 = next.has0, has1 = next.has1;
+            if (it + 1 < count) next = load_scales((it + 1) % S);
             const bool arrived = tc::mbar_wait(&full[w][st], (uint32_t)(it / S) & 1u, kCopyTries);
             if (!__all_sync(0xffffffffu, arrived)) {
                 gone = true;
@@ -538,32 +545,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // scores in base 2: z s, their maxima over the keys that are seen
             float t0 = -INFINITY, t1 = -INFINITY;
             const bool edge = partial || key0 + kTile > cc.len - a.L + 1;
-            uint32_t hid0 = 0u, hid1 = 0u;  // bit 2 j + e: key 8 j + 2 cq + e is hidden from the row
-            if (edge) {
+            // this thread's key 8 j + 2 cq + e of the tile: does the row that sees `seen` keys see it?
+            auto sees = [&](int j, int e, int seen) { return (j < 2 ? has0 : has1) && key0 + 8 * j + 2 * cq + e < seen; };
+            const float s00 = f0 * ks0, s01 = f0 * ks1, s10 = f1 * ks0, s11 = f1 * ks1;
+            if (!edge) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
+                    t0 = fmaxf(t0, fmaxf(z[j][0] * s0, z[j][1] * s0));
+                    t1 = fmaxf(t1, fmaxf(z[j][2] * s1, z[j][3] * s1));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int key = key0 + 8 * j + 2 * cq + e;
-                        const bool there = j < 2 ? has0 : has1;
-                        if (key >= seen0 || !there) hid0 |= 1u << (2 * j + e);
-                        if (key >= seen1 || !there) hid1 |= 1u << (2 * j + e);
+                        if (sees(j, e, seen0)) t0 = fmaxf(t0, z[j][e] * s0);
+                        if (sees(j, e, seen1)) t1 = fmaxf(t1, z[j][2 + e] * s1);
                     }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s0 = f0 * (j < 2 ? ks0 : ks1), s1 = f1 * (j < 2 ? ks0 : ks1);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!((hid0 >> (2 * j + e)) & 1u)) t0 = fmaxf(t0, z[j][e] * s0);
-                    if (!((hid1 >> (2 * j + e)) & 1u)) t1 = fmaxf(t1, z[j][2 + e] * s1);
                 }
             }
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            // the reference moves only when the maximum has grown by more than 2^8: p stays below f16's
+            // range, l and O hold the factor as well, and O is rarely rescaled
+            const float n0 = t0 > m0 + 8.f ? t0 : m0, n1 = t1 > m1 + 8.f ? t1 : m1;
             const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
             float a0 = ex2(m0 - u0), a1 = ex2(m1 - u1);
             m0 = n0;
@@ -573,13 +582,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // p = 2^(z s - m) with one rounding of the difference
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float s0 = f0 * (j < 2 ? ks0 : ks1), s1 = f1 * (j < 2 ? ks0 : ks1);
+                const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float y0 = ex2(fmaf(z[j][e], s0, -u0)), y1 = ex2(fmaf(z[j][2 + e], s1, -u1));
-                    z[j][e] = (hid0 >> (2 * j + e)) & 1u ? 0.f : y0;
-                    z[j][2 + e] = (hid1 >> (2 * j + e)) & 1u ? 0.f : y1;
+                    z[j][e] = ex2(fmaf(z[j][e], s0, -u0));
+                    z[j][2 + e] = ex2(fmaf(z[j][2 + e], s1, -u1));
                 }
+            }
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (!sees(j, e, seen0)) z[j][e] = 0.f;
+                        if (!sees(j, e, seen1)) z[j][2 + e] = 0.f;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
                 l0 += z[j][0] + z[j][1];
                 l1 += z[j][2] + z[j][3];
             }
@@ -775,10 +795,14 @@ cudaError_t launch_decode_d(const AttnDecodeArgs& a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int rows = a.L * a.group < kRows ? a.L * a.group : kRows;
-    kern<<<decode_ctas(), kThreads, smem, s>>>(a, maps, rows);
+    // no more workers than tiles that the page table can hold
+    const int64_t row_tiles = ((int64_t)a.L * a.group + kRows - 1) / kRows;
+    const double most = (double)a.N * a.Hkv * row_tiles * (((int64_t)a.c.max_pages * a.c.page + kTile - 1) / kTile);
+    const int ctas = most < (double)decode_ctas() * kWarps ? (int)((most + kWarps - 1) / kWarps) : decode_ctas();
+    kern<<<ctas, kThreads, smem, s>>>(a, maps, rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_dependent(kda_attn_combine_kernel<TIO, D>, dim3((unsigned)(decode_ctas() * kWarps)), dim3(128), 0, s, a, rows);
+    return launch_dependent(kda_attn_combine_kernel<TIO, D>, dim3((unsigned)(ctas * kWarps)), dim3(128), 0, s, a, rows);
 }
 
 template <typename TIO, bool kE4m3>
