@@ -83,8 +83,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -271,12 +270,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         Cursor ic = cc;
         const int count = (int)(b1 - b0);
         const int box = min(kTile, a.c.page);  // rows of one copy
+        const int page_shift = 31 - __clz(a.c.page);
         bool gone = false;                     // a wait gave up
 
         auto page_id = [&](const Cursor& c, int piece) -> int {
             const int key = c.i * kTile + piece * box;
             if (key >= c.len) return -1;
-            const int p = __ldg(a.c.table + (int64_t)c.n * a.c.max_pages + key / a.c.page);
+            const int p = __ldg(a.c.table + (int64_t)c.n * a.c.max_pages + (key >> page_shift));
             return p;
         };
         int p0 = page_id(ic, 0), p1 = box < kTile ? page_id(ic, 1) : -1;
@@ -510,37 +510,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[j][i] = 0.f;
+            // (four accumulators in turn, so that no product waits for the one before it)
             if constexpr (D >= 64) {
 #pragma unroll
                 for (int c = 0; c < NCH; c += 4) {
+                    uint32_t r[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t r[4];
-                        const int row = 8 * j + (lane & 7), ch = c + (lane >> 3);
-                        ldsm4(r, ka + swizzle<D>((uint32_t)(row * D + ch * 16)));
+                    for (int j = 0; j < 4; ++j)
+                        ldsm4(r[j], ka + swizzle<D>((uint32_t)((8 * j + (lane & 7)) * D + (c + (lane >> 3)) * 16)));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
                             uint32_t b0, b1;
-                            widen<kE4m3>(r[i], b0, b1);
+                            widen<kE4m3>(r[j][i], b0, b1);
 #pragma unroll
                             for (int p = 0; p < PARTS; ++p) mma_f16(z[j], qf[p][c + i], b0, b1);
                         }
-                    }
                 }
             } else {
+                uint32_t r[2][4];
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    uint32_t r[4];
-                    const int row = 8 * (j + (lane >> 4)) + (lane & 7), ch = (lane >> 3) & 1;
-                    ldsm4(r, ka + swizzle<D>((uint32_t)(row * D + ch * 16)));
+                for (int j = 0; j < 2; ++j)
+                    ldsm4(r[j], ka + swizzle<D>((uint32_t)((8 * (2 * j + (lane >> 4)) + (lane & 7)) * D + ((lane >> 3) & 1) * 16)));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
                         uint32_t b0, b1;
-                        widen<kE4m3>(r[i], b0, b1);
+                        widen<kE4m3>(r[j >> 1][2 * (j & 1) + i], b0, b1);
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p) mma_f16(z[j + (i >> 1)], qf[p][i & 1], b0, b1);
+                        for (int p = 0; p < PARTS; ++p) mma_f16(z[j], qf[p][i], b0, b1);
                     }
-                }
             }
             // scores in base 2: z s, their maxima over the keys that are seen
             float t0 = -INFINITY, t1 = -INFINITY;
