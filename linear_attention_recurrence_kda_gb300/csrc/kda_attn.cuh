@@ -59,7 +59,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t 
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16, d = 64 or 128
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
-size_t attn_decode_workspace_bytes(int rows, int d);
+size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt);  // rows: window x group
 
 // cuTensorMapEncodeTiled of the loaded driver, or NULL (kda_attn_api.cu).
 using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

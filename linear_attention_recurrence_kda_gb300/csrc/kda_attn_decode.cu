@@ -1,14 +1,16 @@
 // kda_attn_decode.cu -- the newest tokens of every sequence attend to the paged 8-bit cache
 // (kda_attention_decode).
 //
-// A unit is one sequence, one key head and up to 16 rows (query heads of the group x tokens of the
+// A unit is one sequence, one key head and up to 8 NT rows (query heads of the group x tokens of the
 // window); its keys come in tiles of 32.  The work is cut evenly: with W workers (warps) and all
 // units' tiles in one line, worker w takes tiles [w total / W, (w + 1) total / W), whatever the
 // lengths are.  A worker that holds all of a unit writes its output; otherwise it leaves (max, sum,
 // unnormalised output) in the workspace, and the combine kernel joins the pieces in order.
 //
 // Per tile a warp does, with m16n8k16 f16 products and fp32 accumulators,
-//   z = scale ks (Q K^T),  m' = max(m, max z),  p = 2^(z - m'),  O = O 2^(m - m') + p V,  l likewise
+//   Z^T = scale ks (K Q^T),  m' = max(m, max z),  P = 2^(Z - m'),  O^T = O^T 2^(m - m') + V^T P^T,  l likewise
+// Keys (and channels) are the products' 16 rows and queries their 8 columns: a group of 4 or 8 query
+// heads then fills half as many products, registers and exponentials as with queries for rows.
 // K and V codes become f16 exactly (e4m3 and int8 are subsets of f16).  A row of q is scaled by a
 // power of two so that its largest value lies in [2^14, 2^15): bf16 values are then exact in f16 down
 // to 2^-38 of the row's largest; fp32 values are split into two f16 parts (22 bits), as are their p.
@@ -16,8 +18,9 @@
 //
 // HBM bounds it (2 d bytes per key and head, and a group of query heads per byte is far below the
 // tensor cores' rate), so each warp keeps its own ring of tiles in flight by TMA with no barrier
-// between warps; the 128-byte swizzle frees ldmatrix of bank conflicts, and a 16-byte chunk of a
-// K row serves one k-step with q's channels permuted to match what ldmatrix hands each thread.
+// between warps; the 128-byte swizzle frees ldmatrix of bank conflicts.  What ldmatrix hands a thread
+// sets the order of channels in a product: 16 bytes of a K row serve one k-step with q's channels
+// permuted alike, and even and odd channels of V are rows 0-7 and 8-15 of a product.
 #include <cuda_fp16.h>
 
 #include "kda_attn.cuh"
@@ -28,19 +31,23 @@ namespace kda {
 namespace {
 
 constexpr int kTile = 32;     // keys per tile
-constexpr int kRows = 16;     // rows of a unit
 constexpr int kWarps = 4;     // workers per CTA
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;
 constexpr uint32_t kCopyTries = 1u << 17;  // of up to 20 us each
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int stages_of(int d) { return d == 128 ? 3 : d == 64 ? 6 : 8; }
+// By the unit's rows (8 nt): O takes NT d / 4 registers, so few rows leave room for three CTAs on an SM.
+constexpr int ctas_of(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int stages_of(int nt, int d) { return (nt == 2 ? 3 : 2) * (d == 128 ? 1 : d == 64 ? 2 : 3); }
+
+// Column tiles of 8 rows for a call's rows; fp32 holds two parts of q and takes at most two.
+inline int nt_of(int64_t rows, bool split) { return rows <= 8 ? 1 : rows <= 16 || split ? 2 : 4; }
 
 // Workspace: check word | per-CTA flags | records | (max, sum) of slots | outputs of slots.
 // Worker w owns slots 2 w (a unit begun by an earlier worker) and 2 w + 1 (begun here).
+// A call with fewer units than workers keeps its records by unit, else by the worker that began it.
 struct Record {
-    int32_t n, h, rt, last;  // unit and the last worker that holds a piece of it; n < 0: none
+    int32_t n, h, rt, first, last;  // unit, and the workers that hold its pieces; n < 0: none
 };
 
 struct DecodeLayout {
@@ -72,6 +79,13 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)  // an 8 x 8 matrix of 16-bit values over the warp
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
@@ -170,14 +184,16 @@ __device__ __forceinline__ void next_tile(const AttnDecodeArgs& a, int row_tiles
 
 }  // namespace
 
-template <typename TIO, int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    kda_attn_decode_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps, const int rows_max)
+template <typename TIO, int D, bool kE4m3, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_of(NT))
+    kda_attn_decode_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps, const int rows_max, const bool by_unit)
 {
     constexpr bool kSplit = sizeof(TIO) == 4;  // fp32: q and p as two f16 parts
     constexpr int PARTS = kSplit ? 2 : 1;
-    constexpr int NCH = D / 16;                // 16-byte chunks of a row = k-steps of Q K^T
-    constexpr int S = stages_of(D);
+    constexpr int kRows = 8 * NT;
+    constexpr bool kQShared = NT == 4;         // q's fragments wait in shared memory, not in registers
+    constexpr int NCH = D / 16;                // 16-byte chunks of a row = k-steps of K Q^T
+    constexpr int S = stages_of(NT, D);
     constexpr uint32_t TB = kTile * D;         // bytes of a K (or V) tile
     extern __shared__ unsigned char smem_raw[];
     __shared__ int64_t prefix[kThreads + 1];
@@ -189,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int g = lane >> 2, cq = lane & 3;
     unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = smem + (size_t)w * S * 2 * TB;
+    uint2* qs = reinterpret_cast<uint2*>(smem + (size_t)kWarps * S * 2 * TB) + w * NCH * NT * 32 + lane;  // [NCH][NT][32]
     const DecodeLayout L = decode_layout(gridDim.x * kWarps, rows_max, D);
     const int rows_all = a.L * a.group;
     const int row_tiles = (rows_all + kRows - 1) / kRows;
@@ -229,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int64_t tokrow = (int64_t)a.Hq * D;
     for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
         if (length_of(a, n) == 0) {
+            for (int i = tid; by_unit && i < per_tile; i += kThreads)
+                reinterpret_cast<Record*>(a.ws + L.records)[n * per_tile + i].n = -1;
             TIO* o = static_cast<TIO*>(a.out) + (int64_t)n * a.L * tokrow;
             for (int64_t i = tid; i < a.L * tokrow; i += kThreads) st_io(o, i, 0.f);
         }
@@ -236,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int64_t total = prefix[kThreads] * per_tile;
     const int64_t W = min((int64_t)gridDim.x * kWarps, total);
     const int64_t worker = (int64_t)blockIdx.x * kWarps + w;
-    Record* rec = reinterpret_cast<Record*>(a.ws + L.records) + worker;
+    Record* records = reinterpret_cast<Record*>(a.ws + L.records);
     float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
     float* po = reinterpret_cast<float*>(a.ws + L.o);
-    Record mine{-1, 0, 0, 0};
+    Record mine{-1, 0, 0, 0, 0};
     if (worker < W) {
         const int64_t b0 = worker * total / W, b1 = (worker + 1) * total / W;
         // the unit that holds tile b0: a run of sequences by bisection, then one by one
@@ -314,10 +333,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         int issued = 0;
         while (issued < count && issued < S) issue(issued++);
 
-        uint32_t qf[PARTS][NCH][4];
-        float O[NCH][2][4];
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f, vu = 0.f, vtop = 0.f;
-        int seen0 = 0, seen1 = 0;  // keys that this thread's two rows see
+        // row 8 t + g of the unit as a product's second operand; this thread's results are of rows
+        // 8 t + 2 cq + {0, 1}
+        uint32_t qf[PARTS][kQShared ? 1 : NCH][NT][2];
+        float O[NCH][NT][4];
+        float m[NT][2], l[NT][2], f[NT][2], vu = 0.f, vtop = 0.f;
+        int seen[NT][2];  // keys that the rows see
         bool begun = false;
         auto row_of = [&](int r, int& t, int& head) {
             const int R = cc.rt * kRows + r;
@@ -326,103 +347,90 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             return R < rows_all;
         };
         auto start_unit = [&]() {
-            float x[2][NCH][4];
-            float mx[2];
-            int seen[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int nt = 0; nt < NT; ++nt) {
                 int t, head;
-                const bool ok = row_of(g + 8 * u, t, head);
-                seen[u] = ok ? cc.len - a.L + t + 1 : 0;
-                mx[u] = 0.f;
+                const bool ok = row_of(8 * nt + g, t, head);
+                const int sees = ok ? cc.len - a.L + t + 1 : 0;
                 const TIO* q = static_cast<const TIO*>(a.q) + ((int64_t)cc.n * a.L + t) * a.qs + (int64_t)head * D + 4 * cq;
+                float x[NCH][4], mx = 0.f;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
                     if constexpr (kSplit) {
                         const float4 v = ok ? *reinterpret_cast<const float4*>(q + 16 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[u][c][0] = v.x; x[u][c][1] = v.y; x[u][c][2] = v.z; x[u][c][3] = v.w;
+                        x[c][0] = v.x; x[c][1] = v.y; x[c][2] = v.z; x[c][3] = v.w;
                     } else {
                         const uint2 v = ok ? *reinterpret_cast<const uint2*>(q + 16 * c) : make_uint2(0u, 0u);
-                        x[u][c][0] = __uint_as_float(v.x << 16);
-                        x[u][c][1] = __uint_as_float(v.x & 0xffff0000u);
-                        x[u][c][2] = __uint_as_float(v.y << 16);
-                        x[u][c][3] = __uint_as_float(v.y & 0xffff0000u);
+                        x[c][0] = __uint_as_float(v.x << 16);
+                        x[c][1] = __uint_as_float(v.x & 0xffff0000u);
+                        x[c][2] = __uint_as_float(v.y << 16);
+                        x[c][3] = __uint_as_float(v.y & 0xffff0000u);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[u] = fmaxf(mx[u], fabsf(x[u][c][e]));
                 }
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-            }
-            // a power of two brings the row's largest value to [2^14, 2^15)
-            float f[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                int e = (int)((__float_as_uint(mx[u]) >> 23) & 0xffu) - 127;
-                e = min(max(e, -100), 127);
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e), exponents -113 .. 114
-                f[u] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[u][c][i] *= up;
-            }
-            f0 = f[0] * a.scale * kLog2e;
-            f1 = f[1] * a.scale * kLog2e;
+                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[c][e]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // a power of two brings the row's largest value to [2^14, 2^15)
+                int e = (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+                e = min(max(e, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e), exponents -113 .. 114
+                const float fr = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) {
-                qf[0][c][0] = pack_f16(x[0][c][0], x[0][c][1]);
-                qf[0][c][1] = pack_f16(x[1][c][0], x[1][c][1]);
-                qf[0][c][2] = pack_f16(x[0][c][2], x[0][c][3]);
-                qf[0][c][3] = pack_f16(x[1][c][2], x[1][c][3]);
-                if constexpr (kSplit) {
-                    qf[PARTS - 1][c][0] = rest_f16(x[0][c][0], x[0][c][1], qf[0][c][0]);
-                    qf[PARTS - 1][c][1] = rest_f16(x[1][c][0], x[1][c][1], qf[0][c][1]);
-                    qf[PARTS - 1][c][2] = rest_f16(x[0][c][2], x[0][c][3], qf[0][c][2]);
-                    qf[PARTS - 1][c][3] = rest_f16(x[1][c][2], x[1][c][3], qf[0][c][3]);
+                for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[c][i] *= up;
+                    const uint32_t b0 = pack_f16(x[c][0], x[c][1]), b1 = pack_f16(x[c][2], x[c][3]);
+                    if constexpr (kQShared) {
+                        qs[(c * NT + nt) * 32] = make_uint2(b0, b1);
+                    } else {
+                        qf[0][c][nt][0] = b0;
+                        qf[0][c][nt][1] = b1;
+                        if constexpr (kSplit) {
+                            qf[PARTS - 1][c][nt][0] = rest_f16(x[c][0], x[c][1], b0);
+                            qf[PARTS - 1][c][nt][1] = rest_f16(x[c][2], x[c][3], b1);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[c][nt][i] = 0.f;
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) O[c][u][i] = 0.f;
+                for (int u = 0; u < 2; ++u) {
+                    f[nt][u] = __shfl_sync(0xffffffffu, fr, 8 * cq + 4 * u);
+                    seen[nt][u] = __shfl_sync(0xffffffffu, sees, 8 * cq + 4 * u);
+                    m[nt][u] = -INFINITY;
+                    l[nt][u] = 0.f;
+                }
             }
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
             vu = vtop = 0.f;
-            seen0 = seen[0];
-            seen1 = seen[1];
         };
         // this segment's result: the output where the whole unit was here, else a piece
         auto finish = [&](bool whole, int slot) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                int t, head;
-                const int r = g + 8 * u;
-                if (!row_of(r, t, head)) continue;
-                const float l = u ? l1 : l0;
-                const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
-                float* pd = po + ((int64_t)slot * rows_max + r) * D;
-                TIO* od = static_cast<TIO*>(a.out) + ((int64_t)cc.n * a.L + t) * tokrow + (int64_t)head * D;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < NCH; ++c) {
-                    // channels 16 c + 4 cq + {0, 1, 2, 3}: even ones from the first product, odd from the second
-                    const float4 o = make_float4(O[c][0][2 * u] * mul, O[c][1][2 * u] * mul, O[c][0][2 * u + 1] * mul,
-                                                 O[c][1][2 * u + 1] * mul);
-                    if (!whole) {
-                        *reinterpret_cast<float4*>(pd + 16 * c + 4 * cq) = o;
-                    } else if constexpr (kSplit) {
-                        *reinterpret_cast<float4*>(od + 16 * c + 4 * cq) = o;
-                    } else {
-                        *reinterpret_cast<uint2*>(od + 16 * c + 4 * cq) =
-                            make_uint2(tc::pack_bf16(o.x, o.y), tc::pack_bf16(o.z, o.w));
+                for (int u = 0; u < 2; ++u) {
+                    float sum = l[nt][u];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    int t, head;
+                    const int r = 8 * nt + 2 * cq + u;
+                    if (!row_of(r, t, head)) continue;
+                    const float mul = whole ? (sum == 0.f ? 0.f : vu / sum) : vu;
+                    float* pd = po + ((int64_t)slot * rows_max + r) * D + 2 * g;
+                    TIO* od = static_cast<TIO*>(a.out) + ((int64_t)cc.n * a.L + t) * tokrow + (int64_t)head * D + 2 * g;
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) {
+                        const float2 o = make_float2(O[c][nt][u] * mul, O[c][nt][2 + u] * mul);  // channels 16 c + 2 g + {0, 1}
+                        if (!whole) *reinterpret_cast<float2*>(pd + 16 * c) = o;
+                        else if constexpr (kSplit) *reinterpret_cast<float2*>(od + 16 * c) = o;
+                        else *reinterpret_cast<uint32_t*>(od + 16 * c) = tc::pack_bf16(o.x, o.y);
                     }
+                    if (!whole && g == 0) ml[(int64_t)slot * rows_max + r] = make_float2(m[nt][u], sum);
                 }
-                if (!whole && cq == 0) ml[(int64_t)slot * rows_max + r] = make_float2(u ? m1 : m0, l);
-            }
         };
 
         // a tile's scales are read while the tile before it is computed
@@ -443,7 +451,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         };
         __syncwarp();
         Scales next = load_scales(0);
-        for (int it = 0; it < count && !gone; ++it) {
+        int it = 0;
+        for (; it < count; ++it) {
             const int st = it % S;
             if (!begun) {
                 start_unit();
@@ -480,18 +489,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 for (int r = from; r < to; ++r) {
 #pragma unroll
                     for (int c = 0; c < NCH; ++c) {
-                        uint32_t* at = reinterpret_cast<uint32_t*>(vt + swizzle<D>((uint32_t)(r * D + 16 * c)) + 4 * cq);
-                        const uint32_t u = *at;
-                        const uint32_t nan = __vcmpeq4(u & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        if (nan != 0u) {
-                            // bytes 0, 2 belong to the even channels' product, 1, 3 to the odd one's
+                        // channels 16 c + 2 g + {0, 1}
+                        const uint32_t u = *reinterpret_cast<const uint16_t*>(vt + swizzle<D>((uint32_t)(r * D + 16 * c)) + 2 * g);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((nan >> (8 * e)) & 1u) {
-                                    if (key0 + r < seen0) O[c][e & 1][e >> 1] = NAN;
-                                    if (key0 + r < seen1) O[c][e & 1][2 + (e >> 1)] = NAN;
-                                }
-                            }
+                        for (int e = 0; e < 2; ++e) {
+                            if (((u >> (8 * e)) & 0x7fu) != 0x7fu) continue;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (key0 + r < seen[nt][i]) O[c][nt][2 * e + i] = NAN;
                         }
                     }
                     __syncwarp();
@@ -504,107 +511,89 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 tc::fence_async_smem();
             }
 
-            // z = q K^T over the four groups of eight keys
-            float z[4][4];
+            // z of keys 16 k + g (values 0, 1) and 16 k + g + 8 (values 2, 3) for rows 2 cq + {0, 1}
+            float z[2][NT][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[j][i] = 0.f;
-            // (four accumulators in turn, so that no product waits for the one before it)
-            if constexpr (D >= 64) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < NCH; c += 4) {
-                    uint32_t r[4][4];
+                    for (int i = 0; i < 4; ++i) z[k][nt][i] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ldsm4(r[j], ka + swizzle<D>((uint32_t)((8 * j + (lane & 7)) * D + (c + (lane >> 3)) * 16)));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t b0, b1;
-                            widen<kE4m3>(r[j][i], b0, b1);
-#pragma unroll
-                            for (int p = 0; p < PARTS; ++p) mma_f16(z[j], qf[p][c + i], b0, b1);
-                        }
-                }
-            } else {
+            for (int c = 0; c < NCH; c += 2) {
                 uint32_t r[2][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    ldsm4(r[j], ka + swizzle<D>((uint32_t)((8 * (2 * j + (lane >> 4)) + (lane & 7)) * D + ((lane >> 3) & 1) * 16)));
+                for (int k = 0; k < 2; ++k) ldsm4(r[k], ka + swizzle<D>((uint32_t)((16 * k + (lane & 15)) * D + (c + (lane >> 4)) * 16)));
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t kf[2][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t b0, b1;
-                        widen<kE4m3>(r[j >> 1][2 * (j & 1) + i], b0, b1);
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) mma_f16(z[j], qf[p][i], b0, b1);
+                    for (int k = 0; k < 2; ++k) {
+                        widen<kE4m3>(r[k][2 * i], kf[k][0], kf[k][2]);
+                        widen<kE4m3>(r[k][2 * i + 1], kf[k][1], kf[k][3]);
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 b;
+                        if constexpr (kQShared) b = qs[((c + i) * NT + nt) * 32];
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {
+                            if constexpr (!kQShared) b = make_uint2(qf[p][c + i][nt][0], qf[p][c + i][nt][1]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) mma_f16(z[k][nt], kf[k], b.x, b.y);
+                        }
+                    }
+                }
             }
-            // scores in base 2: z s, their maxima over the keys that are seen
-            float t0 = -INFINITY, t1 = -INFINITY;
+            // Scores in base 2 (z s), their maxima over the keys that are seen, and p = 2^(z s - m) with
+            // one rounding of the difference.  The reference m moves only when the maximum has grown by
+            // more than 2^8: p stays below f16's range, l and O hold the factor as well, and O is rarely
+            // rescaled.
             const bool edge = partial || key0 + kTile > cc.len - a.L + 1;
-            // this thread's key 8 j + 2 cq + e of the tile: does the row that sees `seen` keys see it?
-            auto sees = [&](int j, int e, int seen) { return (j < 2 ? has0 : has1) && key0 + 8 * j + 2 * cq + e < seen; };
-            const float s00 = f0 * ks0, s01 = f0 * ks1, s10 = f1 * ks0, s11 = f1 * ks1;
-            if (!edge) {
+            // does a row that sees `n` keys see this thread's key 16 k + 8 e + g of the tile?
+            auto sees = [&](int k, int e, int n) { return (k == 0 ? has0 : has1) && key0 + 16 * k + 8 * e + g < n; };
+            float alpha[NT][2];
+            bool moved = false;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
-                    t0 = fmaxf(t0, fmaxf(z[j][0] * s0, z[j][1] * s0));
-                    t1 = fmaxf(t1, fmaxf(z[j][2] * s1, z[j][3] * s1));
-                }
-            } else {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
+                for (int u = 0; u < 2; ++u) {
+                    const float s0 = f[nt][u] * ks0, s1 = f[nt][u] * ks1;
+                    float top;
+                    if (!edge) {
+                        top = fmaxf(fmaxf(z[0][nt][u] * s0, z[0][nt][2 + u] * s0), fmaxf(z[1][nt][u] * s1, z[1][nt][2 + u] * s1));
+                    } else {
+                        top = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (sees(k, e, seen[nt][u])) top = fmaxf(top, z[k][nt][2 * e + u] * (k ? s1 : s0));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float now = top > m[nt][u] + 8.f ? top : m[nt][u];
+                    const float ref = now == -INFINITY ? 0.f : now;
+                    alpha[nt][u] = ex2(m[nt][u] - ref);
+                    moved |= now != m[nt][u];
+                    m[nt][u] = now;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (sees(j, e, seen0)) t0 = fmaxf(t0, z[j][e] * s0);
-                        if (sees(j, e, seen1)) t1 = fmaxf(t1, z[j][2 + e] * s1);
+                        z[0][nt][2 * e + u] = ex2(fmaf(z[0][nt][2 * e + u], s0, -ref));
+                        z[1][nt][2 * e + u] = ex2(fmaf(z[1][nt][2 * e + u], s1, -ref));
                     }
-                }
-            }
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-            // the reference moves only when the maximum has grown by more than 2^8: p stays below f16's
-            // range, l and O hold the factor as well, and O is rarely rescaled
-            const float n0 = t0 > m0 + 8.f ? t0 : m0, n1 = t1 > m1 + 8.f ? t1 : m1;
-            const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-            float a0 = ex2(m0 - u0), a1 = ex2(m1 - u1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= a0;
-            l1 *= a1;
-            // p = 2^(z s - m) with one rounding of the difference
+                    if (edge) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s0 = j < 2 ? s00 : s01, s1 = j < 2 ? s10 : s11;
+                        for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    z[j][e] = ex2(fmaf(z[j][e], s0, -u0));
-                    z[j][2 + e] = ex2(fmaf(z[j][2 + e], s1, -u1));
-                }
-            }
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!sees(j, e, seen0)) z[j][e] = 0.f;
-                        if (!sees(j, e, seen1)) z[j][2 + e] = 0.f;
+                            for (int e = 0; e < 2; ++e)
+                                if (!sees(k, e, seen[nt][u])) z[k][nt][2 * e + u] = 0.f;
                     }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                l0 += z[j][0] + z[j][1];
-                l1 += z[j][2] + z[j][3];
-            }
-            // O += p V, sixteen keys (at most one page) at a time
+                    l[nt][u] = l[nt][u] * alpha[nt][u] + ((z[0][nt][u] + z[0][nt][2 + u]) + (z[1][nt][u] + z[1][nt][2 + u]));
+                }
+            bool rescale = __any_sync(0xffffffffu, moved);
+            // O^T += V^T P^T, sixteen keys (at most one page) at a time
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const float vs = s == 0 ? vs0 : vs1;
@@ -618,52 +607,47 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float nu = fmaxf(mag, vtop * 9.094947e-13f);
                     ratio = vu == 0.f ? 0.f : vu / nu;
                     vu = nu;
+                    rescale = true;
                 }
-                const float b0 = a0 * ratio, b1 = a1 * ratio;
-                a0 = a1 = 1.f;
-                if (__any_sync(0xffffffffu, b0 != 1.f || b1 != 1.f)) {
+                if (rescale) {
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float b0 = alpha[nt][0] * ratio, b1 = alpha[nt][1] * ratio;
+                        alpha[nt][0] = alpha[nt][1] = 1.f;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            O[c][u][0] *= b0;
-                            O[c][u][1] *= b0;
-                            O[c][u][2] *= b1;
-                            O[c][u][3] *= b1;
+                        for (int c = 0; c < NCH; ++c) {
+                            O[c][nt][0] *= b0;
+                            O[c][nt][1] *= b1;
+                            O[c][nt][2] *= b0;
+                            O[c][nt][3] *= b1;
                         }
+                    }
+                    rescale = false;
                 }
                 const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs / vu;
-                uint32_t pf[PARTS][4];
-                float y[2][4];
+                uint32_t pf[PARTS][NT][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[j][i] = z[2 * s + j][i] * pv;
-                pf[0][0] = pack_f16(y[0][0], y[0][1]);
-                pf[0][1] = pack_f16(y[0][2], y[0][3]);
-                pf[0][2] = pack_f16(y[1][0], y[1][1]);
-                pf[0][3] = pack_f16(y[1][2], y[1][3]);
-                if constexpr (kSplit) {
-                    pf[PARTS - 1][0] = rest_f16(y[0][0], y[0][1], pf[0][0]);
-                    pf[PARTS - 1][1] = rest_f16(y[0][2], y[0][3], pf[0][1]);
-                    pf[PARTS - 1][2] = rest_f16(y[1][0], y[1][1], pf[0][2]);
-                    pf[PARTS - 1][3] = rest_f16(y[1][2], y[1][3], pf[0][3]);
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = z[s][nt][2 * e] * pv, y1 = z[s][nt][2 * e + 1] * pv;
+                        const uint32_t h = pack_f16(y0, y1);
+                        pf[0][nt][e] = transpose8(h);
+                        if constexpr (kSplit) pf[PARTS - 1][nt][e] = transpose8(rest_f16(y0, y1, h));
+                    }
 #pragma unroll
                 for (int c = 0; c < NCH; c += 2) {
                     uint32_t r[4];
-                    const int row = 16 * s + (lane & 15), ch = c + (lane >> 4);
-                    ldsm4t(r, va + swizzle<D>((uint32_t)(row * D + ch * 16)));
+                    ldsm4t(r, va + swizzle<D>((uint32_t)((16 * s + (lane & 15)) * D + (c + (lane >> 4)) * 16)));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t e0, e1, o0, o1;
-                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x6420), e0, e1);
-                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x7531), o0, o1);
+                        uint32_t vf[4];
+                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x6420), vf[0], vf[2]);
+                        widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x7531), vf[1], vf[3]);
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {
-                            mma_f16(O[c + i][0], pf[p], e0, e1);
-                            mma_f16(O[c + i][1], pf[p], o0, o1);
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p) mma_f16(O[c + i][nt], vf, pf[p][nt][0], pf[p][nt][1]);
                     }
                 }
             }
@@ -673,13 +657,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const bool unit_end = cc.i + 1 == cc.tiles;
             if (unit_end || it + 1 == count) {
                 const bool here = (int64_t)cc.i <= it;  // the unit's first tile was this worker's
+                const int64_t unit = (int64_t)cc.n * per_tile + (int64_t)cc.h * row_tiles + cc.rt;
                 if (here && unit_end) {
                     finish(true, 0);
+                    if (by_unit && lane == 0) records[unit].n = -1;
                 } else {
                     finish(false, (int)(2 * worker + (here ? 1 : 0)));
                     if (here) {
                         const int64_t e = b0 + it + (cc.tiles - cc.i);  // past the unit's last tile
-                        mine = Record{cc.n, cc.h, cc.rt, (int32_t)((e * W + total - 1) / total - 1)};
+                        mine = Record{cc.n, cc.h, cc.rt, (int32_t)worker, (int32_t)((e * W + total - 1) / total - 1)};
+                        if (by_unit && lane == 0) records[unit] = mine;
                     }
                 }
                 begun = false;
@@ -687,33 +674,40 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             next_tile(a, row_tiles, cc);
         }
         if (gone) {
-            // copies still in flight land in shared memory that the CTA gives back: wait for them
-            for (int it = 0; it < issued; ++it) {
-                if (it + S >= issued) (void)tc::mbar_wait(&full[w][it % S], (uint32_t)(it / S) & 1u, kCopyTries);
+            // units begun here that will not be finished: nothing to join
+            for (bool begun_here = cc.i <= it; it < count; begun_here = cc.i == 0, ++it) {
+                if (by_unit && begun_here && lane == 0)
+                    records[(int64_t)cc.n * per_tile + (int64_t)cc.h * row_tiles + cc.rt].n = -1;
+                next_tile(a, row_tiles, cc);
             }
+            // copies still in flight land in shared memory that the CTA gives back: wait for them
+            for (int i = max(0, issued - S); i < issued; ++i) (void)tc::mbar_wait(&full[w][i % S], (uint32_t)(i / S) & 1u, kCopyTries);
             if (lane == 0) atomicOr(&flag, kCheckTimeout);
             mine.n = -1;
         }
     }
-    if (lane == 0) *rec = mine;
+    if (!by_unit && lane == 0) records[worker] = mine;
     __syncthreads();
     if (tid == 0) reinterpret_cast<uint32_t*>(a.ws + L.flags)[blockIdx.x] = flag;
 }
 
 // Joins a unit's pieces: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the workers that hold
-// one, in order.  CTA w looks after the unit that worker w left unfinished, if any; a warp takes a
-// row at a time, a lane D / 32 channels.
+// one, in an order that the pieces' number fixes.  Block x looks after record x; `wpr` warps take a
+// row's pieces in turn (many where few units were cut into many pieces), a lane D / 32 channels.
+constexpr int kCombineWarps = 8;
+
 template <typename TIO, int D>
-__global__ void __launch_bounds__(128) kda_attn_combine_kernel(const AttnDecodeArgs a, const int rows_max)
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    kda_attn_combine_kernel(const AttnDecodeArgs a, const int rows_max, const int workers, const int unit_rows, const int wpr)
 {
     constexpr int V = D / 32;
-    const int workers = gridDim.x;
+    __shared__ float part[kCombineWarps][D + 1];
+    __shared__ uint32_t word;
     const DecodeLayout L = decode_layout(workers, rows_max, D);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     griddep_wait();
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
         // the call's check word: every CTA's flags, so that nothing has to be cleared before the call
-        __shared__ uint32_t word;
         if (threadIdx.x == 0) word = 0u;
         __syncthreads();
         uint32_t f = 0u;
@@ -723,26 +717,26 @@ __global__ void __launch_bounds__(128) kda_attn_combine_kernel(const AttnDecodeA
         __syncthreads();
         if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(a.ws) = word;
     }
-    const int w0 = blockIdx.x;
-    const Record rec = reinterpret_cast<const Record*>(a.ws + L.records)[w0];
+    const Record rec = reinterpret_cast<const Record*>(a.ws + L.records)[blockIdx.x];
     if (rec.n < 0) return;
     const float2* ml = reinterpret_cast<const float2*>(a.ws + L.ml);
     const float* po = reinterpret_cast<const float*>(a.ws + L.o);
-    const int pieces = rec.last - w0 + 1;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * w0 + 1 : 2 * (w0 + i)); };
-    for (int r = threadIdx.x >> 5; r < rows_max; r += blockDim.x / 32) {
-        const int R = rec.rt * kRows + r;
-        if (R >= a.L * a.group) break;
+    const int pieces = rec.last - rec.first + 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * rec.first + 1 : 2 * (rec.first + i)); };
+    const int r = blockIdx.y * (kCombineWarps / wpr) + w / wpr;
+    const int R = rec.rt * unit_rows + r;
+    const bool on = r < rows_max && R < a.L * a.group;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    if (on) {
         float m = -INFINITY;
         for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         const float mu = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll 4
-        for (int i = 0; i < pieces; ++i) {
+        for (int i = w % wpr; i < pieces; i += wpr) {
             const float2 x = ml[slot(i) * rows_max + r];
             const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
             const float f = ex2(x.x - mu);
@@ -757,12 +751,25 @@ __global__ void __launch_bounds__(128) kda_attn_combine_kernel(const AttnDecodeA
                 o[0] += *p * f;
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int t = R / a.group, head = rec.h * a.group + (R - t * a.group);
-        TIO* od = static_cast<TIO*>(a.out) + (((int64_t)rec.n * a.L + t) * a.Hq + head) * D + lane * V;
-#pragma unroll
-        for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
     }
+    if (wpr > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) part[w][lane * V + v] = o[v];
+        if (lane == 0) part[w][D] = l;
+        __syncthreads();
+        if (w % wpr != 0) return;
+        for (int i = 1; i < wpr; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] += part[w + i][lane * V + v];
+            l += part[w + i][D];
+        }
+    }
+    if (!on) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int t = R / a.group, head = rec.h * a.group + (R - t * a.group);
+    TIO* od = static_cast<TIO*>(a.out) + (((int64_t)rec.n * a.L + t) * a.Hq + head) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
 }
 
 namespace {
@@ -783,27 +790,47 @@ bool encode_codes(CUtensorMap* m, const void* base, const AttnDecodeArgs& a)
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int decode_ctas() { return kCtasPerSm * sm_count_of_current_device(); }
+int decode_ctas(int nt) { return ctas_of(nt) * sm_count_of_current_device(); }
+
+template <typename TIO, int D, bool kE4m3, int NT>
+cudaError_t launch_nt(const AttnDecodeArgs& a, cudaStream_t s)
+{
+    Maps maps;
+    if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
+    constexpr int smem = kWarps * (stages_of(NT, D) * 2 * kTile * D + (NT == 4 ? D / 16 * NT * 32 * 8 : 0)) + 1024;
+    static_assert(ctas_of(NT) * (smem + 3072) <= 233472, "the rings of an SM's CTAs fit");
+    auto kern = kda_attn_decode_kernel<TIO, D, kE4m3, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t rows_all = (int64_t)a.L * a.group;
+    const int rows = (int)(rows_all < 8 * NT ? rows_all : 8 * NT);
+    const int64_t units = (int64_t)a.N * a.Hkv * ((rows_all + 8 * NT - 1) / (8 * NT));
+    // no more workers than tiles that the page table can hold
+    const double most = (double)units * (((int64_t)a.c.max_pages * a.c.page + kTile - 1) / kTile);
+    const int full = decode_ctas(NT);
+    const int ctas = most < (double)full * kWarps ? (int)((most + kWarps - 1) / kWarps) : full;
+    const int workers = ctas * kWarps;
+    const bool by_unit = units <= workers;
+    kern<<<ctas, kThreads, smem, s>>>(a, maps, rows, by_unit);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // about workers / units pieces a unit: four or more a warp
+    const int64_t pieces = by_unit ? workers / units : 1;
+    const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
+    const int rpb = kCombineWarps / wpr;
+    const dim3 grid((unsigned)(by_unit ? units : workers), (unsigned)((rows + rpb - 1) / rpb));
+    return launch_dependent(kda_attn_combine_kernel<TIO, D>, grid, dim3(kCombineWarps * 32), 0, s, a, rows, workers, 8 * NT, wpr);
+}
 
 template <typename TIO, int D, bool kE4m3>
 cudaError_t launch_decode_d(const AttnDecodeArgs& a, cudaStream_t s)
 {
-    Maps maps;
-    if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
-    constexpr int smem = kWarps * stages_of(D) * 2 * kTile * D + 1024;
-    static_assert(kCtasPerSm * (smem + 4096) <= 232448, "the rings of an SM's CTAs fit");
-    auto kern = kda_attn_decode_kernel<TIO, D, kE4m3>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int rows = a.L * a.group < kRows ? a.L * a.group : kRows;
-    // no more workers than tiles that the page table can hold
-    const int64_t row_tiles = ((int64_t)a.L * a.group + kRows - 1) / kRows;
-    const double most = (double)a.N * a.Hkv * row_tiles * (((int64_t)a.c.max_pages * a.c.page + kTile - 1) / kTile);
-    const int ctas = most < (double)decode_ctas() * kWarps ? (int)((most + kWarps - 1) / kWarps) : decode_ctas();
-    kern<<<ctas, kThreads, smem, s>>>(a, maps, rows);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kda_attn_combine_kernel<TIO, D>, dim3((unsigned)(ctas * kWarps)), dim3(128), 0, s, a, rows);
+    const int nt = nt_of((int64_t)a.L * a.group, sizeof(TIO) == 4);
+    if (nt == 1) return launch_nt<TIO, D, kE4m3, 1>(a, s);
+    if constexpr (sizeof(TIO) == 2) {
+        if (nt == 4) return launch_nt<TIO, D, kE4m3, 4>(a, s);
+    }
+    return launch_nt<TIO, D, kE4m3, 2>(a, s);
 }
 
 template <typename TIO, bool kE4m3>
@@ -816,7 +843,11 @@ cudaError_t launch_decode_io(const AttnDecodeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int rows, int d) { return decode_layout(decode_ctas() * kWarps, rows, d).total; }
+size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt)
+{
+    const int nt = nt_of(rows, dt == KDA_F32);
+    return decode_layout(decode_ctas(nt) * kWarps, (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
+}
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s)
 {
