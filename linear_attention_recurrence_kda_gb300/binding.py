@@ -102,6 +102,8 @@ _vp = ctypes.c_void_p
 def lib():
     """The loaded libkda.so with argument types declared (raises if it is not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -184,6 +186,8 @@ def _stream(stream=None):
 
 
 def _need(t, name, dtype, shape, device):
+    if t is not None and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -531,6 +535,8 @@ _CODES = {torch.float8_e4m3fn: KDA_CACHE_E4M3, torch.int8: KDA_CACHE_INT8}
 
 def _tokens(t, name, dtype, heads, d, device):
     """Checks t [T, heads, d] with packed heads and channels; returns its stride between tokens."""
+    if t.dtype == dtype and t.shape == (t.shape[0], heads, d) and t.device == device and t.is_contiguous():
+        return heads * d
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
@@ -555,21 +561,25 @@ def _io_dtype(t, name):
 def _cache(cache, block_table, N, hkv, d, device):
     """The KdaCache descriptor of a KvCache and its block table."""
     k, v, k_scale, v_scale = cache
-    if k.dtype not in _CODES:
-        raise TypeError(f"cache.k: dtype {k.dtype}, expected one of {tuple(_CODES)}")
+    dt = k.dtype
+    if dt not in _CODES:
+        raise TypeError(f"cache.k: dtype {dt}, expected one of {tuple(_CODES)}")
     if k.dim() != 4:
         raise ValueError(f"cache.k: shape {tuple(k.shape)}, expected (pages, heads, page_tokens, head_dim)")
-    pages, _, page, _ = k.shape
-    _need(k, "cache.k", k.dtype, (pages, hkv, page, d), device)
-    _need(v, "cache.v", k.dtype, (pages, hkv, page, d), device)
-    _need(k_scale, "cache.k_scale", torch.float32, (pages, hkv), device)
-    _need(v_scale, "cache.v_scale", torch.float32, (pages, hkv), device)
+    shape = k.shape
+    pages, page = shape[0], shape[2]
+    want = (pages, hkv, page, d)
+    _need(k, "cache.k", dt, want, device)
+    _need(v, "cache.v", dt, want, device)
+    want = (pages, hkv)
+    _need(k_scale, "cache.k_scale", torch.float32, want, device)
+    _need(v_scale, "cache.v_scale", torch.float32, want, device)
     if block_table.dim() != 2:
         raise ValueError(f"block_table: shape {tuple(block_table.shape)}, expected (sequences, pages)")
     cols = block_table.shape[1]
     _need(block_table, "block_table", torch.int32, (N, cols), device)
     return KdaCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), pages,
-                    page, cols, _CODES[k.dtype])
+                    page, cols, _CODES[dt])
 
 
 def kda_cache_alloc(num_pages: int, page_tokens: int, num_kv_heads: int, head_dim: int, dtype=torch.float8_e4m3fn,

@@ -3,6 +3,8 @@
 // the tokens that read it (kda_attn_decode.cu).
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 
 #include "kda_internal.cuh"
@@ -59,7 +61,25 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t 
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16, d = 64 or 128
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
-size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt);  // rows: window x group
+size_t attn_decode_workspace_bytes(int64_t rows, int d);  // rows: window x group
+
+// A kernel's dynamic shared memory limit, raised once for each device (the call costs about half a
+// microsecond, which short calls feel).
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};
+    template <typename F>
+    cudaError_t raise(F* kernel, int bytes)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+        if (bit != 0 && (done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // cuTensorMapEncodeTiled of the loaded driver, or NULL (kda_attn_api.cu).
 using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -38,10 +38,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // By the unit's rows (8 nt): O takes NT d / 4 registers, so few rows leave room for three CTAs on an SM.
 constexpr int ctas_of(int nt) { return nt == 1 ? 3 : 2; }
-constexpr int stages_of(int nt, int d) { return (nt == 2 ? 3 : 2) * (d == 128 ? 1 : d == 64 ? 2 : 3); }
+constexpr int stages_of(int nt, int d) { return (nt == 1 ? 2 : 3) * (d == 128 ? 1 : d == 64 ? 2 : 3); }
 
-// Column tiles of 8 rows for a call's rows; fp32 holds two parts of q and takes at most two.
-inline int nt_of(int64_t rows, bool split) { return rows <= 8 ? 1 : rows <= 16 || split ? 2 : 4; }
+// Column tiles of 8 rows for a call's rows.  More than 16 rows make several units that read the same
+// tiles (28 rows, 64 sequences of 3150 keys and 8 heads: 194 us by 16 rows with O in 128 registers less
+// than by 32, which took 202; by 8 rows 270).
+inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // Workspace: check word | per-CTA flags | records | (max, sum) of slots | outputs of slots.
 // Worker w owns slots 2 w (a unit begun by an earlier worker) and 2 w + 1 (begun here).
@@ -191,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
     constexpr bool kSplit = sizeof(TIO) == 4;  // fp32: q and p as two f16 parts
     constexpr int PARTS = kSplit ? 2 : 1;
     constexpr int kRows = 8 * NT;
-    constexpr bool kQShared = NT == 4;         // q's fragments wait in shared memory, not in registers
     constexpr int NCH = D / 16;                // 16-byte chunks of a row = k-steps of K Q^T
     constexpr int S = stages_of(NT, D);
     constexpr uint32_t TB = kTile * D;         // bytes of a K (or V) tile
@@ -205,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
     const int g = lane >> 2, cq = lane & 3;
     unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = smem + (size_t)w * S * 2 * TB;
-    uint2* qs = reinterpret_cast<uint2*>(smem + (size_t)kWarps * S * 2 * TB) + w * NCH * NT * 32 + lane;  // [NCH][NT][32]
     const DecodeLayout L = decode_layout(gridDim.x * kWarps, rows_max, D);
     const int rows_all = a.L * a.group;
     const int row_tiles = (rows_all + kRows - 1) / kRows;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
 
         // row 8 t + g of the unit as a product's second operand; this thread's results are of rows
         // 8 t + 2 cq + {0, 1}
-        uint32_t qf[PARTS][kQShared ? 1 : NCH][NT][2];
+        uint32_t qf[PARTS][NCH][NT][2];
         float O[NCH][NT][4];
         float m[NT][2], l[NT][2], f[NT][2], vu = 0.f, vtop = 0.f;
         int seen[NT][2];  // keys that the rows see
@@ -383,15 +383,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[c][i] *= up;
                     const uint32_t b0 = pack_f16(x[c][0], x[c][1]), b1 = pack_f16(x[c][2], x[c][3]);
-                    if constexpr (kQShared) {
-                        qs[(c * NT + nt) * 32] = make_uint2(b0, b1);
-                    } else {
-                        qf[0][c][nt][0] = b0;
-                        qf[0][c][nt][1] = b1;
-                        if constexpr (kSplit) {
-                            qf[PARTS - 1][c][nt][0] = rest_f16(x[c][0], x[c][1], b0);
-                            qf[PARTS - 1][c][nt][1] = rest_f16(x[c][2], x[c][3], b1);
-                        }
+                    qf[0][c][nt][0] = b0;
+                    qf[0][c][nt][1] = b1;
+                    if constexpr (kSplit) {
+                        qf[PARTS - 1][c][nt][0] = rest_f16(x[c][0], x[c][1], b0);
+                        qf[PARTS - 1][c][nt][1] = rest_f16(x[c][2], x[c][3], b1);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) O[c][nt][i] = 0.f;
@@ -533,16 +529,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                         widen<kE4m3>(r[k][2 * i + 1], kf[k][1], kf[k][3]);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint2 b;
-                        if constexpr (kQShared) b = qs[((c + i) * NT + nt) * 32];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {
-                            if constexpr (!kQShared) b = make_uint2(qf[p][c + i][nt][0], qf[p][c + i][nt][1]);
+                        for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) mma_f16(z[k][nt], kf[k], b.x, b.y);
-                        }
-                    }
+                            for (int k = 0; k < 2; ++k) mma_f16(z[k][nt], kf[k], qf[p][c + i][nt][0], qf[p][c + i][nt][1]);
                 }
             }
             // Scores in base 2 (z s), their maxima over the keys that are seen, and p = 2^(z s - m) with
@@ -723,7 +714,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const float* po = reinterpret_cast<const float*>(a.ws + L.o);
     const int pieces = rec.last - rec.first + 1;
     auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * rec.first + 1 : 2 * (rec.first + i)); };
-    const int r = blockIdx.y * (kCombineWarps / wpr) + w / wpr;
+    const int r = blockIdx.y * (blockDim.x / 32 / wpr) + w / wpr;
     const int R = rec.rt * unit_rows + r;
     const bool on = r < rows_max && R < a.L * a.group;
     float l = 0.f, o[V];
@@ -797,10 +788,11 @@ cudaError_t launch_nt(const AttnDecodeArgs& a, cudaStream_t s)
 {
     Maps maps;
     if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
-    constexpr int smem = kWarps * (stages_of(NT, D) * 2 * kTile * D + (NT == 4 ? D / 16 * NT * 32 * 8 : 0)) + 1024;
+    constexpr int smem = kWarps * stages_of(NT, D) * 2 * kTile * D + 1024;
     static_assert(ctas_of(NT) * (smem + 3072) <= 233472, "the rings of an SM's CTAs fit");
     auto kern = kda_attn_decode_kernel<TIO, D, kE4m3, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t rows_all = (int64_t)a.L * a.group;
     const int rows = (int)(rows_all < 8 * NT ? rows_all : 8 * NT);
@@ -817,19 +809,15 @@ cudaError_t launch_nt(const AttnDecodeArgs& a, cudaStream_t s)
     // about workers / units pieces a unit: four or more a warp
     const int64_t pieces = by_unit ? workers / units : 1;
     const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
-    const int rpb = kCombineWarps / wpr;
+    const int rpb = rows < kCombineWarps / wpr ? rows : kCombineWarps / wpr;
     const dim3 grid((unsigned)(by_unit ? units : workers), (unsigned)((rows + rpb - 1) / rpb));
-    return launch_dependent(kda_attn_combine_kernel<TIO, D>, grid, dim3(kCombineWarps * 32), 0, s, a, rows, workers, 8 * NT, wpr);
+    return launch_dependent(kda_attn_combine_kernel<TIO, D>, grid, dim3((unsigned)(rpb * wpr * 32)), 0, s, a, rows, workers, 8 * NT, wpr);
 }
 
 template <typename TIO, int D, bool kE4m3>
 cudaError_t launch_decode_d(const AttnDecodeArgs& a, cudaStream_t s)
 {
-    const int nt = nt_of((int64_t)a.L * a.group, sizeof(TIO) == 4);
-    if (nt == 1) return launch_nt<TIO, D, kE4m3, 1>(a, s);
-    if constexpr (sizeof(TIO) == 2) {
-        if (nt == 4) return launch_nt<TIO, D, kE4m3, 4>(a, s);
-    }
+    if (nt_of((int64_t)a.L * a.group) == 1) return launch_nt<TIO, D, kE4m3, 1>(a, s);
     return launch_nt<TIO, D, kE4m3, 2>(a, s);
 }
 
@@ -843,9 +831,9 @@ cudaError_t launch_decode_io(const AttnDecodeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt)
+size_t attn_decode_workspace_bytes(int64_t rows, int d)
 {
-    const int nt = nt_of(rows, dt == KDA_F32);
+    const int nt = nt_of(rows);
     return decode_layout(decode_ctas(nt) * kWarps, (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
 }
 

@@ -303,7 +303,8 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
     constexpr int smem = PL * (kRowsTile + 2 * kKeys) * D * 2 + 128;
     static_assert(smem + 4096 <= 232448, "the tiles fit an SM");
     auto kern = kda_attn_prefill_kernel<TIO, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a, kRowsTile / a.group);
     kern<<<(unsigned)(slots * a.Hkv), kThreads, smem, s>>>(a, (int)slots);

@@ -606,7 +606,8 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
         !encode_rows(&maps.v, a.v, D, a.Hkv, a.T, a.vs, 1, kKeys))
         return cudaErrorInvalidValue;
     auto kern = kda_attn_prefill_tc_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::SMEM);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(kern, (int)Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a, 2 * tpt);
     kern<<<(unsigned)(slots * a.Hkv), kThreads, Cfg<D>::SMEM, s>>>(a, maps, (int)slots);
