@@ -385,26 +385,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = warp_wait(&sh.v_load[e & 3], (e >> 2) & 1u) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
                     unsigned char* v = ring + (base + 2 * j + 1) % C::STAGES * C::TILE;
-#pragma unroll 8
-                    for (int i = lane; i < (int)C::TILE / 16; i += 32) {
-                        uint4* at = reinterpret_cast<uint4*>(v + i * 16);
-                        const uint4 u = *at;
-                        auto odd2 = [](uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; };
-                        if (odd2(u.x) || odd2(u.y) || odd2(u.z) || odd2(u.w)) {
-                            const int row = (i >> 3) & 127, key = j * kKeys + row;
+                    // eight vectors at a time: is there any exponent of all ones?  (Adding one to the
+                    // exponent's last place then carries into the sign's.)
+                    for (int i0 = lane; i0 < (int)C::TILE / 16; i0 += 8 * 32) {
+                        uint4 u[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) u[q] = *reinterpret_cast<const uint4*>(v + (i0 + 32 * q) * 16);
+                        uint32_t any = 0u;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            any |= (u[q].x & 0x7fff7fffu) + 0x00800080u;
+                            any |= (u[q].y & 0x7fff7fffu) + 0x00800080u;
+                            any |= (u[q].z & 0x7fff7fffu) + 0x00800080u;
+                            any |= (u[q].w & 0x7fff7fffu) + 0x00800080u;
+                        }
+                        if ((any & 0x80008000u) == 0u) continue;
+                        for (int q = 0; q < 8; ++q) {
+                            const int i = i0 + 32 * q, row = (i >> 3) & 127, key = j * kKeys + row;
                             const int ch = (i >> 10) * 64 + (((i & 7) ^ (row & 7)) << 3);
-                            uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                            uint16_t* x = reinterpret_cast<uint16_t*>(v + i * 16);
                             for (int c = 0; c < 8; ++c) {
-                                const uint32_t b = (x[c >> 1] >> (16 * (c & 1))) & 0xffffu;
+                                const uint32_t b = x[c];
                                 if ((b & 0x7f80u) != 0x7f80u) continue;
                                 if (key < t.last) {
                                     sh.dirty[turn & 1] = odd_tag(turn);
                                     atomicMin(&sh.odd[turn & 1][b & 0x7fu ? 2 : b >> 15][ch + c],
                                               (odd_tag(turn) << 10) | (uint32_t)(key - t.edge * kKeys));
                                 }
-                                x[c >> 1] &= ~(0xffffu << (16 * (c & 1)));
+                                x[c] = 0;
                             }
-                            *at = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                     }
                     tc::fence_async_smem();
@@ -417,30 +426,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
             }
-        } else if (lane == 0) {
+        } else {
             // ---- scheduler: this CTA's own tile, then tiles of CTAs that have not started yet
             uint32_t asked = 0;
             int idx = blockIdx.x;
+            auto take = [&]() {
+                int x = -1;
+                if (lane == 0 && *dead == 0u) x = take_tile(sh.answer, &sh.answer_full, asked);
+                ++asked;
+                return __shfl_sync(0xffffffffu, x, 0);
+            };
             for (uint32_t turn = 0;; ++turn) {
                 TileInfo f{};
                 for (;;) {
                     AttnTile x;
+                    if (idx < 0) break;
                     // the longest rows of every sequence first
-                    if (idx >= 0 && attn_tile(a, slots - 1 - idx / a.Hkv, 2 * tpt, x)) {
+                    if (attn_tile(a, slots - 1 - idx / a.Hkv, 2 * tpt, x)) {
                         f = TileInfo{x.start, x.first, x.last, idx % a.Hkv, 1};
                         break;
                     }
-                    if (idx < 0) break;
-                    idx = take_tile(sh.answer, &sh.answer_full, asked++);
+                    idx = take();
                 }
-                if (!tc::mbar_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u, kTries)) *dead = 1u;
-                if (*dead) f.valid = 0;
-                sh.info[turn & 1] = f;
-                tc::mbar_arrive(&sh.info_full[turn & 1]);
+                if (!warp_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u)) *dead = 1u;
+                if (__any_sync(0xffffffffu, *dead != 0u)) f.valid = 0;
+                if (lane == 0) {
+                    sh.info[turn & 1] = f;
+                    tc::mbar_arrive(&sh.info_full[turn & 1]);
+                }
                 if (!f.valid) break;
                 // not before the tile is nearly done, so that tiles go to whoever is free
-                if (!tc::mbar_wait(&sh.near_end, turn & 1u, kTries)) *dead = 1u;
-                idx = *dead ? -1 : take_tile(sh.answer, &sh.answer_full, asked++);
+                if (!warp_wait(&sh.near_end, turn & 1u)) *dead = 1u;
+                idx = take();
             }
         }
         __syncwarp();

@@ -19,7 +19,9 @@ inline int64_t attn_slots(const AttnArgs& a, int tokens)
     return (a.T / a.N + tokens - 1) / tokens * a.N;
 }
 
-// The tile of a slot; false where it holds no token.  Offsets outside [0, T] are clamped.
+// The tile of a slot; false where it holds no token.  Offsets outside [0, T] are clamped.  Called by
+// whole warps: 32 sequences are looked at in a step, so that a handful of sequences take one round
+// of loads and not a chain of them.
 __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int slot, int tokens, AttnTile& t)
 {
     int64_t start, end;
@@ -32,16 +34,19 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int slot, int token
         start = n * len;
         end = start + len;
     } else {
+        // the last sequence whose slots begin at or before this one
         int lo = 0, hi = a.N - 1;
         while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)a.cu[mid] / tokens + mid <= slot) lo = mid;
-            else hi = mid - 1;
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + ((int)(threadIdx.x & 31) + 1) * step;
+            const bool yes = at <= hi && (int64_t)a.cu[at] / tokens + at <= slot;
+            lo += __popc(__ballot_sync(0xffffffffu, yes)) * step;
+            hi = min(hi, lo + step - 1);
         }
-        const int64_t c0 = a.cu[lo];
+        const int64_t c0 = a.cu[lo], c1 = a.cu[lo + 1];
         j = (int)(slot - (c0 / tokens + lo));
         start = min(max(c0, (int64_t)0), a.T);
-        end = min(max((int64_t)a.cu[lo + 1], (int64_t)0), a.T);
+        end = min(max(c1, (int64_t)0), a.T);
     }
     const int64_t first = (int64_t)j * tokens;
     if (j < 0 || first >= end - start) return false;
