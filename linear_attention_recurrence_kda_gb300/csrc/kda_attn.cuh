@@ -1,5 +1,5 @@
 // kda_attn.cuh -- arguments and launchers of the softmax-attention kernels (declared in kda.h):
-// prompts (kda_attn_prefill.cu, kda_attn_prefill_tc.cu), the 8-bit paged cache (kda_cache.cu) and
+// prompts (kda_attn_prefill_tc.cu for bf16, kda_attn_prefill_f32.cu), the 8-bit paged cache (kda_cache.cu) and
 // the tokens that read it (kda_attn_decode.cu).
 #pragma once
 
@@ -57,8 +57,8 @@ struct AttnDecodeArgs {
     CacheArgs c;
 };
 
-cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t s);
-cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16, d = 64 or 128
+cudaError_t launch_attn_prefill_f32(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
 size_t attn_decode_workspace_bytes(int64_t rows, int d);  // rows: window x group

@@ -127,7 +127,8 @@ kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, 
     if ((st = token_stride(p.k_stride, p.num_kv_heads, p, &a.ks)) != KDA_OK) return st;
     if ((st = token_stride(p.v_stride, p.num_kv_heads, p, &a.vs)) != KDA_OK) return st;
     // one CTA for each tile of tokens and key head: the grid's first axis holds 2^31 - 1
-    const int64_t tile = kda::kMaxGroup / (p.num_heads / p.num_kv_heads);
+    const int group = p.num_heads / p.num_kv_heads;
+    const int64_t tile = group <= 64 ? 64 / group : 1;  // tokens of the smallest tile
     if ((p.total_tokens / tile + p.num_seqs) * p.num_kv_heads > 2147483647LL) return KDA_ERR_UNSUPPORTED;
     if (p.total_tokens > 0 && (!q || !k || !v || !out)) return KDA_ERR_INVALID_ARG;
     for (const void* ptr : {q, k, v, (const void*)out}) {
@@ -152,7 +153,7 @@ kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, 
     a.group = p.num_heads / p.num_kv_heads; a.d = p.head_dim; a.scale = p.scale;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     kda::prof_start("kda_attention_prefill", s);
-    const cudaError_t e = kda::launch_attn_prefill(a, p.io_dtype, s);
+    const cudaError_t e = p.io_dtype == KDA_BF16 ? kda::launch_attn_prefill_tc(a, s) : kda::launch_attn_prefill_f32(a, s);
     kda::prof_stop(s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

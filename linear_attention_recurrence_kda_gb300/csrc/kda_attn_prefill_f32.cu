@@ -1,14 +1,18 @@
-// kda_attn_prefill.cu -- causal attention over packed prompts (kda_attention_prefill): the form for
-// every size and type, on warp-level products.
+// kda_attn_prefill_f32.cu -- causal attention over packed prompts in fp32 (kda_attention_prefill), on
+// warp-level products.
 //
 //   z_ij = scale q_i . k_j,  p_ij = exp(z_ij - m_i),  o_i = sum_j p_ij v_j / sum_j p_ij,  j <= i
 // with the maximum m_i and the sums carried along the keys in fp32 (one pass over K and V).
 //
-// A tile holds 128 rows: the query heads of one key head's group times 128 / group tokens, so that
-// a group's heads share every K and V tile and the diagonal wastes little.  Eight warps take 16 rows
-// each; keys come in tiles of 64.  bf16 operands enter m16n8k16 as they are; an fp32 operand x
-// enters as x1 + x2 + x3 with x1 = bf16(x), x2 = bf16(x - x1), x3 = bf16(x - x1 - x2) (24 bits, fp32's
-// range) and a product as its six terms down to 2^-16 of the first.
+// A tile holds 64 rows (128 for groups of more than 64 heads): the query heads of one key head's group
+// times 64 / group tokens, so that a group's heads share every K and V tile and the diagonal wastes
+// little.  Warps take 16 rows each; keys come in tiles of half as many.  Two CTAs share an SM: with
+// 128 rows and one CTA the longest rows of a few prompts set the time (prompts of 200, 750 and 1300
+// tokens, 10 of 2 heads of 128 channels: 195 us against 169).  An fp32 operand x enters m16n8k16 bf16 products as x1 + x2 + x3 with
+// x1 = bf16(x), x2 = bf16(x - x1), x3 = bf16(x - x1 - x2) (24 bits, fp32's range), a product as its six
+// terms down to 2^-16 of the first.  Those products bound it: at 128 channels 12 a warp and key,
+// about 8 cycles each on a sub-partition that two warps share; a tile's loads overlap with the products of
+// the tile before it where the registers for them are there (up to 64 channels).
 //
 // Hidden keys: a score is replaced, not added to, and an infinity or NaN in V leaves the tile and is
 // noted by channel and position; at the end it joins the rows that see it, so no row meets another
@@ -20,10 +24,6 @@
 namespace kda {
 
 namespace {
-
-constexpr int kRowsTile = 128;
-constexpr int kKeys = 64;
-constexpr int kThreads = 256;
 
 template <int D>
 __device__ __forceinline__ uint32_t tile_off(int row, int chunk)  // 16-byte chunk of a row of D 16-bit values
@@ -53,8 +53,9 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+constexpr int PL = 3;  // bf16 parts of a value
+
 // the bf16 parts of a pair; an infinity or NaN stays in the first alone
-template <int PL>
 __device__ __forceinline__ void split2(float lo, float hi, uint32_t (&part)[PL])
 {
 #pragma unroll
@@ -68,33 +69,42 @@ __device__ __forceinline__ void split2(float lo, float hi, uint32_t (&part)[PL])
     }
 }
 
-// eight values of a row (zeros beyond it)
-template <typename TIO>
-__device__ __forceinline__ void load8(const TIO* p, bool ok, float (&x)[8])
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    if constexpr (sizeof(TIO) == 2) {
-        const uint4 u = ok ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// eight values of a row (zeros beyond it)
+struct Vec8 {
+    float x[8];
+    __device__ __forceinline__ void load(const float* p, bool ok)
+    {
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 a = ok ? reinterpret_cast<const float4*>(p)[0] : z;
         const float4 b = ok ? reinterpret_cast<const float4*>(p)[1] : z;
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-}
+    // the three parts as three 16-byte chunks, `plane` bytes apart
+    __device__ __forceinline__ void store(unsigned char* at, uint32_t plane) const
+    {
+        uint32_t part[4][PL];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], part[e]);
+#pragma unroll
+        for (int p = 0; p < PL; ++p)
+            *reinterpret_cast<uint4*>(at + p * plane) = make_uint4(part[0][p], part[1][p], part[2][p], part[3][p]);
+    }
+};
 
 }  // namespace
 
-template <typename TIO, int D>
-__global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const AttnArgs a, const int slots)
+template <int D, int ROWS>
+__global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_kernel(const AttnArgs a, const int slots)
 {
-    constexpr int PL = sizeof(TIO) == 4 ? 3 : 1;
+    constexpr int kRowsTile = ROWS, kKeys = ROWS / 2, kThreads = 2 * ROWS;
     constexpr int NK = D / 16;
     constexpr uint32_t QB = kRowsTile * D * 2, KB = kKeys * D * 2;
     extern __shared__ unsigned char smem_raw[];
@@ -117,16 +127,25 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
     for (int i = tid; i < kRowsTile * CH; i += kThreads) {
         const int r = i / CH, c = i % CH;
         const int tok = r / a.group;
-        float x[8];
-        load8(static_cast<const TIO*>(a.q) + (t.start + t.first + tok) * a.qs + (int64_t)(h * a.group + r - tok * a.group) * D + c * 8,
-              r < rows, x);
-        uint32_t part[4][PL];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split2<PL>(x[2 * e], x[2 * e + 1], part[e]);
-#pragma unroll
-        for (int p = 0; p < PL; ++p)
-            *reinterpret_cast<uint4*>(sq + p * QB + tile_off<D>(r, c)) = make_uint4(part[0][p], part[1][p], part[2][p], part[3][p]);
+        Vec8 x;
+        x.load(static_cast<const float*>(a.q) + (t.start + t.first + tok) * a.qs + (int64_t)(h * a.group + r - tok * a.group) * D + c * 8,
+               r < rows);
+        x.store(sq + tile_off<D>(r, c), QB);
     }
+    // a key tile: NV vectors of K and of V a thread
+    constexpr int NV = kKeys * CH / kThreads;
+    constexpr bool kAhead = D <= 64;  // the registers hold the next tile while this one is computed
+    Vec8 kx[NV], vx[NV];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            const int i = tid + e * kThreads, r = i / CH, c = i % CH;
+            const bool ok = k0 + r < t.last;
+            kx[e].load(static_cast<const float*>(a.k) + (t.start + k0 + r) * a.ks + (int64_t)h * D + c * 8, ok);
+            vx[e].load(static_cast<const float*>(a.v) + (t.start + k0 + r) * a.vs + (int64_t)h * D + c * 8, ok);
+        }
+    };
+    if (kAhead) load(0);
 
     float O[D / 8][4];
 #pragma unroll
@@ -142,31 +161,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
 
     for (int k0 = 0; k0 < t.last; k0 += kKeys) {
         __syncthreads();
-        for (int i = tid; i < kKeys * CH; i += kThreads) {
-            const int r = i / CH, c = i % CH;
-            const bool ok = k0 + r < t.last;
-            float x[8];
-            uint32_t part[4][PL];
-            load8(static_cast<const TIO*>(a.k) + (t.start + k0 + r) * a.ks + (int64_t)h * D + c * 8, ok, x);
+        if (!kAhead) load(k0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split2<PL>(x[2 * e], x[2 * e + 1], part[e]);
+        for (int e = 0; e < NV; ++e) {
+            const int i = tid + e * kThreads, r = i / CH, c = i % CH;
+            kx[e].store(sk + tile_off<D>(r, c), KB);
 #pragma unroll
-            for (int p = 0; p < PL; ++p)
-                *reinterpret_cast<uint4*>(sk + p * KB + tile_off<D>(r, c)) = make_uint4(part[0][p], part[1][p], part[2][p], part[3][p]);
-            load8(static_cast<const TIO*>(a.v) + (t.start + k0 + r) * a.vs + (int64_t)h * D + c * 8, ok, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!(fabsf(x[e]) < INFINITY)) {
-                    atomicMin(&odd[x[e] != x[e] ? 2 : x[e] > 0.f ? 0 : 1][c * 8 + e], k0 + r);
-                    x[e] = 0.f;
+            for (int x = 0; x < 8; ++x) {
+                float& y = vx[e].x[x];
+                if (!(fabsf(y) < INFINITY)) {
+                    atomicMin(&odd[y != y ? 2 : y > 0.f ? 0 : 1][c * 8 + x], k0 + r);
+                    y = 0.f;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split2<PL>(x[2 * e], x[2 * e + 1], part[e]);
-#pragma unroll
-            for (int p = 0; p < PL; ++p)
-                *reinterpret_cast<uint4*>(sv + p * KB + tile_off<D>(r, c)) = make_uint4(part[0][p], part[1][p], part[2][p], part[3][p]);
+            vx[e].store(sv + tile_off<D>(r, c), KB);
         }
+        if (kAhead && k0 + kKeys < t.last) load(k0 + kKeys);
         __syncthreads();
         if (!warp_on || k0 > warp_last) continue;
 
@@ -182,17 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
 #pragma unroll
             for (int p = 0; p < PL; ++p) ldsm4(qf[p], qa + p * QB + tile_off<D>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
 #pragma unroll
-            for (int j = 0; j < kKeys / 16; ++j) {
+            for (int p = 0; p < PL; ++p) {
+                uint32_t b[kKeys / 16][4];
 #pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    uint32_t b[4];
-                    ldsm4(b, ka + p * KB + tile_off<D>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                for (int j = 0; j < kKeys / 16; ++j)
+                    ldsm4(b[j], ka + p * KB + tile_off<D>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                // eight accumulators in turn, so that no product waits for the one before it
 #pragma unroll
-                    for (int u = 0; u + p < PL; ++u) {
-                        tc::mma16816(z[2 * j], qf[u], b[0], b[1]);
-                        tc::mma16816(z[2 * j + 1], qf[u], b[2], b[3]);
+                for (int u = 0; u + p < PL; ++u)
+#pragma unroll
+                    for (int j = 0; j < kKeys / 16; ++j) {
+                        mma(z[2 * j], qf[u], b[j][0], b[j][1]);
+                        mma(z[2 * j + 1], qf[u], b[j][2], b[j][3]);
                     }
-                }
             }
         }
         if (k0 + kKeys - 1 > t.first + (16 * w) / a.group) {
@@ -244,26 +256,30 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s) {
             uint32_t x[4][PL];
-            split2<PL>(z[2 * s][0], z[2 * s][1], x[0]);
-            split2<PL>(z[2 * s][2], z[2 * s][3], x[1]);
-            split2<PL>(z[2 * s + 1][0], z[2 * s + 1][1], x[2]);
-            split2<PL>(z[2 * s + 1][2], z[2 * s + 1][3], x[3]);
+            split2(z[2 * s][0], z[2 * s][1], x[0]);
+            split2(z[2 * s][2], z[2 * s][3], x[1]);
+            split2(z[2 * s + 1][0], z[2 * s + 1][1], x[2]);
+            split2(z[2 * s + 1][2], z[2 * s + 1][3], x[3]);
             uint32_t pf[PL][4];
 #pragma unroll
             for (int p = 0; p < PL; ++p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pf[p][i] = x[i][p];
+            constexpr int CG = 2;  // chunk pairs in turn
 #pragma unroll
-            for (int c = 0; c < D / 8; c += 2) {
+            for (int c = 0; c < D / 8; c += 2 * CG) {
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
-                    uint32_t b[4];
-                    ldsm4t(b, va + p * KB + tile_off<D>(16 * s + (lane & 15), c + (lane >> 4)));
+                    uint32_t b[CG][4];
 #pragma unroll
-                    for (int u = 0; u + p < PL; ++u) {
-                        tc::mma16816(O[c], pf[u], b[0], b[1]);
-                        tc::mma16816(O[c + 1], pf[u], b[2], b[3]);
-                    }
+                    for (int q = 0; q < CG; ++q) ldsm4t(b[q], va + p * KB + tile_off<D>(16 * s + (lane & 15), c + 2 * q + (lane >> 4)));
+#pragma unroll
+                    for (int u = 0; u + p < PL; ++u)
+#pragma unroll
+                        for (int q = 0; q < CG; ++q) {
+                            mma(O[c + 2 * q], pf[u], b[q][0], b[q][1]);
+                            mma(O[c + 2 * q + 1], pf[u], b[q][2], b[q][3]);
+                        }
                 }
             }
         }
@@ -279,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
         if (r >= rows) continue;
         const int tok = u ? tok1 : tok0;
         const float inv = 1.f / (u ? l1 : l0);
-        TIO* o = static_cast<TIO*>(a.out) + ((t.start + tok) * a.Hq + h * a.group + r % a.group) * D + 2 * cq;
+        float* o = static_cast<float*>(a.out) + ((t.start + tok) * a.Hq + h * a.group + r % a.group) * D + 2 * cq;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
             float x[2];
@@ -288,43 +304,38 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_prefill_kernel(const Att
                 const int ch = 8 * c + 2 * cq + e;
                 x[e] = attn_odd(O[c][2 * u + e] * inv, tok, odd[0][ch], odd[1][ch], odd[2][ch]);
             }
-            if constexpr (PL == 1) *reinterpret_cast<uint32_t*>(o + 8 * c) = tc::pack_bf16(x[0], x[1]);
-            else *reinterpret_cast<float2*>(o + 8 * c) = make_float2(x[0], x[1]);
+            *reinterpret_cast<float2*>(o + 8 * c) = make_float2(x[0], x[1]);
         }
     }
 }
 
 namespace {
 
-template <typename TIO, int D>
-cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
+template <int D, int ROWS>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s)
 {
-    constexpr int PL = sizeof(TIO) == 4 ? 3 : 1;
-    constexpr int smem = PL * (kRowsTile + 2 * kKeys) * D * 2 + 128;
-    static_assert(smem + 4096 <= 232448, "the tiles fit an SM");
-    auto kern = kda_attn_prefill_kernel<TIO, D>;
+    constexpr int smem = PL * 2 * ROWS * D * 2 + 128;  // q, and K and V of half as many rows
+    static_assert(128 / ROWS * (smem + 4096) <= 233472, "the tiles of an SM's CTAs fit");
+    auto kern = kda_attn_prefill_f32_kernel<D, ROWS>;
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
-    const int64_t slots = attn_slots(a, kRowsTile / a.group);
-    kern<<<(unsigned)(slots * a.Hkv), kThreads, smem, s>>>(a, (int)slots);
+    const int64_t slots = attn_slots(a, ROWS / a.group);
+    kern<<<(unsigned)(slots * a.Hkv), 2 * ROWS, smem, s>>>(a, (int)slots);
     return cudaGetLastError();
 }
 
-template <typename TIO>
-cudaError_t launch_io(const AttnArgs& a, cudaStream_t s)
+template <int D>
+cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 {
-    if (a.d == 32) return launch_d<TIO, 32>(a, s);
-    if (a.d == 64) return launch_d<TIO, 64>(a, s);
-    return launch_d<TIO, 128>(a, s);
+    return a.group <= 64 ? launch_rows<D, 64>(a, s) : launch_rows<D, 128>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_prefill(const AttnArgs& a, kda_dtype_t dt, cudaStream_t s)
+cudaError_t launch_attn_prefill_f32(const AttnArgs& a, cudaStream_t s)
 {
-    if (dt == KDA_BF16 && a.d != 32) return launch_attn_prefill_tc(a, s);
-    return dt == KDA_BF16 ? launch_io<__nv_bfloat16>(a, s) : launch_io<float>(a, s);
+    return a.d == 32 ? launch_d<32>(a, s) : a.d == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
 }
 
 }  // namespace kda

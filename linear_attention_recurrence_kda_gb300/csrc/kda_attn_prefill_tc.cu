@@ -1,5 +1,5 @@
 // kda_attn_prefill_tc.cu -- causal attention over packed prompts on the 5th-generation tensor cores:
-// bf16, 64 or 128 channels (kda_attention_prefill).
+// bf16 (kda_attention_prefill).
 //
 //   Z = scale Q K^T,  P = 2^(Z log2 e - m),  O = sum P V,  o = O / l      per row, keys in tiles of 128
 //
@@ -40,7 +40,8 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kInfoReaders = 8 + 3;  // softmax warps, products, copies, cleaner
 
 template <int D> struct Cfg {
-    static constexpr int NB = D / 64;                        // 64-channel blocks of a row
+    static constexpr int DP = D < 64 ? 64 : D;               // 32 channels are padded with zeros by the copies
+    static constexpr int NB = DP / 64;                       // 64-channel blocks of a row
     static constexpr uint32_t BLK = 128 * 128;               // bytes of a block: 128 rows of 128 bytes
     static constexpr uint32_t TILE = NB * BLK;
     static constexpr int STAGES = D == 128 ? 4 : 8;
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (w == 8) {
             // ---- products, in the order Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ... tile after tile
-            const uint32_t id_z = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, D) | (1u << 16);
+            const uint32_t id_z = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, C::DP) | (1u << 16);
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
             uint32_t base = 0, e = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
             bool ok = true;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t v = ra + (it % C::STAGES) * C::TILE;
 #pragma unroll
                 for (int s = 0; s < kKeys / 16; ++s)
-                    mma_ts(tm + 256 + D * hf, tm + 128 * hf + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u), id_o,
+                    mma_ts(tm + 256 + C::DP * hf, tm + 128 * hf + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u), id_o,
                            !first || s > 0);
             };
             for (uint32_t turn = 0; ok && next_tile(turn, t); ++turn) {
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
         const int hf = w >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
-        const uint32_t zt = tm + 128 * hf + lanes, ot = tm + 256 + D * hf + lanes;
+        const uint32_t zt = tm + 128 * hf + lanes, ot = tm + 256 + C::DP * hf + lanes;
         const float cs = a.scale * 1.4426950408889634f;
         const int rt = r / a.group, rh = r - rt * a.group;
         const int wt = (32 * (w & 3)) / a.group;
@@ -635,7 +636,7 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s)
 {
-    return a.d == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
+    return a.d == 32 ? launch_d<32>(a, s) : a.d == 64 ? launch_d<64>(a, s) : launch_d<128>(a, s);
 }
 
 }  // namespace kda

@@ -27,11 +27,11 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int slot, int token
     int64_t start, end;
     int j;
     if (a.cu == nullptr) {
-        const int64_t len = a.T / a.N;
-        const int per = (int)((len + tokens - 1) / tokens);
+        const int len = (int)a.T / a.N;
+        const int per = (len + tokens - 1) / tokens;
         const int n = slot / per;
         j = slot - n * per;
-        start = n * len;
+        start = (int64_t)n * len;
         end = start + len;
     } else {
         // the last sequence whose slots begin at or before this one
@@ -39,14 +39,14 @@ __device__ __forceinline__ bool attn_tile(const AttnArgs& a, int slot, int token
         while (lo < hi) {
             const int step = (hi - lo + 31) / 32;
             const int at = lo + ((int)(threadIdx.x & 31) + 1) * step;
-            const bool yes = at <= hi && (int64_t)a.cu[at] / tokens + at <= slot;
+            const bool yes = at <= hi && a.cu[at] / tokens + at <= slot;  // below 2^31: the grid's size was checked
             lo += __popc(__ballot_sync(0xffffffffu, yes)) * step;
             hi = min(hi, lo + step - 1);
         }
-        const int64_t c0 = a.cu[lo], c1 = a.cu[lo + 1];
-        j = (int)(slot - (c0 / tokens + lo));
-        start = min(max(c0, (int64_t)0), a.T);
-        end = min(max(c1, (int64_t)0), a.T);
+        const int c0 = a.cu[lo], c1 = a.cu[lo + 1];
+        j = slot - (c0 / tokens + lo);
+        start = min(max((int64_t)c0, (int64_t)0), a.T);
+        end = min(max((int64_t)c1, (int64_t)0), a.T);
     }
     const int64_t first = (int64_t)j * tokens;
     if (j < 0 || first >= end - start) return false;
