@@ -381,8 +381,8 @@ kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, 
  *       cu_seqlens[n+1] - cu_seqlens[n] positions of sequence n are written.
  *   cache : host descriptor.  A page and head takes the scale 2^e with the smallest e >= -60 that
  *       keeps its largest finite magnitude within the code's range (448 or 127); a page that already
- *       holds tokens keeps its scale unless the new tokens need a larger one, and then its older
- *       codes are rounded again to the new scale.  Codes are x / scale rounded to nearest, ties to
+ *       holds tokens keeps its scale unless the new tokens need a larger one, and then all its
+ *       other codes are rounded again to the new scale.  Codes are x / scale rounded to nearest, ties to
  *       even; infinities take the largest code, NaN is NaN in e4m3 and 0 in int8.
  *   check : device word of 4 bytes (256-byte aligned), or NULL.  A sequence whose length or page is out of range
  *       is skipped (the page, for a page) and sets bit 0; the word is never cleared by this call and is

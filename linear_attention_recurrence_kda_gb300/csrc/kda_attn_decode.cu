@@ -529,11 +529,22 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                         widen<kE4m3>(r[k][2 * i + 1], kf[k][1], kf[k][3]);
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        // fp32: the products' own sums are cut off, not rounded, so they add the parts of one
+                        // step and ordinary additions the steps
+                        float part[2][4] = {};
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p)
+                        for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) mma_f16(z[k][nt], kf[k], qf[p][c + i][nt][0], qf[p][c + i][nt][1]);
+                            for (int k = 0; k < 2; ++k)
+                                mma_f16(kSplit ? part[k] : z[k][nt], kf[k], qf[p][c + i][nt][0], qf[p][c + i][nt][1]);
+                        if constexpr (kSplit) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) z[k][nt][e] += part[k][e];
+                        }
+                    }
                 }
             }
             // Scores in base 2 (z s), their maxima over the keys that are seen, and p = 2^(z s - m) with
@@ -636,9 +647,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                         widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x6420), vf[0], vf[2]);
                         widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x7531), vf[1], vf[3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float part[4] = {};
 #pragma unroll
-                            for (int p = 0; p < PARTS; ++p) mma_f16(O[c + i][nt], vf, pf[p][nt][0], pf[p][nt][1]);
+                            for (int p = PARTS - 1; p >= 0; --p) mma_f16(kSplit ? part : O[c + i][nt], vf, pf[p][nt][0], pf[p][nt][1]);
+                            if constexpr (kSplit) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) O[c + i][nt][e] += part[e];
+                            }
+                        }
                     }
                 }
             }

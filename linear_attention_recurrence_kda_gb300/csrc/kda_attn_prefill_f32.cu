@@ -191,21 +191,33 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
             uint32_t qf[PL][4];
 #pragma unroll
             for (int p = 0; p < PL; ++p) ldsm4(qf[p], qa + p * QB + tile_off<D>(16 * w + (lane & 15), 2 * s + (lane >> 4)));
+            uint32_t b[PL][kKeys / 16][4];
 #pragma unroll
-            for (int p = 0; p < PL; ++p) {
-                uint32_t b[kKeys / 16][4];
+            for (int p = 0; p < PL; ++p)
 #pragma unroll
                 for (int j = 0; j < kKeys / 16; ++j)
-                    ldsm4(b[j], ka + p * KB + tile_off<D>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
-                // eight accumulators in turn, so that no product waits for the one before it
+                    ldsm4(b[p][j], ka + p * KB + tile_off<D>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+            // The products' own sums are cut off, not rounded, so a step's terms are summed by them, the
+            // small ones first, and the steps by ordinary additions (adding all to one accumulator
+            // lost two bits: an error of 3.7e-6 where fp32 arithmetic has 8e-7).
+            float part[kKeys / 8][4];
 #pragma unroll
-                for (int u = 0; u + p < PL; ++u)
+            for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[j][i] = 0.f;
+#pragma unroll
+            for (int order = PL - 1; order >= 0; --order)
+#pragma unroll
+                for (int p = 0; p <= order; ++p)
 #pragma unroll
                     for (int j = 0; j < kKeys / 16; ++j) {
-                        mma(z[2 * j], qf[u], b[j][0], b[j][1]);
-                        mma(z[2 * j + 1], qf[u], b[j][2], b[j][3]);
+                        mma(part[2 * j], qf[order - p], b[p][j][0], b[p][j][1]);
+                        mma(part[2 * j + 1], qf[order - p], b[p][j][2], b[p][j][3]);
                     }
-            }
+#pragma unroll
+            for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] += part[j][i];
         }
         if (k0 + kKeys - 1 > t.first + (16 * w) / a.group) {
 #pragma unroll
@@ -268,19 +280,29 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
             constexpr int CG = 2;  // chunk pairs in turn
 #pragma unroll
             for (int c = 0; c < D / 8; c += 2 * CG) {
+                uint32_t b[PL][CG][4];
 #pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    uint32_t b[CG][4];
+                for (int p = 0; p < PL; ++p)
 #pragma unroll
-                    for (int q = 0; q < CG; ++q) ldsm4t(b[q], va + p * KB + tile_off<D>(16 * s + (lane & 15), c + 2 * q + (lane >> 4)));
+                    for (int q = 0; q < CG; ++q) ldsm4t(b[p][q], va + p * KB + tile_off<D>(16 * s + (lane & 15), c + 2 * q + (lane >> 4)));
+                float part[2 * CG][4];
 #pragma unroll
-                    for (int u = 0; u + p < PL; ++u)
+                for (int q = 0; q < 2 * CG; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part[q][i] = 0.f;
+#pragma unroll
+                for (int order = PL - 1; order >= 0; --order)
+#pragma unroll
+                    for (int p = 0; p <= order; ++p)
 #pragma unroll
                         for (int q = 0; q < CG; ++q) {
-                            mma(O[c + 2 * q], pf[u], b[q][0], b[q][1]);
-                            mma(O[c + 2 * q + 1], pf[u], b[q][2], b[q][3]);
+                            mma(part[2 * q], pf[order - p], b[p][q][0], b[p][q][1]);
+                            mma(part[2 * q + 1], pf[order - p], b[p][q][2], b[p][q][3]);
                         }
-                }
+#pragma unroll
+                for (int q = 0; q < 2 * CG; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[c + q][i] += part[q][i];
             }
         }
     }

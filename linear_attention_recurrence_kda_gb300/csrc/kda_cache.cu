@@ -2,7 +2,7 @@
 //
 // For a page and head with values x of the new tokens and MAX the code's range (448 or 127):
 //   scale' = max(scale if the page already holds tokens, 2^e),  e >= -60 smallest with max|x| <= MAX 2^e
-//   code   = rne(x / scale'),  older codes <- rne(code * scale / scale') where the scale grew
+//   code   = rne(x / scale'),  the page's other codes <- rne(code * scale / scale') where it grew
 // A power of two makes x / scale exact and costs no precision in e4m3 (its steps are relative);
 // when a scale grows, e4m3 codes only move by an exponent, so the second rounding touches
 // subnormal codes alone.
@@ -226,9 +226,10 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
         for (int i = 0; i < (int)blockDim.x / 32; ++i) amax = fmaxf(amax, warp_max[u & 1][i]);
         const float unit = fmaxf(scale_for<kE4m3>(amax), old);
         if (threadIdx.x == 0) *scale = unit;
-        if (slot0 > 0 && unit != old) {  // the page's earlier rows move to the larger scale
+        if (slot0 > 0 && unit != old) {  // the page's other rows move to the larger scale
             const float ratio = old / unit;
-            for (int r = r0; r < slot0; r += rstep) {
+            for (int r = r0; r < page_tokens; r += rstep) {
+                if (r >= slot0 && r < slot0 + rows) continue;
                 uint2* p = reinterpret_cast<uint2*>(codes + r * a.d + c0);
                 const uint2 q = *p;
                 float x[kVec];

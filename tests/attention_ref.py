@@ -100,7 +100,7 @@ def append(k, v, cache, table, lens_before, fresh):
                     if a > p * page:
                         was = float(sc[at, h])
                         if unit > was:
-                            c[at, h, :a - p * page] = nearest(c[at, h, :a - p * page] * was / unit, dtype)
+                            c[at, h] = nearest(c[at, h] * was / unit, dtype)
                         unit = max(unit, was)
                     sc[at, h] = unit
                     c[at, h, a - p * page:b - p * page] = nearest(y / unit, dtype)
