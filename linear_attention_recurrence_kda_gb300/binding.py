@@ -8,6 +8,7 @@ fallback path, and loading fails loudly if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -568,12 +569,10 @@ def _cache(cache, block_table, N, hkv, d, device):
         raise ValueError(f"cache.k: shape {tuple(k.shape)}, expected (pages, heads, page_tokens, head_dim)")
     shape = k.shape
     pages, page = shape[0], shape[2]
-    want = (pages, hkv, page, d)
-    _need(k, "cache.k", dt, want, device)
-    _need(v, "cache.v", dt, want, device)
-    want = (pages, hkv)
-    _need(k_scale, "cache.k_scale", torch.float32, want, device)
-    _need(v_scale, "cache.v_scale", torch.float32, want, device)
+    _need(k, "cache.k", dt, (pages, hkv, page, d), device)
+    _need(v, "cache.v", dt, shape, device)
+    _need(k_scale, "cache.k_scale", torch.float32, (pages, hkv), device)
+    _need(v_scale, "cache.v_scale", torch.float32, (pages, hkv), device)
     if block_table.dim() != 2:
         raise ValueError(f"block_table: shape {tuple(block_table.shape)}, expected (sequences, pages)")
     cols = block_table.shape[1]
@@ -654,6 +653,12 @@ def kda_attention_decode_workspace_bytes(problem: KdaAttention) -> int:
     return int(lib().kda_attention_decode_workspace_bytes(ctypes.byref(problem)))
 
 
+@functools.lru_cache(maxsize=256)
+def _decode_workspace_bytes(N, T, Hq, Hkv, d, io, device) -> int:
+    """The workspace depends on the sizes and the device alone."""
+    return kda_attention_decode_workspace_bytes(KdaAttention(N, T, Hq, Hkv, d, io, 1.0, 0, 0, 0))
+
+
 def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optional[float] = None, out=None,
                          workspace=None, stream=None):
     """The newest L tokens of each of N sequences attend to the cache, which holds their keys and
@@ -674,7 +679,7 @@ def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optiona
         _need(out, "out", dt, (T, Hq, d), dev)
     prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, 0, 0)
     if workspace is None:
-        wsb = kda_attention_decode_workspace_bytes(prob)
+        wsb = _decode_workspace_bytes(N, T, Hq, Hkv, d, io, dev)
         if wsb == 0:
             raise KdaError(KDA_ERR_INVALID_ARG, "kda_attention_decode_workspace_bytes")
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
