@@ -61,7 +61,12 @@ cudaError_t launch_attn_prefill_f32(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
-size_t attn_decode_workspace_bytes(int64_t rows, int d);  // rows: window x group
+size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt);  // rows: window x group
+
+// The form for many rows a key head (kda_attn_window.cu): does it take this call, what does it need.
+bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt);
+size_t attn_window_workspace_bytes(int64_t rows, int d);
+cudaError_t launch_attn_window(const AttnDecodeArgs& a, cudaStream_t s);
 
 // A kernel's dynamic shared memory limit, raised once for each device (the call costs about half a
 // microsecond, which short calls feel).

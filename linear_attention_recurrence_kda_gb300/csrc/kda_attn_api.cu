@@ -213,7 +213,7 @@ size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem)
     const kda_attention_t& p = *problem;
     if (p.total_tokens < p.num_seqs || p.total_tokens % p.num_seqs != 0) return 0;
     const int64_t rows = p.total_tokens / p.num_seqs * (p.num_heads / p.num_kv_heads);
-    return kda::attn_decode_workspace_bytes(rows, p.head_dim);
+    return kda::attn_decode_workspace_bytes(rows, p.head_dim, p.io_dtype);
 }
 
 kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const kda_cache_t* cache, void* out,

@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include "kda_attn.cuh"
+#include "kda_attn_decode.cuh"
 #include "kda_tc.cuh"
 
 namespace kda {
@@ -44,33 +45,6 @@ constexpr int stages_of(int nt, int d) { return (nt == 1 ? 2 : 3) * (d == 128 ? 
 // tiles (28 rows, 64 sequences of 3150 keys and 8 heads: 194 us by 16 rows with O in 128 registers less
 // than by 32, which took 202; by 8 rows 270).
 inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
-
-// Workspace: check word | per-CTA flags | records | (max, sum) of slots | outputs of slots.
-// Worker w owns slots 2 w (a unit begun by an earlier worker) and 2 w + 1 (begun here).
-// A call with fewer units than workers keeps its records by unit, else by the worker that began it.
-struct Record {
-    int32_t n, h, rt, first, last;  // unit, and the workers that hold its pieces; n < 0: none
-};
-
-struct DecodeLayout {
-    size_t flags, records, ml, o, total;
-};
-
-__host__ __device__ inline DecodeLayout decode_layout(int workers, int rows, int d)
-{
-    DecodeLayout L;
-    size_t at = 256;
-    L.flags = at;
-    at += ((size_t)workers / kWarps * 4 + 255) / 256 * 256;
-    L.records = at;
-    at += ((size_t)workers * sizeof(Record) + 255) / 256 * 256;
-    L.ml = at;
-    at += ((size_t)workers * 2 * rows * 8 + 255) / 256 * 256;
-    L.o = at;
-    at += (size_t)workers * 2 * rows * d * 4;
-    L.total = (at + 255) / 256 * 256;
-    return L;
-}
 
 struct Maps {
     CUtensorMap k, v;
@@ -104,32 +78,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// four codes (bytes of x, low first) to two pairs of f16
-template <bool kE4m3>
-__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi)
-{
-    if constexpr (kE4m3) {
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(x));
-    } else {
-        // byte b ^ 0x80 = b + 128 under the exponent of 1024 is 1024 + 128 + b; 1152 comes off exactly
-        const uint32_t u = x ^ 0x80808080u;
-        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140), g = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), off);
-        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&g), off);
-        lo = *reinterpret_cast<const uint32_t*>(&a);
-        hi = *reinterpret_cast<const uint32_t*>(&b);
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // the part of (lo, hi) that their f16 rounding `h` leaves
 __device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t h)
 {
@@ -148,40 +96,6 @@ template <int D>
 __device__ __forceinline__ uint32_t swizzle(uint32_t off)
 {
     return off ^ (((off >> 7) & (D == 128 ? 7u : D == 64 ? 3u : 1u)) << 4);
-}
-
-// Tokens of sequence n that count: 0 where the length is out of range.
-__device__ __forceinline__ int length_of(const AttnDecodeArgs& a, int n, bool* bad = nullptr)
-{
-    const int len = a.lengths[n];
-    const bool ok = len >= 0 && (int64_t)len <= (int64_t)a.c.max_pages * a.c.page;
-    if (!ok && bad != nullptr) *bad = true;
-    return ok ? len : 0;
-}
-
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// A place in the line of tiles: unit (n, h, rt) and the tile i of its `tiles`.
-struct Cursor {
-    int n, h, rt, i, tiles, len;
-};
-
-__device__ __forceinline__ void next_tile(const AttnDecodeArgs& a, int row_tiles, Cursor& c)
-{
-    if (++c.i < c.tiles) return;
-    c.i = 0;
-    if (++c.rt < row_tiles) return;
-    c.rt = 0;
-    if (++c.h < a.Hkv) return;
-    c.h = 0;
-    do {
-        if (++c.n >= a.N) {
-            c.tiles = 0;
-            return;
-        }
-        c.len = length_of(a, c.n);
-        c.tiles = tiles_of(c.len);
-    } while (c.tiles == 0);
 }
 
 }  // namespace
@@ -206,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
     const int g = lane >> 2, cq = lane & 3;
     unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = smem + (size_t)w * S * 2 * TB;
-    const DecodeLayout L = decode_layout(gridDim.x * kWarps, rows_max, D);
+    const DecodeLayout L = decode_layout(gridDim.x * kWarps, gridDim.x, rows_max, D);
     const int rows_all = a.L * a.group;
     const int row_tiles = (rows_all + kRows - 1) / kRows;
     const int64_t per_tile = (int64_t)a.Hkv * row_tiles;
@@ -224,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
         bool bad = false;
         for (int i = 0; i < chunk; ++i) {
             const int n = tid * chunk + i;
-            if (n < a.N) sum += tiles_of(length_of(a, n, &bad));
+            if (n < a.N) sum += tiles_of<kTile>(length_of(a, n, &bad));
         }
         int64_t x = sum;
 #pragma unroll
@@ -274,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
             cc.n = lo * chunk;
             for (;;) {
                 cc.len = length_of(a, cc.n);
-                cc.tiles = tiles_of(cc.len);
+                cc.tiles = tiles_of<kTile>(cc.len);
                 const int64_t here = cc.tiles * per_tile;
                 if (at + here > b0 || cc.n + 1 >= a.N) break;
                 at += here;
@@ -324,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                     tc::tma_load_3d(kd + TB + box * D, &maps.v, 0, 0, p1 * a.Hkv + ic.h, &full[w][st]);
                 }
             }
-            next_tile(a, row_tiles, ic);
+            next_tile<kTile>(a, row_tiles, ic);
             if (it + 1 < count) {
                 p0 = page_id(ic, 0);
                 p1 = box < kTile ? page_id(ic, 1) : -1;
@@ -679,14 +593,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                 }
                 begun = false;
             }
-            next_tile(a, row_tiles, cc);
+            next_tile<kTile>(a, row_tiles, cc);
         }
         if (gone) {
             // units begun here that will not be finished: nothing to join
             for (bool begun_here = cc.i <= it; it < count; begun_here = cc.i == 0, ++it) {
                 if (by_unit && begun_here && lane == 0)
                     records[(int64_t)cc.n * per_tile + (int64_t)cc.h * row_tiles + cc.rt].n = -1;
-                next_tile(a, row_tiles, cc);
+                next_tile<kTile>(a, row_tiles, cc);
             }
             // copies still in flight land in shared memory that the CTA gives back: wait for them
             for (int i = max(0, issued - S); i < issued; ++i) (void)tc::mbar_wait(&full[w][i % S], (uint32_t)(i / S) & 1u, kCopyTries);
@@ -706,12 +620,13 @@ constexpr int kCombineWarps = 8;
 
 template <typename TIO, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
-    kda_attn_combine_kernel(const AttnDecodeArgs a, const int rows_max, const int workers, const int unit_rows, const int wpr)
+    kda_attn_combine_kernel(const AttnDecodeArgs a, const int rows_max, const int workers, const int nflags, const int unit_rows,
+                            const int wpr)
 {
     constexpr int V = D / 32;
     __shared__ float part[kCombineWarps][D + 1];
     __shared__ uint32_t word;
-    const DecodeLayout L = decode_layout(workers, rows_max, D);
+    const DecodeLayout L = decode_layout(workers, nflags, rows_max, D);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     griddep_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -720,7 +635,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
         __syncthreads();
         uint32_t f = 0u;
         const uint32_t* flags = reinterpret_cast<const uint32_t*>(a.ws + L.flags);
-        for (int i = threadIdx.x; i < workers / kWarps; i += blockDim.x) f |= flags[i];
+        for (int i = threadIdx.x; i < nflags; i += blockDim.x) f |= flags[i];
         if (f) atomicOr(&word, f);
         __syncthreads();
         if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(a.ws) = word;
@@ -823,12 +738,7 @@ cudaError_t launch_nt(const AttnDecodeArgs& a, cudaStream_t s)
     kern<<<ctas, kThreads, smem, s>>>(a, maps, rows, by_unit);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // about workers / units pieces a unit: four or more a warp
-    const int64_t pieces = by_unit ? workers / units : 1;
-    const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
-    const int rpb = rows < kCombineWarps / wpr ? rows : kCombineWarps / wpr;
-    const dim3 grid((unsigned)(by_unit ? units : workers), (unsigned)((rows + rpb - 1) / rpb));
-    return launch_dependent(kda_attn_combine_kernel<TIO, D>, grid, dim3((unsigned)(rpb * wpr * 32)), 0, s, a, rows, workers, 8 * NT, wpr);
+    return launch_attn_join(a, sizeof(TIO) == 4 ? KDA_F32 : KDA_BF16, rows, 8 * NT, workers, ctas, by_unit, units, s);
 }
 
 template <typename TIO, int D, bool kE4m3>
@@ -848,14 +758,34 @@ cudaError_t launch_decode_io(const AttnDecodeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(int64_t rows, int d)
+cudaError_t launch_attn_join(const AttnDecodeArgs& a, kda_dtype_t dt, int rows_max, int unit_rows, int workers, int flags,
+                             bool by_unit, int64_t units, cudaStream_t s)
 {
+    // about workers / units pieces a unit: four or more a warp
+    const int64_t pieces = by_unit ? workers / units : 1;
+    const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
+    const int rpb = rows_max < kCombineWarps / wpr ? rows_max : kCombineWarps / wpr;
+    const dim3 grid((unsigned)(by_unit ? units : workers), (unsigned)((rows_max + rpb - 1) / rpb));
+    auto go = [&](auto kern) {
+        return launch_dependent(kern, grid, dim3((unsigned)(rpb * wpr * 32)), 0, s, a, rows_max, workers, flags, unit_rows, wpr);
+    };
+    if (dt == KDA_F32)
+        return a.d == 32 ? go(kda_attn_combine_kernel<float, 32>)
+                         : a.d == 64 ? go(kda_attn_combine_kernel<float, 64>) : go(kda_attn_combine_kernel<float, 128>);
+    return a.d == 32 ? go(kda_attn_combine_kernel<__nv_bfloat16, 32>)
+                     : a.d == 64 ? go(kda_attn_combine_kernel<__nv_bfloat16, 64>) : go(kda_attn_combine_kernel<__nv_bfloat16, 128>);
+}
+
+size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt)
+{
+    if (attn_window_takes(rows, d, dt)) return attn_window_workspace_bytes(rows, d);
     const int nt = nt_of(rows);
-    return decode_layout(decode_ctas(nt) * kWarps, (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
+    return decode_layout(decode_ctas(nt) * kWarps, decode_ctas(nt), (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s)
 {
+    if (attn_window_takes((int64_t)a.L * a.group, a.d, dt)) return launch_attn_window(a, s);
     const bool e4m3 = a.c.dtype == KDA_CACHE_E4M3;
     if (dt == KDA_BF16) return e4m3 ? launch_decode_io<__nv_bfloat16, true>(a, s) : launch_decode_io<__nv_bfloat16, false>(a, s);
     return e4m3 ? launch_decode_io<float, true>(a, s) : launch_decode_io<float, false>(a, s);

@@ -229,6 +229,99 @@ def test_decode(lens, hq, hkv, window, page, d, code, dtype):
     assert B.kda_workspace_status(ws) == B.KDA_OK
 
 
+MANY = [
+    # lens, query heads, key heads, window: 17 rows and more a key head, up to several tiles of 128
+    ([1], 17, 1, 1), ([0, 5, 127, 128, 129, 256], 8, 1, 3), ([3, 700], 16, 2, 7), ([1000, 64, 333], 24, 3, 5),
+    ([90, 400], 8, 1, 40), ([1300], 128, 1, 2), ([17] * 300, 20, 1, 1), ([3000, 2900] * 20, 8, 2, 7), ([5], 4, 1, 30),
+]
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("page,d", [(16, 128), (64, 64), (128, 128), (32, 128)])
+@pytest.mark.parametrize("lens,hq,hkv,window", MANY, ids=[f"{len(p[0])}x{max(p[0])}h{p[1]}of{p[2]}w{p[3]}" for p in MANY])
+def test_decode_many_rows(lens, hq, hkv, window, page, d, code):
+    """Many rows a key head, which another kernel takes."""
+    table, pool = tables(lens, page)
+    cache = filled(pool, hkv, page, d, code, seed=page + d)
+    q = make(len(lens) * window, hq, 1, d, torch.bfloat16, 2, fused=True)[0]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+    out = B.kda_attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), workspace=ws)
+    check_n = min(len(lens), 6)  # the float64 form of the first sequences; the rest against themselves
+    few = ref.decode(q[:check_n * window], cache, table[:check_n], lens[:check_n])
+    close(out[:check_n * window], few, ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+    assert B.kda_workspace_status(ws) == B.KDA_OK
+    assert torch.equal(out, B.kda_attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV)))
+    n = len(lens) - 1  # the last sequence alone
+    alone = B.kda_attention_decode(q[n * window:], cache, table[n:], torch.tensor(lens[n:], dtype=torch.int32, device=DEV))
+    close(out[n * window:], alone.double().cpu(), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_many_rows_nan_past_the_end_and_in_hidden_keys(page):
+    """As for few rows: stale NaN past the end reaches nothing, a drafted token's NaN the rows that see it alone."""
+    lens, d, L, hq = [150, 95, 7, 300], 128, 6, 4
+    table, pool = tables(lens, page)
+    cache = filled(pool, 1, page, d, torch.float8_e4m3fn)
+    q = make(4 * L, hq, 1, d, torch.bfloat16, 8)[0]
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    clean = B.kda_attention_decode(q, cache, table, lengths)
+    raw = [c.view(torch.uint8).clone() for c in (cache.k, cache.v)]
+    for n, length in enumerate(lens):
+        last = int(table[n, (length - 1) // page])
+        for c in raw:
+            c[last, :, (length - 1) % page + 1:] = 0x7F
+    dirty = B.KvCache(raw[0].view(torch.float8_e4m3fn), raw[1].view(torch.float8_e4m3fn), cache.k_scale, cache.v_scale)
+    assert torch.equal(B.kda_attention_decode(q, dirty, table, lengths), clean)
+    want = clean.clone()
+    # the fourth of six drafted tokens of sequence 0, and a token of sequence 3 that every row sees
+    for n, key, ch in ((0, lens[0] - L + 3, 9), (3, lens[3] - L - 20, 77)):
+        raw[1][int(table[n, key // page]), 0, key % page, ch] = 0xFF
+        first = max(0, key - (lens[n] - L))
+        want[n * L + first:(n + 1) * L, :, ch] = float("nan")
+    out = B.kda_attention_decode(q, dirty, table, lengths)
+    assert bool(((out == want) | (out.isnan() & want.isnan())).all())
+
+
+def test_decode_many_rows_reports_bad_lengths_and_pages():
+    page, d, L, hq = 16, 64, 5, 4
+    table, pool = tables([200, 200, 200], page)
+    cache = filled(pool, 1, page, d, torch.float8_e4m3fn)
+    q = make(3 * L, hq, 1, d, torch.bfloat16, 8)[0]
+    ws = torch.zeros(1 << 25, dtype=torch.uint8, device=DEV)
+    lengths = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    good = B.kda_attention_decode(q, cache, table, lengths(200, 200, 200), workspace=ws)
+    assert B.kda_workspace_status(ws) == B.KDA_OK
+    out = B.kda_attention_decode(q, cache, table, lengths(200, 10_000, 200), workspace=ws)
+    assert B.kda_workspace_status(ws) == B.KDA_ERR_DEVICE_CHECK
+    assert torch.equal(out[:L], good[:L]) and torch.equal(out[2 * L:], good[2 * L:]) and not out[L:2 * L].any()
+    t2 = table.clone()
+    t2[2, 3] = pool + 5  # keys 48 .. 63 of sequence 2 are not there
+    out = B.kda_attention_decode(q, cache, t2, lengths(200, 200, 200), workspace=ws)
+    assert B.kda_workspace_status(ws) == B.KDA_ERR_DEVICE_CHECK
+    assert torch.equal(out[:2 * L], good[:2 * L])
+    k, v = ref.cached(cache, table, 2, 200, 0)
+    keep = torch.cat([torch.arange(48), torch.arange(64, 200)])
+    x = q[2 * L:].detach().double().cpu().reshape(-1, d)
+    seen = [200 - L + t + 1 - 16 for t in range(L) for _ in range(hq)]
+    want = ref.rows(x, k[keep], v[keep], seen, d ** -0.5).view(L, hq, d)
+    close(out[2 * L:], want, ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("hq,window", [(2, 1), (8, 3)], ids=["few", "many"])
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+def test_decode_pages_without_scale(code, hq, window):
+    """Pages whose values are zero, or whose keys are: their weight counts, their values add nothing."""
+    lens, page, d = [640, 333], 16, 128
+    table, pool = tables(lens, page)
+    c = filled(pool, 1, page, d, code)
+    vs, ks = c.v_scale.clone(), c.k_scale.clone()
+    vs[::3], ks[1::4] = 0.0, 0.0
+    cache = B.KvCache(c.k, c.v, ks, vs)
+    q = make(2 * window, hq, 1, d, torch.bfloat16, 3)[0]
+    out = B.kda_attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    close(out, ref.decode(q, cache, table, lens), ref.dequant(c.v, vs), torch.bfloat16, 2.0 ** -11)
+
+
 @pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
 def test_decode_scales_far_apart(code):
     """Pages whose scales differ by up to 2^50, zero scales among them."""
