@@ -1,22 +1,25 @@
 // kda_attn_window.cu -- many rows a key head over the paged 8-bit cache, on the 5th-generation tensor
-// cores (kda_attention_decode: a drafted window, a large group of query heads; bf16, 64 or 128 channels).
+// cores (kda_attention_decode: a drafted window, a large group of query heads; bf16, 128 channels).
 //
-//   Z = scale ks (Q K^T),  P = 2^(Z - m),  O = sum P V,  o = O / l        as in kda_attn_decode.cu
+//   Z^T = scale ks (K Q^T),  P = 2^(Z - m),  O^T = sum V^T P^T,  o = O / l        as in kda_attn_decode.cu
 //
-// With 28 rows a key head a warp-level kernel spends about 1300 instructions on a tile of 32 keys, most
-// of them conversions and products, and reads the cache at a quarter of HBM's rate.  Here a CTA takes
-// up to 128 rows and keys in blocks of 128: the codes are converted once, by warps that do nothing else,
-// into f16 tiles (exactly: e4m3 and int8 are subsets of f16) from which tcgen05.mma forms Z and O; a
-// block then costs a few hundred instructions a warp.
+// With 28 rows a key head the warp-level kernel spends about 1300 instructions on a tile of 32 keys, most
+// of them conversions and products.  Here a CTA takes up to 32 rows and keys in blocks of 128: the
+// codes are converted once, by warps that do nothing else, into f16 tiles (exactly: e4m3 and int8 are
+// subsets of f16), from which tcgen05.mma forms Z^T (keys are the product's 128 rows, queries its 32
+// columns) and O^T (channels the rows).  A thread of the softmax then owns a key and its 32 scores: no lane
+// is idle, a key's scales are the thread's own, and no score crosses lanes but at a change of the
+// reference.  Few columns make the products cheap (about 128 cycles each a block).
 //
-// Blocks alternate between two streams, each with its own maximum, sum and O, so that one stream's
-// softmax runs while the other's products do; at the end of a unit the first stream joins them.
-// Tensor memory: Z0 | Z1 | O0 | O1, P over the first half of its Z as packed f16.  All units' blocks form
-// one line that is cut evenly among the CTAs; pieces of a unit are joined by the join kernel.
+// Blocks alternate between two streams, each with its own reference, sums and O, so that one's softmax
+// runs while the other waits; at the end of a unit the first stream joins them.  Tensor memory: Z0 | Z1 |
+// O0 | O1, 32 columns each; P goes through shared memory.  All units' blocks form one line that is cut
+// evenly among the CTAs; pieces of a unit are joined by the join kernel.
 //
-// Warps 0-3 and 4-7: softmax of the streams (a thread owns a row), 8: products, 9: copies and scales,
-// 10-15: conversion.  A row of q enters scaled by a power of two as in kda_attn_decode.cu, V's scales
-// through P, with O in units of the block's largest scale.
+// Warps 0-3 and 4-7: softmax of the streams, 8: products, 9: copies and scales, 10-15: conversion.  A
+// tile's rows of q enter scaled by one power of two that brings the largest value to [2^14, 2^15) (bf16
+// values are then exact in f16 down to 2^-38 of it), V's scales through P, with O in units of the
+// block's largest scale.
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
 #include "kda_attn_tc.cuh"
@@ -28,37 +31,44 @@ using namespace attn;
 namespace {
 
 constexpr int kBlk = 128;  // keys per block
-constexpr int kRows = 128;
+constexpr int kRows = 32;  // rows of a unit: the products' columns
 constexpr int kThreads = 512;
 constexpr int kConvert = 192;
-constexpr int kRaw = 5;    // raw tiles (K and V in turn) on their way or waiting
+constexpr int kRaw = 4;    // raw tiles (K and V in turn) on their way or waiting
 constexpr int kGroups = kBlk / 16;
 // warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D> struct Cfg {
-    static constexpr int NB = D / 64;
-    static constexpr uint32_t BLK = 128 * 128;     // bytes of a 64-channel block of 128 rows
-    static constexpr uint32_t TILE = NB * BLK;     // an f16 tile
-    static constexpr uint32_t RAW = kBlk * D;      // a tile of codes
-    static constexpr uint32_t SMEM = 4 * TILE + kRaw * RAW + 1024;  // Q, K, two of V
-};
+constexpr int D = 128;
+constexpr uint32_t kColBlk = 128 * 128;         // bytes of 64 channels of 128 keys in f16
+constexpr uint32_t kTileBytes = 2 * kColBlk;    // a K or V block in f16
+constexpr uint32_t kQBlk = kRows * 128;         // 64 channels of the rows of q
+constexpr uint32_t kQBytes = 2 * kQBlk;
+constexpr uint32_t kPBytes = kBlk * kRows * 2;  // P^T: a key's 32 weights are 64 bytes
+constexpr uint32_t kRawBytes = kBlk * D;        // a block of codes
+constexpr uint32_t kSmem = kQBytes + 2 * kPBytes + 4 * kTileBytes + kRaw * kRawBytes + 1024;  // K and V twice
 
 struct Maps {
     CUtensorMap k, v;
 };
 
 struct Shared {
-    uint64_t raw_full[kRaw], raw_free[kRaw], k_ready, k_free, v_ready[2], v_free[2];
+    uint64_t raw_full[kRaw], raw_free[kRaw], k_ready[2], k_free[2], v_ready[2], v_free[2];
     uint64_t q_ready, f_read, z_full[2], p_full[2], o_full[2], joined, join_free, drained;
     uint32_t tmem, dead, flag;
     uint32_t has[8];             // by block: bit g, group g of 16 keys is there
     float ks[8][kGroups], vs[8][kGroups];
-    float f[kRows];              // what a row's scores are multiplied by
-    float part[3][kRows];        // the second stream's maximum, sum and unit
+    float f;                     // what scores are multiplied by, next to the key's scale
+    uint32_t qmax[4];
+    float top[2][4][kRows];      // by stream and warp: the largest score of a row
+    float sum[2][4][kRows];      // a row's sum
+    alignas(16) float ref[2][kRows], by[2][kRows];  // a row's reference, and what its last change multiplies by
+    float unit[2];
+    int64_t at[kRows];           // where a row's output goes
+    float weight[2][kRows];      // the streams' weights in a row's result
     unsigned long long odd[4][128];  // by the segment's turn: the first key with a NaN in a channel (see odd_note)
-    int64_t prefix[kThreads + 1];
+    Cursor begin;                // this CTA's first block
 };
 
 // A run of a unit's blocks.
@@ -87,6 +97,48 @@ struct Walk {
     }
 };
 
+// P^T as the second operand, rows contiguous: 64-byte rows of one key, groups of 8 keys 512 bytes apart,
+// 64-byte swizzle.  V as the first operand, channels contiguous.
+constexpr uint32_t kDescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
+__device__ __forceinline__ void mma_vp(uint32_t d, uint32_t a_lo, uint32_t b_addr, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %5};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(((b_addr & 0x3FFFFu) >> 4) | (1u << 16)), "r"(idesc), "r"(kDescHi), "r"(kDescHi64), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Or over the 128 threads of a stream (its four warps meet here).
+__device__ __forceinline__ bool any4(int stream, bool x)
+{
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y)
+                 : "r"((uint32_t)x), "r"(1 + stream)
+                 : "memory");
+    return y != 0u;
+}
+
+// Lane r's result of reducing x[r] over the warp: each step halves the values a lane still holds.
+template <typename F>
+__device__ __forceinline__ float reduce_rows(float (&x)[32], F f)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool up = (lane & off) != 0;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float give = up ? x[i] : x[i + off];
+            const float keep = up ? x[i + off] : x[i];
+            x[i] = f(keep, __shfl_xor_sync(0xffffffffu, give, off));
+        }
+    }
+    return x[0];
+}
+
 // A noted NaN: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers
 // them), the key's distance from the last key that every row sees in the lower.  Conversion is at
 // most two segments ahead of the softmax, so four arrays in turn never mix.
@@ -97,17 +149,18 @@ __device__ __forceinline__ unsigned long long odd_note(uint32_t turn, int key, i
 
 }  // namespace
 
-template <int D, bool kE4m3>
+template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_attn_window_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps, const int rows_max, const bool by_unit)
 {
-    using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared sh;
-    unsigned char* sq = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    unsigned char* sk = sq + C::TILE;
-    unsigned char* sv = sk + C::TILE;       // two
-    unsigned char* raw = sv + 2 * C::TILE;  // kRaw
+    unsigned char* sk = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* sv = sk + 2 * kTileBytes;   // two (and K's two)
+    unsigned char* sq = sv + 2 * kTileBytes;
+    unsigned char* sp = sq + kQBytes;          // two
+    unsigned char* raw = sp + 2 * kPBytes;     // kRaw
+    int64_t* prefix = reinterpret_cast<int64_t*>(raw);  // until the copies begin
     const int tid = threadIdx.x, lane = tid & 31;
     const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
     const DecodeLayout L = decode_layout(gridDim.x, gridDim.x, rows_max, D);
@@ -122,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&sh.raw_full[i], 1);
             tc::mbar_init(&sh.raw_free[i], kConvert / 32);
         }
-        tc::mbar_init(&sh.k_ready, kConvert / 32);
-        tc::mbar_init(&sh.k_free, 1);
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.k_ready[i], kConvert / 32);
+            tc::mbar_init(&sh.k_free[i], 1);
             tc::mbar_init(&sh.v_ready[i], kConvert / 32);
             tc::mbar_init(&sh.v_free[i], 1);
             tc::mbar_init(&sh.z_full[i], 1);
@@ -141,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int i = tid; i < 4 * 128; i += kThreads) (&sh.odd[0][0])[i] = ~0ull;
-    if (w == 8) tc::tmem_alloc(&sh.tmem, 512);
+    if (w == 8) tc::tmem_alloc(&sh.tmem, 128);
     // blocks before every run of `chunk` sequences
     const int chunk = (a.N + kThreads - 1) / kThreads;
     {
@@ -157,14 +210,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
         }
-        sh.prefix[tid + 1] = x;
-        if (tid == 0) sh.prefix[0] = 0;
+        prefix[tid + 1] = x;
+        if (tid == 0) prefix[0] = 0;
         __syncthreads();
         if (bad) atomicOr(&sh.flag, kCheckBadSeqlens);
         int64_t before = 0;
-        for (int i = 0; i < w; ++i) before += sh.prefix[(i + 1) * 32];
+        for (int i = 0; i < w; ++i) before += prefix[(i + 1) * 32];
         __syncthreads();
-        sh.prefix[tid + 1] = x + before;
+        prefix[tid + 1] = x + before;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -182,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int64_t i = tid; i < a.L * tokrow; i += kThreads) o[i] = __float2bfloat16_rn(0.f);
         }
     }
-    const int64_t total = sh.prefix[kThreads] * per_block;
+    const int64_t total = prefix[kThreads] * per_block;
     const int64_t W = min((int64_t)gridDim.x, total);
     const int64_t b0 = blockIdx.x < W ? blockIdx.x * total / W : 0, b1 = blockIdx.x < W ? (blockIdx.x + 1) * total / W : 0;
     Walk walk;
@@ -193,10 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lo = 0, hi = kThreads - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (sh.prefix[mid] * per_block <= b0) lo = mid;
+            if (prefix[mid] * per_block <= b0) lo = mid;
             else hi = mid - 1;
         }
-        int64_t at = sh.prefix[lo] * per_block;
+        int64_t at = prefix[lo] * per_block;
         Cursor& c = walk.c;
         c.n = lo * chunk;
         for (;;) {
@@ -213,6 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.rt = (int)(unit - (int64_t)c.h * row_tiles);
     };
     start();
+    if (tid == 0) sh.begin = walk.c;
+    tc::fence_async_smem();  // the copies take over where the prefix was
+    __syncthreads();
     Segment s;
 
     if (w >= 8) {
@@ -234,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             bool ok = true;
             while (ok && walk.next(a, row_tiles, s)) {
-                int page = page_of(s, s.i0);
+                // a block's pages are asked for two blocks ahead, its scales one
+                int page = page_of(s, s.i0), page1 = s.count > 1 ? page_of(s, s.i0 + 1) : -1;
                 float scale = scale_of(s, page);
                 for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++blk) {
-                    // the next block's page and scale are on their way meanwhile
-                    const int page1 = i + 1 < s.i0 + s.count ? page_of(s, i + 1) : -1;
+                    const int page2 = i + 2 < s.i0 + s.count ? page_of(s, i + 2) : -1;
                     const float scale1 = scale_of(s, page1);
                     const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
@@ -257,11 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int p = 0; p < kGroups / gpp; ++p) {
                             const int id = __shfl_sync(0xffffffffu, page, p * gpp);
                             if (lane == 0 && id >= 0)
-                                tc::tma_load_3d(raw + st * C::RAW + p * box * D, x ? &maps.v : &maps.k, 0,
+                                tc::tma_load_3d(raw + st * kRawBytes + p * box * D, x ? &maps.v : &maps.k, 0,
                                                 (i * kBlk + p * box) & (a.c.page - 1), id * a.Hkv + s.h, &sh.raw_full[st]);
                         }
                     }
                     page = page1;
+                    page1 = page2;
                     scale = scale1;
                 }
             }
@@ -270,21 +327,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t i = it > kRaw ? it - kRaw : 0; i < it; ++i) (void)tc::mbar_wait(&sh.raw_full[i % kRaw], (i / kRaw) & 1u, kTries);
         } else if (w == 8) {
             // ---- products: Z0 Z1 | O0(0) Z0(2) | O1(1) Z1(3) | ...
-            const uint32_t id_z = tc::idesc_bf16(128, kBlk) & ~((1u << 7) | (1u << 10));  // f16 operands
-            const uint32_t id_o = (tc::idesc_bf16(128, D) & ~((1u << 7) | (1u << 10))) | (1u << 16);
-            const uint32_t qa = tc::smem_u32(sq), ka = tc::smem_u32(sk), va = tc::smem_u32(sv);
+            const uint32_t id_z = tc::idesc_bf16(128, kRows) & ~((1u << 7) | (1u << 10));  // f16 operands
+            const uint32_t id_o = id_z | (1u << 15) | (1u << 16);                          // both with K outermost
+            const uint32_t qa = tc::smem_u32(sq), ka = tc::smem_u32(sk), va = tc::smem_u32(sv), pa = tc::smem_u32(sp);
             uint32_t kc = 0, vc = 0, qc = 0, pc[2] = {0, 0};
             bool ok = true;
             auto issue_z = [&](int st) {
-                if (!warp_wait(&sh.k_ready, kc++ & 1u)) return false;
+                if (!warp_wait(&sh.k_ready[kc & 1], (kc >> 1) & 1u)) return false;
                 tc::fence_after_sync();
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (x >> 2) * C::BLK + (x & 3) * 32;
-                    mma_ss(tm + 128 * st, desc_qk(qa + off), desc_qk(ka + off), id_z, x > 0);
+                    const uint32_t step = (x & 3) * 32;
+                    mma_ss(tm + kRows * st, desc_qk(ka + (kc & 1) * kTileBytes + (x >> 2) * kColBlk + step), desc_qk(qa + (x >> 2) * kQBlk + step), id_z, x > 0);
                 }
                 commit(&sh.z_full[st]);
-                commit(&sh.k_free);
+                commit(&sh.k_free[kc & 1]);
+                ++kc;
                 return true;
             };
             while (ok && walk.next(a, row_tiles, s)) {
@@ -296,11 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                          warp_wait(&sh.p_full[st], (st ? pc[1]++ : pc[0]++) & 1u) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t v = va + (vc & 1) * C::TILE;
+                    const uint32_t v = va + (vc & 1) * kTileBytes;
 #pragma unroll
                     for (int x = 0; x < kBlk / 16; ++x)
-                        mma_ts(tm + 256 + D * st, tm + 128 * st + 8 * x, desc_v(v + x * 2048, D == 128 ? C::BLK : 1024u), id_o,
-                               i > 1 || x > 0);
+                        mma_vp(tm + 2 * kRows + kRows * st, desc_v(v + x * 2048, kColBlk), pa + st * kPBytes + x * 1024, id_o, i > 1 || x > 0);
                     commit(&sh.v_free[vc & 1]);
                     if (i + 2 < s.count) ok = issue_z(st);  // its commit also covers O's product
                     else commit(&sh.o_full[st]);
@@ -323,21 +380,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2 && ok; ++x, ++it) {
                         const uint32_t st = it % kRaw;
                         ok = warp_wait(&sh.raw_full[st], (it / kRaw) & 1u) &&
-                             (x ? warp_wait(&sh.v_free[vc & 1], ((vc >> 1) & 1u) ^ 1u) : warp_wait(&sh.k_free, (kc & 1u) ^ 1u)) &&
+                             (x ? warp_wait(&sh.v_free[vc & 1], ((vc >> 1) & 1u) ^ 1u) : warp_wait(&sh.k_free[kc & 1], ((kc >> 1) & 1u) ^ 1u)) &&
                              !__any_sync(0xffffffffu, *dead != 0u);
                         if (!ok) break;
-                        const unsigned char* src = raw + st * C::RAW;
-                        unsigned char* dst = x ? sv + (vc & 1) * C::TILE : sk;
+                        const unsigned char* src = raw + st * kRawBytes;
+                        unsigned char* dst = (x ? sv : sk) + (vc & 1) * kTileBytes;  // kc and vc go together
                         const uint32_t there = sh.has[blk & 7];
                         const bool edge = x && (key0 + kBlk > s.len - a.L + 1 || there != 0xffu);
-#pragma unroll 2
-                        for (int e = 0; e < (kBlk * RC + kConvert - 1) / kConvert; ++e) {
-                            const int p = me + e * kConvert, row = p / RC, ch = p % RC;
-                            if (p >= kBlk * RC) break;
-                            const uint4 u = *reinterpret_cast<const uint4*>(src + p * 16);
-                            uint32_t c[4] = {u.x, u.y, u.z, u.w};
-                            if (edge) {
-                                // keys that are not there, and NaN that not every row may see, leave the tile
+                        constexpr int kTurns = (kBlk * RC + kConvert - 1) / kConvert;
+                        auto store = [&](int p, const uint32_t (&c)[4]) {
+                            const int row = p / RC, ch = p % RC;
+                            uint32_t h[8];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
+                            unsigned char* at = dst + (ch >> 2) * kColBlk + row * 128;
+                            const int cc = (2 * ch) & 7;
+                            *reinterpret_cast<uint4*>(at + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        };
+                        if (!edge) {
+                            uint4 u[kTurns];
+#pragma unroll
+                            for (int e = 0; e < kTurns; ++e) {
+                                const int p = me + e * kConvert;
+                                if (p < kBlk * RC) u[e] = *reinterpret_cast<const uint4*>(src + p * 16);
+                            }
+#pragma unroll
+                            for (int e = 0; e < kTurns; ++e) {
+                                const int p = me + e * kConvert;
+                                const uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                                if (p < kBlk * RC) store(p, c);
+                            }
+                        } else {
+                            // keys that are not there, and NaN that not every row may see, leave the tile
+                            for (int p = me; p < kBlk * RC; p += kConvert) {
+                                const int row = p / RC, ch = p % RC;
+                                const uint4 u = *reinterpret_cast<const uint4*>(src + p * 16);
+                                uint32_t c[4] = {u.x, u.y, u.z, u.w};
                                 const bool is = key0 + row < s.len && ((there >> (row >> 4)) & 1u) != 0u;
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
@@ -352,19 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         }
                                     }
                                 }
+                                store(p, c);
                             }
-                            uint32_t h[8];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
-                            unsigned char* at = dst + (ch >> 2) * C::BLK + row * 128;
-                            const int cc = (2 * ch) & 7;
-                            *reinterpret_cast<uint4*>(at + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                         }
                         tc::fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tc::mbar_arrive(x ? &sh.v_ready[vc & 1] : &sh.k_ready);
+                            tc::mbar_arrive(x ? &sh.v_ready[vc & 1] : &sh.k_ready[kc & 1]);
                             tc::mbar_arrive(&sh.raw_free[st]);
                         }
                     }
@@ -375,243 +448,243 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        // ---- softmax: stream st takes the segment's blocks st, st + 2, ..., a thread the row of its lane
-        const int st = w >> 2, r = tid & 127, q4 = w & 3;
+        // ---- softmax: stream st takes the segment's blocks st, st + 2, ..., a thread the key of its lane
+        const int st = w >> 2, q4 = w & 3, key_in = tid & 127;
         const uint32_t lanes = (uint32_t)q4 << 21;
-        const uint32_t zt = tm + 128 * st + lanes, ot = tm + 256 + D * st + lanes;
+        const uint32_t zt = tm + kRows * st + lanes, ot = tm + 2 * kRows + kRows * st + lanes;
         uint32_t zc = 0, oc = 0, qc = 0, blk0 = 0, turn = 0, jc = 0;
         float* po = reinterpret_cast<float*>(a.ws + L.o);
         float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
+        auto larger = [](float x, float y) { return fmaxf(x, y); };
+        auto added = [](float x, float y) { return x + y; };
         bool gone = false;
         for (; !gone && walk.next(a, row_tiles, s); ++turn) {
-            const int R = s.rt * kRows + r;
-            const bool on = R < rows_all;
-            const bool warp_on = s.rt * kRows + 32 * q4 < rows_all;
-            const int t = on ? R / a.group : 0, head = s.h * a.group + (on ? R - t * a.group : 0);
-            const int seen = on ? s.len - a.L + t + 1 : 0;
-            float f = 0.f;
+            const int row0 = s.rt * kRows, rows = min(kRows, rows_all - row0);
+            const int whole_seen = s.len - a.L;  // keys before this one are seen by every row
             if (st == 0) {
-                // (the other stream has the last segment's factors)
-                if (turn > 0 && !warp_wait(&sh.f_read, (turn - 1) & 1u)) gone = true;
-                // the row of q, scaled so that its largest value lies in [2^14, 2^15), into the products' layout
-                if (on) {
-                    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)s.n * a.L + t) * a.qs +
-                                                                    (int64_t)head * D);
-                    uint32_t top = 0u;
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 u = __ldg(q + c);
-                        top = __vmaxu2(__vmaxu2(top, u.x & 0x7fff7fffu), __vmaxu2(u.y & 0x7fff7fffu, __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-                    }
-                    int e = (int)(max(top & 0xffffu, top >> 16) >> 7) - 127;
-                    e = min(max(e, -100), 127);
-                    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                    f = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
-                    auto cv = [&](uint32_t x) { return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 u = __ldg(q + c);
-                        *reinterpret_cast<uint4*>(sq + (c >> 3) * C::BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(cv(u.x), cv(u.y), cv(u.z), cv(u.w));
-                    }
+                // the rows of q, scaled by one power of two, into the products' layout: thread (row, quarter)
+                const bool late = turn > 0 && !warp_wait(&sh.f_read, (turn - 1) & 1u);  // the other stream has the last factor
+                const int r = key_in >> 2, quarter = key_in & 3;
+                const int R = row0 + r, t = R / a.group, head = s.h * a.group + (R - t * a.group);
+                const bool on = r < rows;
+                uint4 u[4];
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)s.n * a.L + t) * a.qs + (int64_t)head * D;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) u[c] = on ? __ldg(reinterpret_cast<const uint4*>(q) + 4 * quarter + c) : make_uint4(0u, 0u, 0u, 0u);
+                if (quarter == 0 && on) sh.at[r] = ((int64_t)s.n * a.L + t) * tokrow + (int64_t)head * D;
+                uint32_t top = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    top = __vmaxu2(__vmaxu2(top, u[c].x & 0x7fff7fffu), __vmaxu2(u[c].y & 0x7fff7fffu, __vmaxu2(u[c].z & 0x7fff7fffu, u[c].w & 0x7fff7fffu)));
+                top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+                if (lane == 0) sh.qmax[q4] = top;
+                gone = any4(0, late);
+                top = max(max(sh.qmax[0], sh.qmax[1]), max(sh.qmax[2], sh.qmax[3]));
+                int e = (int)(top >> 7) - 127;
+                e = min(max(e, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                auto cv = [&](uint32_t x) { return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int ch = 4 * quarter + c;
+                    *reinterpret_cast<uint4*>(sq + (ch >> 3) * kQBlk + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(cv(u[c].x), cv(u[c].y), cv(u[c].z), cv(u[c].w));
                 }
-                sh.f[r] = f;
+                if (key_in == 0) sh.f = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sh.q_ready);
-            } else {
-                if (!warp_wait(&sh.q_ready, qc & 1u)) gone = true;
-                f = sh.f[r];
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.f_read);
             }
-            ++qc;
-            float m = -INFINITY, l = 0.f, vu = 0.f, vtop = 0.f;
+            const bool no_q = !warp_wait(&sh.q_ready, qc++ & 1u);
+            const float f = sh.f;
+            gone = any4(st, no_q || gone);
+            if (st == 1 && lane == 0) tc::mbar_arrive(&sh.f_read);
+            float l[kRows], vu = 0.f, vtop = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) l[r] = 0.f;
+            if (key_in < kRows) sh.ref[st][key_in] = -INFINITY;
+            (void)any4(st, false);
             for (int i = st; i < s.count && !gone; i += 2) {
-                gone = !warp_wait(&sh.z_full[st], zc++ & 1u) || __any_sync(0xffffffffu, *dead != 0u);
-                if (gone) break;
+                const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u) || *dead != 0u;
                 tc::fence_after_sync();
-                if (warp_on) {
-                    const int b = (int)((blk0 + i) & 7u), key0 = (s.i0 + i) * kBlk;
-                    const uint32_t there = sh.has[b];
-                    const bool edge = key0 + kBlk > s.len - a.L + 1 || there != 0xffu;
-                    // bit c: key key0 + c of this half is seen
-                    auto seen_of = [&](int half) -> uint64_t {
-                        uint64_t x = 0;
-                        const int k = seen - key0 - 64 * half;
-                        x = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1ull;
+                const int b = (int)((blk0 + i) & 7u), key = (s.i0 + i) * kBlk + key_in;
+                uint32_t z[kRows];
+                tmem_ld32(zt, z);
+                const float ks = sh.ks[b][key_in >> 4], vs = sh.vs[b][key_in >> 4];
+                const bool is = key < s.len && ((sh.has[b] >> (key_in >> 4)) & 1u) != 0u;
+                // rows [from, 32) see this key: later tokens of the window see more
+                const int from = !is ? kRows : key < whole_seen ? 0 : max(0, (key - whole_seen) * a.group - row0);
+                float big = 0.f;
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (!((there >> (4 * half + g)) & 1u)) x &= ~(0xffffull << (16 * g));
-                        return x;
-                    };
-                    float top = -INFINITY;
+                for (int g = 0; g < kGroups; ++g) {
+                    const float v = fabsf(sh.vs[b][g]);
+                    if (v < INFINITY) big = fmaxf(big, v);
+                }
+                const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
+                const float sc = f * ks;
+                // scores less their rows' references; does any pass its own by more than 2^8?
+                float over = -INFINITY;
+                auto less_ref = [&]() {
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t z[64];
-                        tmem_ld32(zt + 64 * half, z);
-                        tmem_ld32(zt + 64 * half + 32, z + 32);
+                    for (int c = 0; c < kRows / 4; ++c) {
+                        const float4 m = *reinterpret_cast<const float4*>(&sh.ref[st][4 * c]);
+                        z[4 * c] = __float_as_uint(fmaf(f_of(z[4 * c]), sc, -m.x));
+                        z[4 * c + 1] = __float_as_uint(fmaf(f_of(z[4 * c + 1]), sc, -m.y));
+                        z[4 * c + 2] = __float_as_uint(fmaf(f_of(z[4 * c + 2]), sc, -m.z));
+                        z[4 * c + 3] = __float_as_uint(fmaf(f_of(z[4 * c + 3]), sc, -m.w));
+                    }
+                };
+                less_ref();
+                if (from == 0) {
+#pragma unroll
+                    for (int r = 0; r < kRows; r += 2) over = max3(over, f_of(z[r]), f_of(z[r + 1]));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (r >= from) over = fmaxf(over, f_of(z[r]));
+                }
+                if (any4(st, over > 8.f || unit || late)) {
+                    gone = any4(st, late);
+                    if (gone) break;
+                    // new references: the largest scores met so far
+                    {
+                        float x[kRows];
+                        tmem_ld32(zt, reinterpret_cast<uint32_t*>(x));
                         tc::tmem_wait_ld();
-                        if (edge) {
-                            const uint64_t vis = seen_of(half);
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                if ((vis >> c) & 1ull) top = fmaxf(top, f_of(z[c]) * (f * sh.ks[b][4 * half + (c >> 4)]));
-                        } else {
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const float sg = f * sh.ks[b][4 * half + g];
-                                float x = -INFINITY, y = -INFINITY;
-#pragma unroll
-                                for (int c = 16 * g; c < 16 * g + 16; c += 4) {
-                                    x = max3(x, f_of(z[c]) * sg, f_of(z[c + 1]) * sg);
-                                    y = max3(y, f_of(z[c + 2]) * sg, f_of(z[c + 3]) * sg);
-                                }
-                                top = max3(top, x, y);
-                            }
-                        }
+                        for (int r = 0; r < kRows; ++r) x[r] = r >= from ? x[r] * sc : -INFINITY;
+                        sh.top[st][q4][lane] = reduce_rows(x, larger);
                     }
-                    // the reference and O's unit (the same for all rows), and O where either has moved
-                    const float now = top > m + 8.f ? top : m;
-                    const float ref = now == -INFINITY ? 0.f : now;
-                    float by = ex2(m - ref);
-                    bool moved = now != m;
-                    m = now;
-                    l *= by;
-                    float big = 0.f;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const float v = fabsf(sh.vs[b][g]);
-                        if (v < INFINITY) big = fmaxf(big, v);
-                    }
-                    if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
+                    (void)any4(st, false);
+                    float ratio = 1.f;
+                    if (unit) {
                         vtop = fmaxf(vtop, big);
                         const float nu = fmaxf(big, vtop * 9.094947e-13f);
-                        by *= vu == 0.f ? 0.f : vu / nu;
+                        ratio = vu == 0.f ? 0.f : vu / nu;
                         vu = nu;
-                        moved = true;
                     }
-                    if (i >= 2 && __any_sync(0xffffffffu, moved)) {
-                        // the products into O up to here ended with the scores that were waited for
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(ot + 32 * c, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f_of(o[e]) * by);
-                            tmem_st32(ot + 32 * c, o);
-                        }
+                    if (q4 == 0) {
+                        const float was = sh.ref[st][lane];
+                        const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
+                        const float now = top > was + 8.f ? top : was;
+                        sh.by[st][lane] = now == -INFINITY ? 0.f : ex2(was - now);
+                        sh.ref[st][lane] = now;
                     }
-                    const float iv = vu == 0.f ? 0.f : 1.f / vu;
+                    (void)any4(st, false);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t z[64];
-                        // (P lies over Z's first half: the second is read before P's second part is written there)
-                        tmem_ld32(zt + 64 * half, z);
-                        tmem_ld32(zt + 64 * half + 32, z + 32);
+                    for (int r = 0; r < kRows; ++r) l[r] *= sh.by[st][r];
+                    if (i >= 2) {
+                        // (the products into O up to here ended with the scores that were waited for)
+                        uint32_t o[kRows];
+                        tmem_ld32(ot, o);
                         tc::tmem_wait_ld();
-                        const uint64_t vis = edge ? seen_of(half) : ~0ull;
-                        uint32_t p[32];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const float sg = f * sh.ks[b][4 * half + g];
-                            const float vs = sh.vs[b][4 * half + g];
-                            const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs * iv;
-                            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                            for (int c = 16 * g; c < 16 * g + 16; c += 2) {
-                                const float2 x = __ffma2_rn(make_float2(f_of(z[c]), f_of(z[c + 1])), make_float2(sg, sg), make_float2(-ref, -ref));
-                                float2 y = make_float2(ex2(x.x), ex2(x.y));
-                                if (edge) {
-                                    if (!((vis >> c) & 1ull)) y.x = 0.f;
-                                    if (!((vis >> (c + 1)) & 1ull)) y.y = 0.f;
-                                }
-                                sum = __fadd2_rn(sum, y);
-                                y = __fmul2_rn(y, make_float2(pv, pv));
-                                p[c >> 1] = pack_f16(y.x, y.y);
-                            }
-                            l += sum.x + sum.y;
-                        }
-                        tmem_st32(zt + 32 * half, p);
+                        for (int r = 0; r < kRows; ++r) o[r] = __float_as_uint(f_of(o[r]) * (sh.by[st][r] * ratio));
+                        tmem_st32(ot, o);
+                        tc::tmem_wait_st();
                     }
-                    tc::tmem_wait_st();
+                    tmem_ld32(zt, z);
+                    less_ref();
                 }
+                const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs / vu;
+                unsigned char* at = sp + st * kPBytes + key_in * 64;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 8 * c + 2 * e;
+                        // a row that has seen nothing has the reference -inf; its weights are replaced below
+                        float2 y = make_float2(ex2(f_of(z[r])), ex2(f_of(z[r + 1])));
+                        if (from > 0) {
+                            if (r < from) y.x = 0.f;
+                            if (r + 1 < from) y.y = 0.f;
+                        }
+                        l[r] += y.x;
+                        l[r + 1] += y.y;
+                        y = __fmul2_rn(y, make_float2(pv, pv));
+                        p[e] = pack_f16(y.x, y.y);
+                    }
+                    *reinterpret_cast<uint4*>(at + ((c ^ ((key_in >> 1) & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+                tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sh.p_full[st]);
             }
             blk0 += s.count;
             const bool both = s.count > 1;
-            if (!gone && st < s.count) gone = !warp_wait(&sh.o_full[st], oc++ & 1u) || __any_sync(0xffffffffu, *dead != 0u);
+            bool late = false;
+            if (!gone && st < s.count) late = !warp_wait(&sh.o_full[st], oc++ & 1u);
+            gone = any4(st, late || gone);
             tc::fence_after_sync();
-            if (both && !gone) {
-                if (st == 1) {
-                    sh.part[0][r] = m;
-                    sh.part[1][r] = l;
-                    sh.part[2][r] = vu;
-                    __syncwarp();
+            if (gone) break;
+            // a row's sum over the keys, by warp; the reference and the unit
+            sh.sum[st][q4][lane] = reduce_rows(l, added);
+            if (q4 == 0 && lane == 0) sh.unit[st] = vu;
+            __syncwarp();
+            if (st == 1) {
+                if (both) {
                     if (lane == 0) tc::mbar_arrive(&sh.joined);
-                    gone = !warp_wait(&sh.join_free, jc++ & 1u);
-                } else {
-                    gone = !warp_wait(&sh.joined, jc++ & 1u);
+                    late = !warp_wait(&sh.join_free, jc++ & 1u);
                 }
+                gone = any4(1, late);
+                continue;
             }
-            if (st == 0 && !gone) {
-                const float m1 = both ? sh.part[0][r] : -INFINITY, l1 = both ? sh.part[1][r] : 0.f, u1 = both ? sh.part[2][r] : 0.f;
-                const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm;
-                const float f0 = ex2(m - ref), f1 = ex2(m1 - ref);
-                const float sum = l * f0 + l1 * f1;
-                const bool whole = s.begun && s.ended;
+            if (both) late = !warp_wait(&sh.joined, jc++ & 1u);
+            gone = any4(0, late);
+            if (gone) break;
+            const bool whole = s.begun && s.ended;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (s.begun ? 1 : 0);
+            if (q4 == 0) {  // lane r: row r's weights of the two streams
+                const float m0 = sh.ref[0][lane], m1 = both ? sh.ref[1][lane] : -INFINITY;
+                const float l0 = (sh.sum[0][0][lane] + sh.sum[0][1][lane]) + (sh.sum[0][2][lane] + sh.sum[0][3][lane]);
+                const float l1 = both ? (sh.sum[1][0][lane] + sh.sum[1][1][lane]) + (sh.sum[1][2][lane] + sh.sum[1][3][lane]) : 0.f;
+                const float mm = fmaxf(m0, m1), ref = mm == -INFINITY ? 0.f : mm;
+                const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+                const float sum = l0 * f0 + l1 * f1;
                 const float mul = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                const float w0 = vu * f0 * mul, w1 = u1 * f1 * mul;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (s.begun ? 1 : 0);
-                if (warp_on) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32], y[32];
-                        tmem_ld32(ot + 32 * c, o);
-                        if (both) tmem_ld32(ot + D + 32 * c, y);
-                        tc::tmem_wait_ld();
-                        float x[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            x[e] = f_of(o[e]) * w0 + (both ? f_of(y[e]) * w1 : 0.f);
-                            if (kE4m3) {
-                                const unsigned long long od = sh.odd[turn & 3][32 * c + e];
-                                if ((uint32_t)(od >> 32) == 0xfffffffeu - turn && (int64_t)(uint32_t)od + s.len - a.L < seen) x[e] = NAN;
-                            }
-                        }
-                        if (!on) continue;
-                        if (whole) {
-                            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)s.n * a.L + t) * tokrow + (int64_t)head * D + 32 * c;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(tc::pack_bf16(x[8 * e], x[8 * e + 1]), tc::pack_bf16(x[8 * e + 2], x[8 * e + 3]),
-                                                                                   tc::pack_bf16(x[8 * e + 4], x[8 * e + 5]), tc::pack_bf16(x[8 * e + 6], x[8 * e + 7]));
-                        } else {
-                            float* pd = po + (slot * rows_max + r) * D + 32 * c;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) *reinterpret_cast<float4*>(pd + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-                        }
-                    }
-                    if (on && !whole) ml[slot * rows_max + r] = make_float2(mm, sum);
-                }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (both && lane == 0) tc::mbar_arrive(&sh.join_free);
+                sh.weight[0][lane] = sh.unit[0] * f0 * mul;
+                sh.weight[1][lane] = both ? sh.unit[1] * f1 * mul : 0.f;
+                if (!whole && lane < rows) ml[slot * rows_max + lane] = make_float2(mm, sum);
             }
+            (void)any4(0, false);
+            uint32_t o[kRows], y[kRows];
+            tmem_ld32(ot, o);
+            if (both) tmem_ld32(ot + kRows, y);
+            tc::tmem_wait_ld();
+            // a NaN in this thread's channel reaches the rows that see its key
+            int nan_from = kRows;
+            if (kE4m3) {
+                const unsigned long long od = sh.odd[turn & 3][key_in];
+                if ((uint32_t)(od >> 32) == 0xfffffffeu - turn) nan_from = (int)max((int64_t)0, min((int64_t)kRows, (int64_t)(uint32_t)od * a.group - row0));
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                float x = f_of(o[r]) * sh.weight[0][r];
+                if (both) x = fmaf(f_of(y[r]), sh.weight[1][r], x);
+                if (r >= nan_from) x = NAN;
+                if (r < rows) {
+                    if (whole) static_cast<__nv_bfloat16*>(a.out)[sh.at[r] + key_in] = __float2bfloat16_rn(x);
+                    else po[(slot * rows_max + r) * D + key_in] = x;
+                }
+            }
+            tc::fence_before_sync();
+            (void)any4(0, false);  // sh.weight and sh.at are read
+            if (both && lane == 0) tc::mbar_arrive(&sh.join_free);
         }
         if (gone) *dead = 1u;
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (w == 8) tc::tmem_dealloc(tm, 512);
+    if (w == 8) tc::tmem_dealloc(tm, 128);
     if (tid == 0) {
         // what this worker leaves to be joined: the unit that it began and did not end
         Record mine{-1, 0, 0, 0, 0};
         const bool failed = sh.dead != 0u;
-        start();
+        walk.left = (int)(b1 - b0);
+        walk.c = sh.begin;
         int64_t pos = b0;
         while (walk.next(a, row_tiles, s)) {
             if (s.begun) {
@@ -645,16 +718,16 @@ bool encode_codes(CUtensorMap* m, const void* base, const AttnDecodeArgs& a)
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kE4m3>
+template <bool kE4m3>
 cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 {
-    static_assert(Cfg<D>::SMEM + sizeof(Shared) <= 232448, "the tiles fit an SM");
+    static_assert(kSmem + sizeof(Shared) <= 232448, "the tiles fit an SM");
     static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "register split");
     Maps maps;
     if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
-    auto kern = kda_attn_window_kernel<D, kE4m3>;
+    auto kern = kda_attn_window_kernel<kE4m3>;
     static SmemLimit limit;
-    cudaError_t e = limit.raise(kern, (int)Cfg<D>::SMEM);
+    cudaError_t e = limit.raise(kern, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int64_t rows_all = (int64_t)a.L * a.group;
     const int rows = (int)(rows_all < kRows ? rows_all : kRows);
@@ -663,7 +736,7 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
     const int full = sm_count_of_current_device();
     const int ctas = most < (double)full ? (int)most : full;
     const bool by_unit = units <= ctas;
-    kern<<<ctas, kThreads, Cfg<D>::SMEM, s>>>(a, maps, rows, by_unit);
+    kern<<<ctas, kThreads, kSmem, s>>>(a, maps, rows, by_unit);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_attn_join(a, KDA_BF16, rows, kRows, ctas, ctas, by_unit, units, s);
@@ -671,7 +744,7 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt) { return dt == KDA_BF16 && d != 32 && rows > 16; }
+bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt) { return dt == KDA_BF16 && d == D && rows > 16; }
 
 size_t attn_window_workspace_bytes(int64_t rows, int d)
 {
@@ -681,9 +754,7 @@ size_t attn_window_workspace_bytes(int64_t rows, int d)
 
 cudaError_t launch_attn_window(const AttnDecodeArgs& a, cudaStream_t s)
 {
-    const bool e4m3 = a.c.dtype == KDA_CACHE_E4M3;
-    if (a.d == 64) return e4m3 ? launch_window_d<64, true>(a, s) : launch_window_d<64, false>(a, s);
-    return e4m3 ? launch_window_d<128, true>(a, s) : launch_window_d<128, false>(a, s);
+    return a.c.dtype == KDA_CACHE_E4M3 ? launch_window_d<true>(a, s) : launch_window_d<false>(a, s);
 }
 
 }  // namespace kda
