@@ -63,8 +63,8 @@ cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
 size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt);  // rows: window x group
 
-// The form for many rows a key head (kda_attn_window.cu): does it take this call, what does it need.
-bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt);
+// The form for many rows a key head (kda_attn_window.cu): does it take a call, what does it need.
+bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt, int64_t capacity);  // keys that a sequence's pages hold
 size_t attn_window_workspace_bytes(int64_t rows, int d);
 cudaError_t launch_attn_window(const AttnDecodeArgs& a, cudaStream_t s);
 

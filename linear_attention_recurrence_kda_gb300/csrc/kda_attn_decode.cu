@@ -42,8 +42,8 @@ constexpr int ctas_of(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int stages_of(int nt, int d) { return (nt == 1 ? 2 : 3) * (d == 128 ? 1 : d == 64 ? 2 : 3); }
 
 // Column tiles of 8 rows for a call's rows.  More than 16 rows make several units that read the same
-// tiles (28 rows, 64 sequences of 3150 keys and 8 heads: 194 us by 16 rows with O in 128 registers less
-// than by 32, which took 202; by 8 rows 270).
+// tiles, or another kernel takes them (kda_attn_window.cu).  Four column tiles, with O in 128 registers,
+// took 202 us where two took 194 (28 rows, 64 sequences of 3150 keys, 8 heads).
 inline int nt_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 struct Maps {
@@ -778,14 +778,15 @@ cudaError_t launch_attn_join(const AttnDecodeArgs& a, kda_dtype_t dt, int rows_m
 
 size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt)
 {
-    if (attn_window_takes(rows, d, dt)) return attn_window_workspace_bytes(rows, d);
     const int nt = nt_of(rows);
-    return decode_layout(decode_ctas(nt) * kWarps, decode_ctas(nt), (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
+    const size_t need = decode_layout(decode_ctas(nt) * kWarps, decode_ctas(nt), (int)(rows < 8 * nt ? rows : 8 * nt), d).total;
+    const size_t window = attn_window_takes(rows, d, dt, INT64_MAX) ? attn_window_workspace_bytes(rows, d) : 0;
+    return need > window ? need : window;  // which form runs depends on the cache
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s)
 {
-    if (attn_window_takes((int64_t)a.L * a.group, a.d, dt)) return launch_attn_window(a, s);
+    if (attn_window_takes((int64_t)a.L * a.group, a.d, dt, (int64_t)a.c.max_pages * a.c.page)) return launch_attn_window(a, s);
     const bool e4m3 = a.c.dtype == KDA_CACHE_E4M3;
     if (dt == KDA_BF16) return e4m3 ? launch_decode_io<__nv_bfloat16, true>(a, s) : launch_decode_io<__nv_bfloat16, false>(a, s);
     return e4m3 ? launch_decode_io<float, true>(a, s) : launch_decode_io<float, false>(a, s);

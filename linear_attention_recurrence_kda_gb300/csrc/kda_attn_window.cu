@@ -11,6 +11,9 @@
 // is idle, a key's scales are the thread's own, and no score crosses lanes but at a change of the
 // reference.  Few columns make the products cheap (about 128 cycles each a block).
 //
+// A block then takes about 2000 cycles, of which shared memory's bandwidth accounts for 1700 (the codes in
+// and out once, 64 KB of f16 written and read by the products, P), where HBM would give one every 1400.
+//
 // Blocks alternate between two streams, each with its own reference, sums and O, so that one's softmax
 // runs while the other waits; at the end of a unit the first stream joins them.  Tensor memory: Z0 | Z1 |
 // O0 | O1, 32 columns each; P goes through shared memory.  All units' blocks form one line that is cut
@@ -48,10 +51,6 @@ constexpr uint32_t kQBytes = 2 * kQBlk;
 constexpr uint32_t kPBytes = kBlk * kRows * 2;  // P^T: a key's 32 weights are 64 bytes
 constexpr uint32_t kRawBytes = kBlk * D;        // a block of codes
 constexpr uint32_t kSmem = kQBytes + 2 * kPBytes + 4 * kTileBytes + kRaw * kRawBytes + 1024;  // K and V twice
-
-struct Maps {
-    CUtensorMap k, v;
-};
 
 struct Shared {
     uint64_t raw_full[kRaw], raw_free[kRaw], k_ready[2], k_free[2], v_ready[2], v_free[2];
@@ -151,7 +150,7 @@ __device__ __forceinline__ unsigned long long odd_note(uint32_t turn, int key, i
 
 template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads, 1)
-    kda_attn_window_kernel(const AttnDecodeArgs a, const __grid_constant__ Maps maps, const int rows_max, const bool by_unit)
+    kda_attn_window_kernel(const AttnDecodeArgs a, const int rows_max, const bool by_unit)
 {
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared sh;
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
                     for (int x = 0; x < 2 && ok; ++x, ++it) {
                         const uint32_t st = it % kRaw;
-                        ok = warp_wait(&sh.raw_free[st], ((it / kRaw) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
+                        ok = warp_wait(&sh.raw_free[st], ((it / kRaw) & 1u) ^ 1u);
                         if (!ok) break;
                         if (x == 0) {
                             if (lane < 8) sh.ks[blk & 7][grp] = scale;
@@ -310,11 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const int pieces = __popc(there) / gpp + (__popc(there) % gpp != 0 ? 1 : 0);
                         if (lane == 0) tc::mbar_arrive_expect_tx(&sh.raw_full[st], (uint32_t)pieces * box * D);
-                        for (int p = 0; p < kGroups / gpp; ++p) {
-                            const int id = __shfl_sync(0xffffffffu, page, p * gpp);
-                            if (lane == 0 && id >= 0)
-                                tc::tma_load_3d(raw + st * kRawBytes + p * box * D, x ? &maps.v : &maps.k, 0,
-                                                (i * kBlk + p * box) & (a.c.page - 1), id * a.Hkv + s.h, &sh.raw_full[st]);
+                        // a page of a head is contiguous: the lane of its first group copies it
+                        __syncwarp();
+                        if (lane < 8 && page >= 0 && grp % gpp == 0) {
+                            const uint8_t* src = (x ? a.c.v : a.c.k) +
+                                                 (((int64_t)page * a.Hkv + s.h) * a.c.page + ((i * kBlk + grp * 16) & (a.c.page - 1))) * D;
+                            tc::bulk_load(raw + st * kRawBytes + grp * 16 * D, src, (uint32_t)box * D, &sh.raw_full[st]);
                         }
                     }
                     page = page1;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < s.count && ok; ++i, ++vc) {
                     const int st = i & 1;
                     ok = warp_wait(&sh.v_ready[vc & 1], (vc >> 1) & 1u) &&
-                         warp_wait(&sh.p_full[st], (st ? pc[1]++ : pc[0]++) & 1u) && !__any_sync(0xffffffffu, *dead != 0u);
+                         warp_wait(&sh.p_full[st], (st ? pc[1]++ : pc[0]++) & 1u);
                     if (!ok) break;
                     tc::fence_after_sync();
                     const uint32_t v = va + (vc & 1) * kTileBytes;
@@ -372,24 +372,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- conversion: 16 codes a thread at a time, into the products' layout
             const int me = tid - 10 * 32;
             constexpr int RC = D / 16;  // 16-code pieces of a row
-            uint32_t it = 0, kc = 0, vc = 0, blk = 0, turn = 0;
+            uint32_t blk = 0, turn = 0;
             bool ok = true;
             for (; ok && walk.next(a, row_tiles, s); ++turn) {
-                for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++blk, ++vc, ++kc) {
+                for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++blk) {
                     const int key0 = i * kBlk;
-                    for (int x = 0; x < 2 && ok; ++x, ++it) {
-                        const uint32_t st = it % kRaw;
-                        ok = warp_wait(&sh.raw_full[st], (it / kRaw) & 1u) &&
-                             (x ? warp_wait(&sh.v_free[vc & 1], ((vc >> 1) & 1u) ^ 1u) : warp_wait(&sh.k_free[kc & 1], ((kc >> 1) & 1u) ^ 1u)) &&
-                             !__any_sync(0xffffffffu, *dead != 0u);
+#pragma unroll 1
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        const uint32_t it = 2 * blk + x, st = it % kRaw;
+                        ok = warp_wait(x ? &sh.v_free[blk & 1] : &sh.k_free[blk & 1], ((blk >> 1) & 1u) ^ 1u) &&
+                             warp_wait(&sh.raw_full[st], (it / kRaw) & 1u);
                         if (!ok) break;
                         const unsigned char* src = raw + st * kRawBytes;
-                        unsigned char* dst = (x ? sv : sk) + (vc & 1) * kTileBytes;  // kc and vc go together
+                        unsigned char* dst = (x ? sv : sk) + (blk & 1) * kTileBytes;
                         const uint32_t there = sh.has[blk & 7];
                         const bool edge = x && (key0 + kBlk > s.len - a.L + 1 || there != 0xffu);
                         constexpr int kTurns = (kBlk * RC + kConvert - 1) / kConvert;
+                        // Sixteen lanes take two rows, eight of them half of each: what they read then fills
+                        // the banks once, and so do their 16-byte stores, which the layout puts at
+                        // even places of one row and odd places of the other.
+                        auto row_of = [](int p) { return 2 * (p >> 4) + ((p >> 2) & 1); };
+                        auto piece_of = [](int p) { return (p & 3) + 4 * (((p >> 2) ^ (p >> 3)) & 1); };
+                        static_assert(RC == 8, "eight pieces a row");
                         auto store = [&](int p, const uint32_t (&c)[4]) {
-                            const int row = p / RC, ch = p % RC;
+                            const int row = row_of(p), ch = piece_of(p);
                             uint32_t h[8];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < kTurns; ++e) {
                                 const int p = me + e * kConvert;
-                                if (p < kBlk * RC) u[e] = *reinterpret_cast<const uint4*>(src + p * 16);
+                                if (p < kBlk * RC) u[e] = *reinterpret_cast<const uint4*>(src + row_of(p) * D + piece_of(p) * 16);
                             }
 #pragma unroll
                             for (int e = 0; e < kTurns; ++e) {
@@ -414,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             // keys that are not there, and NaN that not every row may see, leave the tile
                             for (int p = me; p < kBlk * RC; p += kConvert) {
-                                const int row = p / RC, ch = p % RC;
-                                const uint4 u = *reinterpret_cast<const uint4*>(src + p * 16);
+                                const int row = row_of(p), ch = piece_of(p);
+                                const uint4 u = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
                                 uint32_t c[4] = {u.x, u.y, u.z, u.w};
                                 const bool is = key0 + row < s.len && ((there >> (row >> 4)) & 1u) != 0u;
 #pragma unroll
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::fence_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tc::mbar_arrive(x ? &sh.v_ready[vc & 1] : &sh.k_ready[kc & 1]);
+                            tc::mbar_arrive(x ? &sh.v_ready[blk & 1] : &sh.k_ready[blk & 1]);
                             tc::mbar_arrive(&sh.raw_free[st]);
                         }
                     }
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key_in < kRows) sh.ref[st][key_in] = -INFINITY;
             (void)any4(st, false);
             for (int i = st; i < s.count && !gone; i += 2) {
-                const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u) || *dead != 0u;
+                const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u);
                 tc::fence_after_sync();
                 const int b = (int)((blk0 + i) & 7u), key = (s.i0 + i) * kBlk + key_in;
                 uint32_t z[kRows];
@@ -705,26 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-bool encode_codes(CUtensorMap* m, const void* base, const AttnDecodeArgs& a)
-{
-    const TensorMapEncode enc = attn_tensor_map_encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.c.page, (cuuint64_t)a.c.num_pages * a.Hkv};
-    const cuuint64_t strides[2] = {(cuuint64_t)a.d, (cuuint64_t)a.d * a.c.page};
-    const cuuint32_t box[3] = {(cuuint32_t)a.d, (cuuint32_t)(a.c.page < kBlk ? a.c.page : kBlk), 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool kE4m3>
 cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 {
     static_assert(kSmem + sizeof(Shared) <= 232448, "the tiles fit an SM");
     static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "register split");
-    Maps maps;
-    if (!encode_codes(&maps.k, a.c.k, a) || !encode_codes(&maps.v, a.c.v, a)) return cudaErrorInvalidValue;
     auto kern = kda_attn_window_kernel<kE4m3>;
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, (int)kSmem);
@@ -736,7 +727,7 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
     const int full = sm_count_of_current_device();
     const int ctas = most < (double)full ? (int)most : full;
     const bool by_unit = units <= ctas;
-    kern<<<ctas, kThreads, kSmem, s>>>(a, maps, rows, by_unit);
+    kern<<<ctas, kThreads, kSmem, s>>>(a, rows, by_unit);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_attn_join(a, KDA_BF16, rows, kRows, ctas, ctas, by_unit, units, s);
@@ -744,7 +735,14 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 
 }  // namespace
 
-bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt) { return dt == KDA_BF16 && d == D && rows > 16; }
+// From 25 rows a key head, where the page table holds more than 512 keys a sequence.  Measured here and on
+// the warp-level form, us: 28 rows of 8 heads, 64 sequences of 3150 keys 131 and 194; 56 rows 231 and 365; one
+// sequence of 4000, one head 16.5 and 20.6; but 20 rows of one head, 64 of 1000 24.9 and 22.7; and 28 rows of
+// 8 heads, 256 of 300 140 and 117, where a unit's start and end outweigh its keys.
+bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt, int64_t capacity)
+{
+    return dt == KDA_BF16 && d == D && rows > 24 && capacity > 512;
+}
 
 size_t attn_window_workspace_bytes(int64_t rows, int d)
 {

@@ -113,11 +113,12 @@ def test_prefill_is_the_same_every_time_and_on_another_stream(dtype):
 
 # ---------------------------------------------------------------- the cache
 
-def tables(lens, page, extra=3, seed=0):
+def tables(lens, page, extra=3, seed=0, capacity=0):
+    """Shuffled pages; ``capacity`` keys at least a sequence in the table's columns."""
     need = [-(-n // page) for n in lens]
     pool = sum(need) + extra
     order = torch.randperm(pool, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
-    cols = max(max(need), 1) + 1
+    cols = max(max(max(need), 1) + 1, -(-capacity // page))
     t = torch.full((len(lens), cols), -7, dtype=torch.int32)  # entries past the last page are not read
     at = 0
     for n, m in enumerate(need):
@@ -231,8 +232,8 @@ def test_decode(lens, hq, hkv, window, page, d, code, dtype):
 
 MANY = [
     # lens, query heads, key heads, window: 17 rows and more a key head, up to several tiles of 128
-    ([1], 17, 1, 1), ([0, 5, 127, 128, 129, 256], 8, 1, 3), ([3, 700], 16, 2, 7), ([1000, 64, 333], 24, 3, 5),
-    ([90, 400], 8, 1, 40), ([1300], 128, 1, 2), ([17] * 300, 20, 1, 1), ([3000, 2900] * 20, 8, 2, 7), ([5], 4, 1, 30),
+    ([1], 17, 1, 1), ([1], 25, 1, 1), ([0, 5, 127, 128, 129, 256], 8, 1, 4), ([3, 700], 16, 2, 7), ([1000, 64, 333], 24, 3, 5),
+    ([90, 400], 8, 1, 40), ([1300], 128, 1, 2), ([17] * 300, 26, 1, 1), ([3000, 2900] * 20, 8, 2, 7), ([5], 4, 1, 30),
 ]
 
 
@@ -241,7 +242,7 @@ MANY = [
 @pytest.mark.parametrize("lens,hq,hkv,window", MANY, ids=[f"{len(p[0])}x{max(p[0])}h{p[1]}of{p[2]}w{p[3]}" for p in MANY])
 def test_decode_many_rows(lens, hq, hkv, window, page, d, code):
     """Many rows a key head, which another kernel takes."""
-    table, pool = tables(lens, page)
+    table, pool = tables(lens, page, capacity=600)
     cache = filled(pool, hkv, page, d, code, seed=page + d)
     q = make(len(lens) * window, hq, 1, d, torch.bfloat16, 2, fused=True)[0]
     ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
@@ -259,8 +260,8 @@ def test_decode_many_rows(lens, hq, hkv, window, page, d, code):
 @pytest.mark.parametrize("page", [16, 64])
 def test_decode_many_rows_nan_past_the_end_and_in_hidden_keys(page):
     """As for few rows: stale NaN past the end reaches nothing, a drafted token's NaN the rows that see it alone."""
-    lens, d, L, hq = [150, 95, 7, 300], 128, 6, 4
-    table, pool = tables(lens, page)
+    lens, d, L, hq = [150, 95, 7, 300], 128, 7, 4
+    table, pool = tables(lens, page, capacity=600)
     cache = filled(pool, 1, page, d, torch.float8_e4m3fn)
     q = make(4 * L, hq, 1, d, torch.bfloat16, 8)[0]
     lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
@@ -273,7 +274,7 @@ def test_decode_many_rows_nan_past_the_end_and_in_hidden_keys(page):
     dirty = B.KvCache(raw[0].view(torch.float8_e4m3fn), raw[1].view(torch.float8_e4m3fn), cache.k_scale, cache.v_scale)
     assert torch.equal(B.kda_attention_decode(q, dirty, table, lengths), clean)
     want = clean.clone()
-    # the fourth of six drafted tokens of sequence 0, and a token of sequence 3 that every row sees
+    # the fourth of seven drafted tokens of sequence 0, and a token of sequence 3 that every row sees
     for n, key, ch in ((0, lens[0] - L + 3, 9), (3, lens[3] - L - 20, 77)):
         raw[1][int(table[n, key // page]), 0, key % page, ch] = 0xFF
         first = max(0, key - (lens[n] - L))
@@ -283,8 +284,8 @@ def test_decode_many_rows_nan_past_the_end_and_in_hidden_keys(page):
 
 
 def test_decode_many_rows_reports_bad_lengths_and_pages():
-    page, d, L, hq = 16, 64, 5, 4
-    table, pool = tables([200, 200, 200], page)
+    page, d, L, hq = 16, 128, 7, 4
+    table, pool = tables([200, 200, 200], page, capacity=600)
     cache = filled(pool, 1, page, d, torch.float8_e4m3fn)
     q = make(3 * L, hq, 1, d, torch.bfloat16, 8)[0]
     ws = torch.zeros(1 << 25, dtype=torch.uint8, device=DEV)
@@ -307,7 +308,7 @@ def test_decode_many_rows_reports_bad_lengths_and_pages():
     close(out[2 * L:], want, ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
 
 
-@pytest.mark.parametrize("hq,window", [(2, 1), (8, 3)], ids=["few", "many"])
+@pytest.mark.parametrize("hq,window", [(2, 1), (8, 5)], ids=["few", "many"])
 @pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
 def test_decode_pages_without_scale(code, hq, window):
     """Pages whose values are zero, or whose keys are: their weight counts, their values add nothing."""
