@@ -7,13 +7,15 @@
 // that a group shares every K and V tile) and walks the keys of both.  Products are tcgen05.mma with
 // M = 128: Z from Q and K in shared memory, O += P V with P read from tensor memory and V taken
 // token-major as it lies in shared memory.  Tensor memory: Z0 | Z1 | O0 | O1 (128 columns each at 128
-// channels), P over the first half of its Z as packed bf16.
+// channels), P over the first half of its Z as packed bf16.  Up to 64 channels leave room for P0 | P1:
+// the next Z is then formed while the softmax is at work on the last one.
 //
 // The tensor cores are the bound: 4 x 128 x 128 x 128 multiply-adds per key tile and CTA, 2048 cycles
 // at 4096 a cycle, against 1024 cycles of exponentials (32 a cycle) and about 800 of issue.  So the
 // roles are split by warp and meet only at mbarriers: while one half's products run, the other
-// half's softmax does.  Warps 0-3 and 4-7 own the halves (a thread owns a row), warp 8 issues every
-// product, warp 9 every copy (TMA, 128-byte swizzle, a ring of K and V tiles), warps 10 and 11 look
+// half's softmax does.  Warps 0-3 and 4-7 own the halves (a thread owns a row), warps 8 and 11 issue
+// products, warp 9 schedules and issues every copy (TMA, 128-byte swizzle, a ring of K and V tiles),
+// warp 10 looks
 // after hidden infinities.
 //
 // The row maximum is taken over with a slack of 2^8: O is rescaled only when the maximum has grown
@@ -39,13 +41,16 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 384;
 // warpgroups' registers after the split: 256 x 208 + 128 x 88 = 384 x 168, what the launch holds
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
-constexpr int kInfoReaders = 8 + 3;  // softmax warps, products, copies, cleaner
 
 template <int D> struct Cfg {
     static constexpr int DP = D < 64 ? 64 : D;               // 32 channels are padded with zeros by the copies
     static constexpr int NB = DP / 64;                       // 64-channel blocks of a row
     static constexpr uint32_t BLK = 128 * 128;               // bytes of a block: 128 rows of 128 bytes
     static constexpr uint32_t TILE = NB * BLK;
+    // P has columns of its own where there is room, and the next scores' product need not wait for it
+    static constexpr bool APART = D < 128;
+    // product warps: one for each half where the products are short, else one for both (see there)
+    static constexpr int ISSUERS = D < 128 ? 2 : 1;
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
 };
@@ -60,9 +65,9 @@ struct TileInfo {
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], z_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], z_full[2], z_read[2], p_full[2], o_full[2], drained[2];
     uint64_t v_load[4], v_clean[4];  // V tiles with hidden keys, in turn: the ring holds at most four
-    uint64_t info_full[2], info_empty[2], answer_full, near_end;
+    uint64_t info_full[2], info_empty[2], answer_full;
     alignas(16) uint64_t answer[2];
     TileInfo info[2];
     uint32_t tmem, dead, dirty[2];
@@ -116,22 +121,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&sh.q_full[i], 1);
             tc::mbar_init(&sh.q_empty[i], 1);
             tc::mbar_init(&sh.z_full[i], 1);
+            tc::mbar_init(&sh.z_read[i], 4);
             tc::mbar_init(&sh.p_full[i], 4);
             tc::mbar_init(&sh.o_full[i], 1);
+            tc::mbar_init(&sh.drained[i], 1);
             tc::mbar_init(&sh.info_full[i], 1);
-            tc::mbar_init(&sh.info_empty[i], kInfoReaders);
+            tc::mbar_init(&sh.info_empty[i], 8 + C::ISSUERS + 1);  // softmax warps, products, cleaner
         }
         for (int i = 0; i < C::STAGES; ++i) {
             tc::mbar_init(&sh.kv_full[i], 1);
-            tc::mbar_init(&sh.kv_empty[i], 1);
+            tc::mbar_init(&sh.kv_empty[i], C::ISSUERS);
         }
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&sh.v_load[i], 1);
             tc::mbar_init(&sh.v_clean[i], 32);
         }
         tc::mbar_init(&sh.answer_full, 1);
-        tc::mbar_init(&sh.near_end, 1);
-        tc::mbar_init(&sh.drained, 1);
         sh.dead = 0u;
         sh.dirty[0] = sh.dirty[1] = 0xffffffffu;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -177,9 +182,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         Tile t;
         if (w == 9) {
-            // ---- copies: K0, Q, V0, K1, V1 ... through the ring, tile after tile
-            uint32_t it = 0, e = 0, qc[2] = {0, 0};
-            for (uint32_t turn = 0; next_tile(turn, t); ++turn) {
+            // ---- scheduler and copies.  This CTA's own tile, then tiles of CTAs that have not started yet: the
+            // next is asked for once a tile's last copy has been issued, so that tiles go to whoever is nearly
+            // free.  K0, Q, V0, K1, V1 ... through the ring, tile after tile.
+            uint32_t it = 0, e = 0, qc[2] = {0, 0}, asked = 0;
+            int idx = blockIdx.x;
+            auto take = [&]() {
+                int x = -1;
+                if (lane == 0 && *dead == 0u) x = take_tile(sh.answer, &sh.answer_full, asked);
+                ++asked;
+                return __shfl_sync(0xffffffffu, x, 0);
+            };
+            for (uint32_t turn = 0;; ++turn, idx = take()) {
+                TileInfo f{};
+                for (;;) {
+                    AttnTile x;
+                    if (idx < 0) break;
+                    // the longest rows of every sequence first
+                    if (attn_tile(a, slots - 1 - idx / a.Hkv, 2 * tpt, x)) {
+                        f = TileInfo{x.start, x.first, x.last, idx % a.Hkv, 1};
+                        break;
+                    }
+                    idx = take();
+                }
+                if (!warp_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u)) *dead = 1u;
+                if (__any_sync(0xffffffffu, *dead != 0u)) f.valid = 0;
+                if (lane == 0) {
+                    sh.info[turn & 1] = f;
+                    tc::mbar_arrive(&sh.info_full[turn & 1]);
+                }
+                if (!f.valid) break;
+                if (!next_tile(turn, t)) break;  // what the others see
                 bool ok = true;
                 if (lane == 0) {
                     for (int x = 0; x < 2 * t.n && ok; ++x, ++it) {
@@ -212,11 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (int)(t.start + (x >> 1) * kKeys), bar);
                     }
                 }
-                done_tile(turn);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    *dead = 1u;
-                    break;
-                }
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, ok)) *dead = 1u;  // the next round publishes the end
             }
             // after a wait that gave up, what was issued still lands before the CTA ends
             if (lane == 0 && *dead) {
@@ -226,11 +256,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (void)tc::mbar_wait(&sh.kv_full[i % C::STAGES], (i / C::STAGES) & 1u, kTries);
                 for (uint32_t i = e > 4 ? e - 4 : 0; i < e; ++i) (void)tc::mbar_wait(&sh.v_load[i & 3], (i >> 2) & 1u, kTries);
             }
-        } else if (w == 8) {
-            // ---- products, in the order Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ... tile after tile
+        } else if (w == 8 || (w == 11 && C::ISSUERS == 2)) {
+            // ---- products, in the order Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ... tile after tile; P apart:
+            // Z(0) | Z(1) O(0) | Z(2) O(1) ... by a warp for each half.  (With 64 channels one warp's waits and
+            // issues for both halves took longer than the products: 16384 tokens x 8 heads 261 us by one,
+            // 236 by two; with 128 the fixed order is better: 2 x 8192, 16 of 4 heads 335 and 340.)
+            constexpr int PER = 2 / C::ISSUERS;
+            const int first_half = w == 8 ? 0 : 1;
             const uint32_t id_z = tc::idesc_bf16(128, kKeys), id_o = tc::idesc_bf16(128, C::DP) | (1u << 16);
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
-            uint32_t base = 0, e = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+            uint32_t base = 0, e = 0, qc[PER] = {}, pc[PER] = {}, rc[PER] = {};
             bool ok = true;
             auto full = [&](uint32_t it) { return warp_wait(&sh.kv_full[it % C::STAGES], (it / C::STAGES) & 1u); };
             auto issue_z = [&](int hf, uint32_t it) {
@@ -246,55 +281,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t v = ra + (it % C::STAGES) * C::TILE;
 #pragma unroll
                 for (int s = 0; s < kKeys / 16; ++s)
-                    mma_ts(tm + 256 + C::DP * hf, tm + 128 * hf + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u), id_o,
+                    mma_ts(tm + 256 + C::DP * hf, (C::APART ? tm + 384 + 64 * hf : tm + 128 * hf) + 8 * s, desc_v(v + s * 2048, D == 128 ? C::BLK : 1024u), id_o,
                            !first || s > 0);
             };
+            // a slot is given back only after its copy was seen, also by a half that has no use for it
+            auto release = [&](uint32_t it) { commit(&sh.kv_empty[it % C::STAGES]); };
             for (uint32_t turn = 0; ok && next_tile(turn, t); ++turn) {
+                int nh[PER];
+#pragma unroll
+                for (int u = 0; u < PER; ++u) nh[u] = first_half + u ? t.n1 : t.n0;
                 ok = full(base);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (!ok || (hf == 1 && t.n1 == 0)) continue;
-                    ok = warp_wait(&sh.q_full[hf], qc[hf]++ & 1u);
+                for (int u = 0; u < PER; ++u) {
+                    const int hf = first_half + u;
+                    if (!ok || nh[u] == 0) continue;
+                    ok = warp_wait(&sh.q_full[hf], qc[u]++ & 1u);
                     if (!ok) continue;
                     issue_z(hf, base);
-                    if ((hf ? t.n1 : t.n0) == 1) commit(&sh.q_empty[hf]);
+                    if (nh[u] == 1) commit(&sh.q_empty[hf]);
                 }
-                if (ok) commit(&sh.kv_empty[base % C::STAGES]);
+                if (ok) release(base);
                 for (int j = 0; j < t.n && ok; ++j) {
                     const uint32_t iv = base + 2 * j + 1;
-                    if (j == max(0, t.n - 2) && lane == 0) tc::mbar_arrive(&sh.near_end);
-                    ok = full(iv) && !__any_sync(0xffffffffu, *dead != 0u);
-                    if (ok && j + 1 < t.n) ok = full(iv + 1);
-                    if (ok && j >= t.edge) {
-                        ok = warp_wait(&sh.v_clean[e & 3], (e >> 2) & 1u);
+                    const bool more = j + 1 < t.n;
+                    ok = !__any_sync(0xffffffffu, *dead != 0u) && (!more || full(iv + 1));
+                    if constexpr (C::APART) {
+                        // the next scores, as soon as the last ones have been read
+#pragma unroll
+                        for (int u = 0; u < PER; ++u) {
+                            const int hf = first_half + u;
+                            if (!ok || j >= nh[u]) continue;
+                            ok = warp_wait(&sh.z_read[hf], rc[u]++ & 1u);
+                            if (!ok || j + 1 >= nh[u]) continue;
+                            tc::fence_after_sync();
+                            issue_z(hf, iv + 1);
+                            if (j + 2 == nh[u]) commit(&sh.q_empty[hf]);
+                        }
+                        if (ok && more) release(iv + 1);
+                    }
+                    ok = ok && full(iv);
+                    if (j >= t.edge) {
+                        if (ok && (j < nh[0] || j < nh[PER - 1])) ok = warp_wait(&sh.v_clean[e & 3], (e >> 2) & 1u);
                         ++e;
                     }
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int nh = hf ? t.n1 : t.n0;
-                        if (!ok || j >= nh) continue;
-                        ok = warp_wait(&sh.p_full[hf], pc[hf]++ & 1u);
+                    for (int u = 0; u < PER; ++u) {
+                        const int hf = first_half + u;
+                        if (!ok || j >= nh[u]) continue;
+                        ok = warp_wait(&sh.p_full[hf], pc[u]++ & 1u);
                         if (!ok) continue;
                         tc::fence_after_sync();
                         issue_o(hf, iv, j == 0);
-                        if (j + 1 < nh) {
+                        if (C::APART) {
+                            commit(&sh.o_full[hf]);
+                        } else if (j + 1 < nh[u]) {
                             issue_z(hf, iv + 1);  // its commit also covers O's product
-                            if (j + 2 == nh) commit(&sh.q_empty[hf]);
+                            if (j + 2 == nh[u]) commit(&sh.q_empty[hf]);
                         } else {
                             commit(&sh.o_full[hf]);
                         }
                     }
                     if (!ok) break;
-                    commit(&sh.kv_empty[iv % C::STAGES]);
-                    if (j + 1 < t.n) commit(&sh.kv_empty[(iv + 1) % C::STAGES]);
+                    release(iv);
+                    if (!C::APART && more) release(iv + 1);
                 }
                 base += 2 * t.n;
                 done_tile(turn);
             }
             if (!ok || *dead != 0u) {
                 *dead = 1u;
-                commit(&sh.drained);  // products in flight end before tensor memory is given back
-                (void)warp_wait(&sh.drained, 0);
+                commit(&sh.drained[first_half]);  // products in flight end before tensor memory is given back
+                (void)warp_wait(&sh.drained[first_half], 0);
             }
         } else if (w == 10) {
             // ---- V tiles with hidden keys: infinities and NaN leave the tile
@@ -346,39 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
             }
-        } else {
-            // ---- scheduler: this CTA's own tile, then tiles of CTAs that have not started yet
-            uint32_t asked = 0;
-            int idx = blockIdx.x;
-            auto take = [&]() {
-                int x = -1;
-                if (lane == 0 && *dead == 0u) x = take_tile(sh.answer, &sh.answer_full, asked);
-                ++asked;
-                return __shfl_sync(0xffffffffu, x, 0);
-            };
-            for (uint32_t turn = 0;; ++turn) {
-                TileInfo f{};
-                for (;;) {
-                    AttnTile x;
-                    if (idx < 0) break;
-                    // the longest rows of every sequence first
-                    if (attn_tile(a, slots - 1 - idx / a.Hkv, 2 * tpt, x)) {
-                        f = TileInfo{x.start, x.first, x.last, idx % a.Hkv, 1};
-                        break;
-                    }
-                    idx = take();
-                }
-                if (!warp_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u)) *dead = 1u;
-                if (__any_sync(0xffffffffu, *dead != 0u)) f.valid = 0;
-                if (lane == 0) {
-                    sh.info[turn & 1] = f;
-                    tc::mbar_arrive(&sh.info_full[turn & 1]);
-                }
-                if (!f.valid) break;
-                // not before the tile is nearly done, so that tiles go to whoever is free
-                if (!warp_wait(&sh.near_end, turn & 1u)) *dead = 1u;
-                idx = take();
-            }
         }
         __syncwarp();
     } else {
@@ -387,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hf = w >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
         const uint32_t zt = tm + 128 * hf + lanes, ot = tm + 256 + C::DP * hf + lanes;
+        const uint32_t pt = C::APART ? tm + 384 + 64 * hf + lanes : zt;
         const float cs = a.scale * 1.4426950408889634f;
         const int rt = r / a.group, rh = r - rt * a.group;
         const int wt = (32 * (w & 3)) / a.group;
@@ -407,6 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
                 tc::tmem_wait_ld();
+                if (C::APART) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sh.z_read[hf]);
+                }
                 if (j * kKeys + kKeys - 1 > first + wt) {
                     const int seen = tok + 1 - j * kKeys;
 #pragma unroll
@@ -428,8 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alpha = ex2(m - top);
                     m = top;
                 }
+                if (C::APART && j > 0) {  // the last P has been read, and O holds its product
+                    gone = !warp_wait(&sh.o_full[hf], oc++ & 1u);
+                    if (gone) break;
+                    tc::fence_after_sync();
+                }
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // the products into O up to here ended with the scores that were waited for
+                    // (the products into O up to here have ended: with the scores that were waited for, or see above)
                     l2 = __fmul2_rn(l2, make_float2(alpha, alpha));
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -454,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[i & 1] = __fadd2_rn(sum[i & 1], y);
                         p[i] = tc::pack_bf16(y.x, y.y);
                     }
-                    tmem_st32(zt + 32 * q, p);
+                    tmem_st32(pt + 32 * q, p);
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
