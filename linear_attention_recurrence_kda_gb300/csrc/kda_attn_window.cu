@@ -11,13 +11,14 @@
 // is idle, a key's scales are the thread's own, and no score crosses lanes but at a change of the
 // reference.  Few columns make the products cheap (about 128 cycles each a block).
 //
-// A block then takes about 2000 cycles, of which shared memory's bandwidth accounts for 1700 (the codes in
-// and out once, 64 KB of f16 written and read by the products, P), where HBM would give one every 1400.
+// What bounds it: of an SM's cycles at work, loads and stores keep the path to shared memory busy 51 %, the
+// products' reads 23 %; a unit's start and end cost as much as 5 blocks (64 sequences of 300 to 6000 keys, 28
+// rows of 8 heads: 131 us, 3.2 TB/s, where HBM would allow 62).
 //
 // Blocks alternate between two streams, each with its own reference, sums and O, so that one's softmax
 // runs while the other waits; at the end of a unit the first stream joins them.  Tensor memory: Z0 | Z1 |
-// O0 | O1, 32 columns each; P goes through shared memory.  All units' blocks form one line that is cut
-// evenly among the CTAs; pieces of a unit are joined by the join kernel.
+// O0 | O1, 32 columns each; P goes through shared memory.  All units' blocks, with a gap before each unit for
+// what its start costs, form one line that is cut evenly among the CTAs; pieces of a unit are joined by the join kernel.
 //
 // Warps 0-3 and 4-7: softmax of the streams, 8: products, 9: copies and scales, 10-15: conversion.  A
 // tile's rows of q enter scaled by one power of two that brings the largest value to [2^14, 2^15) (bf16
@@ -39,6 +40,11 @@ constexpr int kThreads = 512;
 constexpr int kConvert = 192;
 constexpr int kRaw = 4;    // raw tiles (K and V in turn) on their way or waiting
 constexpr int kGroups = kBlk / 16;
+// What a unit's start and end cost (q, the first references, the streams' join), in blocks.  Cut by blocks alone,
+// the CTAs that hold short sequences end last: SMs were at work 70 % of the time, now 92 %.  28 rows of 8 heads,
+// us for a cost of 0, 3, 5, 10: 64 sequences of 300 to 6000 keys 176, 139, 133, 138; 200 of 100 to 900
+// 194, 134, 130, 137; 256 of 256 to 600 170, 157, 156, 159; 64 of 3150 132, 130, 131, 132.
+constexpr int kUnitCost = 5;
 // warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,6 +74,7 @@ struct Shared {
     float weight[2][kRows];      // the streams' weights in a row's result
     unsigned long long odd[4][128];  // by the segment's turn: the first key with a NaN in a channel (see odd_note)
     Cursor begin;                // this CTA's first block
+    int left;                    // and its part of the line from there on
 };
 
 // A run of a unit's blocks.
@@ -79,7 +86,8 @@ struct Segment {
 // the segments of a worker, one after the other
 struct Walk {
     Cursor c;
-    int left;
+    int left;  // of the line, from block c on
+    int gap;   // of the line before a unit's first block
     __device__ __forceinline__ bool next(const AttnDecodeArgs& a, int row_tiles, Segment& s)
     {
         if (left <= 0) return false;
@@ -87,7 +95,7 @@ struct Walk {
         s.count = min(left, c.tiles - c.i);
         s.begun = c.i == 0;
         s.ended = c.i + s.count == c.tiles;
-        left -= s.count;
+        left -= s.count + gap;
         if (left > 0) {
             c.i = c.tiles - 1;
             next_tile<kBlk>(a, row_tiles, c);
@@ -194,14 +202,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = tid; i < 4 * 128; i += kThreads) (&sh.odd[0][0])[i] = ~0ull;
     if (w == 8) tc::tmem_alloc(&sh.tmem, 128);
-    // blocks before every run of `chunk` sequences
+    // The line that is cut evenly: each unit takes a place for every block, after a gap for what its start and
+    // end cost (where there are fewer units than CTAs, every piece has a start: no gap).
+    const int gap = by_unit ? 0 : kUnitCost;
+    auto places_of = [&](int tiles) { return tiles > 0 ? tiles + gap : 0; };
+    // places before every run of `chunk` sequences
     const int chunk = (a.N + kThreads - 1) / kThreads;
     {
         int64_t sum = 0;
         bool bad = false;
         for (int i = 0; i < chunk; ++i) {
             const int n = tid * chunk + i;
-            if (n < a.N) sum += tiles_of<kBlk>(length_of(a, n, &bad));
+            if (n < a.N) sum += places_of(tiles_of<kBlk>(length_of(a, n, &bad)));
         }
         int64_t x = sum;
 #pragma unroll
@@ -240,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk;
     auto start = [&]() {  // at this CTA's first block: a run of sequences by bisection, then one by one
         walk.left = (int)(b1 - b0);
+        walk.gap = gap;
         walk.c = Cursor{0, 0, 0, 0, 1, 0};
         if (walk.left <= 0) return;
         int lo = 0, hi = kThreads - 1;
@@ -254,18 +267,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (;;) {
             c.len = length_of(a, c.n);
             c.tiles = tiles_of<kBlk>(c.len);
-            const int64_t here = c.tiles * per_block;
+            const int64_t here = places_of(c.tiles) * per_block;
             if (at + here > b0 || c.n + 1 >= a.N) break;
             at += here;
             ++c.n;
         }
-        const int64_t rest = b0 - at, unit = rest / c.tiles;
-        c.i = (int)(rest - unit * c.tiles);
+        const int64_t rest = b0 - at, unit = rest / places_of(c.tiles);
+        const int place = (int)(rest - unit * places_of(c.tiles));
+        c.i = max(0, place - gap);
+        walk.left -= max(0, gap - place);
         c.h = (int)(unit / row_tiles);
         c.rt = (int)(unit - (int64_t)c.h * row_tiles);
     };
     start();
-    if (tid == 0) sh.begin = walk.c;
+    if (tid == 0) {
+        sh.begin = walk.c;
+        sh.left = walk.left;
+    }
     tc::fence_async_smem();  // the copies take over where the prefix was
     __syncthreads();
     Segment s;
@@ -689,9 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // what this worker leaves to be joined: the unit that it began and did not end
         Record mine{-1, 0, 0, 0, 0};
         const bool failed = sh.dead != 0u;
-        walk.left = (int)(b1 - b0);
+        walk.left = sh.left;
+        walk.gap = gap;
         walk.c = sh.begin;
-        int64_t pos = b0;
+        int64_t pos = b1 - sh.left;
         while (walk.next(a, row_tiles, s)) {
             if (s.begun) {
                 Record rec{-1, 0, 0, 0, 0};
@@ -702,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (by_unit) records[unit_of(s)] = rec;
             }
-            pos += s.count;
+            pos += s.count + gap;
         }
         if (!by_unit) records[blockIdx.x] = mine;
         reinterpret_cast<uint32_t*>(a.ws + L.flags)[blockIdx.x] = sh.flag | (failed ? kCheckTimeout : 0u);
