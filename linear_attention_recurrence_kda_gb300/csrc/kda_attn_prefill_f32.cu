@@ -7,8 +7,10 @@
 // A tile holds 64 rows (128 for groups of more than 64 heads): the query heads of one key head's group
 // times 64 / group tokens, so that a group's heads share every K and V tile and the diagonal wastes
 // little.  Warps take 16 rows each; keys come in tiles of half as many.  Two CTAs share an SM: with
-// 128 rows and one CTA the longest rows of a few prompts set the time (prompts of 200, 750 and 1300
-// tokens, 10 of 2 heads of 128 channels: 195 us against 169).  An fp32 operand x enters m16n8k16 bf16 products as x1 + x2 + x3 with
+// 128 rows and one CTA the longest rows of a few prompts set the time (prompts of 200 to 1300
+// tokens, 10 of 2 heads of 128 channels, one CTA a tile: 208 us against 196).  With few tiles two CTAs of a cluster take
+// a tile's key tiles in turn and join their sums through each other's shared memory (152 us; see launch_d).
+// An fp32 operand x enters m16n8k16 bf16 products as x1 + x2 + x3 with
 // x1 = bf16(x), x2 = bf16(x - x1), x3 = bf16(x - x1 - x2) (24 bits, fp32's range), a product as its six
 // terms down to 2^-16 of the first.  Those products bound it: at 128 channels 12 a warp and key,
 // about 8 cycles each on a sub-partition that two warps share; a tile's loads overlap with the products of
@@ -99,9 +101,29 @@ struct Vec8 {
     }
 };
 
+// an address in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank)
+{
+    uint32_t y;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(tc::smem_u32(p)), "r"(rank));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t load_rank(uint32_t addr)
+{
+    uint32_t y;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(addr) : "memory");
+    return y;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 }  // namespace
 
-template <int D, int ROWS>
+template <int D, int ROWS, int KS>
 __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_kernel(const AttnArgs a, const int slots)
 {
     constexpr int kRowsTile = ROWS, kKeys = ROWS / 2, kThreads = 2 * ROWS;
@@ -116,9 +138,10 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
     const int tpt = kRowsTile / a.group;
     // the longest rows of every sequence first
-    const int h = blockIdx.x % a.Hkv;
+    const int rank = blockIdx.x % KS, place = blockIdx.x / KS;
+    const int h = place % a.Hkv;
     AttnTile t;
-    if (!attn_tile(a, slots - 1 - (int)(blockIdx.x / a.Hkv), tpt, t)) return;
+    if (!attn_tile(a, slots - 1 - place / a.Hkv, tpt, t)) return;  // the whole cluster
     for (int i = tid; i < 3 * D; i += kThreads) (&odd[0][0])[i] = 0x7fffffff;
 
     // rows of q: row r is token t.first + r / group, query head h group + r % group
@@ -145,7 +168,8 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
             vx[e].load(static_cast<const float*>(a.v) + (t.start + k0 + r) * a.vs + (int64_t)h * D + c * 8, ok);
         }
     };
-    if (kAhead) load(0);
+    constexpr int kStep = KS * kKeys;  // the cluster's CTAs take key tiles in turn
+    if (kAhead) load(rank * kKeys);
 
     float O[D / 8][4];
 #pragma unroll
@@ -159,7 +183,7 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     const int warp_last = t.first + (16 * w + 15) / a.group;
     const bool warp_on = 16 * w < rows;
 
-    for (int k0 = 0; k0 < t.last; k0 += kKeys) {
+    for (int k0 = rank * kKeys; k0 < t.last; k0 += kStep) {
         __syncthreads();
         if (!kAhead) load(k0);
 #pragma unroll
@@ -176,7 +200,7 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
             }
             vx[e].store(sv + tile_off<D>(r, c), KB);
         }
-        if (kAhead && k0 + kKeys < t.last) load(k0 + kKeys);
+        if (kAhead && k0 + kStep < t.last) load(k0 + kStep);
         __syncthreads();
         if (!warp_on || k0 > warp_last) continue;
 
@@ -311,20 +335,76 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    int c0 = 0;                                       // this CTA writes chunks of 8 channels from here on
+    const int(*odds)[D] = odd;
+    if constexpr (KS > 1) {
+        // The CTAs' sums, maxima and outputs lie in their shared memory, element-major; each CTA joins its share of the
+        // channels, in the order of the ranks.
+        __shared__ int odd_all[3][D];
+        float* so = reinterpret_cast<float*>(sq);          // [D / 8][4][threads]
+        float* st = so + D / 2 * kThreads;                 // m0, m1, l0, l1 [threads]
+        static_assert((D / 2 + 4) * kThreads * 4 <= PL * 2 * (int)QB, "the sums fit where the tiles were");
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) so[(4 * c + i) * kThreads + tid] = O[c][i];
+        st[tid] = m0;
+        st[kThreads + tid] = m1;
+        st[2 * kThreads + tid] = l0;
+        st[3 * kThreads + tid] = l1;
+        cluster_sync();
+        float n0 = m0, n1 = m1, a0[KS], a1[KS];
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+            a0[x] = __uint_as_float(load_rank(at_rank(st + tid, x)));
+            a1[x] = __uint_as_float(load_rank(at_rank(st + kThreads + tid, x)));
+            n0 = fmaxf(n0, a0[x]);
+            n1 = fmaxf(n1, a1[x]);
+        }
+        if (n0 == -INFINITY) n0 = 0.f;
+        if (n1 == -INFINITY) n1 = 0.f;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+            a0[x] = ex2(a0[x] - n0);
+            a1[x] = ex2(a1[x] - n1);
+            l0 = fmaf(__uint_as_float(load_rank(at_rank(st + 2 * kThreads + tid, x))), a0[x], l0);
+            l1 = fmaf(__uint_as_float(load_rank(at_rank(st + 3 * kThreads + tid, x))), a1[x], l1);
+        }
+        c0 = rank * (D / 8 / KS);
+#pragma unroll
+        for (int c = 0; c < D / 8 / KS; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < KS; ++x)
+                    sum = fmaf(__uint_as_float(load_rank(at_rank(so + (4 * (c0 + c) + i) * kThreads + tid, x))), i < 2 ? a0[x] : a1[x], sum);
+                O[c][i] = sum;
+            }
+        for (int i = tid; i < 3 * D; i += kThreads) {
+            int first = 0x7fffffff;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) first = min(first, (int)load_rank(at_rank(&odd[0][0] + i, x)));
+            (&odd_all[0][0])[i] = first;
+        }
+        odds = odd_all;
+        cluster_sync();  // nobody's shared memory is read any more, and odd_all is complete
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int r = r0 + 8 * u;
         if (r >= rows) continue;
         const int tok = u ? tok1 : tok0;
         const float inv = 1.f / (u ? l1 : l0);
-        float* o = static_cast<float*>(a.out) + ((t.start + tok) * a.Hq + h * a.group + r % a.group) * D + 2 * cq;
+        float* o = static_cast<float*>(a.out) + ((t.start + tok) * a.Hq + h * a.group + r % a.group) * D + 8 * c0 + 2 * cq;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 8 / KS; ++c) {
             float x[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int ch = 8 * c + 2 * cq + e;
-                x[e] = attn_odd(O[c][2 * u + e] * inv, tok, odd[0][ch], odd[1][ch], odd[2][ch]);
+                const int ch = 8 * (c0 + c) + 2 * cq + e;
+                x[e] = attn_odd(O[c][2 * u + e] * inv, tok, odds[0][ch], odds[1][ch], odds[2][ch]);
             }
             *reinterpret_cast<float2*>(o + 8 * c) = make_float2(x[0], x[1]);
         }
@@ -333,24 +413,41 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
 
 namespace {
 
-template <int D, int ROWS>
+template <int D, int ROWS, int KS>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s)
 {
     constexpr int smem = PL * 2 * ROWS * D * 2 + 128;  // q, and K and V of half as many rows
     static_assert(128 / ROWS * (smem + 4096) <= 233472, "the tiles of an SM's CTAs fit");
-    auto kern = kda_attn_prefill_f32_kernel<D, ROWS>;
+    auto kern = kda_attn_prefill_f32_kernel<D, ROWS, KS>;
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a, ROWS / a.group);
-    kern<<<(unsigned)(slots * a.Hkv), 2 * ROWS, smem, s>>>(a, (int)slots);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = KS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(slots * a.Hkv * KS));
+    cfg.blockDim = dim3(2 * ROWS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, (int)slots);
 }
 
+// Up to three tiles an SM, two CTAs share a tile's keys: the longest tiles alone then set the time.  One and two
+// CTAs a tile, 16 of 4 heads of 128 channels unless said, us: a prompt of 1200 tokens (304 tiles) 184 and 124; prompts
+// of 200 to 1300, 10 of 2 heads (380 tiles) 183 and 152; one of 1800 (452 tiles) 281 and 278; of 2400 (604) 430 and
+// 450; 8 of 1000 to 4000 4218 and 4516.  Four CTAs: 174 where two take 152.
 template <int D>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 {
-    return a.group <= 64 ? launch_rows<D, 64>(a, s) : launch_rows<D, 128>(a, s);
+    if (a.group > 64) return launch_rows<D, 128, 1>(a, s);
+    const bool split = attn_slots(a, 64 / a.group) * a.Hkv <= 3 * (int64_t)sm_count_of_current_device();
+    return split ? launch_rows<D, 64, 2>(a, s) : launch_rows<D, 64, 1>(a, s);
 }
 
 }  // namespace

@@ -755,9 +755,9 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 }  // namespace
 
 // From 25 rows a key head, where the page table holds more than 512 keys a sequence.  Measured here and on
-// the warp-level form, us: 28 rows of 8 heads, 64 sequences of 3150 keys 131 and 194; 56 rows 231 and 365; one
-// sequence of 4000, one head 16.5 and 20.6; but 20 rows of one head, 64 of 1000 24.9 and 22.7; and 28 rows of
-// 8 heads, 256 of 300 140 and 117, where a unit's start and end outweigh its keys.
+// the warp-level form, us: 28 rows of 8 heads, 64 sequences of 3150 keys 131 and 191; 56 rows 248 and 369; one
+// sequence of 4000, one head 13.5 and 14.8; but 20 rows of one head, 64 of 1000 23.9 and 20.7; and 28 rows of
+// 8 heads, 256 of 300 133 and 115, where a unit's start and end outweigh its keys (of 500: 152 and 152, of 700 185 and 192).
 bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt, int64_t capacity)
 {
     return dt == KDA_BF16 && d == D && rows > 24 && capacity > 512;

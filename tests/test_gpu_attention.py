@@ -92,6 +92,24 @@ def test_prefill_hidden_infinities_and_nans_stay_hidden(d, dtype):
     assert torch.isfinite(col[:20]).all() and (col[20:60] == float("inf")).all() and col[60:].isnan().all()
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_fp32_many_tiles(d):
+    """More tiles than the form for few of them takes: one CTA a tile."""
+    lens = [5, 70, 0, 33, 131] * 36
+    q, k, v = make(sum(lens), 4, 4, d, torch.float32, 11 + d, fused=True)
+    out = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens))
+    close(out, ref.prefill(q, k, v, lens), v, torch.float32, 0.0)
+    # infinities of both signs in one channel, in different key tiles: NaN to the rows that see both, the first alone before
+    start = sum(lens[:4])
+    v2 = v.clone()
+    v2[start + 9, 0, 1], v2[start + 77, 0, 1] = float("inf"), -float("inf")
+    bad = B.kda_attention_prefill(q, k, v2, cu_seqlens=offsets(lens))
+    want = out.clone()
+    want[start + 9:start + 77, 0, 1], want[start + 77:start + 131, 0, 1] = float("inf"), float("nan")
+    same = (bad == want) | (bad.isnan() & want.isnan())
+    assert bool(same.all()), [tuple(i) for i in (~same).nonzero()[:4].tolist()]
+
+
 def test_prefill_large_scores():
     """Scores of a few thousand: one key takes all the weight, nothing overflows."""
     q, k, v = make(400, 2, 2, 128, torch.bfloat16, 5)
@@ -231,7 +249,7 @@ def test_decode(lens, hq, hkv, window, page, d, code, dtype):
 
 
 MANY = [
-    # lens, query heads, key heads, window: 17 rows and more a key head, up to several tiles of 128
+    # lens, query heads, key heads, window: 17 rows and more a key head, up to several tiles of 32 rows
     ([1], 17, 1, 1), ([1], 25, 1, 1), ([0, 5, 127, 128, 129, 256], 8, 1, 4), ([3, 700], 16, 2, 7), ([1000, 64, 333], 24, 3, 5),
     ([90, 400], 8, 1, 40), ([1300], 128, 1, 2), ([17] * 300, 26, 1, 1), ([3000, 2900] * 20, 8, 2, 7), ([5], 4, 1, 30),
 ]
@@ -255,6 +273,22 @@ def test_decode_many_rows(lens, hq, hkv, window, page, d, code):
     n = len(lens) - 1  # the last sequence alone
     alone = B.kda_attention_decode(q[n * window:], cache, table[n:], torch.tensor(lens[n:], dtype=torch.int32, device=DEV))
     close(out[n * window:], alone.double().cpu(), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("lens,hq,hkv,window", [
+    ([0, 1, 700, 129, 40, 1500] * 30, 13, 1, 2), ([2000] + [9] * 160, 4, 1, 7), ([30, 0] * 90 + [1900], 26, 1, 1),
+    ([400, 128, 0, 257] * 12, 10, 5, 14),
+], ids=["mixed", "long_first", "long_last", "several_row_tiles"])
+def test_decode_many_rows_mixed_lengths(lens, hq, hkv, window, code):
+    """More units than CTAs, short and long: the cut counts what a unit's start costs."""
+    table, pool = tables(lens, 32, capacity=2048)
+    cache = filled(pool, hkv, 32, 128, code, seed=5)
+    q = make(len(lens) * window, hq, 1, 128, torch.bfloat16, 3, fused=True)[0]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+    out = B.kda_attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), workspace=ws)
+    close(out, ref.decode(q, cache, table, lens), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+    assert B.kda_workspace_status(ws) == B.KDA_OK
 
 
 @pytest.mark.parametrize("page", [16, 64])
