@@ -3,8 +3,8 @@
 //
 // A unit is one sequence, one key head and up to 8 NT rows (query heads of the group x tokens of the
 // window); its keys come in tiles of 32.  The work is cut evenly: with W workers (warps) and all
-// units' tiles in one line, worker w takes tiles [w total / W, (w + 1) total / W), whatever the
-// lengths are.  A worker that holds all of a unit writes its output; otherwise it leaves (max, sum,
+// units' tiles in one line, each unit's after a gap for what its start costs, worker w takes the tiles at
+// places [w total / W, (w + 1) total / W), whatever the lengths are.  A worker that holds all of a unit writes its output; otherwise it leaves (max, sum,
 // unnormalised output) in the workspace, and the combine kernel joins the pieces in order.
 //
 // Per tile a warp does, with m16n8k16 f16 products and fp32 accumulators,
@@ -34,6 +34,10 @@ namespace {
 constexpr int kTile = 32;     // keys per tile
 constexpr int kWarps = 4;     // workers per CTA
 constexpr int kThreads = kWarps * 32;
+// What a unit's start and end cost, in tiles.  Cut by tiles alone, the workers that hold short sequences end last.
+// One token, 32 of 8 heads, us for a cost of 0, 2, 4, 8: 300 sequences of 20 to 900 keys 75, 61, 63, 65; 1000 of 10 to
+// 300 102, 72, 75, 81; 256 of 512 to 576 60, 60, 60, 60.
+constexpr int kUnitCost = 2;
 constexpr uint32_t kCopyTries = 1u << 17;  // of up to 20 us each
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -111,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
     constexpr int S = stages_of(NT, D);
     constexpr uint32_t TB = kTile * D;         // bytes of a K (or V) tile
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int64_t prefix[kThreads + 1];
+    __shared__ int64_t prefix[kThreads + 1];  // places, and
+    __shared__ int seqs[kThreads + 1];        // sequences that hold keys, before every run of sequences
     __shared__ alignas(8) uint64_t full[kWarps][S];
     __shared__ int pages[kWarps][S][2];
     __shared__ uint32_t flag;
@@ -131,29 +136,49 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
         for (int i = 0; i < S; ++i) tc::mbar_init(&full[w][i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // tiles before every run of `chunk` sequences
+    // The line that is cut evenly: each unit takes a place for every tile, after a gap for what its start and end
+    // cost (where there are fewer units than workers, every piece has a start: no gap).
+    const int gap = by_unit ? 0 : kUnitCost;
+    auto places_of = [&](int tiles) { return tiles > 0 ? tiles + gap : 0; };
     const int chunk = (a.N + kThreads - 1) / kThreads;
     {
         int64_t sum = 0;
+        int some = 0;
         bool bad = false;
         for (int i = 0; i < chunk; ++i) {
             const int n = tid * chunk + i;
-            if (n < a.N) sum += tiles_of<kTile>(length_of(a, n, &bad));
+            const int tiles = n < a.N ? tiles_of<kTile>(length_of(a, n, &bad)) : 0;
+            sum += places_of(tiles);
+            some += tiles > 0;
         }
         int64_t x = sum;
+        int y = some;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+            const int64_t ux = __shfl_up_sync(0xffffffffu, x, off);
+            const int uy = __shfl_up_sync(0xffffffffu, y, off);
+            if (lane >= off) {
+                x += ux;
+                y += uy;
+            }
         }
         prefix[tid + 1] = x;
-        if (tid == 0) prefix[0] = 0;
+        seqs[tid + 1] = y;
+        if (tid == 0) {
+            prefix[0] = 0;
+            seqs[0] = 0;
+        }
         __syncthreads();
         if (bad) atomicOr(&flag, kCheckBadSeqlens);
         int64_t before = 0;
-        for (int i = 0; i < w; ++i) before += prefix[(i + 1) * 32];
+        int some_before = 0;
+        for (int i = 0; i < w; ++i) {
+            before += prefix[(i + 1) * 32];
+            some_before += seqs[(i + 1) * 32];
+        }
         __syncthreads();
         prefix[tid + 1] = x + before;
+        seqs[tid + 1] = y + some_before;
         __syncthreads();
     }
     // a sequence with nothing in the cache: rows of zeros
@@ -173,35 +198,51 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
     float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
     float* po = reinterpret_cast<float*>(a.ws + L.o);
     Record mine{-1, 0, 0, 0, 0};
+    Cursor cc;
+    int64_t b1 = 0;
+    int count = 0;
     if (worker < W) {
-        const int64_t b0 = worker * total / W, b1 = (worker + 1) * total / W;
-        // the unit that holds tile b0: a run of sequences by bisection, then one by one
-        Cursor cc;
-        {
-            int lo = 0, hi = kThreads - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (prefix[mid] * per_tile <= b0) lo = mid;
-                else hi = mid - 1;
-            }
-            int64_t at = prefix[lo] * per_tile;
-            cc.n = lo * chunk;
-            for (;;) {
-                cc.len = length_of(a, cc.n);
-                cc.tiles = tiles_of<kTile>(cc.len);
-                const int64_t here = cc.tiles * per_tile;
-                if (at + here > b0 || cc.n + 1 >= a.N) break;
-                at += here;
-                ++cc.n;
-            }
-            const int64_t rest = b0 - at;
-            const int64_t unit = rest / cc.tiles;
-            cc.i = (int)(rest - unit * cc.tiles);
-            cc.h = (int)(unit / row_tiles);
-            cc.rt = (int)(unit - (int64_t)cc.h * row_tiles);
+        const int64_t b0 = worker * total / W;
+        b1 = (worker + 1) * total / W;
+        // The first tile at or after a place, and the tiles before it: a run of sequences by bisection, then one
+        // by one.  Lane 1 looks for the worker's end, the others for its start.
+        const int64_t at_end = total - (int64_t)gap * seqs[kThreads] * per_tile;
+        const int64_t b = lane == 1 && b1 < total ? b1 : b0;
+        int lo = 0, hi = kThreads - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] * per_tile <= b) lo = mid;
+            else hi = mid - 1;
         }
+        int64_t at = prefix[lo] * per_tile;
+        int64_t before = at - (int64_t)gap * seqs[lo] * per_tile;
+        cc.n = lo * chunk;
+        for (;;) {
+            cc.len = length_of(a, cc.n);
+            cc.tiles = tiles_of<kTile>(cc.len);
+            const int64_t here = places_of(cc.tiles) * per_tile;
+            if (at + here > b || cc.n + 1 >= a.N) break;
+            at += here;
+            before += cc.tiles * per_tile;
+            ++cc.n;
+        }
+        const int64_t rest = b - at;
+        const int64_t unit = rest / places_of(cc.tiles);
+        cc.i = max(0, (int)(rest - unit * places_of(cc.tiles)) - gap);
+        cc.h = (int)(unit / row_tiles);
+        cc.rt = (int)(unit - (int64_t)cc.h * row_tiles);
+        before += unit * cc.tiles + cc.i;
+        const int64_t end = b1 < total ? __shfl_sync(0xffffffffu, before, 1) : at_end;
+        count = (int)(end - __shfl_sync(0xffffffffu, before, 0));
+        cc.n = __shfl_sync(0xffffffffu, cc.n, 0);
+        cc.h = __shfl_sync(0xffffffffu, cc.h, 0);
+        cc.rt = __shfl_sync(0xffffffffu, cc.rt, 0);
+        cc.i = __shfl_sync(0xffffffffu, cc.i, 0);
+        cc.tiles = __shfl_sync(0xffffffffu, cc.tiles, 0);
+        cc.len = __shfl_sync(0xffffffffu, cc.len, 0);
+    }
+    if (count > 0) {
         Cursor ic = cc;
-        const int count = (int)(b1 - b0);
         const int box = min(kTile, a.c.page);  // rows of one copy
         const int page_shift = 31 - __clz(a.c.page);
         bool gone = false;                     // a wait gave up
@@ -586,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                 } else {
                     finish(false, (int)(2 * worker + (here ? 1 : 0)));
                     if (here) {
-                        const int64_t e = b0 + it + (cc.tiles - cc.i);  // past the unit's last tile
+                        const int64_t e = b1 - 1 + (cc.tiles - cc.i);  // past the unit's last place: this tile has b1 - 1
                         mine = Record{cc.n, cc.h, cc.rt, (int32_t)worker, (int32_t)((e * W + total - 1) / total - 1)};
                         if (by_unit && lane == 0) records[unit] = mine;
                     }

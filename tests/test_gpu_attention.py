@@ -248,6 +248,22 @@ def test_decode(lens, hq, hkv, window, page, d, code, dtype):
     assert B.kda_workspace_status(ws) == B.KDA_OK
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens,hq,hkv,window,d", [
+    ([0, 1, 33, 100, 7] * 100, 8, 8, 1, 32), ([900] + [5] * 260, 16, 8, 1, 128), ([3, 0] * 250 + [700, 64], 8, 8, 3, 64),
+    ([40, 31, 32, 65] * 70, 27, 9, 4, 128),
+], ids=["mixed", "long_first", "long_last", "two_column_tiles"])
+def test_decode_more_units_than_workers(lens, hq, hkv, window, d, dtype):
+    """Short sequences, and a long one among them: the cut counts what a unit's start costs."""
+    table, pool = tables(lens, 16)
+    cache = filled(pool, hkv, 16, d, torch.int8, seed=8)
+    q = make(len(lens) * window, hq, 1, d, dtype, 4, fused=True)[0]
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+    out = B.kda_attention_decode(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), workspace=ws)
+    close(out, ref.decode(q, cache, table, lens), ref.dequant(cache.v, cache.v_scale), dtype, 2.0 ** -11)
+    assert B.kda_workspace_status(ws) == B.KDA_OK
+
+
 MANY = [
     # lens, query heads, key heads, window: 17 rows and more a key head, up to several tiles of 32 rows
     ([1], 17, 1, 1), ([1], 25, 1, 1), ([0, 5, 127, 128, 129, 256], 8, 1, 4), ([3, 700], 16, 2, 7), ([1000, 64, 333], 24, 3, 5),
