@@ -441,7 +441,9 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s)
 // Up to three tiles an SM, two CTAs share a tile's keys: the longest tiles alone then set the time.  One and two
 // CTAs a tile, 16 of 4 heads of 128 channels unless said, us: a prompt of 1200 tokens (304 tiles) 184 and 124; prompts
 // of 200 to 1300, 10 of 2 heads (380 tiles) 183 and 152; one of 1800 (452 tiles) 281 and 278; of 2400 (604) 430 and
-// 450; 8 of 1000 to 4000 4218 and 4516.  Four CTAs: 174 where two take 152.
+// 450; 8 of 1000 to 4000 4218 and 4516; 60 of 100, 10 of 2 heads (1120 tiles) 86 and 120.  Four CTAs: 174 where two take
+// 152.  The lengths are not known here: a prompt of 1500 packed before those 60 begins last and takes 324 us by one
+// and 256 by two, packed after them 236 and 254.
 template <int D>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 {
