@@ -614,8 +614,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                     }
                 }
             }
-            __syncwarp();
+            __syncwarp();  // the stage's tiles and pages[] have been read
             if (issued < count) issue(issued++);
+            __syncwarp();  // lane 0's pages[] of that stage: with two stages the next iteration begins by reading them
 
             const bool unit_end = cc.i + 1 == cc.tiles;
             if (unit_end || it + 1 == count) {

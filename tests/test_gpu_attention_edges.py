@@ -1,0 +1,37 @@
+"""Attention where it can go wrong: page scales that change from tile to tile, against the float64 forms.
+
+Tolerances are those of test_gpu_attention.py, whose head derives them.
+"""
+import pytest
+import torch
+
+import attention_ref as ref
+from linear_attention_recurrence_kda_gb300 import binding as B
+from test_gpu_attention import CODES, DEV, close, filled, make, tables
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("page,d,hq", [(16, 128, 1), (32, 128, 8), (64, 128, 3), (16, 64, 8), (32, 128, 12)])
+def test_decode_page_scales_from_tile_to_tile(page, d, hq, dtype, code):
+    """Neighbouring pages' scales differ by 2^4, over runs of many tiles a warp: each tile takes its own pages' scales."""
+    lens = [5000, 3333] + [1400] * 600
+    pool = -(-max(lens) // page)
+    table = torch.arange(pool, dtype=torch.int32).repeat(len(lens), 1).to(DEV)  # the sequences share their pages
+    c = filled(pool, 1, page, d, code, seed=page)
+    even = (torch.arange(pool) % 2).float()[:, None].to(DEV)
+    cache = B.KvCache(c.k, c.v, torch.exp2(-9 + 4 * even), torch.exp2(-3 - 4 * even))
+    q = make(len(lens), hq, 1, d, dtype, 6)[0]
+    out = B.kda_attention_decode(q, cache, table, i32(*lens))
+    few = 4
+    close(out[:few], ref.decode(q[:few], cache, table[:few], lens[:few]), ref.dequant(c.v, cache.v_scale), dtype, 2.0 ** -11)
+    # the shorter sequences hold the same keys: one row of q at every place of the cut
+    same = B.kda_attention_decode(q[2:3].expand(600, -1, -1).contiguous(), cache, table[2:], i32(*lens[2:]))
+    want = ref.decode(q[2:3], cache, table[2:3], lens[2:3]).expand(600, -1, -1)
+    close(same, want, ref.dequant(c.v, cache.v_scale), dtype, 2.0 ** -11)
