@@ -13,7 +13,7 @@
 // heads then fills half as many products, registers and exponentials as with queries for rows.
 // K and V codes become f16 exactly (e4m3 and int8 are subsets of f16).  A row of q is scaled by a
 // power of two so that its largest value lies in [2^14, 2^15): bf16 values are then exact in f16 down
-// to 2^-38 of the row's largest; fp32 values are split into two f16 parts (22 bits), as are their p.
+// to 2^-31 of the row's largest and end at 2^-38; fp32 values are split into two f16 parts (22 bits), as are their p.
 // V's scale goes into O's unit: O is held in units of `vu`, which follows the pages' scales.
 //
 // HBM bounds it (2 d bytes per key and head, and a group of query heads per byte is far below the

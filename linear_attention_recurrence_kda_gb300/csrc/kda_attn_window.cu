@@ -20,10 +20,10 @@
 // O0 | O1, 32 columns each; P goes through shared memory.  All units' blocks, with a gap before each unit for
 // what its start costs, form one line that is cut evenly among the CTAs; pieces of a unit are joined by the join kernel.
 //
-// Warps 0-3 and 4-7: softmax of the streams, 8: products, 9: copies and scales, 10-15: conversion.  A
-// tile's rows of q enter scaled by one power of two that brings the largest value to [2^14, 2^15) (bf16
-// values are then exact in f16 down to 2^-38 of it), V's scales through P, with O in units of the
-// block's largest scale.
+// Warps 0-3 and 4-7: softmax of the streams, 8: products, 9: copies and scales, 10-15: conversion.  A row of
+// q enters scaled by a power of two that its own largest value sets, so that what one row holds, a NaN
+// or an infinity too, changes no other; V's scales enter through P, with O in units of the block's
+// largest scale.
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
 #include "kda_attn_tc.cuh"
@@ -64,8 +64,8 @@ struct Shared {
     uint32_t tmem, dead, flag;
     uint32_t has[8];             // by block: bit g, group g of 16 keys is there
     float ks[8][kGroups], vs[8][kGroups];
-    float f;                     // what scores are multiplied by, next to the key's scale
-    uint32_t qmax[4];
+    float f[kRows];              // a row's scores are in units of 2^s (see row_unit)
+    uint32_t mixed;              // is some row's unit another than 1?
     float top[2][4][kRows];      // by stream and warp: the largest score of a row
     float sum[2][4][kRows];      // a row's sum
     alignas(16) float ref[2][kRows], by[2][kRows];  // a row's reference, and what its last change multiplies by
@@ -115,6 +115,17 @@ __device__ __forceinline__ void mma_vp(uint32_t d, uint32_t a_lo, uint32_t b_add
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
         "r"(a_lo), "r"(((b_addr & 0x3FFFFu) >> 4) | (1u << 16)), "r"(idesc), "r"(kDescHi), "r"(kDescHi64), "r"((uint32_t)accumulate)
         : "memory");
+}
+
+// The power of two s (of s = 16 c) for rows of q whose largest magnitude lies in [2^(16 c - 8), 2^(16 c + 8)); such a row
+// enters as f16 times 2^(7 - s).  Rows of one c, as a model's are, share their scores' unit, and scores need no
+// factor of their row (one for every row, 64 sequences of 300 to 6000 keys, 28 rows of 8 heads: 142 us against
+// 135).  The largest value lands in [2^-1, 2^15): bf16's eight bits are exact down to 2^-16 of it at worst, and
+// what is cut off below that is at most 2^-24 of it, like an fp32 sum's last place.
+__device__ __forceinline__ int row_unit(uint32_t top)  // the bits of the largest magnitude; zeros: 0
+{
+    const int e = min(max((int)(top >> 7) - 127, -100), 127);
+    return top == 0u ? 0 : min((e + 8) >> 4 << 4, 127);  // the last: 2^127, and its values land below 2^8
 }
 
 // Or over the 128 threads of a stream (its four warps meet here).
@@ -479,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t zc = 0, oc = 0, qc = 0, blk0 = 0, turn = 0, jc = 0;
         float* po = reinterpret_cast<float*>(a.ws + L.o);
         float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
+        const float unit_scale = 0.0078125f * a.scale * kLog2e;  // 2^-7 (see row_unit)
         auto larger = [](float x, float y) { return fmaxf(x, y); };
         auto added = [](float x, float y) { return x + y; };
         bool gone = false;
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = s.rt * kRows, rows = min(kRows, rows_all - row0);
             const int whole_seen = s.len - a.L;  // keys before this one are seen by every row
             if (st == 0) {
-                // the rows of q, scaled by one power of two, into the products' layout: thread (row, quarter)
+                // the rows of q, each scaled by a power of two, into the products' layout: thread (row, quarter)
                 const bool late = turn > 0 && !warp_wait(&sh.f_read, (turn - 1) & 1u);  // the other stream has the last factor
                 const int r = key_in >> 2, quarter = key_in & 3;
                 const int R = row0 + r, t = R / a.group, head = s.h * a.group + (R - t * a.group);
@@ -500,13 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     top = __vmaxu2(__vmaxu2(top, u[c].x & 0x7fff7fffu), __vmaxu2(u[c].y & 0x7fff7fffu, __vmaxu2(u[c].z & 0x7fff7fffu, u[c].w & 0x7fff7fffu)));
-                top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-                if (lane == 0) sh.qmax[q4] = top;
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the row's four threads
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int unit = row_unit(top);
+                const bool some = any4(0, unit != 0);
                 gone = any4(0, late);
-                top = max(max(sh.qmax[0], sh.qmax[1]), max(sh.qmax[2], sh.qmax[3]));
-                int e = (int)(top >> 7) - 127;
-                e = min(max(e, -100), 127);
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                const float up = __uint_as_float((uint32_t)(127 + 7 - unit) << 23);
                 auto cv = [&](uint32_t x) { return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -514,13 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4*>(sq + (ch >> 3) * kQBlk + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
                         make_uint4(cv(u[c].x), cv(u[c].y), cv(u[c].z), cv(u[c].w));
                 }
-                if (key_in == 0) sh.f = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
+                if (quarter == 0) sh.f[r] = __uint_as_float((uint32_t)(127 + unit) << 23);
+                if (key_in == 0) sh.mixed = some;
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sh.q_ready);
             }
             const bool no_q = !warp_wait(&sh.q_ready, qc++ & 1u);
-            const float f = sh.f;
+            const bool mixed = sh.mixed != 0u;
             gone = any4(st, no_q || gone);
             if (st == 1 && lane == 0) tc::mbar_arrive(&sh.f_read);
             float l[kRows], vu = 0.f, vtop = 0.f;
@@ -545,11 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (v < INFINITY) big = fmaxf(big, v);
                 }
                 const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
-                const float sc = f * ks;
+                const float sc = unit_scale * ks;
                 // scores less their rows' references; does any pass its own by more than 2^8?
                 float over = -INFINITY;
                 auto less_ref = [&]() {
                     tc::tmem_wait_ld();
+                    if (mixed) {
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r) z[r] = __float_as_uint(f_of(z[r]) * sh.f[r]);
+                    }
 #pragma unroll
                     for (int c = 0; c < kRows / 4; ++c) {
                         const float4 m = *reinterpret_cast<const float4*>(&sh.ref[st][4 * c]);
@@ -577,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(zt, reinterpret_cast<uint32_t*>(x));
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int r = 0; r < kRows; ++r) x[r] = r >= from ? x[r] * sc : -INFINITY;
+                        for (int r = 0; r < kRows; ++r) x[r] = r >= from ? x[r] * sh.f[r] * sc : -INFINITY;
                         sh.top[st][q4][lane] = reduce_rows(x, larger);
                     }
                     (void)any4(st, false);

@@ -1,4 +1,4 @@
-"""Attention where it can go wrong: page scales that change from tile to tile, against the float64 forms.
+"""Attention where it can go wrong, against the float64 forms: scales far apart, infinities and NaN, many tiles.
 
 Tolerances are those of test_gpu_attention.py, whose head derives them.
 """
@@ -35,3 +35,31 @@ def test_decode_page_scales_from_tile_to_tile(page, d, hq, dtype, code):
     same = B.kda_attention_decode(q[2:3].expand(600, -1, -1).contiguous(), cache, table[2:], i32(*lens[2:]))
     want = ref.decode(q[2:3], cache, table[2:3], lens[2:3]).expand(600, -1, -1)
     close(same, want, ref.dequant(c.v, cache.v_scale), dtype, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("capacity", [0, 600], ids=["narrow_table", "wide_table"])  # many rows: one kernel or the other
+@pytest.mark.parametrize("hq,window,dtype", [(4, 7, torch.bfloat16), (8, 7, torch.bfloat16), (2, 2, torch.bfloat16),
+                                             (4, 7, torch.float32)], ids=["28", "56", "4", "28f32"])
+def test_decode_a_row_of_q_leaves_the_others_alone(hq, window, dtype, capacity):
+    """One row of q with a NaN, an infinity, or far larger or smaller than the rest: every other row stays as it was."""
+    lens, page, d = [150, 95, 300], 16, 128
+    table, pool = tables(lens, page, capacity=capacity)
+    cache = filled(pool, 1, page, d, torch.float8_e4m3fn)
+    q = make(len(lens) * window, hq, 1, d, dtype, 8)[0]
+    clean = B.kda_attention_decode(q, cache, table, i32(*lens))
+    v = ref.dequant(cache.v, cache.v_scale)
+    for n, t, head, change in ((0, window - 1, 0, float("nan")), (1, 0, hq - 1, -float("inf")), (2, window // 2, 1, 2.0 ** 40),
+                               (2, 0, 1, 2.0 ** -60), (0, window - 1, 1, 2.0 ** 90)):
+        row, x = n * window + t, q.clone()
+        if abs(change) < float("inf"):
+            x[row, head] *= change
+        else:
+            x[row, head, 5] = change
+        out = B.kda_attention_decode(x, cache, table, i32(*lens))
+        others = torch.ones(out.shape[:2], dtype=torch.bool, device=DEV)
+        others[row, head] = False
+        assert torch.equal(out[others], clean[others]), (change, int((out[others] != clean[others]).sum()))
+        if abs(change) < 1:
+            close(out, ref.decode(x, cache, table, lens), v, dtype, 2.0 ** -11)
+        elif not abs(change) < float("inf"):
+            assert not out[row, head].isfinite().any()
