@@ -89,15 +89,19 @@ struct Vec8 {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-    // the three parts as three 16-byte chunks, `plane` bytes apart
-    __device__ __forceinline__ void store(unsigned char* at, uint32_t plane) const
+    // the three parts as three 16-byte chunks, `plane` bytes apart; true: there is an infinity or NaN among the values
+    __device__ __forceinline__ bool store(unsigned char* at, uint32_t plane) const
     {
         uint32_t part[4][PL];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], part[e]);
+        float top = 0.f;  // 0 x finite is 0, 0 x anything else NaN
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaf(x[e], 0.f, top);
 #pragma unroll
         for (int p = 0; p < PL; ++p)
             *reinterpret_cast<uint4*>(at + p * plane) = make_uint4(part[0][p], part[1][p], part[2][p], part[3][p]);
+        return top != 0.f;
     }
 };
 
@@ -134,6 +138,7 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     unsigned char* sk = sq + PL * QB;
     unsigned char* sv = sk + PL * KB;
     __shared__ int odd[3][D];  // first key with +inf, -inf, NaN in the channel
+    __shared__ uint32_t wild[2][kKeys / 32];  // by a key tile's turn: keys with an infinity or NaN in K
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
     const int tpt = kRowsTile / a.group;
@@ -143,6 +148,7 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     AttnTile t;
     if (!attn_tile(a, slots - 1 - place / a.Hkv, tpt, t)) return;  // the whole cluster
     for (int i = tid; i < 3 * D; i += kThreads) (&odd[0][0])[i] = 0x7fffffff;
+    if (tid < kKeys / 32) wild[0][tid] = 0u;
 
     // rows of q: row r is token t.first + r / group, query head h group + r % group
     const int rows = min(tpt, t.last - t.first) * a.group;
@@ -183,13 +189,14 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
     const int warp_last = t.first + (16 * w + 15) / a.group;
     const bool warp_on = 16 * w < rows;
 
-    for (int k0 = rank * kKeys; k0 < t.last; k0 += kStep) {
+    for (int k0 = rank * kKeys, turn = 0; k0 < t.last; k0 += kStep, turn ^= 1) {
         __syncthreads();
+        if (tid < kKeys / 32) wild[turn ^ 1][tid] = 0u;  // the last tile's readers are past it
         if (!kAhead) load(k0);
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
             const int i = tid + e * kThreads, r = i / CH, c = i % CH;
-            kx[e].store(sk + tile_off<D>(r, c), KB);
+            if (kx[e].store(sk + tile_off<D>(r, c), KB)) atomicOr(&wild[turn][r / 32], 1u << (r % 32));
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 float& y = vx[e].x[x];
@@ -242,6 +249,35 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
             for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) z[j][i] += part[j][i];
+        }
+        // An infinity in a key would meet the parts of q one by one, which differ in sign or are zero: NaN, where q
+        // itself gives one infinity.  Such keys' scores are formed from the fp32 values.
+#pragma unroll 1
+        for (int i = 0; i < kKeys / 32; ++i) {
+#pragma unroll 1
+            for (uint32_t m = wild[turn][i]; m != 0u; m &= m - 1u) {
+                const int key = 32 * i + __ffs(m) - 1;
+                const float* k = static_cast<const float*>(a.k) + (t.start + k0 + key) * a.ks + (int64_t)h * D;
+                float s[2] = {0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = min(r0 + 8 * u, rows - 1), tok = r / a.group;
+                    const float* q = static_cast<const float*>(a.q) + (t.start + t.first + tok) * a.qs + (int64_t)(h * a.group + r - tok * a.group) * D;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(q + c), y = *reinterpret_cast<const float4*>(k + c);
+                        s[u] = fmaf(x.w, y.w, fmaf(x.z, y.z, fmaf(x.y, y.y, fmaf(x.x, y.x, s[u]))));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (8 * j + 2 * cq + e == key) {
+                            z[j][e] = s[0];
+                            z[j][2 + e] = s[1];
+                        }
+            }
         }
         if (k0 + kKeys - 1 > t.first + (16 * w) / a.group) {
 #pragma unroll

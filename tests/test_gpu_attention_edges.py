@@ -7,7 +7,7 @@ import torch
 
 import attention_ref as ref
 from linear_attention_recurrence_kda_gb300 import binding as B
-from test_gpu_attention import CODES, DEV, close, filled, make, tables
+from test_gpu_attention import CODES, DEV, close, filled, make, offsets, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,37 @@ def test_decode_a_row_of_q_leaves_the_others_alone(hq, window, dtype, capacity):
             close(out, ref.decode(x, cache, table, lens), v, dtype, 2.0 ** -11)
         elif not abs(change) < float("inf"):
             assert not out[row, head].isfinite().any()
+
+
+def minus_infinity_first(d, dtype):
+    """128 keys that every row scores at -inf, and more behind them: those count alone."""
+    lens, hidden = [400, 150], 128
+    q, k, v = make(sum(lens), 4, 2, d, dtype, 12)
+    q, k = q.clone(), k.clone()
+    q[:, :, 3] = q[:, :, 3].abs() + 0.1
+    k[:hidden, 0, 3] = -float("inf")
+    k[400:400 + hidden, 1, 3] = -float("inf")
+    out = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens))
+    start = 0
+    for n, length in enumerate(lens):  # key head n has the hidden keys
+        s = slice(start + hidden, start + length)
+        heads = slice(2 * n, 2 * n + 2)
+        want = ref.prefill(q[s, heads], k[s, n:n + 1], v[s, n:n + 1], [length - hidden])
+        close(out[s, heads], want, v, dtype, 2.0 ** -8)
+        start += length
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_fp32_keys_with_infinities(d):
+    """A key whose score is -inf weighs nothing; one whose score is +inf or NaN makes the rows that see it NaN."""
+    minus_infinity_first(d, torch.float32)
+    q, k, v = make(150, 2, 1, d, torch.float32, 16)
+    q, k = q.clone(), k.clone()
+    q[:, :, 3] = q[:, :, 3].abs() + 0.1
+    q[:, :, 4] = 0
+    clean = B.kda_attention_prefill(q, k, v)
+    for bad, ch in ((float("inf"), 3), (float("nan"), 3), (-float("inf"), 4)):
+        k2 = k.clone()
+        k2[70, 0, ch] = bad
+        out = B.kda_attention_prefill(q, k2, v)
+        assert torch.equal(out[:70], clean[:70]) and bool(out[70:].isnan().all())
