@@ -57,17 +57,16 @@ __device__ __forceinline__ float ex2(float x)
 
 constexpr int PL = 3;  // bf16 parts of a value
 
-// the bf16 parts of a pair; an infinity or NaN stays in the first alone
+// The bf16 parts of a pair.  The first is at most the largest finite bf16 value: a value near fp32's largest
+// would round to infinity, and its rest to the other one.
 __device__ __forceinline__ void split2(float lo, float hi, uint32_t (&part)[PL])
 {
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(part[0]) : "f"(hi), "f"(lo));
 #pragma unroll
-    for (int p = 0; p < PL; ++p) {
-        const uint32_t h = tc::pack_bf16(lo, hi);
-        part[p] = h;
-        if (p + 1 < PL) {
-            lo = fabsf(lo) < INFINITY ? lo - __uint_as_float(h << 16) : 0.f;
-            hi = fabsf(hi) < INFINITY ? hi - __uint_as_float(h & 0xffff0000u) : 0.f;
-        }
+    for (int p = 0; p + 1 < PL; ++p) {
+        lo -= __uint_as_float(part[p] << 16);
+        hi -= __uint_as_float(part[p] & 0xffff0000u);
+        part[p + 1] = tc::pack_bf16(lo, hi);
     }
 }
 

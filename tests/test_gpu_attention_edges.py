@@ -97,3 +97,34 @@ def test_prefill_fp32_keys_with_infinities(d):
         k2[70, 0, ch] = bad
         out = B.kda_attention_prefill(q, k2, v)
         assert torch.equal(out[:70], clean[:70]) and bool(out[70:].isnan().all())
+
+
+@pytest.mark.parametrize("copies", [1, 80], ids=["few_tiles", "many_tiles"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_fp32_largest_finite_values(d, copies):
+    """The largest finite value in V reaches the rows that see it, as itself, and no other row."""
+    top = torch.finfo(torch.float32).max
+    lens = [150, 90] * copies
+    q, k, v = make(sum(lens), 4, 2, d, torch.float32, 9)
+    clean = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens))
+    v2 = v.clone()
+    v2[140, 1, 5], v2[150 + 60, 0, 7], v2[0, 0, 2] = top, -top, top
+    out = B.kda_attention_prefill(q, k, v2, cu_seqlens=offsets(lens))
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[140:150, 2:, 5] = same[150 + 60:240, :2, 7] = same[:150, :2, 2] = False
+    assert torch.equal(out[same], clean[same]), int((out[same] != clean[same]).sum())
+    want = ref.prefill(q[:240], k[:240], v2[:240], lens[:2])
+    close(out[:240], want, v2, torch.float32, 0.0)
+
+
+def test_prefill_fp32_largest_finite_keys():
+    """The largest finite values in k and q: scores are what they are, here up to about 10."""
+    top, lens = torch.finfo(torch.float32).max, [200]
+    q, k, v = make(200, 2, 2, 64, torch.float32, 10)
+    g = torch.Generator().manual_seed(1)
+    x = torch.rand(200, 2, generator=g).to(DEV) * 2 - 1
+    k, q = k.clone(), q.clone()
+    q[:, 0, 3], k[:, 0, 3] = x[:, 0] * 1e-30, torch.where(x[:, 1] > 0, top, x[:, 1])
+    q[:, 1, 3], k[:, 1, 3] = torch.where(x[:, 1] > 0, -top, x[:, 1]), x[:, 0] * 1e-30
+    out = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens), scale=3e-8)
+    close(out, ref.prefill(q, k, v, lens, scale=3e-8), v, torch.float32, 0.0)
