@@ -14,7 +14,10 @@
 // K and V codes become f16 exactly (e4m3 and int8 are subsets of f16).  A row of q is scaled by a
 // power of two so that its largest value lies in [2^14, 2^15): bf16 values are then exact in f16 down
 // to 2^-31 of the row's largest and end at 2^-38; fp32 values are split into two f16 parts (22 bits), as are their p.
-// V's scale goes into O's unit: O is held in units of `vu`, which follows the pages' scales.
+// V's scale goes into O's unit: O is held in units of `vu`, which follows the pages' scales.  Of weights
+// relative to the largest, what is cut off is at most half a step of f16 (2^-11 of the weight; fp32: 2^-22) or,
+// far below the largest, 2^-32 (fp32: 2^-44) in units of `vu`, itself at most 64 times the page's own scale: over
+// thousands of small weights, which together may count for as much as the largest, that stays small.
 //
 // HBM bounds it (2 d bytes per key and head, and a group of query heads per byte is far below the
 // tensor cores' rate), so each warp keeps its own ring of tiles in flight by TMA with no barrier
@@ -82,12 +85,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// the part of (lo, hi) that their f16 rounding `h` leaves
-__device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t h)
+// the part of (lo, hi) that their f16 rounding `h` leaves, times `up`
+__device__ __forceinline__ uint32_t rest_f16(float lo, float hi, uint32_t h, float up = 1.f)
 {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_f16(lo - f.x, hi - f.y);
+    return pack_f16((lo - f.x) * up, (hi - f.y) * up);
 }
+
+// What a weight's second part is multiplied by.  A weight p of at most 2^15 (2^7 for the largest when the
+// reference was set) leaves a rest of at most 2^3, or 2^-25 where p is below f16's normal range; times 2^11 the
+// rest keeps bits down to 2^-36.
+constexpr float kRestUp = 2048.f;
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -503,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                 }
             }
             // Scores in base 2 (z s), their maxima over the keys that are seen, and p = 2^(z s - m) with
-            // one rounding of the difference.  The reference m moves only when the maximum has grown by
-            // more than 2^8: p stays below f16's range, l and O hold the factor as well, and O is rarely
-            // rescaled.
+            // one rounding of the difference.  The reference m is set 2^7 below the largest score and moves
+            // only when the maximum has grown by more than 2^8: p stays below 2^15, in f16's range and as
+            // far up in it as can be, l and O hold the factor as well, and O is rarely rescaled.
             const bool edge = partial || key0 + kTile > cc.len - a.L + 1;
             // does a row that sees `n` keys see this thread's key 16 k + 8 e + g of the tile?
             auto sees = [&](int k, int e, int n) { return (k == 0 ? has0 : has1) && key0 + 16 * k + 8 * e + g < n; };
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float now = top > m[nt][u] + 8.f ? top : m[nt][u];
+                    const float now = top > m[nt][u] + 15.f ? top - 7.f : m[nt][u];
                     const float ref = now == -INFINITY ? 0.f : now;
                     alpha[nt][u] = ex2(m[nt][u] - ref);
                     moved |= now != m[nt][u];
@@ -590,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                         const float y0 = z[s][nt][2 * e] * pv, y1 = z[s][nt][2 * e + 1] * pv;
                         const uint32_t h = pack_f16(y0, y1);
                         pf[0][nt][e] = transpose8(h);
-                        if constexpr (kSplit) pf[PARTS - 1][nt][e] = transpose8(rest_f16(y0, y1, h));
+                        if constexpr (kSplit) pf[PARTS - 1][nt][e] = transpose8(rest_f16(y0, y1, h, kRestUp));
                     }
 #pragma unroll
                 for (int c = 0; c < NCH; c += 2) {
@@ -603,12 +611,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                         widen<kE4m3>(__byte_perm(r[2 * i], r[2 * i + 1], 0x7531), vf[1], vf[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float part[4] = {};
-#pragma unroll
-                            for (int p = PARTS - 1; p >= 0; --p) mma_f16(kSplit ? part : O[c + i][nt], vf, pf[p][nt][0], pf[p][nt][1]);
                             if constexpr (kSplit) {
+                                float part[2][4] = {};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) O[c + i][nt][e] += part[e];
+                                for (int p = 0; p < PARTS; ++p) mma_f16(part[p], vf, pf[p][nt][0], pf[p][nt][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) O[c + i][nt][e] += fmaf(part[1][e], 1.f / kRestUp, part[0][e]);
+                            } else {
+                                mma_f16(O[c + i][nt], vf, pf[0][nt][0], pf[0][nt][1]);
                             }
                         }
                     }

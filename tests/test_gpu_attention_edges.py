@@ -128,3 +128,38 @@ def test_prefill_fp32_largest_finite_keys():
     q[:, 1, 3], k[:, 1, 3] = torch.where(x[:, 1] > 0, -top, x[:, 1]), x[:, 0] * 1e-30
     out = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens), scale=3e-8)
     close(out, ref.prefill(q, k, v, lens, scale=3e-8), v, torch.float32, 0.0)
+
+
+def flat_tail(n, at, high, code, first):
+    """A cache of one sequence's ``n`` keys of which one, at ``at``, scores ``high`` more in base 2 than the others for a q
+    that is one in channel 0 (with scale ln 2); its value is zero, the others' one.  ``first``: the first page's
+    values are zeros on a scale 64 times the others'."""
+    page, d = 128, 128
+    pages = n // page
+    k, v = torch.zeros(pages, 1, page, d), torch.full((pages, 1, page, d), 64.0)
+    vs = torch.full((pages, 1), 2.0 ** -6)
+    k[at // page, 0, at % page, 0] = 2 * high
+    v[at // page, 0, at % page] = 0
+    if first:
+        v[0], vs[0] = 0, 1.0
+    return B.KvCache(k.to(code).to(DEV), v.to(code).to(DEV), torch.full((pages, 1), 0.5).to(DEV), vs.to(DEV))
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("hq,dtype,at,high,first", [
+    (1, torch.float32, 0, 26, False), (12, torch.float32, 0, 26, False), (1, torch.float32, 256, 20, True),
+    (12, torch.float32, 256, 20, True), (1, torch.bfloat16, 256, 20, True), (12, torch.bfloat16, 256, 20, True),
+], ids=["f32", "f32_12", "f32_scale", "f32_12_scale", "bf16_scale", "bf16_12_scale"])
+def test_decode_one_key_before_a_long_flat_tail(hq, dtype, at, high, first, code):
+    """Thousands of weights far below the largest add up to something: 4095 of 2^-26 of it, or of 2^-20 after a page
+    whose values are on a larger scale."""
+    n, many = 4096, 2000
+    cache = flat_tail(n, at, high, code, first)
+    table = torch.arange(n // 128, dtype=torch.int32).repeat(many, 1).to(DEV)
+    q = torch.zeros(many, hq, 128, dtype=dtype, device=DEV)
+    q[:, :, 0] = 1
+    ln2 = 0.6931471805599453
+    out = B.kda_attention_decode(q, cache, table, i32(*[n] * many), scale=ln2)
+    want = ref.decode(q[:1], cache, table[:1], [n], scale=ln2)
+    assert float(want.max()) > (2.0 ** -17 if dtype == torch.float32 else 2.0 ** -11)  # not lost in the tolerance
+    close(out, want.expand(many, -1, -1), ref.dequant(cache.v, cache.v_scale), dtype, 2.0 ** -11)
