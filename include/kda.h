@@ -410,7 +410,9 @@ size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem);
  *       with a concurrently running call.
  * A length outside [0, max_pages * page_tokens] counts as 0 and a page outside [0, num_pages) as
  * not there; kda_workspace_status(workspace, ...) then reports KDA_ERR_DEVICE_CHECK.  Codes enter
- * the products exactly; q and the weights enter as f16 (fp32 io: as sums of two f16 parts).
+ * the products exactly; q and the weights enter as f16 (fp32 io: as sums of two f16 parts).  What a
+ * weight loses is at most 2^-11 of itself (fp32 io: 2^-22) or, where that is more, 2^-32 of the row's
+ * largest weight (2^-44), 2^-26 (2^-38) on a page whose value scale is 64 times below another's.
  */
 kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const kda_cache_t* cache, void* out,
                                   const kda_attention_t* problem, void* workspace, size_t workspace_bytes, void* stream);

@@ -23,7 +23,7 @@
 // Warps 0-3 and 4-7: softmax of the streams, 8: products, 9: copies and scales, 10-15: conversion.  A row of
 // q enters scaled by a power of two that its own largest value sets, so that what one row holds, a NaN
 // or an infinity too, changes no other; V's scales enter through P, with O in units of the block's
-// largest scale.
+// largest scale.  Weights enter as f16, up to 2^15, with the reference 2^7 below the largest (see kda_attn_decode.cu).
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
 #include "kda_attn_tc.cuh"
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
                 const float sc = unit_scale * ks;
-                // scores less their rows' references; does any pass its own by more than 2^8?
+                // scores less their rows' references; does any pass 2^15 (the largest had 2^7 when its reference was set)?
                 float over = -INFINITY;
                 auto less_ref = [&]() {
                     tc::tmem_wait_ld();
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < kRows; ++r)
                         if (r >= from) over = fmaxf(over, f_of(z[r]));
                 }
-                if (any4(st, over > 8.f || unit || late)) {
+                if (any4(st, over > 15.f || unit || late)) {
                     gone = any4(st, late);
                     if (gone) break;
                     // new references: the largest scores met so far
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q4 == 0) {
                         const float was = sh.ref[st][lane];
                         const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
-                        const float now = top > was + 8.f ? top : was;
+                        const float now = top > was + 15.f ? top - 7.f : was;
                         sh.by[st][lane] = now == -INFINITY ? 0.f : ex2(was - now);
                         sh.ref[st][lane] = now;
                     }

@@ -163,3 +163,18 @@ def test_decode_one_key_before_a_long_flat_tail(hq, dtype, at, high, first, code
     want = ref.decode(q[:1], cache, table[:1], [n], scale=ln2)
     assert float(want.max()) > (2.0 ** -17 if dtype == torch.float32 else 2.0 ** -11)  # not lost in the tolerance
     close(out, want.expand(many, -1, -1), ref.dequant(cache.v, cache.v_scale), dtype, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+def test_decode_many_rows_one_key_before_a_long_flat_tail(code):
+    """As above for the kernel that takes many rows, whose blocks of 128 keys alternate between two streams."""
+    n, many, hq = 4096, 300, 28
+    cache = flat_tail(n, 256, 20, code, True)
+    table = torch.arange(n // 128, dtype=torch.int32).repeat(many, 1).to(DEV)
+    q = torch.zeros(many, hq, 128, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = 1
+    ln2 = 0.6931471805599453
+    out = B.kda_attention_decode(q, cache, table, i32(*[n] * many), scale=ln2)
+    want = ref.decode(q[:1], cache, table[:1], [n], scale=ln2)
+    assert float(want.max()) > 2.0 ** -11
+    close(out, want.expand(many, -1, -1), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
