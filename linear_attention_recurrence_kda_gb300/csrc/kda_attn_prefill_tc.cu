@@ -25,6 +25,8 @@
 // Hidden keys: scores are replaced by -inf.  An infinity or NaN in V would spread over 0 x inf, so a
 // tile that some row does not see whole is cleaned of them first (noted by channel and key), and
 // the rows that see them get them at the end.
+#include <cfloat>
+
 #include "kda_attn.cuh"
 #include "kda_attn_tc.cuh"
 #include "kda_attn_tile.cuh"
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * cs;
                 float alpha = 1.f;
                 if (j == 0) {
-                    m = top;
+                    m = fmaxf(top, -FLT_MAX);  // scores that are all -inf weigh nothing, and keys that follow count
                 } else if (top > m + 8.f) {
                     alpha = ex2(m - top);
                     m = top;

@@ -178,3 +178,8 @@ def test_decode_many_rows_one_key_before_a_long_flat_tail(code):
     want = ref.decode(q[:1], cache, table[:1], [n], scale=ln2)
     assert float(want.max()) > 2.0 ** -11
     close(out, want.expand(many, -1, -1), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_scores_of_minus_infinity_come_first(d):
+    minus_infinity_first(d, torch.bfloat16)
