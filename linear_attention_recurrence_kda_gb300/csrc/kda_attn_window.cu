@@ -24,6 +24,8 @@
 // q enters scaled by a power of two that its own largest value sets, so that what one row holds, a NaN
 // or an infinity too, changes no other; V's scales enter through P, with O in units of the block's
 // largest scale.  Weights enter as f16, up to 2^15, with the reference 2^7 below the largest (see kda_attn_decode.cu).
+#include <cfloat>
+
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
 #include "kda_attn_tc.cuh"
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l[kRows], vu = 0.f, vtop = 0.f;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) l[r] = 0.f;
-            if (key_in < kRows) sh.ref[st][key_in] = -INFINITY;
+            if (key_in < kRows) sh.ref[st][key_in] = -FLT_MAX;  // finite: a score of -inf then weighs nothing
             (void)any4(st, false);
             for (int i = st; i < s.count && !gone; i += 2) {
                 const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u);
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float was = sh.ref[st][lane];
                         const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
                         const float now = top > was + 15.f ? top - 7.f : was;
-                        sh.by[st][lane] = now == -INFINITY ? 0.f : ex2(was - now);
+                        sh.by[st][lane] = ex2(was - now);
                         sh.ref[st][lane] = now;
                     }
                     (void)any4(st, false);
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = 8 * c + 2 * e;
-                        // a row that has seen nothing has the reference -inf; its weights are replaced below
+                        // a row that has seen nothing has the first reference; its weights are replaced below
                         float2 y = make_float2(ex2(f_of(z[r])), ex2(f_of(z[r + 1])));
                         if (from > 0) {
                             if (r < from) y.x = 0.f;
@@ -679,11 +681,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = s.begun && s.ended;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (s.begun ? 1 : 0);
             if (q4 == 0) {  // lane r: row r's weights of the two streams
-                const float m0 = sh.ref[0][lane], m1 = both ? sh.ref[1][lane] : -INFINITY;
+                const float m0 = sh.ref[0][lane], m1 = both ? sh.ref[1][lane] : -FLT_MAX;
                 const float l0 = (sh.sum[0][0][lane] + sh.sum[0][1][lane]) + (sh.sum[0][2][lane] + sh.sum[0][3][lane]);
                 const float l1 = both ? (sh.sum[1][0][lane] + sh.sum[1][1][lane]) + (sh.sum[1][2][lane] + sh.sum[1][3][lane]) : 0.f;
-                const float mm = fmaxf(m0, m1), ref = mm == -INFINITY ? 0.f : mm;
-                const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+                const float mm = fmaxf(m0, m1);
+                const float f0 = ex2(m0 - mm), f1 = ex2(m1 - mm);
                 const float sum = l0 * f0 + l1 * f1;
                 const float mul = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                 sh.weight[0][lane] = sh.unit[0] * f0 * mul;

@@ -183,3 +183,22 @@ def test_decode_many_rows_one_key_before_a_long_flat_tail(code):
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_prefill_scores_of_minus_infinity_come_first(d):
     minus_infinity_first(d, torch.bfloat16)
+
+
+@pytest.mark.parametrize("capacity", [0, 600], ids=["narrow_table", "wide_table"])
+def test_decode_scores_of_minus_infinity_alone(capacity):
+    """A row whose every score is -inf has no weight: zeros, from either kernel, and the other rows as they were."""
+    lens, page, d, hq, window = [150, 300], 16, 128, 4, 7
+    table, pool = tables(lens, page, capacity=capacity)
+    c = filled(pool, 1, page, d, torch.int8)
+    k = c.k.clone()
+    k[..., 0] = -3
+    cache = B.KvCache(k, c.v, c.k_scale, c.v_scale)
+    q = make(2 * window, hq, 1, d, torch.bfloat16, 13)[0]
+    clean = B.kda_attention_decode(q, cache, table, i32(*lens))
+    x = q.clone()
+    x[9, 2, 0] = float("inf")
+    out = B.kda_attention_decode(x, cache, table, i32(*lens))
+    want = clean.clone()
+    want[9, 2] = 0
+    assert torch.equal(out, want)
