@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
                     }
                 }
             }
-            // Scores in base 2 (z s), their maxima over the keys that are seen, and p = 2^(z s - m) with
-            // one rounding of the difference.  The reference m is set 2^7 below the largest score and moves
+            // Scores in base 2 (z s, rounded, so that however large they are the difference from the maximum is
+            // at most zero), their maxima over the keys that are seen, and p = 2^(z s - m).  The reference m is set 2^7 below the largest score and moves
             // only when the maximum has grown by more than 2^8: p stays below 2^15, in f16's range and as
             // far up in it as can be, l and O hold the factor as well, and O is rarely rescaled.
             const bool edge = partial || key0 + kTile > cc.len - a.L + 1;
@@ -524,29 +524,34 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT))
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float s0 = f[nt][u] * ks0, s1 = f[nt][u] * ks1;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        z[0][nt][2 * e + u] = __fmul_rn(z[0][nt][2 * e + u], s0);
+                        z[1][nt][2 * e + u] = __fmul_rn(z[1][nt][2 * e + u], s1);
+                    }
                     float top;
                     if (!edge) {
-                        top = fmaxf(fmaxf(z[0][nt][u] * s0, z[0][nt][2 + u] * s0), fmaxf(z[1][nt][u] * s1, z[1][nt][2 + u] * s1));
+                        top = fmaxf(fmaxf(z[0][nt][u], z[0][nt][2 + u]), fmaxf(z[1][nt][u], z[1][nt][2 + u]));
                     } else {
                         top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                if (sees(k, e, seen[nt][u])) top = fmaxf(top, z[k][nt][2 * e + u] * (k ? s1 : s0));
+                                if (sees(k, e, seen[nt][u])) top = fmaxf(top, z[k][nt][2 * e + u]);
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float now = top > m[nt][u] + 15.f ? top - 7.f : m[nt][u];
+                    const float now = top - m[nt][u] > 15.f ? top - 7.f : m[nt][u];
                     const float ref = now == -INFINITY ? 0.f : now;
                     alpha[nt][u] = ex2(m[nt][u] - ref);
                     moved |= now != m[nt][u];
                     m[nt][u] = now;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        z[0][nt][2 * e + u] = ex2(fmaf(z[0][nt][2 * e + u], s0, -ref));
-                        z[1][nt][2 * e + u] = ex2(fmaf(z[1][nt][2 * e + u], s1, -ref));
+                        z[0][nt][2 * e + u] = ex2(z[0][nt][2 * e + u] - ref);
+                        z[1][nt][2 * e + u] = ex2(z[1][nt][2 * e + u] - ref);
                     }
                     if (edge) {
 #pragma unroll

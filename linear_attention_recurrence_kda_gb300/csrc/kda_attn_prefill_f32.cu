@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        // m is the rounded maximum in base 2: every use takes the same value, so its rounding cancels
+        // m is the rounded maximum in base 2, and scores are rounded like it before it comes off: the largest weight is
+        // one however large the scores are (unrounded they may differ from m by more than exponents hold)
         const float n0 = fmaxf(m0, t0 * cs), n1 = fmaxf(m1, t1 * cs);
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
         const float a0 = ex2(m0 - u0), a1 = ex2(m1 - u1);
@@ -308,10 +309,10 @@ __global__ void __launch_bounds__(2 * ROWS, 128 / ROWS) kda_attn_prefill_f32_ker
         l1 *= a1;
 #pragma unroll
         for (int j = 0; j < kKeys / 8; ++j) {
-            z[j][0] = ex2(fmaf(z[j][0], cs, -u0));
-            z[j][1] = ex2(fmaf(z[j][1], cs, -u0));
-            z[j][2] = ex2(fmaf(z[j][2], cs, -u1));
-            z[j][3] = ex2(fmaf(z[j][3], cs, -u1));
+            z[j][0] = ex2(__fmul_rn(z[j][0], cs) - u0);
+            z[j][1] = ex2(__fmul_rn(z[j][1], cs) - u0);
+            z[j][2] = ex2(__fmul_rn(z[j][2], cs) - u1);
+            z[j][3] = ex2(__fmul_rn(z[j][3], cs) - u1);
             l0 += z[j][0] + z[j][1];
             l1 += z[j][2] + z[j][3];
         }

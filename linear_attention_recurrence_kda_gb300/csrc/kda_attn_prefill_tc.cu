@@ -478,7 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st32(ot + 32 * c, o);
                     }
                 }
-                const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-m, -m);
+                float mul = cs, off = -m;
+                if (fabsf(m) > 1048576.f) {
+                    // z cs - m rounds once; beyond 2^20 the rounding of m alone would show, and from 2^31 on pass the
+                    // exponents that there are: round z cs as m was
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) z[i] = __float_as_uint(__fmul_rn(f_of(z[i]), cs) - m);
+                    mul = 1.f;
+                    off = 0.f;
+                }
+                __syncwarp();
+                const float2 cs2 = make_float2(mul, mul), nm2 = make_float2(off, off);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {

@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
                 const float sc = unit_scale * ks;
-                // scores less their rows' references; does any pass 2^15 (the largest had 2^7 when its reference was set)?
+                // Scores less their rows' references; does any pass 2^15 (the largest had 2^7 when its reference was set)?
+                // They are rounded before that, as the references are, so that however large they are none passes the
+                // largest (not packed: a packed product and sum would become one with a single rounding).
                 float over = -INFINITY;
                 auto less_ref = [&]() {
                     tc::tmem_wait_ld();
@@ -572,10 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kRows / 4; ++c) {
                         const float4 m = *reinterpret_cast<const float4*>(&sh.ref[st][4 * c]);
-                        z[4 * c] = __float_as_uint(fmaf(f_of(z[4 * c]), sc, -m.x));
-                        z[4 * c + 1] = __float_as_uint(fmaf(f_of(z[4 * c + 1]), sc, -m.y));
-                        z[4 * c + 2] = __float_as_uint(fmaf(f_of(z[4 * c + 2]), sc, -m.z));
-                        z[4 * c + 3] = __float_as_uint(fmaf(f_of(z[4 * c + 3]), sc, -m.w));
+                        z[4 * c] = __float_as_uint(__fmul_rn(f_of(z[4 * c]), sc) - m.x);
+                        z[4 * c + 1] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 1]), sc) - m.y);
+                        z[4 * c + 2] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 2]), sc) - m.z);
+                        z[4 * c + 3] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 3]), sc) - m.w);
                     }
                 };
                 less_ref();
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q4 == 0) {
                         const float was = sh.ref[st][lane];
                         const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
-                        const float now = top > was + 15.f ? top - 7.f : was;
+                        const float now = top - was > 15.f ? top - 7.f : was;
                         sh.by[st][lane] = ex2(was - now);
                         sh.ref[st][lane] = now;
                     }

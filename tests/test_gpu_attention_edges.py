@@ -202,3 +202,27 @@ def test_decode_scores_of_minus_infinity_alone(capacity):
     want = clean.clone()
     want[9, 2] = 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("up", [2.0 ** 13, 2.0 ** 17, 2.0 ** 45])
+def test_prefill_huge_scores(up, d, dtype):
+    """Scores up to 2^95, whose rounding alone is larger than fp32's exponents: the largest takes the weight."""
+    lens = [300, 1, 130]
+    q, k, v = make(sum(lens), 4, 2, d, dtype, 17)
+    out = B.kda_attention_prefill(q * up, k * up, v, cu_seqlens=offsets(lens))
+    close(out, ref.prefill(q * up, k * up, v, lens), v, dtype, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("up", [2.0 ** 24, 2.0 ** 30, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("hq,window,dtype", [(2, 1, torch.bfloat16), (4, 3, torch.bfloat16), (4, 7, torch.bfloat16),
+                                             (2, 2, torch.float32)], ids=["2", "12", "28", "4f32"])
+def test_decode_huge_scores(hq, window, dtype, up, code):
+    lens, page, d = [700, 40, 131], 32, 128
+    table, pool = tables(lens, page, capacity=768)
+    cache = filled(pool, 1, page, d, code, seed=9)
+    q = make(len(lens) * window, hq, 1, d, dtype, 18)[0] * up
+    out = B.kda_attention_decode(q, cache, table, i32(*lens))
+    close(out, ref.decode(q, cache, table, lens), ref.dequant(cache.v, cache.v_scale), dtype, 2.0 ** -11)
