@@ -226,3 +226,33 @@ def test_decode_huge_scores(hq, window, dtype, up, code):
     q = make(len(lens) * window, hq, 1, d, dtype, 18)[0] * up
     out = B.kda_attention_decode(q, cache, table, i32(*lens))
     close(out, ref.decode(q, cache, table, lens), ref.dequant(cache.v, cache.v_scale), dtype, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (3, 3), (40, 2)], ids=["4of2", "3of3", "40of2"])
+def test_prefill_more_tiles_than_sms(hq, hkv, d):
+    """bf16, several hundred tiles: a CTA takes one after another.  NaN and infinities, in tiles of any turn, reach the rows
+    that see them and no other."""
+    dtype = torch.bfloat16
+    lens = [5, 70, 0, 33, 131, 300] * (40 if hq == 3 else 24 if hq == 4 else 6) + [900, 1]
+    q, k, v = make(sum(lens), hq, hkv, d, dtype, 14 + d, fused=True)
+    out = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens))
+    close(out, ref.prefill(q, k, v, lens), v, dtype, 2.0 ** -8)
+    nan, inf, group = float("nan"), float("inf"), hq // hkv
+    v2, want, start = v.clone(), out.clone(), 0
+    for i, n in enumerate(lens):
+        h, ch = i % hkv, (5 * i) % d
+        rows = want[start:start + n, h * group:(h + 1) * group, ch]
+        if n >= 33 and i % 3 != 2:  # one odd value, late in the sequence
+            at, bad = n - 1 - i % 20, (nan, inf, -inf)[i % 5 % 3]
+            v2[start + at, h, ch] = bad
+            rows[at:] = bad
+        elif n >= 131:  # one of each sign
+            v2[start + n // 2, h, ch], v2[start + n - 3, h, ch] = inf, -inf
+            rows[n // 2:], rows[n - 3:] = inf, nan
+        start += n
+    bad = B.kda_attention_prefill(q, k, v2, cu_seqlens=offsets(lens))
+    same = (bad == want) | (bad.isnan() & want.isnan())
+    assert bool(same.all()), (int((~same).sum()), [tuple(i) for i in (~same).nonzero()[:4].tolist()])
+    # and the same again: nothing is left over
+    assert torch.equal(out, B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens)))
