@@ -7,7 +7,7 @@ import torch
 
 import attention_ref as ref
 from linear_attention_recurrence_kda_gb300 import binding as B
-from test_gpu_attention import CODES, DEV, close, filled, make, offsets, tables
+from test_gpu_attention import CODES, DEV, close, filled, make, offsets, same_codes, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,26 @@ def test_prefill_more_tiles_than_sms(hq, hkv, d):
     assert bool(same.all()), (int((~same).sum()), [tuple(i) for i in (~same).nonzero()[:4].tolist()])
     # and the same again: nothing is left over
     assert torch.equal(out, B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("count,hkv,page,d", [(150, 9, 16, 64), (230, 9, 16, 128), (60, 17, 64, 32), (420, 5, 128, 128)])
+def test_append_many_pages_and_heads(count, hkv, page, d, code, dtype):
+    """Pages enough that a CTA takes several heads one after another, the last group of heads smaller than the others;
+    partly filled pages, some of which grow."""
+    before = [(7 * i) % (2 * page) for i in range(count)]
+    fresh = [(13 * i) % min(2 * page + 9, 60) for i in range(count)]
+    table, pool = tables([a + b for a, b in zip(before, fresh)], page)
+    cache = filled(pool, hkv, page, d, code, seed=3)
+    g = torch.Generator().manual_seed(15)
+    size = torch.exp2(torch.randint(-6, 7, (sum(fresh), 1, 1), generator=g).float())
+    kv = (torch.randn(sum(fresh), 2 * hkv, d, generator=g) * size).to(dtype)
+    kv[::97, 0, 3], kv[::89, hkv, 5] = float("inf"), float("nan")
+    kv = kv.to(DEV)
+    k, v = kv[:, :hkv], kv[:, hkv:]
+    want = ref.append(k, v, cache, table, before, fresh)
+    check = torch.zeros(64, dtype=torch.int32, device=DEV)
+    B.kda_cache_append(k, v, cache, table, i32(*[a + b for a, b in zip(before, fresh)]), cu_seqlens=offsets(fresh), check=check)
+    same_codes(cache, want)
+    assert B.kda_workspace_status(check) == B.KDA_OK
