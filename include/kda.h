@@ -366,7 +366,9 @@ typedef struct {
  *   out : [T_tot, num_heads, head_dim] io dtype, packed; must not overlap any input.
  * num_heads / num_kv_heads is at most 128.  No workspace.  bf16 products accumulate in fp32 with
  * the weights exp(z_ij - max) rounded to bf16; fp32 operands enter as sums of three bf16 parts
- * (24 bits).
+ * (24 bits).  bf16: a bounded wait inside the kernel that gives up (after ~2.6 s; a tile's
+ * first waits sooner where KDA_DEBUG_HANDOFF_TRIES is set, see kda_forward) leaves NaN in the rows that
+ * were not finished.
  */
 kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, void* out,
                                    const kda_attention_t* problem, void* stream);

@@ -30,6 +30,7 @@
 #include "kda_attn.cuh"
 #include "kda_attn_tc.cuh"
 #include "kda_attn_tile.cuh"
+#include "kda_checks.cuh"
 #include "kda_tc.cuh"
 
 namespace kda {
@@ -71,7 +72,7 @@ struct Shared {
     uint64_t v_load[4], v_clean[4];  // V tiles with hidden keys, in turn: the ring holds at most four
     uint64_t info_full[2], info_empty[2], answer_full;
     alignas(16) uint64_t answer[2];
-    TileInfo info[2];
+    TileInfo info[2], lost;  // lost: taken when a wait had given up, and not published
     uint32_t tmem, dead, dirty[2];
     uint32_t odd[2][3][128];  // by the tile's parity: first key with +inf, -inf, NaN in a channel
 };
@@ -107,7 +108,7 @@ __device__ __forceinline__ int take_tile(uint64_t* answer, uint64_t* bar, uint32
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kda_attn_prefill_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int slots)
+    kda_attn_prefill_tc_kernel(const AttnArgs a, const __grid_constant__ Maps maps, const int slots, const uint32_t tries)
 {
     using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::mbar_init(&sh.answer_full, 1);
         sh.dead = 0u;
+        sh.info[0].valid = sh.info[1].valid = sh.lost.valid = 0;
         sh.dirty[0] = sh.dirty[1] = 0xffffffffu;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -152,18 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* dead = &sh.dead;
 
     // A role's next tile: waits until the scheduler has published it.  False: there is none (or a
-    // wait gave up).  The role gives the slot back with done_tile.
+    // wait gave up).  The role gives the slot back with done_tile.  (These waits alone, once a tile, take their
+    // limit from the call: with a variable one in the inner waits long prompts took 3 % more.)
     struct Tile {
         int64_t start;
         int first, last, head, n0, n1, n, edge;
     };
     auto next_tile = [&](uint32_t turn, Tile& t) -> bool {
-        if (!warp_wait(&sh.info_full[turn & 1], (turn >> 1) & 1u)) {
+        if (!warp_wait(&sh.info_full[turn & 1], (turn >> 1) & 1u, tries)) {
             *dead = 1u;
             return false;
         }
         const TileInfo& i = sh.info[turn & 1];
-        if (!i.valid) return false;
+        if (!i.valid || __any_sync(0xffffffffu, *dead != 0u)) return false;
         t.start = i.start;
         t.first = i.first;
         t.last = i.last;
@@ -207,13 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     idx = take();
                 }
-                if (!warp_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u)) *dead = 1u;
-                if (__any_sync(0xffffffffu, *dead != 0u)) f.valid = 0;
+                if (!warp_wait(&sh.info_empty[turn & 1], ((turn >> 1) & 1u) ^ 1u, tries)) *dead = 1u;
+                const bool over = __any_sync(0xffffffffu, *dead != 0u);  // the slot may hold a tile that is not finished
                 if (lane == 0) {
-                    sh.info[turn & 1] = f;
+                    (over ? sh.lost : sh.info[turn & 1]) = f;
                     tc::mbar_arrive(&sh.info_full[turn & 1]);
                 }
-                if (!f.valid) break;
+                if (over || !f.valid) break;
                 if (!next_tile(turn, t)) break;  // what the others see
                 bool ok = true;
                 if (lane == 0) {
@@ -250,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (!__all_sync(0xffffffffu, ok)) *dead = 1u;  // the next round publishes the end
             }
-            // after a wait that gave up, what was issued still lands before the CTA ends
-            if (lane == 0 && *dead) {
+            // what was issued lands before the CTA ends, also where another role's wait gave up
+            if (lane == 0) {
                 for (int hf = 0; hf < 2; ++hf)
                     if (qc[hf] > 0) (void)tc::mbar_wait(&sh.q_full[hf], (qc[hf] - 1) & 1u, kTries);
                 for (uint32_t i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
@@ -350,11 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 base += 2 * t.n;
                 done_tile(turn);
             }
-            if (!ok || *dead != 0u) {
-                *dead = 1u;
-                commit(&sh.drained[first_half]);  // products in flight end before tensor memory is given back
-                (void)warp_wait(&sh.drained[first_half], 0);
-            }
+            if (!ok) *dead = 1u;
+            commit(&sh.drained[first_half]);  // products in flight end before tensor memory is given back
+            (void)warp_wait(&sh.drained[first_half], 0);
         } else if (w == 10) {
             // ---- V tiles with hidden keys: infinities and NaN leave the tile
             uint32_t base = 0, e = 0;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (gone) *dead = 1u;
                 tc::fence_after_sync();
                 const int rows = (min(first + tpt, t.last) - first) * a.group;
-                const float inv = gone ? NAN : 1.f / (l2.x + l2.y);  // a wait that gave up shows in the output
+                const float inv = 1.f / (l2.x + l2.y);
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                                      ((t.start + tok) * a.Hq + t.head * a.group + rh) * D;
                 const bool dirty = *(volatile uint32_t*)&sh.dirty[turn & 1] == odd_tag(turn);
@@ -560,6 +561,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     if (w == 8) tc::tmem_dealloc(tm, 512);
+    if (sh.dead != 0u) {
+        // A wait gave up, which shows in the output: NaN in every row of the tiles that this CTA had taken and may
+        // not have finished (the last two that were published, and one that was not).
+        for (const TileInfo& x : {sh.info[0], sh.info[1], sh.lost}) {
+            const int64_t row = (int64_t)a.group * D, n = x.valid ? (x.last - x.first) * row : 0;
+            for (int64_t i = tid; i < n; i += kThreads)
+                static_cast<__nv_bfloat16*>(a.out)[((x.start + x.first + i / row) * a.Hkv + x.head) * row + i % row] = __float2bfloat16_rn(NAN);
+        }
+    }
 }
 
 namespace {
@@ -594,7 +604,7 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
     cudaError_t e = limit.raise(kern, (int)Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t slots = attn_slots(a, 2 * tpt);
-    kern<<<(unsigned)(slots * a.Hkv), kThreads, Cfg<D>::SMEM, s>>>(a, maps, (int)slots);
+    kern<<<(unsigned)(slots * a.Hkv), kThreads, Cfg<D>::SMEM, s>>>(a, maps, (int)slots, checks::handoff_tries(kTries));
     return cudaGetLastError();
 }
 

@@ -72,9 +72,9 @@ __device__ __forceinline__ void commit(uint64_t* bar)
 }
 
 // mbar_wait by a whole warp; true only where every lane's wait ended
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t tries = kTries)
 {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kTries));
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, tries));
 }
 
 __device__ __forceinline__ float ex2(float x)

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -48,6 +49,18 @@ inline kda_status_t check_device_pointer(const void* p)
         if (attr.device != dev) return KDA_ERR_INVALID_ARG;
     }
     return KDA_OK;
+}
+
+// Tries of a kernel's hand-off waits before it gives up: `normal`, or fewer where KDA_DEBUG_HANDOFF_TRIES says so (a
+// debugging aid, off unless set, read on every call: it exercises the timeout path).
+inline uint32_t handoff_tries(uint32_t normal)
+{
+    if (const char* env = std::getenv("KDA_DEBUG_HANDOFF_TRIES")) {
+        char* end = nullptr;
+        const unsigned long v = std::strtoul(env, &end, 10);
+        if (end != env && *end == '\0' && v < normal) return (uint32_t)v;
+    }
+    return normal;
 }
 
 }  // namespace checks

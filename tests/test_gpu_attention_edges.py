@@ -279,3 +279,21 @@ def test_append_many_pages_and_heads(count, hkv, page, d, code, dtype):
     B.kda_cache_append(k, v, cache, table, i32(*[a + b for a, b in zip(before, fresh)]), cu_seqlens=offsets(fresh), check=check)
     same_codes(cache, want)
     assert B.kda_workspace_status(check) == B.KDA_OK
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prefill_waits_that_give_up_show(monkeypatch, d):
+    """bf16: rows that a given-up wait left unfinished are NaN, all of them where no wait is tried; the next call is right."""
+    lens = [900, 70, 131, 1, 300] * 24
+    q, k, v = make(sum(lens), 8, 4, d, torch.bfloat16, 19)
+    clean = B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens))
+    for tries in ("0", "1", "3"):
+        monkeypatch.setenv("KDA_DEBUG_HANDOFF_TRIES", tries)
+        out = torch.full_like(clean, 123.0)
+        B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens), out=out)
+        torch.cuda.synchronize()
+        monkeypatch.delenv("KDA_DEBUG_HANDOFF_TRIES")
+        lost = out.isnan().all(-1)
+        assert torch.equal(out[~lost], clean[~lost]), (tries, int((out == 123.0).all(-1).sum()))
+        assert tries != "0" or bool(lost.all())
+        assert torch.equal(B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens)), clean)
