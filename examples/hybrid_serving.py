@@ -45,6 +45,7 @@ class HybridStack:
         for i, m in enumerate(need):
             table[i, :m] = torch.arange(at, at + m)
             at += m
+        self.begun = False  # do the sequences hold tokens?
         self.table = table.to(self.device)
         self.lengths = torch.zeros(n, dtype=torch.int32, device=self.device)
         self.memory = [torch.zeros(n, self.heads, self.D, self.D, device=self.device) if kind == "k" else
@@ -67,7 +68,11 @@ class HybridStack:
         return x + o.reshape(o.shape[0], -1) @ w["out"]
 
     def prompt(self, x, lens):
-        """The packed prompts x [sum(lens), width]; returns the stack's output for every token."""
+        """The packed prompts x [sum(lens), width]; returns the stack's output for every token.  The attention layers'
+        prompts attend to their own tokens alone, so that with such layers they must be the sequences' first."""
+        if self.begun and "a" in self.layers:
+            raise ValueError("the sequences hold tokens that a prompt's attention layers would not see: start() anew, or step()")
+        self.begun = True
         cu = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).to(self.device)
         self.lengths += cu[1:] - cu[:-1]
         for i, (kind, w) in enumerate(zip(self.layers, self.w)):
@@ -83,6 +88,7 @@ class HybridStack:
 
     def step(self, x):
         """One token of every sequence, x [n, width]."""
+        self.begun = True
         self.lengths += 1
         for i, (kind, w) in enumerate(zip(self.layers, self.w)):
             if kind == "k":
