@@ -186,6 +186,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, result=True):
+    """A tensor for a call on ``stream`` (None: the current one), from that stream's pool: the current stream's earlier
+    work on the block, and its next, do not run beside the call.  ``result``: it goes on to the current stream."""
+    if stream is not None:
+        current = torch.cuda.current_stream(device)
+        if stream != current:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            if result:
+                t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t, name, dtype, shape, device):
     if t is not None and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return
@@ -610,7 +624,7 @@ def kda_attention_prefill(q, k, v, cu_seqlens=None, num_seqs: Optional[int] = No
     else:
         N = 1 if num_seqs is None else int(num_seqs)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        out = _empty((T, Hq, d), dt, dev, stream)
     else:
         _need(out, "out", dt, (T, Hq, d), dev)
     prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, ks, vs)
@@ -674,7 +688,7 @@ def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optiona
     _need(lengths, "lengths", torch.int32, (N,), dev)
     c = _cache(cache, block_table, N, Hkv, d, dev)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        out = _empty((T, Hq, d), dt, dev, stream)
     else:
         _need(out, "out", dt, (T, Hq, d), dev)
     prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, 0, 0)
@@ -682,9 +696,7 @@ def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optiona
         wsb = _decode_workspace_bytes(N, T, Hq, Hkv, d, io, dev)
         if wsb == 0:
             raise KdaError(KDA_ERR_INVALID_ARG, "kda_attention_decode_workspace_bytes")
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)  # not reused by the current stream before `stream` is done with it
+        workspace = _empty(wsb, torch.uint8, dev, stream, result=False)
     st = lib().kda_attention_decode(q.data_ptr(), lengths.data_ptr(), ctypes.byref(c), out.data_ptr(),
                                     ctypes.byref(prob), workspace.data_ptr(),
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream))
