@@ -258,10 +258,10 @@ def kda_forward(q, k, v, z, A, beta, initial_state=None, cu_seqlens=None, out=No
     if initial_state is not None:
         _need(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=dt, device=dev)
+        out = _empty((T, H, dv), dt, dev, stream)
     _need(out, "out", dt, (T, H, dv), dev)
     if final_state is None and want_final:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _empty((N, H, dk, dv), torch.float32, dev, stream)
     if final_state is not None:
         _need(final_state, "final_state", torch.float32, (N, H, dk, dv), dev)
     prob = make_problem(N, T, max_seqlen, H, dk, dv, dt, g_min)
@@ -269,7 +269,7 @@ def kda_forward(q, k, v, z, A, beta, initial_state=None, cu_seqlens=None, out=No
     if wsb == 0:
         raise KdaError(KDA_ERR_INVALID_ARG, "kda_forward_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(wsb, torch.uint8, dev, stream, result=False)
     st = lib().kda_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(initial_state),
                            _ptr(cu_seqlens), _ptr(out), _ptr(final_state), ctypes.byref(prob), _ptr(workspace),
                            ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream))
@@ -304,10 +304,10 @@ def kda_forward_static_scratch(q, k, v, z, A, beta, initial_state=None, cu_seqle
     if initial_state is not None:
         _need(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=dt, device=dev)
+        out = _empty((T, H, dv), dt, dev, stream)
     _need(out, "out", dt, (T, H, dv), dev)
     if final_state is None and want_final:
-        final_state = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        final_state = _empty((N, H, dk, dv), torch.float32, dev, stream)
     if final_state is not None:
         _need(final_state, "final_state", torch.float32, (N, H, dk, dv), dev)
     prob = make_problem(N, T, max_seqlen, H, dk, dv, dt, g_min)
@@ -351,17 +351,17 @@ def kda_backward(q, k, v, z, A, beta, d_out, d_final_state=None, initial_state=N
     for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
         if t is not None:
             _need(t, name, torch.float32, (N, H, dk, dv), dev)
-    dq, dk_, dz = (torch.empty((T, H, dk), dtype=dt, device=dev) for _ in range(3))
-    dv_ = torch.empty((T, H, dv), dtype=dt, device=dev)
-    dA = torch.empty((H,), dtype=torch.float32, device=dev)
-    dbeta = torch.empty((T, H), dtype=torch.float32, device=dev)
-    dS0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev) if want_d_initial else None
+    dq, dk_, dz = (_empty((T, H, dk), dt, dev, stream) for _ in range(3))
+    dv_ = _empty((T, H, dv), dt, dev, stream)
+    dA = _empty((H,), torch.float32, dev, stream)
+    dbeta = _empty((T, H), torch.float32, dev, stream)
+    dS0 = _empty((N, H, dk, dv), torch.float32, dev, stream) if want_d_initial else None
     prob = make_problem(N, T, max_seqlen, H, dk, dv, dt, g_min)
     wsb = kda_backward_workspace_bytes(prob)
     if wsb == 0:
         raise KdaError(KDA_ERR_INVALID_ARG, "kda_backward_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(wsb, torch.uint8, dev, stream, result=False)
     st = lib().kda_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(initial_state),
                             _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
                             _ptr(dz), _ptr(dA), _ptr(dbeta), _ptr(dS0), ctypes.byref(prob), _ptr(workspace),
@@ -392,14 +392,14 @@ def kda_forward_summary(q, k, v, z, A, beta, cu_seqlens=None, num_seqs: int = 1,
         _need(t, name, dt, shp, dev)
     _need(A, "A", torch.float32, (H,), dev)
     _need(beta, "beta", torch.float32, (T, H), dev)
-    M = torch.empty((N, H, dk, dk), dtype=torch.float32, device=dev)
-    St = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    M = _empty((N, H, dk, dk), torch.float32, dev, stream)
+    St = _empty((N, H, dk, dv), torch.float32, dev, stream)
     prob = make_problem(N, T, max_seqlen, H, dk, dv, dt, g_min)
     if workspace is None:
         wsb = int(lib().kda_forward_summary_workspace_bytes(ctypes.byref(prob)))
         if wsb == 0:
             raise KdaError(KDA_ERR_INVALID_ARG, "kda_forward_summary_workspace_bytes")
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(wsb, torch.uint8, dev, stream, result=False)
     st = lib().kda_forward_summary(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(cu_seqlens), _ptr(M),
                                    _ptr(St), ctypes.byref(prob), _ptr(workspace),
                                    ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream))
@@ -422,7 +422,7 @@ def kda_state_scan(transition, state_from_zero, initial_state=None, count: Optio
     if initial_state is not None:
         _need(initial_state, "initial_state", torch.float32, (N, H, dk, dv), dev)
     if state_out is None:
-        state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        state_out = _empty((N, H, dk, dv), torch.float32, dev, stream)
     _need(state_out, "state_out", torch.float32, (N, H, dk, dv), dev)
     prob = make_problem(N, N, 1, H, dk, dv, torch.float32)
     st = lib().kda_state_scan(_ptr(transition), _ptr(state_from_zero), _ptr(initial_state), ctypes.c_int32(count),
@@ -445,7 +445,7 @@ def kda_decode_step(q, k, v, z, A, beta, state, out=None, g_min: float = G_MIN, 
     _need(beta, "beta", torch.float32, (N, H), dev)
     _need(state, "state", torch.float32, (N, H, dk, dv), dev)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=dt, device=dev)
+        out = _empty((N, H, dv), dt, dev, stream)
     _need(out, "out", dt, (N, H, dv), dev)
     prob = make_problem(N, N, 1, H, dk, dv, dt, g_min)
     st = lib().kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A), _ptr(beta), _ptr(state), _ptr(out),
@@ -478,11 +478,11 @@ def kda_decode_replay(q, k, v, z, A, beta, state_in, accepted=None, state_out=No
     if accepted is not None:
         _need(accepted, "accepted", torch.int32, (N,), dev)
     if out is None and want_out:
-        out = torch.empty((T, H, dv), dtype=dt, device=dev)
+        out = _empty((T, H, dv), dt, dev, stream)
     if out is not None:
         _need(out, "out", dt, (T, H, dv), dev)
     if state_out is None and want_state:
-        state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+        state_out = _empty((N, H, dk, dv), torch.float32, dev, stream)
     if state_out is not None:
         _need(state_out, "state_out", torch.float32, (N, H, dk, dv), dev)
     prob = make_problem(N, T, T // N, H, dk, dv, dt, g_min)
@@ -513,9 +513,9 @@ def kda_prologue(xq, xk, xv, wq, wk, wv, cu_seqlens=None, num_seqs: Optional[int
         _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
     else:
         N = 1 if num_seqs is None else int(num_seqs)
-    q = torch.empty_like(xq) if q is None else q
-    k = torch.empty_like(xk) if k is None else k
-    v = torch.empty_like(xv) if v is None else v
+    q = _empty(xq.shape, xq.dtype, dev, stream) if q is None else q
+    k = _empty(xk.shape, xk.dtype, dev, stream) if k is None else k
+    v = _empty(xv.shape, xv.dtype, dev, stream) if v is None else v
     for name, t, shp in (("q", q, (T, H, dk)), ("k", k, (T, H, dk)), ("v", v, (T, H, dv))):
         _need(t, name, dt, shp, dev)
     prob = make_problem(N, T, 0, H, dk, dv, dt)
@@ -532,9 +532,10 @@ def kda_epilogue(o, gate, weight, eps: float = 1e-5, y=None, stream=None):
     T, H, dv = o.shape
     dev = o.device
     dt = o.dtype
+    _need(o, "o", dt, (T, H, dv), dev)
     _need(gate, "gate", dt, (T, H, dv), dev)
     _need(weight, "weight", torch.float32, (dv,), dev)
-    y = torch.empty_like(o) if y is None else y
+    y = _empty(o.shape, o.dtype, dev, stream) if y is None else y
     _need(y, "y", dt, (T, H, dv), dev)
     prob = make_problem(1, T, 0, H, dv, dv, dt)
     st = lib().kda_epilogue(_ptr(o), _ptr(gate), _ptr(weight), ctypes.c_float(eps), _ptr(y), ctypes.byref(prob),

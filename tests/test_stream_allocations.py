@@ -60,6 +60,38 @@ def test_attention(watched):
     assert where == ["current"] * 2 and len(recorded) == 2
 
 
+T, H, D = 8, 2, 64
+F32 = torch.float32
+QKVZ = lambda: [t(T, H, D) for _ in range(4)] + [t(H, dtype=F32), t(T, H, dtype=F32)]  # noqa: E731
+STATE = lambda n=1: t(n, H, D, D, dtype=F32)  # noqa: E731
+CALLS = {  # name: (call, results that it allocates, workspaces)
+    "forward": (lambda s: B.kda_forward(*QKVZ(), stream=s), 2, 1),
+    "forward_static_scratch": (lambda s: B.kda_forward_static_scratch(*QKVZ(), stream=s), 2, 0),
+    "backward": (lambda s: B.kda_backward(*QKVZ(), t(T, H, D), stream=s), 7, 1),
+    "forward_summary": (lambda s: B.kda_forward_summary(*QKVZ(), stream=s), 2, 1),
+    "state_scan": (lambda s: B.kda_state_scan(t(2, 1, H, D, D, dtype=F32), t(2, 1, H, D, D, dtype=F32), stream=s), 1, 0),
+    "decode_step": (lambda s: B.kda_decode_step(*QKVZ(), STATE(T), stream=s), 1, 0),
+    "decode_replay": (lambda s: B.kda_decode_replay(*QKVZ(), STATE(), stream=s), 2, 0),
+    "prologue": (lambda s: B.kda_prologue(*[t(T, H, D)] * 3, *[t(H, D, 4, dtype=F32)] * 3, stream=s), 3, 0),
+    "epilogue": (lambda s: B.kda_epilogue(t(T, H, D), t(T, H, D), t(D, dtype=F32), stream=s), 1, 0),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_call(watched, name):
+    where, recorded = watched
+    call, results, workspaces = CALLS[name]
+    side = Side()
+    refused(call, side)
+    assert where == [side] * (results + workspaces), where
+    assert recorded == ["current"] * results, recorded
+
+
+def test_epilogue_refuses_a_strided_input():
+    with pytest.raises(ValueError):
+        B.kda_epilogue(t(H, T, D).transpose(0, 1), t(T, H, D), t(D, dtype=F32))
+
+
 @pytest.mark.gpu
 def test_blocks_that_the_current_stream_still_writes():
     """Blocks of the sizes that a call allocates are freed with work on them pending; the call on another stream is right."""
