@@ -12,6 +12,18 @@ class Side:
     cuda_stream = 0
 
 
+class Library:
+    """In the library's place: every call is refused, nothing is launched (a Grace-based GPU would address the host's
+    tensors)."""
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *a: 256
+        if name == "kda_status_string":
+            return lambda status: b"KDA_ERR_INVALID_ARG"
+        return lambda *a: B.KDA_ERR_INVALID_ARG
+
+
 @pytest.fixture
 def watched(monkeypatch):
     """(where, recorded): the stream of every allocation, and the tensors handed to the current stream."""
@@ -28,11 +40,15 @@ def watched(monkeypatch):
         where.append(now[-1])
         return real(*a, **kw)
 
+    monkeypatch.setattr(B, "lib", Library)
+    monkeypatch.setattr(B, "_stream", lambda stream=None: None)
+    B._decode_workspace_bytes.cache_clear()
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append(s), raising=False)
-    return where, recorded
+    yield where, recorded
+    B._decode_workspace_bytes.cache_clear()
 
 
 def t(*shape, dtype=torch.bfloat16):
@@ -40,8 +56,7 @@ def t(*shape, dtype=torch.bfloat16):
 
 
 def refused(call, *a, **kw):
-    """The call allocates, and is then refused: its tensors are the host's (or there is no device at all)."""
-    with pytest.raises(RuntimeError):
+    with pytest.raises(B.KdaError):
         call(*a, **kw)
 
 
