@@ -407,7 +407,7 @@ size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem);
  *       kda_attention_prefill.
  *   lengths : [N] int32 on the device, keys of each sequence in the cache, the window's included.
  *   out : [N*L, num_heads, head_dim] io dtype, packed; must not overlap any argument.
- *   problem : total_tokens = N*L with L >= 1.
+ *   problem : total_tokens = N*L with L >= 1; L * num_heads / num_kv_heads below 2^31 - 65536.
  *   workspace : kda_attention_decode_workspace_bytes(problem) bytes, 256-byte aligned, not shared
  *       with a concurrently running call.
  * A length outside [0, max_pages * page_tokens] counts as 0 and a page outside [0, num_pages) as

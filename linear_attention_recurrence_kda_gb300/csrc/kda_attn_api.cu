@@ -47,6 +47,14 @@ size_t strided_bytes(int64_t tokens, int64_t stride, int64_t row, size_t elem)
     return tokens > 0 ? ((size_t)(tokens - 1) * (size_t)stride + (size_t)row) * elem : 0;
 }
 
+// Tokens against the cache: whole windows, whose rows of one key head are counted in 32 bits.
+kda_status_t check_windows(const kda_attention_t& p)
+{
+    if (p.total_tokens < p.num_seqs || p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    if (p.total_tokens / p.num_seqs * (p.num_heads / p.num_kv_heads) > 2147483647LL - 65536) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
 struct CacheRanges {
     Range r[5];
 };
@@ -211,7 +219,7 @@ size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem)
 {
     if (check_attention(problem, true) != KDA_OK) return 0;
     const kda_attention_t& p = *problem;
-    if (p.total_tokens < p.num_seqs || p.total_tokens % p.num_seqs != 0) return 0;
+    if (check_windows(p) != KDA_OK) return 0;
     const int64_t rows = p.total_tokens / p.num_seqs * (p.num_heads / p.num_kv_heads);
     return kda::attn_decode_workspace_bytes(rows, p.head_dim, p.io_dtype);
 }
@@ -222,7 +230,7 @@ kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const k
     kda_status_t st = check_attention(problem, true);
     if (st != KDA_OK) return st;
     const kda_attention_t& p = *problem;
-    if (p.total_tokens < p.num_seqs || p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    if ((st = check_windows(p)) != KDA_OK) return st;
     kda::AttnDecodeArgs a{};
     if ((st = token_stride(p.q_stride, p.num_heads, p, &a.qs)) != KDA_OK) return st;
     CacheRanges rc;
