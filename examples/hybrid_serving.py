@@ -40,7 +40,7 @@ class HybridStack:
         """States and caches for sequences of at most ``capacity`` tokens (a list)."""
         n = len(capacity)
         need = [-(-c // self.PAGE) for c in capacity]
-        table = torch.zeros(n, max(need), dtype=torch.int32)
+        table = torch.full((n, max(need)), -1, dtype=torch.int32)  # past a sequence's capacity there is no page
         at = 0
         for i, m in enumerate(need):
             table[i, :m] = torch.arange(at, at + m)

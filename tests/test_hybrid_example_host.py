@@ -38,3 +38,10 @@ def test_kda_layers_alone_continue(monkeypatch):
     s.prompt(x, [3, 4])
     s.prompt(x, [4, 3])
     assert s.lengths.tolist() == [7, 7]
+
+
+def test_pages_that_a_sequence_does_not_own_are_not_in_its_row(monkeypatch):
+    """A sequence that outgrows its capacity must not write into another's pages: those entries are no page at all."""
+    s = stack(monkeypatch, "a")
+    s.start([200, 10, 64, 65])
+    assert s.table.tolist() == [[0, 1, 2, 3], [4, -1, -1, -1], [5, -1, -1, -1], [6, 7, -1, -1]]
