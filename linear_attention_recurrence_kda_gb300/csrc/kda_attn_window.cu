@@ -25,6 +25,7 @@
 // or an infinity too, changes no other; V's scales enter through P, with O in units of the block's
 // largest scale.  Weights enter as f16, up to 2^15, with the reference 2^7 below the largest (see kda_attn_decode.cu).
 #include <cfloat>
+#include <type_traits>
 
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
@@ -50,6 +51,7 @@ constexpr int kUnitCost = 5;
 // warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 0x1p-11f;  // products, which stay below 2^31, may pass 2^20 as scores by a factor above this
 
 constexpr int D = 128;
 constexpr uint32_t kColBlk = 128 * 128;         // bytes of 64 channels of 128 keys in f16
@@ -66,7 +68,7 @@ struct Shared {
     uint32_t tmem, dead, flag;
     uint32_t has[8];             // by block: bit g, group g of 16 keys is there
     float ks[8][kGroups], vs[8][kGroups];
-    float f[kRows];              // a row's scores are in units of 2^s (see row_unit)
+    alignas(16) float f[kRows];  // a row's scores are in units of 2^s (see row_unit)
     uint32_t mixed;              // is some row's unit another than 1?
     float top[2][4][kRows];      // by stream and warp: the largest score of a row
     float sum[2][4][kRows];      // a row's sum
@@ -122,7 +124,7 @@ __device__ __forceinline__ void mma_vp(uint32_t d, uint32_t a_lo, uint32_t b_add
 // The power of two s (of s = 16 c) for rows of q whose largest magnitude lies in [2^(16 c - 8), 2^(16 c + 8)); such a row
 // enters as f16 times 2^(7 - s).  Rows of one c, as a model's are, share their scores' unit, and scores need no
 // factor of their row (one for every row, 64 sequences of 300 to 6000 keys, 28 rows of 8 heads: 142 us against
-// 135).  The largest value lands in [2^-1, 2^15): bf16's eight bits are exact down to 2^-16 of it at worst, and
+// 134).  The largest value lands in [2^-1, 2^15): bf16's eight bits are exact down to 2^-16 of it at worst, and
 // what is cut off below that is at most 2^-24 of it, like an fp32 sum's last place.
 __device__ __forceinline__ int row_unit(uint32_t top)  // the bits of the largest magnitude; zeros: 0
 {
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int unit = row_unit(top);
                 const bool some = any4(0, unit != 0);
-                gone = any4(0, late);
+                gone = late;  // made the same for all below
                 const float up = __uint_as_float((uint32_t)(127 + 7 - unit) << 23);
                 auto cv = [&](uint32_t x) { return pack_f16(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
 #pragma unroll
@@ -543,121 +545,141 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < kRows; ++r) l[r] = 0.f;
             if (key_in < kRows) sh.ref[st][key_in] = -FLT_MAX;  // finite: a score of -inf then weighs nothing
             (void)any4(st, false);
-            for (int i = st; i < s.count && !gone; i += 2) {
-                const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u);
-                tc::fence_after_sync();
-                const int b = (int)((blk0 + i) & 7u), key = (s.i0 + i) * kBlk + key_in;
-                uint32_t z[kRows];
-                tmem_ld32(zt, z);
-                const float ks = sh.ks[b][key_in >> 4], vs = sh.vs[b][key_in >> 4];
-                const bool is = key < s.len && ((sh.has[b] >> (key_in >> 4)) & 1u) != 0u;
-                // rows [from, 32) see this key: later tokens of the window see more
-                const int from = !is ? kRows : key < whole_seen ? 0 : max(0, (key - whole_seen) * a.group - row0);
-                float big = 0.f;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const float v = fabsf(sh.vs[b][g]);
-                    if (v < INFINITY) big = fmaxf(big, v);
-                }
-                const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
-                const float sc = unit_scale * ks;
-                // Scores less their rows' references; does any pass 2^15 (the largest had 2^7 when its reference was set)?
-                // They are rounded before that, as the references are, so that however large they are none passes the
-                // largest (not packed: a packed product and sum would become one with a single rounding).
-                float over = -INFINITY;
-                auto less_ref = [&]() {
-                    tc::tmem_wait_ld();
-                    if (mixed) {
-#pragma unroll
-                        for (int r = 0; r < kRows; ++r) z[r] = __float_as_uint(f_of(z[r]) * sh.f[r]);
-                    }
-#pragma unroll
-                    for (int c = 0; c < kRows / 4; ++c) {
-                        const float4 m = *reinterpret_cast<const float4*>(&sh.ref[st][4 * c]);
-                        z[4 * c] = __float_as_uint(__fmul_rn(f_of(z[4 * c]), sc) - m.x);
-                        z[4 * c + 1] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 1]), sc) - m.y);
-                        z[4 * c + 2] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 2]), sc) - m.z);
-                        z[4 * c + 3] = __float_as_uint(__fmul_rn(f_of(z[4 * c + 3]), sc) - m.w);
-                    }
-                };
-                less_ref();
-                if (from == 0) {
-#pragma unroll
-                    for (int r = 0; r < kRows; r += 2) over = max3(over, f_of(z[r]), f_of(z[r + 1]));
-                } else {
-#pragma unroll
-                    for (int r = 0; r < kRows; ++r)
-                        if (r >= from) over = fmaxf(over, f_of(z[r]));
-                }
-                if (any4(st, over > 15.f || unit || late)) {
-                    gone = any4(st, late);
-                    if (gone) break;
-                    // new references: the largest scores met so far
-                    {
-                        float x[kRows];
-                        tmem_ld32(zt, reinterpret_cast<uint32_t*>(x));
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int r = 0; r < kRows; ++r) x[r] = r >= from ? x[r] * sh.f[r] * sc : -INFINITY;
-                        sh.top[st][q4][lane] = reduce_rows(x, larger);
-                    }
-                    (void)any4(st, false);
-                    float ratio = 1.f;
-                    if (unit) {
-                        vtop = fmaxf(vtop, big);
-                        const float nu = fmaxf(big, vtop * 9.094947e-13f);
-                        ratio = vu == 0.f ? 0.f : vu / nu;
-                        vu = nu;
-                    }
-                    if (q4 == 0) {
-                        const float was = sh.ref[st][lane];
-                        const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
-                        const float now = top - was > 15.f ? top - 7.f : was;
-                        sh.by[st][lane] = ex2(was - now);
-                        sh.ref[st][lane] = now;
-                    }
-                    (void)any4(st, false);
-#pragma unroll
-                    for (int r = 0; r < kRows; ++r) l[r] *= sh.by[st][r];
-                    if (i >= 2) {
-                        // (the products into O up to here ended with the scores that were waited for)
-                        uint32_t o[kRows];
-                        tmem_ld32(ot, o);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int r = 0; r < kRows; ++r) o[r] = __float_as_uint(f_of(o[r]) * (sh.by[st][r] * ratio));
-                        tmem_st32(ot, o);
-                        tc::tmem_wait_st();
-                    }
+            // (two copies: with the rows' own units in the one that runs, ordinary blocks took 3 to 7 % longer)
+            auto blocks = [&](auto own) {
+                constexpr bool kOwn = decltype(own)::value;
+                for (int i = st; i < s.count && !gone; i += 2) {
+                    const bool late = !warp_wait(&sh.z_full[st], zc++ & 1u);
+                    tc::fence_after_sync();
+                    const int b = (int)((blk0 + i) & 7u), key = (s.i0 + i) * kBlk + key_in;
+                    uint32_t z[kRows];
                     tmem_ld32(zt, z);
-                    less_ref();
-                }
-                const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs / vu;
-                unsigned char* at = sp + st * kPBytes + key_in * 64;
+                    const float ks = sh.ks[b][key_in >> 4], vs = sh.vs[b][key_in >> 4];
+                    const bool is = key < s.len && ((sh.has[b] >> (key_in >> 4)) & 1u) != 0u;
+                    // rows [from, 32) see this key: later tokens of the window see more
+                    const int from = !is ? kRows : key < whole_seen ? 0 : max(0, (key - whole_seen) * a.group - row0);
+                    float big = 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 8 * c + 2 * e;
-                        // a row that has seen nothing has the first reference; its weights are replaced below
-                        float2 y = make_float2(ex2(f_of(z[r])), ex2(f_of(z[r + 1])));
-                        if (from > 0) {
-                            if (r < from) y.x = 0.f;
-                            if (r + 1 < from) y.y = 0.f;
-                        }
-                        l[r] += y.x;
-                        l[r + 1] += y.y;
-                        y = __fmul2_rn(y, make_float2(pv, pv));
-                        p[e] = pack_f16(y.x, y.y);
+                    for (int g = 0; g < kGroups; ++g) {
+                        const float v = fabsf(sh.vs[b][g]);
+                        if (v < INFINITY) big = fmaxf(big, v);
                     }
-                    *reinterpret_cast<uint4*>(at + ((c ^ ((key_in >> 1) & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                    const bool unit = !(big <= vu && big * 64.f >= vu) && big > 0.f;  // the same for every thread
+                    const float sc = unit_scale * ks;
+                    // Scores less their rows' references; does any pass 2^15 (the largest had 2^7 when its reference was set)?
+                    // Where rows have units of their own, or scores may pass 2^20 (|z| < 2^31), this is not yet the answer.
+                    const bool far = fabsf(sc) > kFar;
+                    float over = -INFINITY;
+                    auto less_ref = [&](float mul) {
+#pragma unroll
+                        for (int c = 0; c < kRows / 4; ++c) {
+                            const float4 m = *reinterpret_cast<const float4*>(&sh.ref[st][4 * c]);
+                            z[4 * c] = __float_as_uint(fmaf(f_of(z[4 * c]), mul, -m.x));
+                            z[4 * c + 1] = __float_as_uint(fmaf(f_of(z[4 * c + 1]), mul, -m.y));
+                            z[4 * c + 2] = __float_as_uint(fmaf(f_of(z[4 * c + 2]), mul, -m.z));
+                            z[4 * c + 3] = __float_as_uint(fmaf(f_of(z[4 * c + 3]), mul, -m.w));
+                        }
+                    };
+                    tc::tmem_wait_ld();
+                    less_ref(sc);
+                    if (from == 0) {
+#pragma unroll
+                        for (int r = 0; r < kRows; r += 2) over = max3(over, f_of(z[r]), f_of(z[r + 1]));
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r)
+                            if (r >= from) over = fmaxf(over, f_of(z[r]));
+                    }
+                    if (any4(st, over > 15.f || unit || late || kOwn || far)) {
+                        gone = any4(st, late);
+                        if (gone) break;
+                        // new references: the largest scores met so far
+                        {
+                            float x[kRows];
+                            tmem_ld32(zt, reinterpret_cast<uint32_t*>(x));
+                            tc::tmem_wait_ld();
+                            if constexpr (kOwn) {
+#pragma unroll
+                                for (int r = 0; r < kRows; ++r) x[r] *= sh.f[r];
+                            }
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) x[r] = r >= from ? x[r] * sc : -INFINITY;
+                            sh.top[st][q4][lane] = reduce_rows(x, larger);
+                        }
+                        (void)any4(st, false);
+                        float ratio = 1.f;
+                        if (unit) {
+                            vtop = fmaxf(vtop, big);
+                            const float nu = fmaxf(big, vtop * 9.094947e-13f);
+                            ratio = vu == 0.f ? 0.f : vu / nu;
+                            vu = nu;
+                        }
+                        if (q4 == 0) {
+                            const float was = sh.ref[st][lane];
+                            const float top = fmaxf(fmaxf(sh.top[st][0][lane], sh.top[st][1][lane]), fmaxf(sh.top[st][2][lane], sh.top[st][3][lane]));
+                            const float now = top - was > 15.f ? top - 7.f : was;
+                            sh.by[st][lane] = ex2(was - now);
+                            sh.ref[st][lane] = now;
+                        }
+                        (void)any4(st, false);
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r) l[r] *= sh.by[st][r];
+                        if (i >= 2) {
+                            // (the products into O up to here ended with the scores that were waited for)
+                            uint32_t o[kRows];
+                            tmem_ld32(ot, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) o[r] = __float_as_uint(f_of(o[r]) * (sh.by[st][r] * ratio));
+                            tmem_st32(ot, o);
+                            tc::tmem_wait_st();
+                        }
+                        // The scores anew, in the rows' units.  Large ones are rounded, as their reference was, before it comes off,
+                        // so that none passes the largest, however large they are.
+                        tmem_ld32(zt, z);
+                        tc::tmem_wait_ld();
+                        if constexpr (kOwn) {
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) {
+                                const float x = f_of(z[r]) * sh.f[r], m = sh.ref[st][r];
+                                z[r] = __float_as_uint(sh.f[r] * fabsf(sc) > kFar ? __fmul_rn(x, sc) - m : fmaf(x, sc, -m));
+                            }
+                        } else {
+                            const float mul = far ? 1.f : sc, up = far ? sc : 1.f;
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) z[r] = __float_as_uint(__fmul_rn(f_of(z[r]), up));
+                            less_ref(mul);
+                        }
+                    }
+                    const float pv = vu == 0.f ? (vs == vs ? 0.f : vs) : vs / vu;
+                    unsigned char* at = sp + st * kPBytes + key_in * 64;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 8 * c + 2 * e;
+                            // a row that has seen nothing has the first reference; its weights are replaced below
+                            float2 y = make_float2(ex2(f_of(z[r])), ex2(f_of(z[r + 1])));
+                            if (from > 0) {
+                                if (r < from) y.x = 0.f;
+                                if (r + 1 < from) y.y = 0.f;
+                            }
+                            l[r] += y.x;
+                            l[r + 1] += y.y;
+                            y = __fmul2_rn(y, make_float2(pv, pv));
+                            p[e] = pack_f16(y.x, y.y);
+                        }
+                        *reinterpret_cast<uint4*>(at + ((c ^ ((key_in >> 1) & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                    tc::fence_async_smem();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sh.p_full[st]);
                 }
-                tc::fence_async_smem();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.p_full[st]);
-            }
+            };
+            if (mixed) blocks(std::true_type{});
+            else blocks(std::false_type{});
             blk0 += s.count;
             const bool both = s.count > 1;
             bool late = false;

@@ -297,3 +297,19 @@ def test_prefill_waits_that_give_up_show(monkeypatch, d):
         assert torch.equal(out[~lost], clean[~lost]), (tries, int((out == 123.0).all(-1).sum()))
         assert tries != "0" or bool(lost.all())
         assert torch.equal(B.kda_attention_prefill(q, k, v, cu_seqlens=offsets(lens)), clean)
+
+
+@pytest.mark.parametrize("code", CODES, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("up", [2.0 ** 8, 2.0 ** 20, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("hq,window", [(2, 1), (4, 7)], ids=["2", "28"])
+def test_decode_huge_key_scales(hq, window, up, code):
+    """Huge scores from the keys' scales, on some of the pages alone: those of the others count for nothing or all."""
+    lens, page, d = [700, 40, 131], 32, 128
+    table, pool = tables(lens, page, capacity=768)
+    c = filled(pool, 1, page, d, code, seed=9)
+    ks = c.k_scale.clone()
+    ks[::3] *= up
+    cache = B.KvCache(c.k, c.v, ks, c.v_scale)
+    q = make(len(lens) * window, hq, 1, d, torch.bfloat16, 18)[0]
+    out = B.kda_attention_decode(q, cache, table, i32(*lens))
+    close(out, ref.decode(q, cache, table, lens), ref.dequant(cache.v, cache.v_scale), torch.bfloat16, 2.0 ** -11)
