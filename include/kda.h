@@ -312,6 +312,10 @@ kda_status_t kda_epilogue(const void* o, const void* gate, const float* weight, 
  * Softmax attention next to the recurrence, for the full-attention layers that a hybrid stack puts
  * between its KDA layers ("Kimi K3" reading notes, section 7, "Scaling to 1M Tokens: NoPE and KDA
  * Context Parallelism": such layers carry no position encoding, so a key enters a cache as it is).
+ * The form is that of grouped heads of 32, 64 or 128 channels with keys and values of their own.  The
+ * notes' own stack has Gated MLA there, whose heads all read one latent of 576 scalars a token: that is
+ * another form, which these calls do not hold.  A prompt begins its sequence: a call sees no keys but
+ * its own (tokens after a cached context go through kda_attention_decode as a window).
  * Query head h reads key head h / (num_heads / num_kv_heads):
  *
  *   z_ij = scale * (q_i . k_j)      j over the keys that row i sees

@@ -9,13 +9,14 @@
 // little.  Warps take 16 rows each; keys come in tiles of half as many.  Two CTAs share an SM: with
 // 128 rows and one CTA the longest rows of a few prompts set the time (prompts of 200 to 1300
 // tokens, 10 of 2 heads of 128 channels, one CTA a tile: 208 us against 196).  With few tiles two CTAs of a cluster take
-// a tile's key tiles in turn and join their sums through each other's shared memory (152 us; see launch_d).
+// a tile's key tiles in turn and join their sums through each other's shared memory (see launch_d).
 // An fp32 operand x enters m16n8k16 bf16 products as x1 + x2 + x3 with
-// x1 = bf16(x), x2 = bf16(x - x1), x3 = bf16(x - x1 - x2) (24 bits, fp32's range), a product as its six
+// x1 = bf16(x), finite wherever x is, x2 = bf16(x - x1), x3 = bf16(x - x1 - x2) (24 bits, fp32's range), a product as its six
 // terms down to 2^-16 of the first.  Those products bound it: at 128 channels 12 a warp and key,
 // about 8 cycles each on a sub-partition that two warps share; a tile's loads overlap with the products of
 // the tile before it where the registers for them are there (up to 64 channels).
 //
+// Keys with an infinity or NaN take their scores from the fp32 values, one by one.
 // Hidden keys: a score is replaced, not added to, and an infinity or NaN in V leaves the tile and is
 // noted by channel and position; at the end it joins the rows that see it, so no row meets another
 // sequence's or a later token's infinities.
@@ -475,11 +476,11 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s)
 }
 
 // Up to three tiles an SM, two CTAs share a tile's keys: the longest tiles alone then set the time.  One and two
-// CTAs a tile, 16 of 4 heads of 128 channels unless said, us: a prompt of 1200 tokens (304 tiles) 184 and 124; prompts
-// of 200 to 1300, 10 of 2 heads (380 tiles) 183 and 152; one of 1800 (452 tiles) 281 and 278; of 2400 (604) 430 and
-// 450; 8 of 1000 to 4000 4218 and 4516; 60 of 100, 10 of 2 heads (1120 tiles) 86 and 120.  Four CTAs: 174 where two take
-// 152.  The lengths are not known here: a prompt of 1500 packed before those 60 begins last and takes 324 us by one
-// and 256 by two, packed after them 236 and 254.
+// CTAs a tile, 16 of 4 heads of 128 channels unless said, us: a prompt of 1200 tokens (304 tiles) 182 and 127; prompts
+// of 200 to 1300, 10 of 2 heads (380 tiles) 181 and 158; one of 1800 (452 tiles) 279 and 286; of 2400 (604) 419 and
+// 456; 8 of 1000 to 4000 4198 and 4551; 60 of 100, 10 of 2 heads (1120 tiles) 82 and 126.  (Four CTAs: 174 where two took
+// 152.)  The lengths are not known here: a prompt of 1500 packed before those 60 begins last and takes 315 us by one
+// and 266 by two, packed after them 231 and 262.
 template <int D>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t s)
 {

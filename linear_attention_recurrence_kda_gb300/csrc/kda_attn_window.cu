@@ -11,9 +11,9 @@
 // is idle, a key's scales are the thread's own, and no score crosses lanes but at a change of the
 // reference.  Few columns make the products cheap (about 128 cycles each a block).
 //
-// What bounds it: of an SM's cycles at work, loads and stores keep the path to shared memory busy 51 %, the
-// products' reads 23 %; a unit's start and end cost as much as 5 blocks (64 sequences of 300 to 6000 keys, 28
-// rows of 8 heads: 131 us, 3.2 TB/s, where HBM would allow 62).
+// What bounds it: of an SM's cycles at work, loads and stores keep the path to shared memory busy 49 %, the
+// products' reads 22 %; a unit's start and end cost as much as 5 blocks (64 sequences of 300 to 6000 keys, 28
+// rows of 8 heads: 134 us with the join, 3.1 TB/s, where HBM would allow 62).
 //
 // Blocks alternate between two streams, each with its own reference, sums and O, so that one's softmax
 // runs while the other waits; at the end of a unit the first stream joins them.  Tensor memory: Z0 | Z1 |
@@ -45,8 +45,8 @@ constexpr int kRaw = 4;    // raw tiles (K and V in turn) on their way or waitin
 constexpr int kGroups = kBlk / 16;
 // What a unit's start and end cost (q, the first references, the streams' join), in blocks.  Cut by blocks alone,
 // the CTAs that hold short sequences end last: SMs were at work 70 % of the time, now 92 %.  28 rows of 8 heads,
-// us for a cost of 0, 3, 5, 10: 64 sequences of 300 to 6000 keys 176, 139, 133, 138; 200 of 100 to 900
-// 194, 134, 130, 137; 256 of 256 to 600 170, 157, 156, 159; 64 of 3150 132, 130, 131, 132.
+// us for a cost of 0, 3, 5, 10: 64 sequences of 300 to 6000 keys 174, 140, 134, 141; 200 of 100 to 900
+// 196, 138, 132, 138; 256 of 256 to 600 173, 160, 158, 161; 64 of 3150 134, 132, 133, 134.
 constexpr int kUnitCost = 5;
 // warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
 constexpr int kRegsSoftmax = 168, kRegsOther = 88;
@@ -798,9 +798,10 @@ cudaError_t launch_window_d(const AttnDecodeArgs& a, cudaStream_t s)
 }  // namespace
 
 // From 25 rows a key head, where the page table holds more than 512 keys a sequence.  Measured here and on
-// the warp-level form, us: 28 rows of 8 heads, 64 sequences of 3150 keys 131 and 191; 56 rows 248 and 369; one
-// sequence of 4000, one head 13.5 and 14.8; but 20 rows of one head, 64 of 1000 23.9 and 20.7; and 28 rows of
-// 8 heads, 256 of 300 133 and 115, where a unit's start and end outweigh its keys (of 500: 152 and 152, of 700 185 and 192).
+// the warp-level form, us: 28 rows of 8 heads, 64 sequences of 3150 keys 133 and 193; 56 rows 249 and 365; one
+// sequence of 4000, one head 13.8 and 16.1; but 20 rows of one head, 64 of 1000 23.7 and 20.6; and 28 rows of
+// 8 heads, 256 of 300 136 and 113, where a unit's start and end outweigh its keys (of 500: 154 and 151, of 700 188 and
+// 191).  The lengths are not known here: a table that is wide for its sequences takes this form for short ones too.
 bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt, int64_t capacity)
 {
     return dt == KDA_BF16 && d == D && rows > 24 && capacity > 512;
