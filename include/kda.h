@@ -398,6 +398,59 @@ kda_status_t kda_attention_prefill(const void* q, const void* k, const void* v, 
 kda_status_t kda_cache_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths,
                               const kda_cache_t* cache, const kda_attention_t* problem, uint32_t* check, void* stream);
 
+/*
+ * Rotary positions (host memory).  The first rot_dim channels of a head are taken in pairs and each pair is turned
+ * by an angle, position * freq:
+ *
+ *   y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin       channels past rot_dim stay as they are
+ *
+ * A token has a position on each axis (one for text; time, row and column for images and video) and a pair follows one of them.
+ * The pages' own full-attention layers carry no positions; these calls serve stacks with grouped heads that do.
+ */
+typedef struct {
+    int32_t rot_dim;   /* channels that turn: a multiple of 16, at most head_dim                     */
+    int32_t axes;      /* positions of a token: 1 to 4                                              */
+    int32_t adjacent;  /* pair i is channels (i, i + rot_dim / 2), or (2 i, 2 i + 1) where this is 1 */
+    int32_t reserved;  /* 0                                                                         */
+    uint8_t axis[64];  /* the axis of pair i < rot_dim / 2, below axes                               */
+    double freq[64];   /* radians a position of pair i < rot_dim / 2, at most 2^16 in magnitude      */
+} kda_rotary_t;
+
+/*
+ * Queries and keys turned by their positions, for prompts and for training (the gradient of a turn is the turn back:
+ * `inverse` 1 on the gradients).
+ *
+ *   q : [T_tot, num_heads, head_dim], k : [T_tot, num_kv_heads, head_dim] io dtype, strides as for
+ *       kda_attention_prefill; either may be NULL (with its output).
+ *   cu_seqlens : as for kda_forward (device [N+1], or NULL for N equal lengths).  Not validated on the device:
+ *       invalid offsets give unspecified outputs (never an access outside the tensors).  Rows past the last
+ *       sequence's are left as they were.
+ *   lengths : [N] int32 on the device, tokens of each sequence INCLUDING the T_tot new ones as for kda_cache_append,
+ *       or NULL where the sequences begin with them.  Not read where positions are given.
+ *   positions : [axes, T_tot] int32 on the device, any values; or NULL: a token's place in its sequence, from 0, on every axis.
+ *   q_out, k_out : packed outputs like q and k, or q and k themselves (in place, strides and all); no other overlap.
+ *   problem : num_seqs, total_tokens, num_heads, num_kv_heads, head_dim, io_dtype, q_stride, k_stride (the rest unused).
+ * Angles are reduced exactly (a position times freq as a 64-bit fraction of a turn), so that far positions lose nothing
+ * to fp32; arithmetic is fp32, rounded to the io dtype once.
+ */
+kda_status_t kda_rotary(const void* q, const void* k, const int32_t* cu_seqlens, const int32_t* lengths,
+                        const int32_t* positions, void* q_out, void* k_out, const kda_attention_t* problem,
+                        const kda_rotary_t* rotary, int32_t inverse, void* stream);
+
+/*
+ * kda_cache_append of keys turned by their positions, in one launch: k is turned in fp32 and rounded once, to the codes
+ * (its scale follows the turned values); v enters as it is.  q, where given, is turned in the same call.
+ *
+ *   q : [T_tot, num_heads, head_dim] io dtype (q_stride), or NULL;  q_out : as for kda_rotary.
+ *   positions : as for kda_rotary; NULL: a token's place in its sequence, lengths[n] - (new tokens) + i.
+ *   rows of q past the last sequence's are left as they were; a sequence that is skipped (see kda_cache_append) has its
+ *   queries turned all the same.
+ * All else as for kda_cache_append.  num_heads is not used where q is NULL.
+ */
+kda_status_t kda_rotary_append(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths,
+                               const int32_t* positions, void* q_out, const kda_cache_t* cache, const kda_attention_t* problem,
+                               const kda_rotary_t* rotary, uint32_t* check, void* stream);
+
 /* Bytes of device workspace kda_attention_decode needs (0 if the descriptor is invalid). */
 size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem);
 

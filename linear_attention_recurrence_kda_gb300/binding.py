@@ -41,7 +41,7 @@ EXPORTS = ("kda_forward_workspace_bytes", "kda_forward", "kda_decode_step", "kda
            "kda_epilogue", "kda_static_scratch_status", "kda_backward_workspace_bytes", "kda_backward",
            "kda_forward_summary_workspace_bytes", "kda_forward_summary", "kda_state_scan",
            "kda_attention_prefill", "kda_cache_append", "kda_attention_decode_workspace_bytes",
-           "kda_attention_decode")
+           "kda_attention_decode", "kda_rotary", "kda_rotary_append")
 
 # Size of the library's own scratch array used by kda_forward_static_scratch.
 KDA_STATIC_SCRATCH_BYTES = 8 << 20
@@ -78,6 +78,12 @@ class KdaCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
                 ("page_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class KdaRotary(ctypes.Structure):
+    """Mirror of kda_rotary_t."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("axis", ctypes.c_uint8 * 64), ("freq", ctypes.c_double * 64)]
 
 
 class KvCache(NamedTuple):
@@ -157,6 +163,11 @@ def lib():
             L.kda_attention_decode_workspace_bytes.argtypes = [PA]
             L.kda_attention_decode.restype = ctypes.c_int
             L.kda_attention_decode.argtypes = [_vp, _vp, PC, _vp, PA, _vp, ctypes.c_size_t, _vp]
+            PR = ctypes.POINTER(KdaRotary)
+            L.kda_rotary.restype = ctypes.c_int
+            L.kda_rotary.argtypes = [_vp] * 7 + [PA, PR, ctypes.c_int32, _vp]
+            L.kda_rotary_append.restype = ctypes.c_int
+            L.kda_rotary_append.argtypes = [_vp] * 7 + [PC, PA, PR, _vp, _vp]
             L.kda_abi_version.restype = ctypes.c_uint32
             L.kda_abi_version.argtypes = []
             _lib = L
@@ -662,6 +673,134 @@ def kda_cache_append(k, v, cache: KvCache, block_table, lengths, cu_seqlens=None
                                 lengths.data_ptr(), ctypes.byref(c), ctypes.byref(prob), _ptr(check), _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_cache_append")
+
+
+@functools.lru_cache(maxsize=256)
+def make_rotary(rot_dim: int, base: float = 10000.0, freqs: Optional[tuple] = None, sections: Optional[tuple] = None,
+                axis: Optional[tuple] = None, adjacent: bool = False) -> KdaRotary:
+    """A rotary descriptor (see include/kda.h) of ``rot_dim`` channels: pair i turns by ``freqs[i]`` radians a position
+    (default base ** (-2 i / rot_dim)).  ``sections``: how many pairs follow each axis, in order; or ``axis``: the axis of
+    every pair; neither: one axis.  ``adjacent``: pairs are channels (2 i, 2 i + 1) and not (i, i + rot_dim / 2).
+    Sequences are given as tuples; equal arguments give the same descriptor, which is not to be changed."""
+    pairs = int(rot_dim) // 2
+    if rot_dim < 2 or rot_dim % 2 or pairs > 64:
+        raise ValueError(f"rot_dim {rot_dim}: an even number of at most 128 channels is needed")
+    if sections is not None and axis is not None:
+        raise ValueError("sections and axis say the same thing: give one")
+    if sections is not None:
+        if any(int(n) < 0 for n in sections):
+            raise ValueError(f"sections {sections}: a count of pairs is negative")
+        axes, axis = len(sections), tuple(a for a, n in enumerate(sections) for _ in range(int(n)))
+    elif axis is not None:
+        axes = max(axis, default=0) + 1
+        if any(not 0 <= int(a) < 4 for a in axis):
+            raise ValueError(f"axis {axis}: axes are 0 to 3")
+    else:
+        axes, axis = 1, (0,) * pairs
+    if freqs is None:
+        freqs = tuple(float(base) ** (-2.0 * i / rot_dim) for i in range(pairs))
+    if len(axis) != pairs or len(freqs) != pairs:
+        raise ValueError(f"{rot_dim} channels are {pairs} pairs: got axes for {len(axis)}, frequencies for {len(freqs)}")
+    if not 1 <= axes <= 4:
+        raise ValueError(f"{axes} axes: 1 to 4")
+    return KdaRotary(int(rot_dim), axes, int(bool(adjacent)), 0, (ctypes.c_uint8 * 64)(*[int(a) for a in axis]),
+                     (ctypes.c_double * 64)(*freqs))
+
+
+def _turned(x, name, out, dtype, heads, d, device, stream):
+    """The output of a tensor that turns, and the input's stride: a packed tensor, or the input itself."""
+    stride = _tokens(x, name, dtype, heads, d, device)
+    if out is None:
+        return _empty((x.shape[0], heads, d), dtype, device, stream), stride
+    if out.data_ptr() == x.data_ptr() and x.shape[0] > 0:
+        if _tokens(out, f"{name}_out", dtype, heads, d, device) != stride or out.shape != x.shape:
+            raise ValueError(f"{name}_out: in place it has {name}'s own shape and strides")
+    else:
+        _need(out, f"{name}_out", dtype, (x.shape[0], heads, d), device)
+    return out, stride
+
+
+def _seqs(cu_seqlens, lengths, num_seqs, device):
+    """The number of sequences, with cu_seqlens and lengths checked."""
+    if cu_seqlens is not None:
+        N = cu_seqlens.shape[0] - 1
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), device)
+    elif lengths is not None:
+        N = lengths.shape[0]
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (N,), device)
+    return N
+
+
+def kda_rotary(rotary: KdaRotary, q=None, k=None, positions=None, cu_seqlens=None, num_seqs: Optional[int] = None,
+               lengths=None, q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """Queries and keys turned by their positions (see include/kda.h): q [T, Hq, d], k [T, Hkv, d] in bf16 or fp32 (either
+    may be None; strides as for :func:`kda_attention_prefill`); positions [axes, T] int32, or None: every token's place in
+    its sequence (cu_seqlens [N+1] int32, or N equal lengths; ``lengths`` [N] int32 where sequences hold tokens before
+    these).  ``inverse`` turns back: q and k are then gradients of turned ones.  ``q_out`` may be q and ``k_out`` k
+    (in place).  Returns (q_out, k_out)."""
+    if q is None and k is None:
+        raise ValueError("q or k is required")
+    x, name = (k, "k") if q is None else (q, "q")
+    T, heads, d = x.shape
+    dev, dt = x.device, x.dtype
+    io = _io_dtype(x, name)
+    if q is not None and k is not None and k.shape[0] != T:
+        raise ValueError(f"q, k hold {T}, {k.shape[0]} tokens")
+    N = _seqs(cu_seqlens, lengths, num_seqs, dev)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (rotary.axes, T), dev)
+    Hq = heads if q is not None else k.shape[1]
+    Hkv = k.shape[1] if k is not None else Hq
+    qs = ks = 0
+    if q is not None:
+        q_out, qs = _turned(q, "q", q_out, dt, Hq, d, dev, stream)
+    if k is not None:
+        k_out, ks = _turned(k, "k", k_out, dt, Hkv, d, dev, stream)
+    prob = KdaAttention(N, T, Hq, Hkv, d, io, 1.0, qs, ks, 0)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = lib().kda_rotary(p(q), p(k), p(cu_seqlens), p(lengths), p(positions), p(q_out) if q is not None else None,
+                          p(k_out) if k is not None else None, ctypes.byref(prob), ctypes.byref(rotary),
+                          1 if inverse else 0, _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rotary")
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def kda_rotary_append(rotary: KdaRotary, k, v, cache: KvCache, block_table, lengths, q=None, positions=None,
+                      cu_seqlens=None, q_out=None, check=None, stream=None):
+    """:func:`kda_cache_append` of keys turned by their positions, in one launch (see include/kda.h): positions
+    [axes, T] int32, or None: every token's place in its sequence, as ``lengths`` give it.  ``q`` [T, Hq, d], where given, is
+    turned in the same call.  Returns q_out (``q_out`` may be q: in place), or None without q."""
+    T, Hkv, d = k.shape
+    dev, dt = k.device, k.dtype
+    io = _io_dtype(k, "k")
+    N = lengths.shape[0]
+    ks, vs = _tokens(k, "k", dt, Hkv, d, dev), _tokens(v, "v", dt, Hkv, d, dev)
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError(f"k, v, q hold {T}, {v.shape[0]}, {T if q is None else q.shape[0]} tokens")
+    _need(lengths, "lengths", torch.int32, (N,), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (rotary.axes, T), dev)
+    if check is not None and (check.numel() * check.element_size() < 256 or not check.is_contiguous() or check.device != dev):
+        raise ValueError("check: 256 contiguous bytes on the inputs' device are needed")
+    c = _cache(cache, block_table, N, Hkv, d, dev)
+    Hq, qs = Hkv, 0
+    if q is not None:
+        Hq = q.shape[1]
+        q_out, qs = _turned(q, "q", q_out, dt, Hq, d, dev, stream)
+    prob = KdaAttention(N, T, Hq, Hkv, d, io, 1.0, qs, ks, vs)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = lib().kda_rotary_append(p(q), k.data_ptr(), v.data_ptr(), p(cu_seqlens), lengths.data_ptr(), p(positions),
+                                 p(q_out) if q is not None else None, ctypes.byref(c), ctypes.byref(prob),
+                                 ctypes.byref(rotary), p(check), _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rotary_append")
+    return q_out if q is not None else None
 
 
 def kda_attention_decode_workspace_bytes(problem: KdaAttention) -> int:

@@ -6,6 +6,7 @@
 
 #include "kda_attn.cuh"
 #include "kda_checks.cuh"
+#include "kda_rotary.cuh"
 
 using namespace kda::checks;
 
@@ -100,6 +101,107 @@ kda::CacheArgs cache_args(const kda_cache_t& c)
     return a;
 }
 
+// The rotary descriptor, and its frequencies as fractions of a turn.
+kda_status_t check_rotary(const kda_rotary_t* r, const kda_attention_t& p, bool inverse, kda::TurnArgs* out)
+{
+    if (r == nullptr) return KDA_ERR_INVALID_ARG;
+    if (r->rot_dim < 1 || r->rot_dim > p.head_dim || r->axes < 1 || r->axes > 4) return KDA_ERR_INVALID_ARG;
+    if ((r->adjacent != 0 && r->adjacent != 1) || r->reserved != 0) return KDA_ERR_INVALID_ARG;
+    if (r->rot_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
+    out->rot = r->rot_dim;
+    out->axes = r->axes;
+    out->adjacent = r->adjacent;
+    out->d = p.head_dim;
+    for (int i = 0; i < r->rot_dim / 2; ++i) {
+        if (r->axis[i] >= r->axes || !(std::fabs(r->freq[i]) <= 65536.0)) return KDA_ERR_INVALID_ARG;
+        const double turns = r->freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+        const double part = turns - std::nearbyint(turns);      // exact, within a half
+        const uint64_t mag = (uint64_t)std::ldexp(std::fabs(part), 64);
+        out->turn[i] = (part < 0.0) != inverse ? 0 - mag : mag;
+        out->axis[i] = r->axis[i];
+    }
+    return KDA_OK;
+}
+
+// One tensor that turns: its range, its output's, and where they lie (packed, or the input itself).
+kda_status_t check_turned(const void* in, void* out, int64_t heads, int64_t stride, const kda_attention_t& p, int which,
+                          kda::TurnRows* rows, Range* r_in, Range* r_out)
+{
+    rows->heads[which] = in != nullptr ? (int32_t)heads : 0;
+    *r_in = *r_out = Range{0, 0};
+    if ((in == nullptr) != (out == nullptr)) return KDA_ERR_INVALID_ARG;
+    if (in == nullptr) return KDA_OK;
+    if (!aligned(in, 16) || !aligned(out, 16)) return KDA_ERR_INVALID_ARG;
+    const int64_t row = heads * p.head_dim;
+    const size_t io = io_size(p.io_dtype);
+    rows->in[which] = in;
+    rows->out[which] = out;
+    rows->in_stride[which] = stride;
+    rows->out_stride[which] = in == out ? stride : row;
+    *r_in = range_of(in, strided_bytes(p.total_tokens, stride, row, io));
+    *r_out = in == out ? *r_in : range_of(out, (size_t)p.total_tokens * row * io);
+    if (in != out && overlaps(*r_in, *r_out)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// Rows of one stride that lie between one another without touching, as the views of one projection do.
+bool interleaved(const void* a, size_t row_a, int64_t stride_a, const void* b, size_t row_b, int64_t stride_b, size_t io)
+{
+    if (stride_a != stride_b) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const size_t off = x < y ? y - x : x - y, gap = (size_t)stride_a * io;
+    return x < y ? off >= row_a && off + row_b <= gap : off >= row_b && off + row_a <= gap;
+}
+
+// The arguments of an append, past its descriptor.  `out`: what the call writes beside the cache (turned queries).
+kda_status_t check_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,
+                          const kda_attention_t& p, uint32_t* check, const Range* more_in, int more, Range out, kda::AppendArgs& a)
+{
+    kda_status_t st;
+    if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    if ((st = token_stride(p.k_stride, p.num_kv_heads, p, &a.ks)) != KDA_OK) return st;
+    if ((st = token_stride(p.v_stride, p.num_kv_heads, p, &a.vs)) != KDA_OK) return st;
+    CacheRanges rc;
+    if ((st = check_cache(cache, p, &rc)) != KDA_OK) return st;
+    if (lengths == nullptr || (p.total_tokens > 0 && (!k || !v))) return KDA_ERR_INVALID_ARG;
+    if (p.total_tokens / cache->page_tokens + 2LL * p.num_seqs > 2147483647LL) return KDA_ERR_UNSUPPORTED;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lengths, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(check, 256)) return KDA_ERR_INVALID_ARG;
+    const size_t io = io_size(p.io_dtype);
+    const int64_t row = (int64_t)p.num_kv_heads * p.head_dim;
+    const Range in[5] = {range_of(k, strided_bytes(p.total_tokens, a.ks, row, io)),
+                         range_of(v, strided_bytes(p.total_tokens, a.vs, row, io)),
+                         range_of(lengths, (size_t)p.num_seqs * 4),
+                         range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0), rc.r[4]};
+    const Range rk = range_of(check, check ? 4 : 0);
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in) {
+            if (overlaps(rc.r[i], r)) return KDA_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < i; ++j) {
+            if (overlaps(rc.r[i], rc.r[j])) return KDA_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < more; ++j) {
+            if (overlaps(rc.r[i], more_in[j])) return KDA_ERR_INVALID_ARG;
+        }
+        if (overlaps(rk, rc.r[i]) || overlaps(out, rc.r[i])) return KDA_ERR_INVALID_ARG;
+    }
+    for (const Range& r : in) {
+        if (overlaps(rk, r) || overlaps(out, r)) return KDA_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < more; ++j) {
+        if (overlaps(rk, more_in[j])) return KDA_ERR_INVALID_ARG;
+    }
+    if (overlaps(rk, out)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : {k, v, (const void*)lengths, (const void*)cu_seqlens, (const void*)check}) {
+        if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
+    }
+    if ((st = check_cache_pointers(*cache)) != KDA_OK) return st;
+    a.k = k; a.v = v; a.cu = cu_seqlens; a.lengths = lengths; a.check = check;
+    a.T = p.total_tokens; a.N = p.num_seqs; a.Hkv = p.num_kv_heads; a.d = p.head_dim; a.c = cache_args(*cache);
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -172,45 +274,104 @@ kda_status_t kda_cache_append(const void* k, const void* v, const int32_t* cu_se
     kda_status_t st = check_attention(problem, false);
     if (st != KDA_OK) return st;
     const kda_attention_t& p = *problem;
-    if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
     kda::AppendArgs a{};
-    if ((st = token_stride(p.k_stride, p.num_kv_heads, p, &a.ks)) != KDA_OK) return st;
-    if ((st = token_stride(p.v_stride, p.num_kv_heads, p, &a.vs)) != KDA_OK) return st;
-    CacheRanges rc;
-    if ((st = check_cache(cache, p, &rc)) != KDA_OK) return st;
-    if (lengths == nullptr || (p.total_tokens > 0 && (!k || !v))) return KDA_ERR_INVALID_ARG;
-    if (p.total_tokens / cache->page_tokens + 2LL * p.num_seqs > 2147483647LL) return KDA_ERR_UNSUPPORTED;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(lengths, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
-    if (!aligned(check, 256)) return KDA_ERR_INVALID_ARG;
-    const size_t io = io_size(p.io_dtype);
-    const int64_t row = (int64_t)p.num_kv_heads * p.head_dim;
-    const Range in[5] = {range_of(k, strided_bytes(p.total_tokens, a.ks, row, io)),
-                         range_of(v, strided_bytes(p.total_tokens, a.vs, row, io)),
-                         range_of(lengths, (size_t)p.num_seqs * 4),
-                         range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0), rc.r[4]};
-    const Range rk = range_of(check, check ? 4 : 0);
-    for (int i = 0; i < 4; ++i) {
-        for (const Range& r : in) {
-            if (overlaps(rc.r[i], r)) return KDA_ERR_INVALID_ARG;
-        }
-        for (int j = 0; j < i; ++j) {
-            if (overlaps(rc.r[i], rc.r[j])) return KDA_ERR_INVALID_ARG;
-        }
-        if (overlaps(rk, rc.r[i])) return KDA_ERR_INVALID_ARG;
-    }
-    for (const Range& r : in) {
-        if (overlaps(rk, r)) return KDA_ERR_INVALID_ARG;
-    }
-    for (const void* ptr : {k, v, (const void*)lengths, (const void*)cu_seqlens, (const void*)check}) {
-        if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
-    }
-    if ((st = check_cache_pointers(*cache)) != KDA_OK) return st;
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, nullptr, 0, Range{0, 0}, a)) != KDA_OK) return st;
     if (p.total_tokens == 0) return KDA_OK;
-    a.k = k; a.v = v; a.cu = cu_seqlens; a.lengths = lengths; a.check = check;
-    a.T = p.total_tokens; a.N = p.num_seqs; a.Hkv = p.num_kv_heads; a.d = p.head_dim; a.c = cache_args(*cache);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     kda::prof_start("kda_cache_append", s);
     const cudaError_t e = kda::launch_cache_append(a, p.io_dtype, s);
+    kda::prof_stop(s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_rotary_append(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths,
+                               const int32_t* positions, void* q_out, const kda_cache_t* cache, const kda_attention_t* problem,
+                               const kda_rotary_t* rotary, uint32_t* check, void* stream)
+{
+    kda_status_t st = check_attention(problem, q != nullptr);
+    if (st != KDA_OK) return st;
+    const kda_attention_t& p = *problem;
+    kda::TurnArgs t{};
+    kda::TurnRows r{};
+    if ((st = check_rotary(rotary, p, false, &t)) != KDA_OK) return st;
+    int64_t qs = 0;
+    if (q != nullptr && (st = token_stride(p.q_stride, p.num_heads, p, &qs)) != KDA_OK) return st;
+    if (!aligned(positions, 4)) return KDA_ERR_INVALID_ARG;
+    Range more[2], out;
+    if ((st = check_turned(q, q_out, p.num_heads, qs, p, 0, &r, &more[0], &out)) != KDA_OK) return st;
+    more[1] = range_of(positions, positions ? (size_t)p.total_tokens * t.axes * 4 : 0);
+    if (overlaps(out, more[1])) return KDA_ERR_INVALID_ARG;
+    kda::AppendArgs a{};
+    // queries turned in place among the keys and values of one projection share their range, not their rows
+    int64_t ks = 0, vs = 0;
+    if ((st = token_stride(p.k_stride, p.num_kv_heads, p, &ks)) != KDA_OK) return st;
+    if ((st = token_stride(p.v_stride, p.num_kv_heads, p, &vs)) != KDA_OK) return st;
+    const size_t io = io_size(p.io_dtype), row = (size_t)p.num_heads * p.head_dim * io, krow = (size_t)p.num_kv_heads * p.head_dim * io;
+    const bool among = q != nullptr && q == q_out && k != nullptr && v != nullptr && interleaved(q, row, qs, k, krow, ks, io) &&
+                       interleaved(q, row, qs, v, krow, vs, io);
+    if (among) {
+        for (const Range& x : {range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0),
+                               range_of(lengths, lengths ? (size_t)p.num_seqs * 4 : 0)}) {
+            if (overlaps(out, x)) return KDA_ERR_INVALID_ARG;
+        }
+    }
+    const Range apart = among ? Range{0, 0} : out;
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, more, 2, apart, a)) != KDA_OK) return st;
+    for (const void* ptr : {q, (const void*)positions, (const void*)q_out}) {
+        if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
+    }
+    if (p.total_tokens == 0) return KDA_OK;
+    t.positions = positions; t.cu = cu_seqlens; t.lengths = lengths; t.T = p.total_tokens; t.N = p.num_seqs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    kda::prof_start("kda_rotary_append", s);
+    const cudaError_t e = kda::launch_rotary_append(a, t, r, p.io_dtype, s);
+    kda::prof_stop(s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_rotary(const void* q, const void* k, const int32_t* cu_seqlens, const int32_t* lengths,
+                        const int32_t* positions, void* q_out, void* k_out, const kda_attention_t* problem,
+                        const kda_rotary_t* rotary, int32_t inverse, void* stream)
+{
+    kda_status_t st = check_attention(problem, q != nullptr);
+    if (st != KDA_OK) return st;
+    const kda_attention_t& p = *problem;
+    if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    if (inverse != 0 && inverse != 1) return KDA_ERR_INVALID_ARG;
+    kda::TurnArgs t{};
+    kda::TurnRows r{};
+    if ((st = check_rotary(rotary, p, inverse != 0, &t)) != KDA_OK) return st;
+    int64_t qs = 0, ks = 0;
+    if (q != nullptr && (st = token_stride(p.q_stride, p.num_heads, p, &qs)) != KDA_OK) return st;
+    if (k != nullptr && (st = token_stride(p.k_stride, p.num_kv_heads, p, &ks)) != KDA_OK) return st;
+    if (p.total_tokens > 0 && q == nullptr && k == nullptr) return KDA_ERR_INVALID_ARG;
+    Range in[5], out[2];
+    if ((st = check_turned(q, q_out, p.num_heads, qs, p, 0, &r, &in[0], &out[0])) != KDA_OK) return st;
+    if ((st = check_turned(k, k_out, p.num_kv_heads, ks, p, 1, &r, &in[1], &out[1])) != KDA_OK) return st;
+    if (!aligned(cu_seqlens, 4) || !aligned(lengths, 4) || !aligned(positions, 4)) return KDA_ERR_INVALID_ARG;
+    in[2] = range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0);
+    in[3] = range_of(lengths, lengths ? (size_t)p.num_seqs * 4 : 0);
+    in[4] = range_of(positions, positions ? (size_t)p.total_tokens * t.axes * 4 : 0);
+    // in place, q and k may be views of one projection
+    const size_t io = io_size(p.io_dtype);
+    const bool both = q != nullptr && k != nullptr && q == q_out && k == k_out &&
+                      interleaved(q, (size_t)p.num_heads * p.head_dim * io, qs, k, (size_t)p.num_kv_heads * p.head_dim * io, ks, io);
+    for (int o = 0; o < 2; ++o) {
+        for (int i = 0; i < 5; ++i) {
+            if (i == o || (i < 2 && both)) continue;
+            if (overlaps(out[o], in[i])) return KDA_ERR_INVALID_ARG;
+        }
+    }
+    if (!both && overlaps(out[0], out[1])) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, k, (const void*)cu_seqlens, (const void*)lengths, (const void*)positions, (const void*)q_out,
+                            (const void*)k_out}) {
+        if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
+    }
+    if (p.total_tokens == 0) return KDA_OK;
+    t.positions = positions; t.cu = cu_seqlens; t.lengths = lengths; t.T = p.total_tokens; t.N = p.num_seqs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    kda::prof_start("kda_rotary", s);
+    const cudaError_t e = kda::launch_rotary(t, r, p.io_dtype, s);
     kda::prof_stop(s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -1,4 +1,5 @@
-// kda_cache.cu -- keys and values of new tokens into a paged 8-bit cache (kda_cache_append).
+// kda_cache.cu -- keys and values of new tokens into a paged 8-bit cache (kda_cache_append), the keys as they are or turned
+// by their positions (kda_rotary_append).
 //
 // For a page and head with values x of the new tokens and MAX the code's range (448 or 127):
 //   scale' = max(scale if the page already holds tokens, 2^e),  e >= -60 smallest with max|x| <= MAX 2^e
@@ -14,9 +15,14 @@
 // in bf16: 128 us, half the copy rate), so where there is work enough a CTA does several, the next
 // ones' rows on their way by asynchronous copies while one is rounded (80 us, 5.3 TB/s, issue-bound; with the next
 // one's rows in registers 114 us, for want of bytes in flight).
+//
+// Keys that turn: the sines and cosines of the page's tokens are formed once into a table in shared memory and serve the
+// CTA's heads; a row's other channel of each pair lies with a neighbour in the same warp.  The turned values stay in
+// registers, in fp32, between the maximum and the rounding.  Warps past the pages' CTAs turn q.
 #include <cuda_fp8.h>
 
 #include "kda_attn.cuh"
+#include "kda_rotary.cuh"
 
 namespace kda {
 
@@ -26,6 +32,19 @@ constexpr int kVec = 8;        // values a thread holds of a row
 constexpr int kMaxThreads = 256;
 constexpr int kMaxStages = 4;   // units whose rows are on their way or held
 constexpr int kMinExp = -60;
+constexpr int kMaxRows = 8;    // rows of a page that a thread may hold: 128 of 16 threads each by 256 threads
+
+// What a call does to its keys and queries on the way: nothing, or a turn.
+struct AsTheyAre {
+    static constexpr bool kTurns = false;
+};
+struct Turned {
+    static constexpr bool kTurns = true;
+    TurnArgs t;
+    TurnRows q;
+    int64_t tasks;  // warps of q
+    int32_t groups, slots, table;  // CTAs along x that hold pages; bytes before the table of sines
+};
 
 // a thread's eight values of a row: asynchronous copy to shared memory, and back to registers
 template <typename TIO>
@@ -132,12 +151,21 @@ __device__ __forceinline__ float scale_for(float amax)
 
 }  // namespace
 
-template <typename TIO, bool kE4m3>
-__global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArgs a, int slots_per_equal, int heads, int stages, int stage_bytes)
+template <typename TIO, bool kE4m3, typename How>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_cache_append_kernel(AppendArgs a, int slots_per_equal, int heads, int stages, int stage_bytes, const __grid_constant__ How how)
 {
     extern __shared__ __align__(16) unsigned char ring[];  // [stages][stage_bytes]
     __shared__ float warp_max[2][kMaxThreads / 32];
     const int page_tokens = a.c.page;
+    if constexpr (How::kTurns) {
+        if ((int)blockIdx.x >= how.slots) {
+            const int64_t cta = (int64_t)((int)blockIdx.x - how.slots) * gridDim.y + blockIdx.y;
+            const int64_t task = cta * (blockDim.x / 32) + (threadIdx.x >> 5);
+            if (task < how.tasks) turn_task<TIO>(how.t, how.q, task, how.groups);
+            return;
+        }
+    }
     // the sequence and which of its pages: sequence n owns the CTAs from cu[n] / page + 2 n on, at
     // least as many as pages it can touch (equal lengths: slots_per_equal each)
     int n, j;
@@ -195,6 +223,48 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    if constexpr (How::kTurns) {
+        // [rows][pairs] of (cos, sin); the first unit's barrier comes before anything is read, see below
+        float2* table = reinterpret_cast<float2*>(ring + how.table);
+        const int pairs = how.t.rot >> 1;
+        for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
+            const int r = i / pairs, pair = i - r * pairs;
+            const int64_t token = t0 + (p0 - first) + r;
+            const int position = how.t.positions != nullptr ? how.t.positions[(int64_t)how.t.axis[pair] * a.T + token] : (int)(p0 + r);
+            float s, c;
+            sincos_of(how.t, pair, position, s, c);
+            table[i] = make_float2(c, s);
+        }
+    }
+    // A thread's eight channels of its row i, turned: the other channels of their pairs lie in the same row, eight
+    // apart in the same warp.
+    auto turned8 = [&](const unsigned char* held, int i, float (&x)[kVec]) {
+        if constexpr (How::kTurns) {
+            const unsigned char* at = held + i * mine_step;
+            get8<TIO>(at, x);
+            const int rot = how.t.rot, half = rot >> 1;
+            if (c0 >= rot) return;
+            const float2* row = reinterpret_cast<const float2*>(ring + how.table) + (r0 + i * rstep) * half;
+            if (how.t.adjacent) {
+#pragma unroll
+                for (int e = 0; e < kVec / 2; ++e) {
+                    const float2 cs = row[(c0 >> 1) + e];
+                    const float p = x[2 * e], q = x[2 * e + 1];
+                    x[2 * e] = fmaf(p, cs.x, -q * cs.y);
+                    x[2 * e + 1] = fmaf(q, cs.x, p * cs.y);
+                }
+            } else {
+                const bool up = c0 >= half;
+                float y[kVec];
+                get8<TIO>(at + (up ? -half : half) * (int)sizeof(TIO), y);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float2 cs = row[(up ? c0 - half : c0) + e];
+                    x[e] = up ? fmaf(x[e], cs.x, y[e] * cs.y) : fmaf(x[e], cs.x, -y[e] * cs.y);
+                }
+            }
+        }
+    };
     auto round = [&](int u, int slot) {
         const int64_t ph = (int64_t)page * a.Hkv + h0 + (u >> 1);
         uint8_t* codes = (u & 1 ? a.c.v : a.c.k) + ph * page_tokens * a.d;
@@ -204,10 +274,27 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
         // magnitudes compare as integers; where the largest is an infinity or NaN, which set no scale,
         // the rows are looked through again for the largest that is neither
         uint32_t top = 0u;
+        float turned[How::kTurns ? kMaxRows : 1][kVec];
+        const bool turn = How::kTurns && (u & 1) == 0;
+        float amax = 0.f;
+        if (turn) {
+            __syncwarp();  // the neighbours' copies have landed, too
+#pragma unroll
+            for (int i = 0; i < kMaxRows; ++i) {
+                if (i >= mine_rows) continue;
+                turned8(held, i, turned[How::kTurns ? i : 0]);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float m = fabsf(turned[How::kTurns ? i : 0][e]);
+                    amax = m < INFINITY ? fmaxf(amax, m) : amax;
+                }
+            }
+        } else {
 #pragma unroll 4
-        for (int i = 0; i < mine_rows; ++i) top = max8<TIO>(held + i * mine_step, top);
-        float amax = largest<TIO>(top);
-        if (!(amax < INFINITY)) {
+            for (int i = 0; i < mine_rows; ++i) top = max8<TIO>(held + i * mine_step, top);
+            amax = largest<TIO>(top);
+        }
+        if (!turn && !(amax < INFINITY)) {
             amax = 0.f;
             for (int i = 0; i < mine_rows; ++i) {
                 float x[kVec];
@@ -245,6 +332,12 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
         }
         const float inv = 1.f / unit;
         uint8_t* dst = codes + (slot0 + r0) * a.d + c0;
+        if (turn) {
+#pragma unroll
+            for (int i = 0; i < kMaxRows; ++i)
+                if (i < mine_rows) *reinterpret_cast<uint2*>(dst + i * rstep * a.d) = encode8<kE4m3>(turned[How::kTurns ? i : 0], inv);
+            return;
+        }
 #pragma unroll 4
         for (int i = 0; i < mine_rows; ++i) {
             float x[kVec];
@@ -253,6 +346,7 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
         }
     };
     for (int u = 0; u < stages - 1; ++u) load(u, u);
+    if constexpr (How::kTurns) __syncthreads();  // the table
     int slot = 0, ahead = stages - 1;
     for (int u = 0; u < units; ++u) {
         load(u + stages - 1, ahead);
@@ -267,7 +361,10 @@ __global__ void __launch_bounds__(kMaxThreads) kda_cache_append_kernel(AppendArg
     }
 }
 
-cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s)
+namespace {
+
+template <typename How>
+cudaError_t launch(const AppendArgs& a, How how, kda_dtype_t dt, cudaStream_t s)
 {
     // a call of at most c tokens a sequence holds min(c, page) rows in a CTA, so that few tokens
     // take few threads (one token of 128 channels: one warp)
@@ -281,24 +378,46 @@ cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_
     // several heads a CTA while about eight CTAs an SM remain
     int heads = 1;
     while (2 * heads <= a.Hkv && slots * ((a.Hkv + 2 * heads - 1) / (2 * heads)) >= 8LL * sm_count_of_current_device()) heads *= 2;
-    const dim3 grid((unsigned)slots, (unsigned)((a.Hkv + heads - 1) / heads));
+    dim3 grid((unsigned)slots, (unsigned)((a.Hkv + heads - 1) / heads));
     const int stage_bytes = (int)rows * a.d * (dt == KDA_BF16 ? 2 : 4);  // at most 64 KB
     int stages = 65536 / stage_bytes;
     stages = stages > kMaxStages ? kMaxStages : stages < 2 ? 2 : stages;
-    const int smem = stages * stage_bytes;
+    int smem = stages * stage_bytes;
+    if constexpr (How::kTurns) {
+        how.slots = (int)slots;
+        how.table = smem;
+        smem += (int)rows * how.t.rot / 2 * (int)sizeof(float2);  // at most 64 KB
+        if (how.q.heads[0] > 0) how.tasks = turn_tasks(how.t, how.q, &how.groups);
+        const int64_t per = (int64_t)grid.y * (threads / 32);  // of q's warps that a place of x holds
+        const int64_t x = slots + (how.tasks + per - 1) / per;
+        if (x > 2147483647LL) return cudaErrorInvalidValue;
+        grid.x = (unsigned)x;
+    }
     auto go = [&](auto kern, SmemLimit& limit) {
-        const cudaError_t e = limit.raise(kern, 2 * 65536);
-        if (e == cudaSuccess) kern<<<grid, threads, smem, s>>>(a, per_equal, heads, stages, stage_bytes);
+        const cudaError_t e = limit.raise(kern, (How::kTurns ? 3 : 2) * 65536);
+        if (e == cudaSuccess) kern<<<grid, threads, smem, s>>>(a, per_equal, heads, stages, stage_bytes, how);
         return e;
     };
     static SmemLimit limit[4];
     const bool e4m3 = a.c.dtype == KDA_CACHE_E4M3;
-    const cudaError_t e = dt == KDA_BF16 ? (e4m3 ? go(kda_cache_append_kernel<__nv_bfloat16, true>, limit[0])
-                                                 : go(kda_cache_append_kernel<__nv_bfloat16, false>, limit[1]))
-                                         : (e4m3 ? go(kda_cache_append_kernel<float, true>, limit[2])
-                                                 : go(kda_cache_append_kernel<float, false>, limit[3]));
+    const cudaError_t e = dt == KDA_BF16 ? (e4m3 ? go(kda_cache_append_kernel<__nv_bfloat16, true, How>, limit[0])
+                                                 : go(kda_cache_append_kernel<__nv_bfloat16, false, How>, limit[1]))
+                                         : (e4m3 ? go(kda_cache_append_kernel<float, true, How>, limit[2])
+                                                 : go(kda_cache_append_kernel<float, false, How>, limit[3]));
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s) { return launch(a, AsTheyAre{}, dt, s); }
+
+cudaError_t launch_rotary_append(const AppendArgs& a, const TurnArgs& t, const TurnRows& q, kda_dtype_t dt, cudaStream_t s)
+{
+    Turned how{};
+    how.t = t;
+    how.q = q;
+    return launch(a, how, dt, s);
 }
 
 }  // namespace kda

@@ -1,0 +1,33 @@
+// kda_rotary.cu -- queries and keys turned by their positions (kda_rotary).
+//
+//   y_a = x_a cos(p f) - x_b sin(p f),   y_b = x_b cos(p f) + x_a sin(p f)        pair by pair, see kda_rotary.cuh
+//
+// Every value is read and written once; HBM bounds it.
+#include "kda_rotary.cuh"
+
+namespace kda {
+
+namespace {
+constexpr int kThreads = 256;
+}
+
+template <typename TIO>
+__global__ void __launch_bounds__(kThreads) kda_rotary_kernel(const __grid_constant__ TurnArgs t, const __grid_constant__ TurnRows r, const int64_t tasks, const int groups)
+{
+    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (task < tasks) turn_task<TIO>(t, r, task, groups);
+}
+
+cudaError_t launch_rotary(const TurnArgs& t, const TurnRows& rows, kda_dtype_t dt, cudaStream_t s)
+{
+    TurnRows r = rows;
+    int groups = 1;
+    const int64_t tasks = turn_tasks(t, r, &groups);
+    const int64_t ctas = (tasks + kThreads / 32 - 1) / (kThreads / 32);
+    if (ctas > 2147483647LL) return cudaErrorInvalidValue;
+    if (dt == KDA_BF16) kda_rotary_kernel<__nv_bfloat16><<<(unsigned)ctas, kThreads, 0, s>>>(t, r, tasks, groups);
+    else kda_rotary_kernel<float><<<(unsigned)ctas, kThreads, 0, s>>>(t, r, tasks, groups);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
