@@ -476,6 +476,30 @@ size_t kda_attention_decode_workspace_bytes(const kda_attention_t* problem);
 kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const kda_cache_t* cache, void* out,
                                   const kda_attention_t* problem, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace kda_attention_extend needs (0 if the descriptor is invalid). */
+size_t kda_attention_extend_workspace_bytes(const kda_attention_t* problem);
+
+/*
+ * A chunk of new tokens of every sequence, of any length each, attends to the paged 8-bit cache, which holds their keys
+ * and values already (kda_cache_append, kda_rotary_append): a prompt that arrives in pieces, the next turn of a
+ * conversation, or a serving step in which some sequences bring one token and others a piece of their prompt.
+ * Token i of the L_n new ones of sequence n sees the first lengths[n] - L_n + i + 1 keys of its sequence.
+ *
+ *   q : [T_tot, num_heads, head_dim] io dtype, q_stride as for kda_attention_prefill.
+ *   cu_seqlens : device [N+1] offsets of every sequence's new tokens, or NULL for T_tot / N each.  Offsets are not
+ *       validated on the device: invalid offsets give unspecified outputs (never an access outside the tensors).
+ *       Rows of out past the last sequence's are left as they were.
+ *   lengths : [N] int32 on the device, keys of each sequence in the cache, the new tokens' included.
+ *   out : [T_tot, num_heads, head_dim] io dtype, packed; must not overlap any argument.
+ *   workspace : kda_attention_extend_workspace_bytes(problem) bytes, 256-byte aligned, not shared with a concurrently
+ *       running call.
+ * Lengths, pages and the check word (kda_workspace_status(workspace, ...)) as for kda_attention_decode, and so are the
+ * products' operands: codes exactly, q and the weights as f16 (fp32 io: as sums of two f16 parts).
+ */
+kda_status_t kda_attention_extend(const void* q, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,
+                                  void* out, const kda_attention_t* problem, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 /*
  * kda_forward for callers that cannot allocate device memory: a library or plugin that runs
  * inside a host application which owns every device allocation (its own pool or arena) and gives

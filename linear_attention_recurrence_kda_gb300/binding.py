@@ -41,7 +41,8 @@ EXPORTS = ("kda_forward_workspace_bytes", "kda_forward", "kda_decode_step", "kda
            "kda_epilogue", "kda_static_scratch_status", "kda_backward_workspace_bytes", "kda_backward",
            "kda_forward_summary_workspace_bytes", "kda_forward_summary", "kda_state_scan",
            "kda_attention_prefill", "kda_cache_append", "kda_attention_decode_workspace_bytes",
-           "kda_attention_decode", "kda_rotary", "kda_rotary_append")
+           "kda_attention_decode", "kda_rotary", "kda_rotary_append", "kda_attention_extend_workspace_bytes",
+           "kda_attention_extend")
 
 # Size of the library's own scratch array used by kda_forward_static_scratch.
 KDA_STATIC_SCRATCH_BYTES = 8 << 20
@@ -163,6 +164,10 @@ def lib():
             L.kda_attention_decode_workspace_bytes.argtypes = [PA]
             L.kda_attention_decode.restype = ctypes.c_int
             L.kda_attention_decode.argtypes = [_vp, _vp, PC, _vp, PA, _vp, ctypes.c_size_t, _vp]
+            L.kda_attention_extend_workspace_bytes.restype = ctypes.c_size_t
+            L.kda_attention_extend_workspace_bytes.argtypes = [PA]
+            L.kda_attention_extend.restype = ctypes.c_int
+            L.kda_attention_extend.argtypes = [_vp] * 3 + [PC, _vp, PA, _vp, ctypes.c_size_t, _vp]
             PR = ctypes.POINTER(KdaRotary)
             L.kda_rotary.restype = ctypes.c_int
             L.kda_rotary.argtypes = [_vp] * 7 + [PA, PR, ctypes.c_int32, _vp]
@@ -842,6 +847,52 @@ def kda_attention_decode(q, cache: KvCache, block_table, lengths, scale: Optiona
                                     ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_attention_decode")
+    return out
+
+
+def kda_attention_extend_workspace_bytes(problem: KdaAttention) -> int:
+    return int(lib().kda_attention_extend_workspace_bytes(ctypes.byref(problem)))
+
+
+@functools.lru_cache(maxsize=256)
+def _extend_workspace_bytes(N, T, Hq, Hkv, d, io, device) -> int:
+    """The workspace depends on the sizes and the device alone."""
+    return kda_attention_extend_workspace_bytes(KdaAttention(N, T, Hq, Hkv, d, io, 1.0, 0, 0, 0))
+
+
+def kda_attention_extend(q, cache: KvCache, block_table, lengths, cu_seqlens=None, scale: Optional[float] = None, out=None,
+                         workspace=None, stream=None):
+    """A chunk of new tokens of every sequence, of any length each, attends to the cache, which holds their keys and
+    values already (see include/kda.h): q [T, Hq, d] (strides as for :func:`kda_attention_prefill`); block_table
+    [N, pages] int32; lengths [N] int32, keys in the cache with the new tokens'; cu_seqlens [N+1] int32 offsets of every
+    sequence's new tokens, or None for T / N each.  Token i of L_n sees the first lengths[n] - L_n + i + 1 keys.  Returns
+    out [T, Hq, d]; rows past the last sequence's are left as they are."""
+    T, Hq, d = q.shape
+    N = lengths.shape[0]
+    Hkv = cache.k.shape[1] if cache.k.dim() == 4 else 0
+    dev, dt = q.device, q.dtype
+    io = _io_dtype(q, "q")
+    qs = _tokens(q, "q", dt, Hq, d, dev)
+    _need(lengths, "lengths", torch.int32, (N,), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    c = _cache(cache, block_table, N, Hkv, d, dev)
+    if out is None:
+        out = _empty((T, Hq, d), dt, dev, stream)
+    else:
+        _need(out, "out", dt, (T, Hq, d), dev)
+    prob = KdaAttention(N, T, Hq, Hkv, d, io, d ** -0.5 if scale is None else float(scale), qs, 0, 0)
+    if workspace is None:
+        wsb = _extend_workspace_bytes(N, T, Hq, Hkv, d, io, dev)
+        if wsb == 0:
+            raise KdaError(KDA_ERR_INVALID_ARG, "kda_attention_extend_workspace_bytes")
+        workspace = _empty(wsb, torch.uint8, dev, stream, result=False)
+    st = lib().kda_attention_extend(q.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                                    lengths.data_ptr(), ctypes.byref(c), out.data_ptr(), ctypes.byref(prob),
+                                    workspace.data_ptr(), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+                                    _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attention_extend")
     return out
 
 

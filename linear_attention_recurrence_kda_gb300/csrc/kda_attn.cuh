@@ -57,11 +57,26 @@ struct AttnDecodeArgs {
     CacheArgs c;
 };
 
+struct AttnExtendArgs {
+    const void* q;
+    const int32_t* cu;       // NULL: T / N new tokens each
+    const int32_t* lengths;  // with the new tokens
+    void* out;
+    unsigned char* ws;
+    int64_t T, qs;
+    int32_t N, Hq, Hkv, group, d;
+    float scale;
+    CacheArgs c;
+};
+
 cudaError_t launch_attn_prefill_f32(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, cudaStream_t s);  // bf16
 cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, kda_dtype_t dt, cudaStream_t s);
 size_t attn_decode_workspace_bytes(int64_t rows, int d, kda_dtype_t dt);  // rows: window x group
+
+cudaError_t launch_attn_extend(const AttnExtendArgs& a, kda_dtype_t dt, cudaStream_t s);
+size_t attn_extend_workspace_bytes(int64_t tokens, int group, int d, kda_dtype_t dt);
 
 // The form for many rows a key head (kda_attn_window.cu): does it take a call, what does it need.
 bool attn_window_takes(int64_t rows, int d, kda_dtype_t dt, int64_t capacity);  // keys that a sequence's pages hold

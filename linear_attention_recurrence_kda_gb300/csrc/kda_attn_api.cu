@@ -425,4 +425,52 @@ kda_status_t kda_attention_decode(const void* q, const int32_t* lengths, const k
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+size_t kda_attention_extend_workspace_bytes(const kda_attention_t* problem)
+{
+    if (check_attention(problem, true) != KDA_OK) return 0;
+    const kda_attention_t& p = *problem;
+    return kda::attn_extend_workspace_bytes(p.total_tokens, p.num_heads / p.num_kv_heads, p.head_dim, p.io_dtype);
+}
+
+kda_status_t kda_attention_extend(const void* q, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,
+                                  void* out, const kda_attention_t* problem, void* workspace, size_t workspace_bytes,
+                                  void* stream)
+{
+    kda_status_t st = check_attention(problem, true);
+    if (st != KDA_OK) return st;
+    const kda_attention_t& p = *problem;
+    if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    kda::AttnExtendArgs a{};
+    if ((st = token_stride(p.q_stride, p.num_heads, p, &a.qs)) != KDA_OK) return st;
+    CacheRanges rc;
+    if ((st = check_cache(cache, p, &rc)) != KDA_OK) return st;
+    if (lengths == nullptr || (p.total_tokens > 0 && (!q || !out))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARG;
+    const size_t io = io_size(p.io_dtype);
+    const int64_t row = (int64_t)p.num_heads * p.head_dim;
+    const Range rq = range_of(q, strided_bytes(p.total_tokens, a.qs, row, io));
+    const Range rl = range_of(lengths, (size_t)p.num_seqs * 4);
+    const Range ru = range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0);
+    const Range ro = range_of(out, (size_t)p.total_tokens * row * io);
+    const size_t need = kda_attention_extend_workspace_bytes(problem);
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    const Range rw = range_of(workspace, need);
+    for (const Range& r : {rq, rl, ru, rc.r[0], rc.r[1], rc.r[2], rc.r[3], rc.r[4]}) {
+        if (overlaps(ro, r) || overlaps(rw, r)) return KDA_ERR_INVALID_ARG;
+    }
+    if (overlaps(rw, ro)) return KDA_ERR_INVALID_ARG;
+    for (const void* ptr : {q, (const void*)cu_seqlens, (const void*)lengths, (const void*)out, (const void*)workspace}) {
+        if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
+    }
+    if ((st = check_cache_pointers(*cache)) != KDA_OK) return st;
+    a.q = q; a.cu = cu_seqlens; a.lengths = lengths; a.out = out; a.ws = static_cast<unsigned char*>(workspace);
+    a.T = p.total_tokens; a.N = p.num_seqs; a.Hq = p.num_heads; a.Hkv = p.num_kv_heads;
+    a.group = p.num_heads / p.num_kv_heads; a.d = p.head_dim; a.scale = p.scale; a.c = cache_args(*cache);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    kda::prof_start("kda_attention_extend", s);
+    const cudaError_t e = kda::launch_attn_extend(a, p.io_dtype, s);
+    kda::prof_stop(s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
 }  // extern "C"
