@@ -1,118 +1,943 @@
-// kda_attn_extend.cu -- chunks of new tokens, of any length each, attend to the paged 8-bit cache
-// (kda_attention_extend).
+// kda_attn_extend.cu -- chunks of new tokens, of any length each, attend to the paged 8-bit cache, on the 5th-generation
+// tensor cores (kda_attention_extend).
 //
-//   z_j = scale (q . k_j),   o = sum_j e^(z_j) v_j / sum_j e^(z_j)       over the keys j <= place of the row's token
+//   Z = scale ks (Q K^T),  P = 2^(Z log2 e - m),  O = sum P (vs V),  o = O / l        per row, keys in tiles of 128
 //
-// A warp takes a row: its keys one by one, running maximum and sum, the channels spread over the lanes.
+// A unit is one sequence, one key head and up to 256 rows (a group's query heads times 256 / group tokens), in two halves of
+// 128; a CTA walks the unit's keys for both.  Codes are converted to f16 once a tile, exactly (e4m3 and int8 are
+// subsets of f16), by warps that do nothing else, straight from global memory into the products' layout.  The products are
+// tcgen05.mma with M = 128: Z from Q and K in shared memory, O += P V with P read from tensor memory and V token-major as it
+// lies.  Tensor memory: Z0 | Z1 | O0 | O1, P as packed f16 over its Z.  A thread of the softmax owns a row.
+//
+// All units' keys, with a gap before each unit for what its start costs, form one line that is cut evenly among the CTAs,
+// whatever the lengths are; pieces of a unit are joined by a second kernel in a fixed order.  A unit's key tiles grow with
+// its rows' places (causality), so the line is counted in keys, in closed form.
+//
+// Warps 0-3 and 4-7: softmax of the halves, 8: products, 9: pages and scales, 10-15: conversion.  They meet at mbarriers.
+//
+// A row of q enters as f16 times a power of two that brings its largest value to [2^14, 2^15): bf16's eight bits are
+// exact down to 2^-31 of it.  Weights are held against a reference 2^7 below the row's largest score, which moves only when the
+// maximum has grown by more than 2^8, so that they fill f16's range up to 2^15; l sums the unrounded weights in fp32.  V's scales
+// enter through P, with O in units that follow the pages' scales.
+//
+// fp32 io (kSplit): q and the weights as two f16 parts (22 bits), one half of 128 rows; Q's parts take the halves' places and
+// so do P's, each with a product of its own.  The products' own sums are cut off, not rounded, so they add one tile's keys
+// and ordinary additions the tiles.
+//
+// Hidden keys: scores are replaced by -inf.  A NaN code in a value would spread over 0 x NaN, so a tile that some row does not see
+// whole is cleaned of them (noted by channel and key), and the rows that see them get them at the end.
+#include <cfloat>
 #include <type_traits>
-
-#include <cuda_fp16.h>
 
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
+#include "kda_attn_tc.cuh"
 
 namespace kda {
 
+using namespace attn;
+
 namespace {
-constexpr int kWarps = 8;
+
+constexpr int kKeys = 128;
+constexpr int kThreads = 512;
+constexpr int kConvert = 192;
+constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
+constexpr int kGroups = kKeys / 16;
+constexpr int kGap = 256;      // what a unit's start and end cost, in keys
+// warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRestUp = 2048.f;  // what a weight's second part is multiplied by (see kda_attn_decode.cu)
+
+template <int D, bool kSplit> struct Cfg {
+    static constexpr int DP = D < 64 ? 64 : D;        // 32 channels are padded with zeros
+    static constexpr int NB = DP / 64;                // 64-channel blocks of a row
+    static constexpr uint32_t BLK = 128 * 128;        // bytes of a block: 128 rows of 128 bytes
+    static constexpr uint32_t TILE = NB * BLK;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr int HALVES = kSplit ? 1 : 2;
+    // tensor memory, columns: where the outputs of the halves (or of P's parts) are, and the sum over tiles (kSplit)
+    static constexpr int O = kSplit ? 128 : 256, ACC = 384;
+};
+
+struct Shared {
+    uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], drained;
+    uint32_t tmem, dead, flag;
+    uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there
+    int ph[kInfo][kGroups];                                 // its page and head in the cache
+    alignas(16) float ks[kInfo][kGroups], vs[kInfo][kGroups];
+    unsigned long long odd[kInfo][128];  // by the segment's turn: the first key with a NaN in a channel
+};
+
+// ---------------------------------------------------------------- the line of work
+
+// The new tokens of a sequence that see some key: tokens [start, start + rows) of q, behind `ctx` keys.
+struct Seq {
+    int64_t start;
+    int rows, ctx, skip;  // skip: tokens before them that see none
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnExtendArgs& a, int n, bool* bad = nullptr)
+{
+    int64_t c0, c1;
+    if (a.cu != nullptr) {
+        c0 = min(max((int64_t)a.cu[n], (int64_t)0), a.T);
+        c1 = min(max((int64_t)a.cu[n + 1], c0), a.T);
+    } else {
+        const int64_t len = a.T / a.N;
+        c0 = n * len;
+        c1 = c0 + len;
+    }
+    const int len = a.lengths[n];
+    const bool ok = len >= 0 && (int64_t)len <= (int64_t)a.c.max_pages * a.c.page;
+    if (!ok && bad != nullptr) *bad = true;
+    Seq s;
+    const int fresh = (int)(c1 - c0), keys = ok ? len : 0;
+    s.skip = max(0, fresh - keys);
+    s.start = c0 + s.skip;
+    s.rows = fresh - s.skip;
+    s.ctx = keys - s.rows;
+    return s;
+}
+
+// Places of a sequence's units of `tpu` tokens (one key head): a gap and the keys that the last token sees, each.
+__device__ __forceinline__ int units_of(const Seq& s, int tpu) { return (s.rows + tpu - 1) / tpu; }
+__device__ __forceinline__ int64_t places_before(const Seq& s, int tpu, int64_t k)  // of the units before the k-th
+{
+    return k * (kGap + s.ctx) + (int64_t)tpu * (k * (k + 1) / 2);
+}
+__device__ __forceinline__ int64_t places_of(const Seq& s, int tpu)
+{
+    const int k = units_of(s, tpu);
+    return k == 0 ? 0 : places_before(s, tpu, k - 1) + kGap + s.ctx + s.rows;
+}
+
+// A run of a unit's key tiles.
+struct Segment {
+    int n, h, rt, i0, count, tiles;
+    int first, last, ctx;   // the unit's tokens [first, last) of its sequence's, and the keys before the sequence's first
+    int64_t start, place;   // token of q of the sequence's first; where the unit's keys begin in the line
+    __device__ __forceinline__ bool begun() const { return i0 == 0; }
+    __device__ __forceinline__ bool ended() const { return i0 + count == tiles; }
+};
+
+// The segments of a CTA, one after the other: the tiles whose first key has its place in [., end).
+struct Walk {
+    Seq s;
+    int n, h, rt, i, units;
+    int64_t at, end;  // place of the unit's gap
+    __device__ __forceinline__ bool next(const AttnExtendArgs& a, int tpu, Segment& g)
+    {
+        for (;;) {
+            if (n >= a.N) return false;
+            const int last = min((rt + 1) * tpu, s.rows), keys = s.ctx + last, tiles = (keys - 1) / kKeys + 1;
+            const int64_t room = end - (at + kGap + (int64_t)kKeys * i);
+            if (i < tiles) {
+                if (room <= 0) return false;
+                g.n = n; g.h = h; g.rt = rt; g.i0 = i; g.tiles = tiles;
+                g.count = (int)min((int64_t)(tiles - i), (room + kKeys - 1) / kKeys);
+                g.first = rt * tpu; g.last = last; g.ctx = s.ctx; g.start = s.start; g.place = at + kGap;
+                i += g.count;
+                return true;
+            }
+            at += kGap + keys;
+            i = 0;
+            if (++rt < units) continue;
+            rt = 0;
+            if (++h < a.Hkv) continue;
+            h = 0;
+            do {
+                if (++n >= a.N) return false;
+                s = seq_of(a, n);
+            } while (s.rows == 0);
+            units = units_of(s, tpu);
+        }
+    }
+};
+
+// What is noted in odd[]: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers them), the
+// key in the lower.  A tile's pages are not known before the softmax is done with the tile kInfo before it, and with its segment
+// where it was the last: conversion is less than kInfo segments ahead, and as many arrays in turn never mix.
+__device__ __forceinline__ unsigned long long odd_note(uint32_t turn, int key)
+{
+    return ((unsigned long long)(0xfffffffeu - turn) << 32) | (uint32_t)key;
+}
+
+__device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) { KDA_TMEM_LD16(taddr, v); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) { KDA_TMEM_ST16(taddr, v); }
+
+}  // namespace
+
+template <typename TIO, int D, bool kE4m3>
+__global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const AttnExtendArgs a, const int rows_max)
+{
+    constexpr bool kSplit = sizeof(TIO) == 4;
+    using C = Cfg<D, kSplit>;
+    constexpr int S = C::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Shared sh;
+    unsigned char* sq = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* ring = sq + 2 * C::TILE;
+    int64_t* prefix = reinterpret_cast<int64_t*>(sq);  // until the work begins
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
+    const DecodeLayout L = decode_layout(gridDim.x, gridDim.x, rows_max, D);
+    const int tpt = 128 / a.group, tpu = C::HALVES * tpt;  // tokens of a half, of a unit
+    const int64_t tokrow = (int64_t)a.Hq * D;
+
+    griddep_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.q_full[i], 4);
+            tc::mbar_init(&sh.z_full[i], 1);
+            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.o_full[i], 1);
+        }
+        for (int i = 0; i < S; ++i) {
+            tc::mbar_init(&sh.kv_full[i], kConvert / 32);
+            tc::mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kInfo; ++i) {
+            tc::mbar_init(&sh.info_full[i], 1);
+            tc::mbar_init(&sh.info_free[i], 4 * C::HALVES);
+        }
+        tc::mbar_init(&sh.drained, 1);
+        sh.dead = 0u;
+        sh.flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int i = tid; i < kInfo * 128; i += kThreads) (&sh.odd[0][0])[i] = ~0ull;
+    if (w == 8) tc::tmem_alloc(&sh.tmem, 512);
+    // places before every run of `chunk` sequences
+    const int chunk = (a.N + kThreads - 1) / kThreads;
+    {
+        int64_t sum = 0;
+        bool bad = false;
+        for (int i = 0; i < chunk; ++i) {
+            const int n = tid * chunk + i;
+            if (n < a.N) sum += places_of(seq_of(a, n, &bad), tpu) * a.Hkv;
+        }
+        int64_t x = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        prefix[tid + 1] = x;
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+        if (bad) atomicOr(&sh.flag, kCheckBadSeqlens);
+        int64_t before = 0;
+        for (int i = 0; i < w; ++i) before += prefix[(i + 1) * 32];
+        __syncthreads();
+        prefix[tid + 1] = x + before;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = sh.tmem;
+    volatile uint32_t* dead = &sh.dead;
+
+    // tokens that see no key: rows of zeros
+    for (int n = blockIdx.x; n < a.N; n += gridDim.x) {
+        const Seq s = seq_of(a, n);
+        TIO* o = static_cast<TIO*>(a.out) + (s.start - s.skip) * tokrow;
+        for (int64_t i = tid; i < s.skip * tokrow; i += kThreads) st_io(o, i, 0.f);
+    }
+    // This CTA's part of the line.  No more parts than leave each 128 places, so that a unit's middle parts hold a tile each.
+    const int64_t total = prefix[kThreads];
+    const int64_t W = max((int64_t)1, min((int64_t)gridDim.x, total / kKeys));
+    const int64_t b0 = blockIdx.x < W ? blockIdx.x * total / W : total, b1 = blockIdx.x < W ? (blockIdx.x + 1) * total / W : total;
+    Walk begin;
+    begin.end = b1;
+    begin.n = a.N;
+    if (b0 < b1) {  // a run of sequences by bisection, then one by one; its head and rows
+        int lo = 0, hi = kThreads - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= b0) lo = mid;
+            else hi = mid - 1;
+        }
+        int64_t at = prefix[lo], one;
+        int n = lo * chunk;
+        for (;;) {
+            begin.s = seq_of(a, n);
+            one = places_of(begin.s, tpu);
+            if (at + one * a.Hkv > b0 || n + 1 >= a.N) break;
+            at += one * a.Hkv;
+            ++n;
+        }
+        begin.n = n;
+        begin.units = units_of(begin.s, tpu);
+        begin.h = (int)((b0 - at) / one);
+        at += begin.h * one;
+        lo = 0;
+        hi = begin.units - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (at + places_before(begin.s, tpu, mid) <= b0) lo = mid;
+            else hi = mid - 1;
+        }
+        begin.rt = lo;
+        begin.at = at + places_before(begin.s, tpu, lo);
+        begin.i = (int)max((int64_t)0, (b0 - begin.at - kGap + kKeys - 1) / kKeys);
+    }
+    __syncthreads();  // the prefix is read
+    if constexpr (D < 64) {
+        for (int i = tid; i < (int)(S * C::TILE / 16); i += kThreads) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_async_smem();
+        __syncthreads();
+    }
+    Walk walk = begin;
+    Segment s;
+    // key tiles of this segment that a half has rows for
+    auto tiles_of_half = [&](const Segment& g, int hf) {
+        const int first = g.first + hf * tpt;
+        if (first >= g.last) return 0;
+        const int tiles = (g.ctx + min(first + tpt, g.last) - 1) / kKeys + 1;
+        return min(max(tiles - g.i0, 0), g.count);
+    };
+
+    if (w >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (w == 9) {
+            // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
+            const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
+            uint32_t t = 0;
+            bool ok = true;
+            while (ok && walk.next(a, tpu, s)) {
+                const int keys = s.ctx + s.last;
+                auto page_of = [&](int i) -> int {
+                    const int key = i * kKeys + grp * 16;
+                    if (i >= s.i0 + s.count || key >= keys) return -1;
+                    const int p = __ldg(a.c.table + (int64_t)s.n * a.c.max_pages + (key >> page_shift));
+                    return p >= 0 && p < a.c.num_pages ? p : -2;
+                };
+                auto scale_of = [&](int p) {
+                    return p >= 0 && lane < 16 ? __ldg((lane < 8 ? a.c.k_scale : a.c.v_scale) + (int64_t)p * a.Hkv + s.h) : 0.f;
+                };
+                // a tile's pages are asked for two tiles ahead, its scales one
+                int page = page_of(s.i0), page1 = page_of(s.i0 + 1);
+                float scale = scale_of(page);
+                for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++t) {
+                    const int page2 = page_of(i + 2);
+                    const float scale1 = scale_of(page1);
+                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
+                    if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
+                    const uint32_t slot = t % kInfo;
+                    ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
+                    if (!ok) break;
+                    if (lane < 8) {
+                        sh.ks[slot][grp] = scale;
+                        sh.ph[slot][grp] = page >= 0 ? page * a.Hkv + s.h : 0;
+                    } else if (lane < 16) {
+                        sh.vs[slot][grp] = scale;
+                    }
+                    if (lane == 0) sh.there[slot] = there;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sh.info_full[slot]);
+                    page = page1;
+                    page1 = page2;
+                    scale = scale1;
+                }
+            }
+            if (!ok) *dead = 1u;
+        } else if (w == 8) {
+            // ---- products: Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ...
+            const uint32_t f16 = ~((1u << 7) | (1u << 10));
+            const uint32_t id_z = tc::idesc_bf16(128, kKeys) & f16, id_o = (tc::idesc_bf16(128, C::DP) & f16) | (1u << 16);
+            const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
+            uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+            bool ok = true;
+            auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u); };
+            auto issue_z = [&](int hf, uint32_t x) {
+                const uint32_t k = ra + (x % S) * C::TILE;
+                // kSplit: both parts of Q into the one Z, the small ones first
+#pragma unroll
+                for (int p = kSplit ? 1 : 0; p >= 0; --p) {
+                    const uint32_t q = qa + (kSplit ? p : hf) * C::TILE;
+#pragma unroll
+                    for (int e = 0; e < D / 16; ++e) {
+                        const uint32_t off = (e >> 2) * C::BLK + (e & 3) * 32;
+                        mma_ss(tm + 128 * hf, desc_qk(q + off), desc_qk(k + off), id_z, e > 0 || (kSplit && p == 0));
+                    }
+                }
+                commit(&sh.z_full[hf]);
+            };
+            auto issue_o = [&](int hf, uint32_t x, bool first) {
+                const uint32_t v = ra + (x % S) * C::TILE;
+#pragma unroll
+                for (int p = 0; p < (kSplit ? 2 : 1); ++p)
+#pragma unroll
+                    for (int e = 0; e < kKeys / 16; ++e)
+                        mma_ts(tm + C::O + C::DP * (kSplit ? p : hf), tm + 128 * hf + 64 * p + 8 * e, desc_v(v + e * 2048, D == 128 ? C::BLK : 1024u),
+                               id_o, (!kSplit && !first) || e > 0);
+            };
+            // a slot is given back only after it was seen full, also by a half that has no use for it
+            auto release = [&](uint32_t x) { commit(&sh.kv_empty[x % S]); };
+            while (ok && walk.next(a, tpu, s)) {
+                int nh[2] = {tiles_of_half(s, 0), C::HALVES == 2 ? tiles_of_half(s, 1) : 0};
+                ok = full(it);
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf) {
+                    if (!ok || nh[hf] == 0) continue;
+                    ok = warp_wait(&sh.q_full[hf], qc[hf]++ & 1u);
+                    if (!ok) continue;
+                    tc::fence_after_sync();
+                    issue_z(hf, it);
+                }
+                if (ok) release(it);
+                for (int j = 0; j < s.count && ok; ++j) {
+                    const uint32_t iv = it + 2 * j + 1;
+                    const bool more = j + 1 < s.count;
+                    ok = !__any_sync(0xffffffffu, *dead != 0u) && (!more || full(iv + 1)) && full(iv);
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf) {
+                        if (!ok || j >= nh[hf]) continue;
+                        ok = warp_wait(&sh.p_full[hf], pc[hf]++ & 1u);
+                        if (!ok) continue;
+                        tc::fence_after_sync();
+                        issue_o(hf, iv, j == 0);
+                        if (j + 1 < nh[hf]) issue_z(hf, iv + 1);  // its commit also covers O's product
+                        else commit(&sh.o_full[hf]);
+                    }
+                    if (!ok) break;
+                    release(iv);
+                    if (more) release(iv + 1);
+                }
+                it += 2 * s.count;
+            }
+            if (!ok) *dead = 1u;
+            commit(&sh.drained);  // products in flight end before tensor memory is given back
+            (void)warp_wait(&sh.drained, 0);
+        } else {
+            // ---- conversion: 16 codes a thread at a time, from global memory into the products' layout; K's codes of the next
+            // tile and V's of this one are on their way while the last ones are converted
+            constexpr int RC = D / 16;  // 16-code pieces of a row
+            constexpr int kTurns = (kKeys * RC + kConvert - 1) / kConvert;
+            const int me = tid - 10 * 32;
+            // 128 channels: sixteen lanes take two rows, eight of them half of each, so that their 16-byte stores, which the
+            // layout puts at even places of one row and odd places of the other, fill the banks once
+            auto row_of = [](int p) { return RC == 8 ? 2 * (p >> 4) + ((p >> 2) & 1) : p / RC; };
+            auto piece_of = [](int p) { return RC == 8 ? (p & 3) + 4 * (((p >> 2) ^ (p >> 3)) & 1) : p % RC; };
+            struct Tile {
+                uint32_t there, turn;
+                int key0, keys, hidden;  // hidden: the first key that some row does not see
+            };
+            uint4 kb[kTurns], vb[kTurns];
+            Tile now{}, ahead{};
+            uint32_t t = 0, it = 0, turn = 0;  // tile whose pages are next, item (K or V) that is next
+            bool ok = true;
+            int i = 0;
+            bool have = walk.next(a, tpu, s);
+            auto fetch = [&](const Tile& x, uint32_t slot, bool value, uint4 (&u)[kTurns]) {
+                const uint8_t* base = value ? a.c.v : a.c.k;
+#pragma unroll
+                for (int e = 0; e < kTurns; ++e) {
+                    const int p = me + e * kConvert, row = row_of(p);
+                    u[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (p >= kKeys * RC || x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u) continue;
+                    const int64_t at = ((int64_t)sh.ph[slot][row >> 4] * a.c.page + ((x.key0 + row) & (a.c.page - 1))) * D + piece_of(p) * 16;
+                    u[e] = __ldg(reinterpret_cast<const uint4*>(base + at));
+                }
+            };
+            // pages of the next tile, and its K on the way
+            auto step = [&]() {
+                if (!warp_wait(&sh.info_full[t % kInfo], (t / kInfo) & 1u) || __any_sync(0xffffffffu, *dead != 0u)) return false;
+                ahead.there = sh.there[t % kInfo];
+                ahead.turn = turn;
+                ahead.key0 = (s.i0 + i) * kKeys;
+                ahead.keys = s.ctx + s.last;
+                ahead.hidden = s.ctx + s.first + 1;
+                fetch(ahead, t % kInfo, false, kb);
+                if (++i == s.count) {
+                    have = walk.next(a, tpu, s);
+                    i = 0;
+                    ++turn;
+                }
+                return true;
+            };
+            auto put = [&](const Tile& x, bool value, const uint4 (&u)[kTurns]) {
+                const uint32_t st = it % S;
+                if (!warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u)) return false;
+                unsigned char* dst = ring + st * C::TILE;
+                const bool edge = kE4m3 && value && x.key0 > x.hidden - kKeys;
+#pragma unroll
+                for (int e = 0; e < kTurns; ++e) {
+                    const int p = me + e * kConvert, row = row_of(p), ch = piece_of(p);
+                    if (p >= kKeys * RC) continue;
+                    uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+                    if (edge) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t nan = __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            if (nan != 0u) {
+                                for (int y = 0; y < 4; ++y)
+                                    if ((nan >> (8 * y)) & 1u)
+                                        atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + y], odd_note(x.turn, x.key0 + row));
+                                c[q] &= ~nan;
+                            }
+                        }
+                    }
+                    uint32_t h[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
+                    unsigned char* at = dst + (ch >> 2) * C::BLK + row * 128;
+                    const int cc = (2 * ch) & 7;
+                    *reinterpret_cast<uint4*>(at + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.kv_full[st]);
+                ++it;
+                return true;
+            };
+            bool any = have;
+            if (any) ok = step();
+            while (ok && any) {
+                now = ahead;
+                fetch(now, t % kInfo, true, vb);
+                ok = put(now, false, kb);
+                ++t;
+                any = have;
+                if (ok && any) ok = step();
+                ok = ok && put(now, true, vb);
+            }
+            if (!ok) *dead = 1u;
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
+        const int hf = w >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
+        const uint32_t zt = tm + 128 * hf + lanes, ot = tm + C::O + C::DP * hf + lanes, at = tm + C::ACC + lanes;
+        const int rt = r / a.group, rh = r - rt * a.group;
+        uint32_t zc = 0, oc = 0, t = 0, turn = 0;
+        float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
+        float* po = reinterpret_cast<float*>(a.ws + L.o);
+        bool gone = false;
+        for (; (hf < C::HALVES) && !gone && walk.next(a, tpu, s); ++turn) {
+            const int nh = tiles_of_half(s, hf);
+            const int tok = s.first + hf * tpt + rt;
+            const bool on = rt < tpt && tok < s.last;
+            const TIO* q = static_cast<const TIO*>(a.q) + (s.start + tok) * a.qs + (int64_t)(s.h * a.group + rh) * D;
+            float cs = 0.f;
+            if (nh > 0) {
+                // the row of q, scaled by a power of two, into the products' layout (the half's last products have ended)
+                auto load8 = [&](int c, float (&x)[8]) {
+                    if constexpr (kSplit) {
+                        const float4 u = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float4 v = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                    } else {
+                        const uint4 u = on ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[2 * e] = __uint_as_float(y[e] << 16);
+                            x[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
+                        }
+                    }
+                };
+                float mx = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    float x[8];
+                    load8(c, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+                }
+                const int e = min(max((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
+                cs = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
+#pragma unroll
+                for (int c = 0; c < C::DP / 8; ++c) {
+                    uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+                    if (c < D / 8) {
+                        float x[8];
+                        load8(c, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+                            hi[i] = pack_f16(x0, x1);
+                            if constexpr (kSplit) {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+                                lo[i] = pack_f16(x0 - f.x, x1 - f.y);
+                            }
+                        }
+                    }
+                    const uint32_t to = (c >> 3) * C::BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4*>(sq + hf * C::TILE + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (kSplit) *reinterpret_cast<uint4*>(sq + C::TILE + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                tc::fence_async_smem();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.q_full[hf]);
+            }
+            const int seen = on ? s.ctx + tok + 1 : INT32_MAX;  // keys that the row sees
+            const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
+            float m = -FLT_MAX, vu = 0.f, vtop = 0.f;  // finite: a score of -inf then weighs nothing
+            float2 l2 = f2(0.f, 0.f);
+            for (int j = 0; j < s.count; ++j, ++t) {
+                const int slot = t % kInfo;
+                if (j < nh) {
+                    gone = !warp_wait(&sh.z_full[hf], zc++ & 1u);
+                    if (gone) break;
+                    tc::fence_after_sync();
+                    uint32_t z[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
+                    const float4 k0 = *reinterpret_cast<const float4*>(&sh.ks[slot][0]), k1 = *reinterpret_cast<const float4*>(&sh.ks[slot][4]);
+                    const float v_of = sh.vs[slot][lane & 7];
+                    const uint32_t there = sh.there[slot];
+                    // the unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the largest
+                    // met (what is in O would grow past fp32)
+                    float big = fabsf(v_of) < INFINITY ? fabsf(v_of) : 0.f;
+#pragma unroll
+                    for (int off = 4; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                    float ratio = 1.f;
+                    if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
+                        vtop = fmaxf(vtop, big);
+                        const float nu = fmaxf(big, vtop * 0x1p-40f);
+                        ratio = vu == 0.f ? 0.f : vu / nu;
+                        vu = nu;
+                    }
+                    const float pv_of = vu == 0.f ? (v_of == v_of ? 0.f : v_of) : v_of / vu;
+                    const float kg[8] = {k0.x * cs, k0.y * cs, k0.z * cs, k0.w * cs, k1.x * cs, k1.y * cs, k1.z * cs, k1.w * cs};
+                    const int key0 = (s.i0 + j) * kKeys;
+                    const bool edge = key0 > warp_seen - kKeys || there != 0xffu;
+                    tc::tmem_wait_ld();
+                    // scores in base 2, each rounded before the reference comes off, so that none passes the largest however
+                    // large they are
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const float2 x = __fmul2_rn(f2(f_of(z[2 * i]), f_of(z[2 * i + 1])), f2(kg[i >> 3], kg[i >> 3]));
+                        z[2 * i] = __float_as_uint(x.x);
+                        z[2 * i + 1] = __float_as_uint(x.y);
+                    }
+                    if (edge) {
+                        const int mine = seen - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i >= mine || ((there >> (i >> 4)) & 1u) == 0u) z[i] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(f_of(z[2 * e]), f_of(z[2 * e + 1]));
+#pragma unroll
+                    for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], f_of(z[i + 2 * e]), f_of(z[i + 2 * e + 1]));
+                    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    const float ref = top - m > 15.f ? top - 7.f : m;
+                    const float alpha = ex2(m - ref);
+                    m = ref;
+                    l2 = __fmul2_rn(l2, f2(alpha, alpha));
+                    // (the products into O up to here ended with the scores that were waited for)
+                    if constexpr (kSplit) {
+                        if (j > 0) {
+                            const float f = alpha * ratio;
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o0[16], o1[16], ac[16];
+                                tmem_ld16(ot + 16 * c, o0);
+                                tmem_ld16(ot + C::DP + 16 * c, o1);
+                                if (j > 1) tmem_ld16(at + 16 * c, ac);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float x = fmaf(f_of(o1[i]), 1.f / kRestUp, f_of(o0[i]));
+                                    ac[i] = __float_as_uint((j > 1 ? f_of(ac[i]) + x : x) * f);
+                                }
+                                tmem_st16(at + 16 * c, ac);
+                            }
+                            tc::tmem_wait_st();
+                        }
+                    } else if (j > 0 && __any_sync(0xffffffffu, alpha * ratio != 1.f)) {
+                        const float f = alpha * ratio;
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(ot + 16 * c, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f_of(o[i]) * f);
+                            tmem_st16(ot + 16 * c, o);
+                        }
+                    }
+                    float2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                    float pv = 0.f;
+                    constexpr int kPart = kSplit ? 16 : 32;  // pairs of keys at a time
+#pragma unroll
+                    for (int c = 0; c < 64 / kPart; ++c) {
+                        uint32_t p[kPart], p1[kSplit ? kPart : 1];
+#pragma unroll
+                        for (int i = 0; i < kPart; ++i) {
+                            const int e = kPart * c + i;
+                            if ((e & 7) == 0) pv = __shfl_sync(0xffffffffu, pv_of, e >> 3);
+                            const float2 x = __fadd2_rn(f2(f_of(z[2 * e]), f_of(z[2 * e + 1])), f2(-m, -m));
+                            const float2 y = f2(ex2(x.x), ex2(x.y));
+                            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
+                            float2 v = __fmul2_rn(y, f2(pv, pv));
+                            if (edge) {  // a hidden key's scale may be no number
+                                if (y.x == 0.f) v.x = 0.f;
+                                if (y.y == 0.f) v.y = 0.f;
+                            }
+                            p[i] = pack_f16(v.x, v.y);
+                            if constexpr (kSplit) {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+                                p1[i] = pack_f16((v.x - f.x) * kRestUp, (v.y - f.y) * kRestUp);
+                            }
+                        }
+                        if constexpr (kSplit) {
+                            tmem_st16(zt + 16 * c, p);
+                            tmem_st16(zt + 64 + 16 * c, p1);
+                        } else {
+                            tmem_st32(zt + 32 * c, p);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sh.p_full[hf]);
+                    l2 = __fadd2_rn(l2, __fadd2_rn(sum[0], sum[1]));
+                }
+                if (j >= nh) {  // (not before the tile is known: the barrier still counts the slot's last one)
+                    gone = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u);
+                    if (gone) break;
+                }
+                // the last tile's when the segment is over: conversion then is less than kInfo segments ahead (see odd_note)
+                __syncwarp();
+                if (lane == 0 && j + 1 < s.count) tc::mbar_arrive(&sh.info_free[slot]);
+            }
+            if (gone) break;
+            if (nh > 0) {
+                gone = !warp_wait(&sh.o_full[hf], oc++ & 1u);
+                gone = __any_sync(0xffffffffu, gone || *dead != 0u);
+                if (gone) break;
+                tc::fence_after_sync();
+            }
+            const bool whole = s.begun() && s.ended();
+            const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
+            const float l = l2.x + l2.y;
+            const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
+            TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D;
+            if (on && !whole) ml[place] = make_float2(m, l);
+            const int hidden = s.ctx + s.first + 1;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                if (nh > 0) {
+                    if constexpr (kSplit) {
+                        uint32_t o1[16], ac[16];
+                        tmem_ld16(ot + 16 * c, o);
+                        tmem_ld16(ot + C::DP + 16 * c, o1);
+                        if (nh > 1) tmem_ld16(at + 16 * c, ac);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = fmaf(f_of(o1[i]), 1.f / kRestUp, f_of(o[i]));
+                            o[i] = __float_as_uint(nh > 1 ? f_of(ac[i]) + x : x);
+                        }
+                    } else {
+                        tmem_ld16(ot + 16 * c, o);
+                        tc::tmem_wait_ld();
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0u;
+                }
+                if (!on) continue;
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    y[i] = f_of(o[i]) * mul;
+                    if (kE4m3 && (s.i0 + s.count - 1) * kKeys > hidden - kKeys) {
+                        const unsigned long long od = sh.odd[turn % kInfo][16 * c + i];
+                        if ((uint32_t)(od >> 32) == 0xfffffffeu - turn && (int)(uint32_t)od < seen) y[i] = NAN;
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(po + place * D + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                } else if constexpr (kSplit) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(out + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                } else {
+                    uint32_t b[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) b[i] = tc::pack_bf16(y[2 * i], y[2 * i + 1]);
+                    *reinterpret_cast<uint4*>(out + 16 * c) = make_uint4(b[0], b[1], b[2], b[3]);
+                    *reinterpret_cast<uint4*>(out + 16 * c + 8) = make_uint4(b[4], b[5], b[6], b[7]);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.info_free[(t - 1) % kInfo]);
+        }
+        if (gone) *dead = 1u;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (w == 8) tc::tmem_dealloc(tm, 512);
+    if (tid == 0) {
+        // what this CTA leaves to be joined: the unit that it began and did not end
+        Record rec{-1, 0, 0, 0, 0};
+        const bool failed = sh.dead != 0u;
+        walk = begin;
+        while (walk.next(a, tpu, s)) {
+            if (failed || !s.begun() || s.ended()) continue;
+            const int64_t e = s.place + (int64_t)kKeys * (s.tiles - 1);  // the last tile's place
+            rec = Record{s.n, s.h, s.rt, (int32_t)blockIdx.x, (int32_t)(((e + 1) * W - 1) / total)};
+        }
+        reinterpret_cast<Record*>(a.ws + L.records)[blockIdx.x] = rec;
+        reinterpret_cast<uint32_t*>(a.ws + L.flags)[blockIdx.x] = sh.flag | (failed ? kCheckTimeout : 0u);
+    }
+}
+
+// Joins a unit's pieces: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the CTAs that hold one, in an order
+// that the pieces' number fixes.  Block x looks after the unit that CTA x began; `wpr` warps take a row's pieces in turn.
+constexpr int kJoinWarps = 8;
+
+template <typename TIO, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    kda_attn_extend_join_kernel(const AttnExtendArgs a, const int rows_max, const int workers, const int tpu, const int half_tokens, const int wpr)
+{
+    constexpr int V = D / 32;
+    __shared__ float part[kJoinWarps][D + 1];
+    __shared__ uint32_t word;
+    const DecodeLayout L = decode_layout(workers, workers, rows_max, D);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        // the call's check word: every CTA's flags, so that nothing has to be cleared before the call
+        if (threadIdx.x == 0) word = 0u;
+        __syncthreads();
+        uint32_t f = 0u;
+        const uint32_t* flags = reinterpret_cast<const uint32_t*>(a.ws + L.flags);
+        for (int i = threadIdx.x; i < workers; i += blockDim.x) f |= flags[i];
+        if (f) atomicOr(&word, f);
+        __syncthreads();
+        if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(a.ws) = word;
+    }
+    const Record rec = reinterpret_cast<const Record*>(a.ws + L.records)[blockIdx.x];
+    if (rec.n < 0) return;
+    const Seq s = seq_of(a, rec.n);
+    const int r = blockIdx.y * (kJoinWarps / wpr) + w / wpr;  // row of the unit: 128 a half
+    const int in_half = r & 127, tok = rec.rt * tpu + (r >> 7) * half_tokens + in_half / a.group;
+    const bool on = r < rows_max && in_half < half_tokens * a.group && tok < min((rec.rt + 1) * tpu, s.rows);
+    const float2* ml = reinterpret_cast<const float2*>(a.ws + L.ml);
+    const float* po = reinterpret_cast<const float*>(a.ws + L.o);
+    const int pieces = rec.last - rec.first + 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * rec.first + 1 : 2 * (rec.first + i)); };
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    if (on) {
+        float m = -FLT_MAX;
+        for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+#pragma unroll 4
+        for (int i = w % wpr; i < pieces; i += wpr) {
+            const float2 x = ml[slot(i) * rows_max + r];
+            const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
+            const float f = ex2(x.x - m);
+            l += x.y * f;
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(p);
+                o[0] += y.x * f; o[1] += y.y * f; o[2] += y.z * f; o[3] += y.w * f;
+            } else if constexpr (V == 2) {
+                const float2 y = *reinterpret_cast<const float2*>(p);
+                o[0] += y.x * f; o[1] += y.y * f;
+            } else {
+                o[0] += *p * f;
+            }
+        }
+    }
+    if (wpr > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) part[w][lane * V + v] = o[v];
+        if (lane == 0) part[w][D] = l;
+        __syncthreads();
+        if (w % wpr != 0) return;
+        for (int i = 1; i < wpr; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] += part[w + i][lane * V + v];
+            l += part[w + i][D];
+        }
+    }
+    if (!on) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    TIO* od = static_cast<TIO*>(a.out) + ((s.start + tok) * a.Hq + rec.h * a.group + in_half % a.group) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
+}
+
+namespace {
+
+// Rows of a piece: a unit's, or fewer where the call has no more in one half.
+int piece_rows(int64_t tokens, int group, kda_dtype_t dt)
+{
+    const int64_t half = 128 / group;
+    return tokens > half && dt == KDA_BF16 ? 256 : tokens >= half ? 128 : (int)(tokens * group);
 }
 
 template <typename TIO, int D, bool kE4m3>
-__global__ void __launch_bounds__(kWarps * 32) kda_attn_extend_kernel(const AttnExtendArgs a)
+cudaError_t launch_extend(const AttnExtendArgs& a, cudaStream_t s)
 {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t token = row / a.Hq;
-    const int head = (int)(row - token * a.Hq), h = head / a.group;
-    if (token >= a.T) return;
-    int64_t start, end;
-    int n;
-    if (a.cu == nullptr) {
-        const int64_t len = a.T / a.N;
-        n = (int)(token / len);
-        start = n * len;
-        end = start + len;
-    } else {
-        int lo = 0, hi = a.N - 1;
-        while (lo < hi) {
-            const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-            lo += __popc(__ballot_sync(0xffffffffu, at <= hi && a.cu[at] <= token)) * step;
-            hi = min(hi, lo + step - 1);
-        }
-        n = lo;
-        start = a.cu[n];
-        end = a.cu[n + 1];
-        if (token < start || token >= end) return;
-    }
-    const int64_t len = a.lengths[n];
-    const bool bad = len < 0 || len > (int64_t)a.c.max_pages * a.c.page;
-    if (bad && lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), kCheckBadSeqlens);
-    const int64_t seen = bad ? 0 : min(len, len - (end - start) + (token - start) + 1);
-    const TIO* q = static_cast<const TIO*>(a.q) + token * a.qs + (int64_t)head * D + lane * V;
-    float x[V], o[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        x[v] = ld_io(q, v) * a.scale * kLog2e;
-        o[v] = 0.f;
-    }
-    auto value = [](const uint8_t* p) {
-        if constexpr (kE4m3) {
-            uint32_t lo, hi;
-            widen<true>(*p, lo, hi);
-            return __half2float(__ushort_as_half((unsigned short)(lo & 0xffffu)));
-        } else {
-            return (float)(int8_t)*p;
-        }
-    };
-    for (int64_t j = 0; j < seen; ++j) {
-        const int p = a.c.table[(int64_t)n * a.c.max_pages + j / a.c.page];
-        if (p < 0 || p >= a.c.num_pages) {
-            if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(a.ws), kCheckBadSeqlens);
-            continue;
-        }
-        const int64_t ph = (int64_t)p * a.Hkv + h, at = (ph * a.c.page + j % a.c.page) * D + lane * V;
-        float z = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) z = fmaf(x[v], value(a.c.k + at + v), z);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-        z *= a.c.k_scale[ph];
-        const float now = fmaxf(fmaxf(m, z), -3.4e38f), f = exp2f(m - now), w = exp2f(z - now), vs = a.c.v_scale[ph];
-        m = now;
-        l = fmaf(l, f, w);
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(o[v], f, w * (value(a.c.v + at + v) * vs));
-    }
-    TIO* out = static_cast<TIO*>(a.out) + (token * a.Hq + head) * D + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) st_io(out, v, l == 0.f ? 0.f : o[v] / l);
+    constexpr bool kSplit = sizeof(TIO) == 4;
+    using C = Cfg<D, kSplit>;
+    static_assert(C::SMEM + sizeof(Shared) <= 232448, "the tiles fit an SM");
+    static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "register split");
+    auto kern = kda_attn_extend_kernel<TIO, D, kE4m3>;
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(kern, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int ctas = sm_count_of_current_device();
+    const int rows = piece_rows(a.T, a.group, kSplit ? KDA_F32 : KDA_BF16);
+    kern<<<ctas, kThreads, C::SMEM, s>>>(a, rows);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // about ctas / units pieces a unit: four or more a warp
+    const int half_tokens = 128 / a.group, tpu = C::HALVES * half_tokens;
+    const int64_t units = (a.T + tpu - 1) / tpu * a.Hkv, pieces = ctas / units;
+    const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
+    const dim3 grid((unsigned)ctas, (unsigned)((rows * wpr + kJoinWarps - 1) / kJoinWarps));
+    return launch_dependent(kda_attn_extend_join_kernel<TIO, D>, grid, dim3(kJoinWarps * 32), 0, s, a, rows, ctas, tpu, half_tokens, wpr);
 }
 
-size_t attn_extend_workspace_bytes(int64_t, int, int, kda_dtype_t) { return 256; }
+template <typename TIO, int D>
+cudaError_t launch_code(const AttnExtendArgs& a, cudaStream_t s)
+{
+    return a.c.dtype == KDA_CACHE_E4M3 ? launch_extend<TIO, D, true>(a, s) : launch_extend<TIO, D, false>(a, s);
+}
+
+template <typename TIO>
+cudaError_t launch_d(const AttnExtendArgs& a, cudaStream_t s)
+{
+    return a.d == 32 ? launch_code<TIO, 32>(a, s) : a.d == 64 ? launch_code<TIO, 64>(a, s) : launch_code<TIO, 128>(a, s);
+}
+
+}  // namespace
+
+size_t attn_extend_workspace_bytes(int64_t tokens, int group, int d, kda_dtype_t dt)
+{
+    const int ctas = sm_count_of_current_device();
+    return decode_layout(ctas, ctas, piece_rows(tokens, group, dt), d).total;
+}
 
 cudaError_t launch_attn_extend(const AttnExtendArgs& a, kda_dtype_t dt, cudaStream_t s)
 {
-    cudaError_t e = cudaMemsetAsync(a.ws, 0, 4, s);
-    if (e != cudaSuccess || a.T == 0) return e;
-    const int64_t ctas = (a.T * a.Hq + kWarps - 1) / kWarps;
-    if (ctas > 2147483647LL) return cudaErrorInvalidValue;
-    auto go = [&](auto kern) { kern<<<(unsigned)ctas, kWarps * 32, 0, s>>>(a); };
-    auto by_code = [&](auto io, auto d) {
-        using TIO = decltype(io);
-        constexpr int D = decltype(d)::value;
-        if (a.c.dtype == KDA_CACHE_E4M3) go(kda_attn_extend_kernel<TIO, D, true>);
-        else go(kda_attn_extend_kernel<TIO, D, false>);
-    };
-    auto by_d = [&](auto io) {
-        if (a.d == 32) by_code(io, std::integral_constant<int, 32>{});
-        else if (a.d == 64) by_code(io, std::integral_constant<int, 64>{});
-        else by_code(io, std::integral_constant<int, 128>{});
-    };
-    if (dt == KDA_BF16) by_d(__nv_bfloat16{});
-    else by_d(float{});
-    return cudaGetLastError();
+    if (a.T == 0) return cudaMemsetAsync(a.ws, 0, 4, s);  // the check word
+    return dt == KDA_BF16 ? launch_d<__nv_bfloat16>(a, s) : launch_d<float>(a, s);
 }
 
 }  // namespace kda
