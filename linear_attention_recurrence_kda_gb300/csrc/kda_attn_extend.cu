@@ -45,8 +45,7 @@ constexpr int kConvert = 192;
 constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
 constexpr int kGroups = kKeys / 16;
 constexpr int kGap = 256;      // what a unit's start and end cost, in keys
-// warpgroups' registers after the split: 256 x 168 + 256 x 88 = 512 x 128, what the launch holds
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
+constexpr uint32_t kOdd = 256u;  // some scale of the tile is not a positive finite number
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRestUp = 2048.f;  // what a weight's second part is multiplied by (see kda_attn_decode.cu)
 
@@ -60,15 +59,6 @@ template <int D, bool kSplit> struct Cfg {
     static constexpr int HALVES = kSplit ? 1 : 2;
     // tensor memory, columns: where the outputs of the halves (or of P's parts) are, and the sum over tiles (kSplit)
     static constexpr int O = kSplit ? 128 : 256, ACC = 384;
-};
-
-struct Shared {
-    uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], drained;
-    uint32_t tmem, dead, flag;
-    uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there
-    int ph[kInfo][kGroups];                                 // its page and head in the cache
-    alignas(16) float ks[kInfo][kGroups], vs[kInfo][kGroups];
-    unsigned long long odd[kInfo][128];  // by the segment's turn: the first key with a NaN in a channel
 };
 
 // ---------------------------------------------------------------- the line of work
@@ -155,6 +145,16 @@ struct Walk {
             units = units_of(s, tpu);
         }
     }
+};
+
+struct Shared {
+    uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], drained;
+    uint32_t tmem, dead, flag;
+    uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; kOdd: see there
+    int64_t off[kInfo][kGroups];                            // where its first row is in the cache
+    alignas(16) float ks[kInfo][kGroups], vs[kInfo][kGroups];
+    unsigned long long odd[kInfo][128];  // by the segment's turn: the first key with a NaN in a channel
+    Walk begin;  // this CTA's first tile
 };
 
 // What is noted in odd[]: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers them), the
@@ -252,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     const int64_t total = prefix[kThreads];
     const int64_t W = max((int64_t)1, min((int64_t)gridDim.x, total / kKeys));
     const int64_t b0 = blockIdx.x < W ? blockIdx.x * total / W : total, b1 = blockIdx.x < W ? (blockIdx.x + 1) * total / W : total;
-    Walk begin;
-    begin.end = b1;
-    begin.n = a.N;
+    Walk walk;
+    walk.end = b1;
+    walk.n = a.N;
     if (b0 < b1) {  // a run of sequences by bisection, then one by one; its head and rows
         int lo = 0, hi = kThreads - 1;
         while (lo < hi) {
@@ -265,34 +265,34 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         int64_t at = prefix[lo], one;
         int n = lo * chunk;
         for (;;) {
-            begin.s = seq_of(a, n);
-            one = places_of(begin.s, tpu);
+            walk.s = seq_of(a, n);
+            one = places_of(walk.s, tpu);
             if (at + one * a.Hkv > b0 || n + 1 >= a.N) break;
             at += one * a.Hkv;
             ++n;
         }
-        begin.n = n;
-        begin.units = units_of(begin.s, tpu);
-        begin.h = (int)((b0 - at) / one);
-        at += begin.h * one;
+        walk.n = n;
+        walk.units = units_of(walk.s, tpu);
+        walk.h = (int)((b0 - at) / one);
+        at += walk.h * one;
         lo = 0;
-        hi = begin.units - 1;
+        hi = walk.units - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (at + places_before(begin.s, tpu, mid) <= b0) lo = mid;
+            if (at + places_before(walk.s, tpu, mid) <= b0) lo = mid;
             else hi = mid - 1;
         }
-        begin.rt = lo;
-        begin.at = at + places_before(begin.s, tpu, lo);
-        begin.i = (int)max((int64_t)0, (b0 - begin.at - kGap + kKeys - 1) / kKeys);
+        walk.rt = lo;
+        walk.at = at + places_before(walk.s, tpu, lo);
+        walk.i = (int)max((int64_t)0, (b0 - walk.at - kGap + kKeys - 1) / kKeys);
     }
+    if (tid == 0) sh.begin = walk;
     __syncthreads();  // the prefix is read
     if constexpr (D < 64) {
         for (int i = tid; i < (int)(S * C::TILE / 16); i += kThreads) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
         tc::fence_async_smem();
         __syncthreads();
     }
-    Walk walk = begin;
     Segment s;
     // key tiles of this segment that a half has rows for
     auto tiles_of_half = [&](const Segment& g, int hf) {
@@ -303,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     };
 
     if (w >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (w == 9) {
             // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
             const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
@@ -317,23 +316,33 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     const int p = __ldg(a.c.table + (int64_t)s.n * a.c.max_pages + (key >> page_shift));
                     return p >= 0 && p < a.c.num_pages ? p : -2;
                 };
+                // a page's piece of the tile on its way to L2, for k and v: the lane of its first group
+                const int box = min(kKeys, a.c.page), gpp = box / 16;
+                auto to_l2 = [&](int p, int i) {
+                    if (p < 0 || lane >= 16 || grp % gpp != 0) return;
+                    const uint8_t* at = (lane < 8 ? a.c.k : a.c.v) + (((int64_t)p * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D;
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(box * D) : "memory");
+                };
                 auto scale_of = [&](int p) {
                     return p >= 0 && lane < 16 ? __ldg((lane < 8 ? a.c.k_scale : a.c.v_scale) + (int64_t)p * a.Hkv + s.h) : 0.f;
                 };
                 // a tile's pages are asked for two tiles ahead, its scales one
                 int page = page_of(s.i0), page1 = page_of(s.i0 + 1);
                 float scale = scale_of(page);
+                to_l2(page, s.i0);
                 for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++t) {
                     const int page2 = page_of(i + 2);
                     const float scale1 = scale_of(page1);
-                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
+                    to_l2(page1, i + 1);
+                    uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
+                    if (__any_sync(0xffffffffu, page >= 0 && lane < 16 && !(scale > 0.f && scale < INFINITY))) there |= kOdd;
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
                     const uint32_t slot = t % kInfo;
                     ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
                     if (lane < 8) {
                         sh.ks[slot][grp] = scale;
-                        sh.ph[slot][grp] = page >= 0 ? page * a.Hkv + s.h : 0;
+                        sh.off[slot][grp] = page >= 0 ? (((int64_t)page * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D : 0;
                     } else if (lane < 16) {
                         sh.vs[slot][grp] = scale;
                     }
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 for (int p = 0; p < (kSplit ? 2 : 1); ++p)
 #pragma unroll
                     for (int e = 0; e < kKeys / 16; ++e)
-                        mma_ts(tm + C::O + C::DP * (kSplit ? p : hf), tm + 128 * hf + 64 * p + 8 * e, desc_v(v + e * 2048, D == 128 ? C::BLK : 1024u),
+                        mma_ts(tm + C::O + C::DP * (kSplit ? p : hf), tm + 128 * hf + (kSplit ? 32 * (e >> 1) + 16 * p + 8 * (e & 1) : 8 * e), desc_v(v + e * 2048, D == 128 ? C::BLK : 1024u),
                                id_o, (!kSplit && !first) || e > 0);
             };
             // a slot is given back only after it was seen full, also by a half that has no use for it
@@ -422,8 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             const int me = tid - 10 * 32;
             // 128 channels: sixteen lanes take two rows, eight of them half of each, so that their 16-byte stores, which the
             // layout puts at even places of one row and odd places of the other, fill the banks once
-            auto row_of = [](int p) { return RC == 8 ? 2 * (p >> 4) + ((p >> 2) & 1) : p / RC; };
-            auto piece_of = [](int p) { return RC == 8 ? (p & 3) + 4 * (((p >> 2) ^ (p >> 3)) & 1) : p % RC; };
+            constexpr int kStep = kConvert / RC;  // rows from a thread's piece to its next: multiples of 8
+            const int row0 = RC == 8 ? 2 * (me >> 4) + ((me >> 2) & 1) : me / RC;
+            const int ch = RC == 8 ? (me & 3) + 4 * (((me >> 2) ^ (me >> 3)) & 1) : me % RC;
+            static_assert(kConvert % RC == 0 && kStep % 8 == 0, "a thread's pieces lie in one column of the layout");
+            unsigned char* const to = ring + (ch >> 2) * C::BLK + row0 * 128;
+            const int c0 = ((2 * ch) & 7) ^ (row0 & 7), c1 = c0 ^ 1;
             struct Tile {
                 uint32_t there, turn;
                 int key0, keys, hidden;  // hidden: the first key that some row does not see
@@ -435,14 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             int i = 0;
             bool have = walk.next(a, tpu, s);
             auto fetch = [&](const Tile& x, uint32_t slot, bool value, uint4 (&u)[kTurns]) {
-                const uint8_t* base = value ? a.c.v : a.c.k;
+                const uint8_t* base = (value ? a.c.v : a.c.k) + ch * 16;
+                const bool whole = (x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys;
 #pragma unroll
                 for (int e = 0; e < kTurns; ++e) {
-                    const int p = me + e * kConvert, row = row_of(p);
+                    const int row = row0 + kStep * e;
                     u[e] = make_uint4(0u, 0u, 0u, 0u);
-                    if (p >= kKeys * RC || x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u) continue;
-                    const int64_t at = ((int64_t)sh.ph[slot][row >> 4] * a.c.page + ((x.key0 + row) & (a.c.page - 1))) * D + piece_of(p) * 16;
-                    u[e] = __ldg(reinterpret_cast<const uint4*>(base + at));
+                    if ((e + 1) * kStep > kKeys && row >= kKeys) continue;
+                    if (!whole && (x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u)) continue;
+                    // (volatile: on its way from here on, not from where it is used)
+                    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w)
+                                 : "l"(base + sh.off[slot][row >> 4] + (row & 15) * D));
                 }
             };
             // pages of the next tile, and its K on the way
@@ -464,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             auto put = [&](const Tile& x, bool value, const uint4 (&u)[kTurns]) {
                 const uint32_t st = it % S;
                 if (!warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u)) return false;
-                unsigned char* dst = ring + st * C::TILE;
+                unsigned char* dst = to + st * C::TILE;
                 const bool edge = kE4m3 && value && x.key0 > x.hidden - kKeys;
 #pragma unroll
                 for (int e = 0; e < kTurns; ++e) {
-                    const int p = me + e * kConvert, row = row_of(p), ch = piece_of(p);
-                    if (p >= kKeys * RC) continue;
+                    const int row = row0 + kStep * e;
+                    if ((e + 1) * kStep > kKeys && row >= kKeys) continue;
                     uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
                     if (edge) {
 #pragma unroll
@@ -486,10 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     uint32_t h[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
-                    unsigned char* at = dst + (ch >> 2) * C::BLK + row * 128;
-                    const int cc = (2 * ch) & 7;
-                    *reinterpret_cast<uint4*>(at + ((cc ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c0 * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c1 * 16) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
                 tc::fence_async_smem();
                 __syncwarp();
@@ -512,7 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
         const int hf = w >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
@@ -584,17 +598,16 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             const int seen = on ? s.ctx + tok + 1 : INT32_MAX;  // keys that the row sees
             const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
             float m = -FLT_MAX, vu = 0.f, vtop = 0.f;  // finite: a score of -inf then weighs nothing
-            float2 l2 = f2(0.f, 0.f);
+            float l = 0.f;
             for (int j = 0; j < s.count; ++j, ++t) {
                 const int slot = t % kInfo;
                 if (j < nh) {
                     gone = !warp_wait(&sh.z_full[hf], zc++ & 1u);
                     if (gone) break;
                     tc::fence_after_sync();
-                    uint32_t z[128];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
-                    const float4 k0 = *reinterpret_cast<const float4*>(&sh.ks[slot][0]), k1 = *reinterpret_cast<const float4*>(&sh.ks[slot][4]);
+                    // Z is read twice, 32 keys at a time: for the maximum, and for the weights, which go over what has been read
+                    uint32_t z[2][32];
+                    tmem_ld32(zt, z[0]);
                     const float v_of = sh.vs[slot][lane & 7];
                     const uint32_t there = sh.there[slot];
                     // the unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the largest
@@ -609,37 +622,67 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         ratio = vu == 0.f ? 0.f : vu / nu;
                         vu = nu;
                     }
-                    const float pv_of = vu == 0.f ? (v_of == v_of ? 0.f : v_of) : v_of / vu;
-                    const float kg[8] = {k0.x * cs, k0.y * cs, k0.z * cs, k0.w * cs, k1.x * cs, k1.y * cs, k1.z * cs, k1.w * cs};
-                    const int key0 = (s.i0 + j) * kKeys;
-                    const bool edge = key0 > warp_seen - kKeys || there != 0xffu;
-                    tc::tmem_wait_ld();
-                    // scores in base 2, each rounded before the reference comes off, so that none passes the largest however
-                    // large they are
+                    const float pv_of = ((there >> (lane & 7)) & 1u) == 0u ? 1.f : vu == 0.f ? (v_of == v_of ? 0.f : v_of) : v_of / vu;
+                    const int key0 = (s.i0 + j) * kKeys, mine = seen - key0;
+                    const bool edge = key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu;
+                    const bool odd = (there & kOdd) != 0u;
+                    // a key of the tile (general form): is it seen by this row, and its score in base 2
+                    auto shown = [&](int i) { return i < mine && ((there >> (i >> 4)) & 1u) != 0u; };
+                    auto k_of = [&](int c) {
+                        const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][2 * c]);
+                        return f2(x.x * cs, x.y * cs);
+                    };
+                    // f(chunk, its number) over the four chunks of 32 keys, the next one's load in flight
+                    auto chunks = [&](auto f) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            tc::tmem_wait_ld();
+                            tmem_ld32(zt + 32 * c + 32, z[1]);
+                            f(z[0], c);
+                            tc::tmem_wait_ld();
+                            if (c == 0) tmem_ld32(zt + 64, z[0]);
+                            f(z[1], c + 1);
+                        }
+                    };
+                    // the same where keys are hidden or scales or scores are out of the ordinary: one copy, a chunk at a time
+                    auto chunks_one_by_one = [&](auto f) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tc::tmem_wait_ld();
+                            f(z[0], c);
+                            if (c < 3) tmem_ld32(zt + 32 * c + 32, z[0]);
+                        }
+                    };
+                    float top = -INFINITY;
+                    if (!odd && !edge) {
+                        chunks([&](uint32_t (&x)[32], int c) {
+                            const float2 kg = k_of(c);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const float2 x = __fmul2_rn(f2(f_of(z[2 * i]), f_of(z[2 * i + 1])), f2(kg[i >> 3], kg[i >> 3]));
-                        z[2 * i] = __float_as_uint(x.x);
-                        z[2 * i + 1] = __float_as_uint(x.y);
+                            for (int g = 0; g < 2; ++g) {
+                                float m0 = fmaxf(f_of(x[16 * g]), f_of(x[16 * g + 1])), m1 = fmaxf(f_of(x[16 * g + 2]), f_of(x[16 * g + 3]));
+#pragma unroll
+                                for (int i = 4; i < 16; i += 4) {
+                                    m0 = max3(m0, f_of(x[16 * g + i]), f_of(x[16 * g + i + 1]));
+                                    m1 = max3(m1, f_of(x[16 * g + i + 2]), f_of(x[16 * g + i + 3]));
+                                }
+                                top = fmaxf(top, fmaxf(m0, m1) * (g ? kg.y : kg.x));
+                            }
+                        });
+                    } else {
+                        chunks_one_by_one([&](uint32_t (&x)[32], int c) {
+                            const float2 kg = k_of(c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float y = __fmul_rn(f_of(x[i]), i < 16 ? kg.x : kg.y);
+                                if (shown(32 * c + i)) top = fmaxf(top, y);
+                            }
+                        });
                     }
-                    if (edge) {
-                        const int mine = seen - key0;
-#pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i >= mine || ((there >> (i >> 4)) & 1u) == 0u) z[i] = 0xff800000u;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(f_of(z[2 * e]), f_of(z[2 * e + 1]));
-#pragma unroll
-                    for (int i = 8; i < 128; i += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], f_of(z[i + 2 * e]), f_of(z[i + 2 * e + 1]));
-                    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    tmem_ld32(zt, z[0]);
                     const float ref = top - m > 15.f ? top - 7.f : m;
                     const float alpha = ex2(m - ref);
                     m = ref;
-                    l2 = __fmul2_rn(l2, f2(alpha, alpha));
+                    l *= alpha;
                     // (the products into O up to here ended with the scores that were waited for)
                     if constexpr (kSplit) {
                         if (j > 0) {
@@ -672,42 +715,68 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                             tmem_st16(ot + 16 * c, o);
                         }
                     }
-                    float2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-                    float pv = 0.f;
-                    constexpr int kPart = kSplit ? 16 : 32;  // pairs of keys at a time
-#pragma unroll
-                    for (int c = 0; c < 64 / kPart; ++c) {
-                        uint32_t p[kPart], p1[kSplit ? kPart : 1];
-#pragma unroll
-                        for (int i = 0; i < kPart; ++i) {
-                            const int e = kPart * c + i;
-                            if ((e & 7) == 0) pv = __shfl_sync(0xffffffffu, pv_of, e >> 3);
-                            const float2 x = __fadd2_rn(f2(f_of(z[2 * e]), f_of(z[2 * e + 1])), f2(-m, -m));
-                            const float2 y = f2(ex2(x.x), ex2(x.y));
-                            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
-                            float2 v = __fmul2_rn(y, f2(pv, pv));
-                            if (edge) {  // a hidden key's scale may be no number
-                                if (y.x == 0.f) v.x = 0.f;
-                                if (y.y == 0.f) v.y = 0.f;
-                            }
-                            p[i] = pack_f16(v.x, v.y);
-                            if constexpr (kSplit) {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-                                p1[i] = pack_f16((v.x - f.x) * kRestUp, (v.y - f.y) * kRestUp);
-                            }
-                        }
+                    // Weights times their value's scale: the scale goes into the exponent and comes off the sums, group by group.
+                    // Not where a scale is none, and not beyond 2^20, where a score is rounded, as the reference was,
+                    // before the reference comes off, so that none passes the largest however large they are.
+                    const bool slow = odd || __any_sync(0xffffffffu, fabsf(m) > 1048576.f);
+                    const float lg_of = __log2f(pv_of), ip_of = 1.f / pv_of;
+                    auto store = [&](const uint32_t (&p)[16], const uint32_t (&p1)[kSplit ? 16 : 1], int c) {
+                        tmem_st16(zt + (kSplit ? 32 : 16) * c, p);
+                        if constexpr (kSplit) tmem_st16(zt + 32 * c + 16, p1);
+                    };
+                    auto pack = [&](float2 y, uint32_t& hi, uint32_t& lo) {
+                        hi = pack_f16(y.x, y.y);
                         if constexpr (kSplit) {
-                            tmem_st16(zt + 16 * c, p);
-                            tmem_st16(zt + 64 + 16 * c, p1);
-                        } else {
-                            tmem_st32(zt + 32 * c, p);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                            lo = pack_f16((y.x - f.x) * kRestUp, (y.y - f.y) * kRestUp);
                         }
+                    };
+                    if (!slow && !edge) {
+                        chunks([&](uint32_t (&x)[32], int c) {
+                            uint32_t p[16], p1[kSplit ? 16 : 1];
+                            const float2 kg = k_of(c);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float off = __shfl_sync(0xffffffffu, lg_of, 2 * c + g) - m, ip = __shfl_sync(0xffffffffu, ip_of, 2 * c + g);
+                                const float2 k2 = g ? f2(kg.y, kg.y) : f2(kg.x, kg.x), o2 = f2(off, off);
+                                float2 sum = f2(0.f, 0.f);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int e = 16 * g + 2 * i;
+                                    float2 y = __ffma2_rn(f2(f_of(x[e]), f_of(x[e + 1])), k2, o2);
+                                    y = f2(ex2(y.x), ex2(y.y));
+                                    sum = __fadd2_rn(sum, y);
+                                    pack(y, p[8 * g + i], p1[kSplit ? 8 * g + i : 0]);
+                                }
+                                l = fmaf(sum.x + sum.y, ip, l);
+                            }
+                            store(p, p1, c);
+                        });
+                    } else {
+                        chunks_one_by_one([&](uint32_t (&x)[32], int c) {
+                            uint32_t p[16], p1[kSplit ? 16 : 1];
+                            const float2 kg = k_of(c);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float pv = __shfl_sync(0xffffffffu, pv_of, 2 * c + g), k = g ? kg.y : kg.x;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int e = 16 * g + 2 * i, key = 32 * c + e;
+                                    // (rounded apart: the packed forms fuse)
+                                    float2 y = f2(__fsub_rn(__fmul_rn(f_of(x[e]), k), m), __fsub_rn(__fmul_rn(f_of(x[e + 1]), k), m));
+                                    y = f2(shown(key) ? ex2(y.x) : 0.f, shown(key + 1) ? ex2(y.y) : 0.f);
+                                    l += y.x + y.y;
+                                    // (a hidden key's scale may be no number)
+                                    pack(f2(y.x == 0.f ? 0.f : y.x * pv, y.y == 0.f ? 0.f : y.y * pv), p[8 * g + i], p1[kSplit ? 8 * g + i : 0]);
+                                }
+                            }
+                            store(p, p1, c);
+                        });
                     }
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sh.p_full[hf]);
-                    l2 = __fadd2_rn(l2, __fadd2_rn(sum[0], sum[1]));
                 }
                 if (j >= nh) {  // (not before the tile is known: the barrier still counts the slot's last one)
                     gone = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u);
@@ -726,7 +795,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             }
             const bool whole = s.begun() && s.ended();
             const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
-            const float l = l2.x + l2.y;
             const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
             TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D;
             if (on && !whole) ml[place] = make_float2(m, l);
@@ -791,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         // what this CTA leaves to be joined: the unit that it began and did not end
         Record rec{-1, 0, 0, 0, 0};
         const bool failed = sh.dead != 0u;
-        walk = begin;
+        walk = sh.begin;
         while (walk.next(a, tpu, s)) {
             if (failed || !s.begun() || s.ended()) continue;
             const int64_t e = s.place + (int64_t)kKeys * (s.tiles - 1);  // the last tile's place
@@ -896,7 +964,6 @@ cudaError_t launch_extend(const AttnExtendArgs& a, cudaStream_t s)
     constexpr bool kSplit = sizeof(TIO) == 4;
     using C = Cfg<D, kSplit>;
     static_assert(C::SMEM + sizeof(Shared) <= 232448, "the tiles fit an SM");
-    static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= kThreads * 128, "register split");
     auto kern = kda_attn_extend_kernel<TIO, D, kE4m3>;
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, (int)C::SMEM);
