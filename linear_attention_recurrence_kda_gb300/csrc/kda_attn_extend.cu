@@ -57,6 +57,9 @@ template <int D, bool kSplit> struct Cfg {
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
     static constexpr int HALVES = kSplit ? 1 : 2;
+    // warpgroups' registers after the split, of the 512 x 128 that the launch holds; kSplit leaves a softmax group idle
+    static constexpr int REGS_SOFTMAX = kSplit ? 240 : 176, REGS_IDLE = 24, REGS_OTHER = kSplit ? 88 : 80;
+    static_assert(128 * REGS_SOFTMAX + 128 * (kSplit ? REGS_IDLE : REGS_SOFTMAX) + 256 * REGS_OTHER <= kThreads * 128, "register split");
     // tensor memory, columns: where the outputs of the halves (or of P's parts) are, and the sum over tiles (kSplit)
     static constexpr int O = kSplit ? 128 : 256, ACC = 384;
 };
@@ -152,9 +155,15 @@ struct Shared {
     uint32_t tmem, dead, flag;
     uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; kOdd: see there
     int64_t off[kInfo][kGroups];                            // where its first row is in the cache
-    alignas(16) float ks[kInfo][kGroups], vs[kInfo][kGroups];
+    // a tile's scales of K; V's in the unit of O (pv), their logarithm and their reciprocal; the unit, and the last one over it
+    alignas(16) float ks[kInfo][kGroups], pv[kInfo][kGroups], lg[kInfo][kGroups], ip[kInfo][kGroups];
+    float2 unit[kInfo];
+    uint32_t dirty[kInfo];           // by the segment's turn: turn + 1 where something is noted in odd[]
     unsigned long long odd[kInfo][128];  // by the segment's turn: the first key with a NaN in a channel
-    Walk begin;  // this CTA's first tile
+    Walk begin;                // this CTA's first tile
+    Walk walk[kThreads / 32];  // by warp: where it is, and its segment (registers are short)
+    Segment seg[kThreads / 32];
+    uint32_t more[kThreads / 32];
 };
 
 // What is noted in odd[]: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers them), the
@@ -211,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int i = tid; i < kInfo * 128; i += kThreads) (&sh.odd[0][0])[i] = ~0ull;
+    if (tid < kInfo) sh.dirty[tid] = 0u;
     if (w == 8) tc::tmem_alloc(&sh.tmem, 512);
     // places before every run of `chunk` sequences
     const int chunk = (a.N + kThreads - 1) / kThreads;
@@ -293,7 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         tc::fence_async_smem();
         __syncthreads();
     }
-    Segment s;
+    // the warp's next segment
+    const Segment& s = sh.seg[w];
+    if (lane == 0) sh.walk[w] = walk;
+    auto next_segment = [&]() {
+        __syncwarp();
+        if (lane == 0) sh.more[w] = sh.walk[w].next(a, tpu, sh.seg[w]) ? 1u : 0u;
+        __syncwarp();
+        return *(volatile uint32_t*)&sh.more[w] != 0u;
+    };
     // key tiles of this segment that a half has rows for
     auto tiles_of_half = [&](const Segment& g, int hf) {
         const int first = g.first + hf * tpt;
@@ -303,12 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     };
 
     if (w >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         if (w == 9) {
             // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
             const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
             uint32_t t = 0;
             bool ok = true;
-            while (ok && walk.next(a, tpu, s)) {
+            while (ok && next_segment()) {
                 const int keys = s.ctx + s.last;
                 auto page_of = [&](int i) -> int {
                     const int key = i * kKeys + grp * 16;
@@ -328,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 };
                 // a tile's pages are asked for two tiles ahead, its scales one
                 int page = page_of(s.i0), page1 = page_of(s.i0 + 1);
+                float vu = 0.f, vtop = 0.f;
                 float scale = scale_of(page);
                 to_l2(page, s.i0);
                 for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++t) {
@@ -337,6 +357,21 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
                     if (__any_sync(0xffffffffu, page >= 0 && lane < 16 && !(scale > 0.f && scale < INFINITY))) there |= kOdd;
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
+                    // The unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the
+                    // largest met (what is in O would grow past fp32).  Lanes 8-15 have the scales.
+                    float big = page >= 0 && fabsf(scale) < INFINITY ? fabsf(scale) : 0.f;
+#pragma unroll
+                    for (int off = 4; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                    big = __shfl_sync(0xffffffffu, big, 8);
+                    float ratio = 1.f;
+                    if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
+                        vtop = fmaxf(vtop, big);
+                        const float nu = fmaxf(big, vtop * 0x1p-40f);
+                        ratio = vu == 0.f ? 0.f : vu / nu;
+                        vu = nu;
+                    }
+                    const float pv = page < 0 ? 1.f : vu == 0.f ? (scale == scale ? 0.f : scale) : scale / vu;
+                    const float lg = log2f(pv), ip = 1.f / pv;
                     const uint32_t slot = t % kInfo;
                     ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
@@ -344,9 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         sh.ks[slot][grp] = scale;
                         sh.off[slot][grp] = page >= 0 ? (((int64_t)page * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D : 0;
                     } else if (lane < 16) {
-                        sh.vs[slot][grp] = scale;
+                        sh.pv[slot][grp] = pv;
+                        sh.lg[slot][grp] = lg;
+                        sh.ip[slot][grp] = ip;
+                    } else if (lane == 16) {
+                        sh.there[slot] = there;
+                        sh.unit[slot] = f2(vu, ratio);
                     }
-                    if (lane == 0) sh.there[slot] = there;
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sh.info_full[slot]);
                     page = page1;
@@ -388,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             };
             // a slot is given back only after it was seen full, also by a half that has no use for it
             auto release = [&](uint32_t x) { commit(&sh.kv_empty[x % S]); };
-            while (ok && walk.next(a, tpu, s)) {
+            while (ok && next_segment()) {
                 int nh[2] = {tiles_of_half(s, 0), C::HALVES == 2 ? tiles_of_half(s, 1) : 0};
                 ok = full(it);
 #pragma unroll
@@ -424,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             commit(&sh.drained);  // products in flight end before tensor memory is given back
             (void)warp_wait(&sh.drained, 0);
         } else {
-            // ---- conversion: 16 codes a thread at a time, from global memory into the products' layout; K's codes of the next
-            // tile and V's of this one are on their way while the last ones are converted
+            // ---- conversion: 16 codes a thread at a time, from global memory into the products' layout; a register that has been
+            // converted takes the next item's codes, which are on their way until that item's turn
             constexpr int RC = D / 16;  // 16-code pieces of a row
             constexpr int kTurns = (kKeys * RC + kConvert - 1) / kConvert;
             const int me = tid - 10 * 32;
@@ -438,51 +477,49 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             unsigned char* const to = ring + (ch >> 2) * C::BLK + row0 * 128;
             const int c0 = ((2 * ch) & 7) ^ (row0 & 7), c1 = c0 ^ 1;
             struct Tile {
-                uint32_t there, turn;
+                uint32_t there, turn, slot;
                 int key0, keys, hidden;  // hidden: the first key that some row does not see
             };
-            uint4 kb[kTurns], vb[kTurns];
+            uint4 u[kTurns];
             Tile now{}, ahead{};
-            uint32_t t = 0, it = 0, turn = 0;  // tile whose pages are next, item (K or V) that is next
-            bool ok = true;
+            uint32_t t = 0, it = 0, turn = 0;  // tile, item (K or V of a tile), segment
             int i = 0;
-            bool have = walk.next(a, tpu, s);
-            auto fetch = [&](const Tile& x, uint32_t slot, bool value, uint4 (&u)[kTurns]) {
-                const uint8_t* base = (value ? a.c.v : a.c.k) + ch * 16;
-                const bool whole = (x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys;
-#pragma unroll
-                for (int e = 0; e < kTurns; ++e) {
-                    const int row = row0 + kStep * e;
-                    u[e] = make_uint4(0u, 0u, 0u, 0u);
-                    if ((e + 1) * kStep > kKeys && row >= kKeys) continue;
-                    if (!whole && (x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u)) continue;
-                    // (volatile: on its way from here on, not from where it is used)
-                    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w)
-                                 : "l"(base + sh.off[slot][row >> 4] + (row & 15) * D));
-                }
+            bool ok = true, have = next_segment();
+            auto fetch = [&](int e, const uint8_t* base, const Tile& x, bool whole) {
+                const int row = row0 + kStep * e;
+                u[e] = make_uint4(0u, 0u, 0u, 0u);
+                if ((e + 1) * kStep > kKeys && row >= kKeys) return;
+                if (!whole && (x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u)) return;
+                // (volatile: on its way from here on, not from where it is used)
+                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w)
+                             : "l"(base + sh.off[x.slot][row >> 4] + (row & 15) * D));
             };
-            // pages of the next tile, and its K on the way
+            auto whole_of = [](const Tile& x) { return (x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys; };
+            // the next tile, once its pages are known
             auto step = [&]() {
                 if (!warp_wait(&sh.info_full[t % kInfo], (t / kInfo) & 1u) || __any_sync(0xffffffffu, *dead != 0u)) return false;
-                ahead.there = sh.there[t % kInfo];
+                ahead.slot = t % kInfo;
+                ahead.there = sh.there[ahead.slot];
                 ahead.turn = turn;
                 ahead.key0 = (s.i0 + i) * kKeys;
                 ahead.keys = s.ctx + s.last;
                 ahead.hidden = s.ctx + s.first + 1;
-                fetch(ahead, t % kInfo, false, kb);
+                ++t;
                 if (++i == s.count) {
-                    have = walk.next(a, tpu, s);
+                    have = next_segment();
                     i = 0;
                     ++turn;
                 }
                 return true;
             };
-            auto put = [&](const Tile& x, bool value, const uint4 (&u)[kTurns]) {
+            // item x into its place, item y (if any) on its way
+            auto put = [&](const Tile& x, bool value, const Tile& y, bool next) {
                 const uint32_t st = it % S;
                 if (!warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u)) return false;
                 unsigned char* dst = to + st * C::TILE;
-                const bool edge = kE4m3 && value && x.key0 > x.hidden - kKeys;
+                const bool edge = kE4m3 && value && x.key0 > x.hidden - kKeys, whole = whole_of(y);
+                const uint8_t* base = (value ? a.c.k : a.c.v) + ch * 16;  // of y: the other tensor
 #pragma unroll
                 for (int e = 0; e < kTurns; ++e) {
                     const int row = row0 + kStep * e;
@@ -493,9 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         for (int q = 0; q < 4; ++q) {
                             const uint32_t nan = __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                             if (nan != 0u) {
-                                for (int y = 0; y < 4; ++y)
-                                    if ((nan >> (8 * y)) & 1u)
-                                        atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + y], odd_note(x.turn, x.key0 + row));
+                                for (int b = 0; b < 4; ++b)
+                                    if ((nan >> (8 * b)) & 1u)
+                                        atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + b], odd_note(x.turn, x.key0 + row));
+                                sh.dirty[x.turn % kInfo] = x.turn + 1u;
                                 c[q] &= ~nan;
                             }
                         }
@@ -505,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
                     *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c0 * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c1 * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+                    if (next) fetch(e, base, y, whole);
                 }
                 tc::fence_async_smem();
                 __syncwarp();
@@ -513,20 +552,25 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 return true;
             };
             bool any = have;
-            if (any) ok = step();
-            while (ok && any) {
+            if (any && (ok = step())) {
                 now = ahead;
-                fetch(now, t % kInfo, true, vb);
-                ok = put(now, false, kb);
-                ++t;
+#pragma unroll
+                for (int e = 0; e < kTurns; ++e) fetch(e, a.c.k + ch * 16, now, whole_of(now));
+            }
+            while (ok && any) {
+                ok = put(now, false, now, true);
                 any = have;
                 if (ok && any) ok = step();
-                ok = ok && put(now, true, vb);
+                ok = ok && put(now, true, ahead, any);
+                now = ahead;
             }
             if (!ok) *dead = 1u;
         }
         __syncwarp();
+    } else if (kSplit && w >= 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_IDLE));
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
         // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
         const int hf = w >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
@@ -536,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
         float* po = reinterpret_cast<float*>(a.ws + L.o);
         bool gone = false;
-        for (; (hf < C::HALVES) && !gone && walk.next(a, tpu, s); ++turn) {
+        for (; !gone && next_segment(); ++turn) {
             const int nh = tiles_of_half(s, hf);
             const int tok = s.first + hf * tpt + rt;
             const bool on = rt < tpt && tok < s.last;
@@ -544,14 +588,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             float cs = 0.f;
             if (nh > 0) {
                 // the row of q, scaled by a power of two, into the products' layout (the half's last products have ended)
+                // twice, the second time from L1: a row held between would take the scores' registers
                 auto load8 = [&](int c, float (&x)[8]) {
                     if constexpr (kSplit) {
-                        const float4 u = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float4 y = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
                         const float4 v = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
                     } else {
-                        const uint4 u = on ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+                        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             x[2 * e] = __uint_as_float(y[e] << 16);
@@ -559,18 +604,22 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         }
                     }
                 };
+                constexpr int kBatch = kSplit ? 4 : D >= 64 ? 8 : 4;
                 float mx = 0.f;
+#pragma unroll 1
+                for (int c4 = 0; c4 < D / 8; c4 += kBatch) {
+                    float x[kBatch][8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    float x[8];
-                    load8(c, x);
+                    for (int c = 0; c < kBatch; ++c) load8(c4 + c, x[c]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+                    for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[c][e]));
                 }
                 const int e = min(max((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127, -100), 127);
                 const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
                 cs = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
-#pragma unroll
+#pragma unroll 2
                 for (int c = 0; c < C::DP / 8; ++c) {
                     uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
                     if (c < D / 8) {
@@ -597,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             }
             const int seen = on ? s.ctx + tok + 1 : INT32_MAX;  // keys that the row sees
             const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
-            float m = -FLT_MAX, vu = 0.f, vtop = 0.f;  // finite: a score of -inf then weighs nothing
+            float m = -FLT_MAX, vu = 0.f;  // finite: a score of -inf then weighs nothing
             float l = 0.f;
             for (int j = 0; j < s.count; ++j, ++t) {
                 const int slot = t % kInfo;
@@ -605,24 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     gone = !warp_wait(&sh.z_full[hf], zc++ & 1u);
                     if (gone) break;
                     tc::fence_after_sync();
-                    // Z is read twice, 32 keys at a time: for the maximum, and for the weights, which go over what has been read
-                    uint32_t z[2][32];
-                    tmem_ld32(zt, z[0]);
-                    const float v_of = sh.vs[slot][lane & 7];
                     const uint32_t there = sh.there[slot];
-                    // the unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the largest
-                    // met (what is in O would grow past fp32)
-                    float big = fabsf(v_of) < INFINITY ? fabsf(v_of) : 0.f;
-#pragma unroll
-                    for (int off = 4; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                    float ratio = 1.f;
-                    if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
-                        vtop = fmaxf(vtop, big);
-                        const float nu = fmaxf(big, vtop * 0x1p-40f);
-                        ratio = vu == 0.f ? 0.f : vu / nu;
-                        vu = nu;
-                    }
-                    const float pv_of = ((there >> (lane & 7)) & 1u) == 0u ? 1.f : vu == 0.f ? (v_of == v_of ? 0.f : v_of) : v_of / vu;
+                    const float2 unit = sh.unit[slot];
+                    const float ratio = unit.y;
+                    vu = unit.x;
                     const int key0 = (s.i0 + j) * kKeys, mine = seen - key0;
                     const bool edge = key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu;
                     const bool odd = (there & kOdd) != 0u;
@@ -632,44 +667,41 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][2 * c]);
                         return f2(x.x * cs, x.y * cs);
                     };
-                    // f(chunk, its number) over the four chunks of 32 keys, the next one's load in flight
+                    // f(chunk, its number) over the four chunks of 32 keys, where keys are hidden or scales or scores are out of the
+                    // ordinary: one copy, read chunk by chunk
                     auto chunks = [&](auto f) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; c += 2) {
-                            tc::tmem_wait_ld();
-                            tmem_ld32(zt + 32 * c + 32, z[1]);
-                            f(z[0], c);
-                            tc::tmem_wait_ld();
-                            if (c == 0) tmem_ld32(zt + 64, z[0]);
-                            f(z[1], c + 1);
-                        }
-                    };
-                    // the same where keys are hidden or scales or scores are out of the ordinary: one copy, a chunk at a time
-                    auto chunks_one_by_one = [&](auto f) {
-#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(zt + 32 * c, x);
                             tc::tmem_wait_ld();
-                            f(z[0], c);
-                            if (c < 3) tmem_ld32(zt + 32 * c + 32, z[0]);
+                            f(x, c);
                         }
                     };
+                    // (Z is read whole for the maximum; its second half is read again for the weights, which leaves registers for them)
+                    uint32_t z[128];
                     float top = -INFINITY;
                     if (!odd && !edge) {
-                        chunks([&](uint32_t (&x)[32], int c) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
                             const float2 kg = k_of(c);
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                float m0 = fmaxf(f_of(x[16 * g]), f_of(x[16 * g + 1])), m1 = fmaxf(f_of(x[16 * g + 2]), f_of(x[16 * g + 3]));
+                                const uint32_t* x = z + 32 * c + 16 * g;
+                                float m0 = fmaxf(f_of(x[0]), f_of(x[1])), m1 = fmaxf(f_of(x[2]), f_of(x[3]));
 #pragma unroll
                                 for (int i = 4; i < 16; i += 4) {
-                                    m0 = max3(m0, f_of(x[16 * g + i]), f_of(x[16 * g + i + 1]));
-                                    m1 = max3(m1, f_of(x[16 * g + i + 2]), f_of(x[16 * g + i + 3]));
+                                    m0 = max3(m0, f_of(x[i]), f_of(x[i + 1]));
+                                    m1 = max3(m1, f_of(x[i + 2]), f_of(x[i + 3]));
                                 }
                                 top = fmaxf(top, fmaxf(m0, m1) * (g ? kg.y : kg.x));
                             }
-                        });
+                        }
                     } else {
-                        chunks_one_by_one([&](uint32_t (&x)[32], int c) {
+                        chunks([&](uint32_t (&x)[32], int c) {
                             const float2 kg = k_of(c);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
@@ -678,7 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                             }
                         });
                     }
-                    tmem_ld32(zt, z[0]);
                     const float ref = top - m > 15.f ? top - 7.f : m;
                     const float alpha = ex2(m - ref);
                     m = ref;
@@ -719,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     // Not where a scale is none, and not beyond 2^20, where a score is rounded, as the reference was,
                     // before the reference comes off, so that none passes the largest however large they are.
                     const bool slow = odd || __any_sync(0xffffffffu, fabsf(m) > 1048576.f);
-                    const float lg_of = __log2f(pv_of), ip_of = 1.f / pv_of;
                     auto store = [&](const uint32_t (&p)[16], const uint32_t (&p1)[kSplit ? 16 : 1], int c) {
                         tmem_st16(zt + (kSplit ? 32 : 16) * c, p);
                         if constexpr (kSplit) tmem_st16(zt + 32 * c + 16, p1);
@@ -732,12 +762,12 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         }
                     };
                     if (!slow && !edge) {
-                        chunks([&](uint32_t (&x)[32], int c) {
+                        auto weigh = [&](const uint32_t* x, int c) {
                             uint32_t p[16], p1[kSplit ? 16 : 1];
-                            const float2 kg = k_of(c);
+                            const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][2 * c]), ips = *reinterpret_cast<const float2*>(&sh.ip[slot][2 * c]);
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const float off = __shfl_sync(0xffffffffu, lg_of, 2 * c + g) - m, ip = __shfl_sync(0xffffffffu, ip_of, 2 * c + g);
+                                const float off = (g ? lg.y : lg.x) - m, ip = g ? ips.y : ips.x;
                                 const float2 k2 = g ? f2(kg.y, kg.y) : f2(kg.x, kg.x), o2 = f2(off, off);
                                 float2 sum = f2(0.f, 0.f);
 #pragma unroll
@@ -751,14 +781,21 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                                 l = fmaf(sum.x + sum.y, ip, l);
                             }
                             store(p, p1, c);
-                        });
+                        };
+                        tmem_ld32(zt + 64, z + 64);
+                        weigh(z, 0);
+                        tmem_ld32(zt + 96, z + 96);
+                        weigh(z + 32, 1);
+                        tc::tmem_wait_ld();
+                        weigh(z + 64, 2);
+                        weigh(z + 96, 3);
                     } else {
-                        chunks_one_by_one([&](uint32_t (&x)[32], int c) {
+                        chunks([&](uint32_t (&x)[32], int c) {
                             uint32_t p[16], p1[kSplit ? 16 : 1];
                             const float2 kg = k_of(c);
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const float pv = __shfl_sync(0xffffffffu, pv_of, 2 * c + g), k = g ? kg.y : kg.x;
+                                const float pv = sh.pv[slot][2 * c + g], k = g ? kg.y : kg.x;
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const int e = 16 * g + 2 * i, key = 32 * c + e;
@@ -798,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
             TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D;
             if (on && !whole) ml[place] = make_float2(m, l);
-            const int hidden = s.ctx + s.first + 1;
+            const bool dirty = kE4m3 && *(volatile uint32_t*)&sh.dirty[turn % kInfo] == turn + 1u;
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
@@ -825,9 +862,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 if (!on) continue;
                 float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    y[i] = f_of(o[i]) * mul;
-                    if (kE4m3 && (s.i0 + s.count - 1) * kKeys > hidden - kKeys) {
+                for (int i = 0; i < 16; ++i) y[i] = f_of(o[i]) * mul;
+                if (dirty) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
                         const unsigned long long od = sh.odd[turn % kInfo][16 * c + i];
                         if ((uint32_t)(od >> 32) == 0xfffffffeu - turn && (int)(uint32_t)od < seen) y[i] = NAN;
                     }
@@ -859,7 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         // what this CTA leaves to be joined: the unit that it began and did not end
         Record rec{-1, 0, 0, 0, 0};
         const bool failed = sh.dead != 0u;
-        walk = sh.begin;
+        Walk walk = sh.begin;
+        Segment s;
         while (walk.next(a, tpu, s)) {
             if (failed || !s.begun() || s.ended()) continue;
             const int64_t e = s.place + (int64_t)kKeys * (s.tiles - 1);  // the last tile's place
