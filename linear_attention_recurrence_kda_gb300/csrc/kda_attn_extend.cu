@@ -57,9 +57,6 @@ template <int D, bool kSplit> struct Cfg {
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
     static constexpr int HALVES = kSplit ? 1 : 2;
-    // warpgroups' registers after the split, of the 512 x 128 that the launch holds; kSplit leaves a softmax group idle
-    static constexpr int REGS_SOFTMAX = kSplit ? 240 : 176, REGS_IDLE = 24, REGS_OTHER = kSplit ? 88 : 80;
-    static_assert(128 * REGS_SOFTMAX + 128 * (kSplit ? REGS_IDLE : REGS_SOFTMAX) + 256 * REGS_OTHER <= kThreads * 128, "register split");
     // tensor memory, columns: where the outputs of the halves (or of P's parts) are, and the sum over tiles (kSplit)
     static constexpr int O = kSplit ? 128 : 256, ACC = 384;
 };
@@ -321,7 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     };
 
     if (w >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         if (w == 9) {
             // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
             const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
@@ -399,9 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             const uint32_t f16 = ~((1u << 7) | (1u << 10));
             const uint32_t id_z = tc::idesc_bf16(128, kKeys) & f16, id_o = (tc::idesc_bf16(128, C::DP) & f16) | (1u << 16);
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
-            uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+            uint32_t it = 0, phase = 0;  // phase: bits 0, 1 of q, 2, 3 of P
             bool ok = true;
             auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u); };
+            auto flip = [&](uint64_t* bar, uint32_t bit) {
+                const bool got = warp_wait(bar, (phase >> bit) & 1u);
+                phase ^= 1u << bit;
+                return got;
+            };
             auto issue_z = [&](int hf, uint32_t x) {
                 const uint32_t k = ra + (x % S) * C::TILE;
                 // kSplit: both parts of Q into the one Z, the small ones first
@@ -428,36 +429,30 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             // a slot is given back only after it was seen full, also by a half that has no use for it
             auto release = [&](uint32_t x) { commit(&sh.kv_empty[x % S]); };
             while (ok && next_segment()) {
-                int nh[2] = {tiles_of_half(s, 0), C::HALVES == 2 ? tiles_of_half(s, 1) : 0};
-                ok = full(it);
-#pragma unroll
-                for (int hf = 0; hf < C::HALVES; ++hf) {
-                    if (!ok || nh[hf] == 0) continue;
-                    ok = warp_wait(&sh.q_full[hf], qc[hf]++ & 1u);
-                    if (!ok) continue;
-                    tc::fence_after_sync();
-                    issue_z(hf, it);
-                }
-                if (ok) release(it);
-                for (int j = 0; j < s.count && ok; ++j) {
+                const int n0 = tiles_of_half(s, 0), n1 = C::HALVES == 2 ? tiles_of_half(s, 1) : 0, count = s.count;
+                // iteration j: the halves' O of tile j, each followed by its Z of tile j + 1 (one copy of either: the roles' code
+                // shares a small instruction cache)
+#pragma unroll 1
+                for (int j = -1; j < count && ok; ++j) {
                     const uint32_t iv = it + 2 * j + 1;
-                    const bool more = j + 1 < s.count;
-                    ok = !__any_sync(0xffffffffu, *dead != 0u) && (!more || full(iv + 1)) && full(iv);
-#pragma unroll
+                    const bool more = j + 1 < count;
+                    ok = !__any_sync(0xffffffffu, *dead != 0u) && (!more || full(iv + 1)) && (j < 0 || full(iv));
+#pragma unroll 1
                     for (int hf = 0; hf < C::HALVES; ++hf) {
-                        if (!ok || j >= nh[hf]) continue;
-                        ok = warp_wait(&sh.p_full[hf], pc[hf]++ & 1u);
+                        const int nh = hf ? n1 : n0;
+                        if (!ok || j >= nh || nh == 0) continue;
+                        ok = j < 0 ? flip(&sh.q_full[hf], hf) : flip(&sh.p_full[hf], 2 + hf);
                         if (!ok) continue;
                         tc::fence_after_sync();
-                        issue_o(hf, iv, j == 0);
-                        if (j + 1 < nh[hf]) issue_z(hf, iv + 1);  // its commit also covers O's product
+                        if (j >= 0) issue_o(hf, iv, j == 0);
+                        if (j + 1 < nh) issue_z(hf, iv + 1);  // its commit also covers O's product
                         else commit(&sh.o_full[hf]);
                     }
                     if (!ok) break;
-                    release(iv);
+                    if (j >= 0) release(iv);
                     if (more) release(iv + 1);
                 }
-                it += 2 * s.count;
+                it += 2 * count;
             }
             if (!ok) *dead = 1u;
             commit(&sh.drained);  // products in flight end before tensor memory is given back
@@ -485,17 +480,29 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             uint32_t t = 0, it = 0, turn = 0;  // tile, item (K or V of a tile), segment
             int i = 0;
             bool ok = true, have = next_segment();
-            auto fetch = [&](int e, const uint8_t* base, const Tile& x, bool whole) {
+            // (volatile: on its way from here on, not from where it is used)
+            auto load = [&](int e, const uint8_t* base, uint32_t slot) {
                 const int row = row0 + kStep * e;
-                u[e] = make_uint4(0u, 0u, 0u, 0u);
-                if ((e + 1) * kStep > kKeys && row >= kKeys) return;
-                if (!whole && (x.key0 + row >= x.keys || ((x.there >> (row >> 4)) & 1u) == 0u)) return;
-                // (volatile: on its way from here on, not from where it is used)
                 asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w)
-                             : "l"(base + sh.off[x.slot][row >> 4] + (row & 15) * D));
+                             : "l"(base + sh.off[slot][row >> 4] + (row & 15) * D));
             };
-            auto whole_of = [](const Tile& x) { return (x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys; };
+            auto inside = [&](int e) { return (e + 1) * kStep <= kKeys || row0 + kStep * e < kKeys; };
+            auto fetch = [&](const Tile& x, bool value) {
+                const uint8_t* base = (value ? a.c.v : a.c.k) + ch * 16;
+                if ((x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys) {
+#pragma unroll
+                    for (int e = 0; e < kTurns; ++e)
+                        if (inside(e)) load(e, base, x.slot);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kTurns; ++e) {
+                        const int row = row0 + kStep * e;
+                        u[e] = make_uint4(0u, 0u, 0u, 0u);
+                        if (inside(e) && x.key0 + row < x.keys && ((x.there >> (row >> 4)) & 1u) != 0u) load(e, base, x.slot);
+                    }
+                }
+            };
             // the next tile, once its pages are known
             auto step = [&]() {
                 if (!warp_wait(&sh.info_full[t % kInfo], (t / kInfo) & 1u) || __any_sync(0xffffffffu, *dead != 0u)) return false;
@@ -513,64 +520,71 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 }
                 return true;
             };
-            // item x into its place, item y (if any) on its way
-            auto put = [&](const Tile& x, bool value, const Tile& y, bool next) {
+            // item x into its place
+            auto put = [&](const Tile& x, bool value) {
                 const uint32_t st = it % S;
                 if (!warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u)) return false;
                 unsigned char* dst = to + st * C::TILE;
-                const bool edge = kE4m3 && value && x.key0 > x.hidden - kKeys, whole = whole_of(y);
-                const uint8_t* base = (value ? a.c.k : a.c.v) + ch * 16;  // of y: the other tensor
+                if (kE4m3 && value && x.key0 > x.hidden - kKeys) {
+                    // NaN that not every row may see leave the tile
 #pragma unroll
-                for (int e = 0; e < kTurns; ++e) {
-                    const int row = row0 + kStep * e;
-                    if ((e + 1) * kStep > kKeys && row >= kKeys) continue;
-                    uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-                    if (edge) {
+                    for (int e = 0; e < kTurns; ++e) {
+                        uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const uint32_t nan = __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            if (nan != 0u) {
-                                for (int b = 0; b < 4; ++b)
-                                    if ((nan >> (8 * b)) & 1u)
-                                        atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + b], odd_note(x.turn, x.key0 + row));
-                                sh.dirty[x.turn % kInfo] = x.turn + 1u;
-                                c[q] &= ~nan;
-                            }
+                            const uint32_t nan = inside(e) ? __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+                            if (nan == 0u) continue;
+#pragma unroll 1
+                            for (int b = 0; b < 4; ++b)
+                                if ((nan >> (8 * b)) & 1u)
+                                    atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + b], odd_note(x.turn, x.key0 + row0 + kStep * e));
+                            sh.dirty[x.turn % kInfo] = x.turn + 1u;
+                            c[q] &= ~nan;
                         }
+                        u[e] = make_uint4(c[0], c[1], c[2], c[3]);
                     }
-                    uint32_t h[8];
+                }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) widen<kE4m3>(c[q], h[2 * q], h[2 * q + 1]);
+                for (int e = 0; e < kTurns; ++e) {
+                    if (!inside(e)) continue;
+                    uint32_t h[8];
+                    widen<kE4m3>(u[e].x, h[0], h[1]);
+                    widen<kE4m3>(u[e].y, h[2], h[3]);
+                    widen<kE4m3>(u[e].z, h[4], h[5]);
+                    widen<kE4m3>(u[e].w, h[6], h[7]);
                     *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c0 * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c1 * 16) = make_uint4(h[4], h[5], h[6], h[7]);
-                    if (next) fetch(e, base, y, whole);
                 }
+                return true;
+            };
+            auto done = [&]() {
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.kv_full[st]);
+                if (lane == 0) tc::mbar_arrive(&sh.kv_full[it % S]);
                 ++it;
-                return true;
             };
             bool any = have;
             if (any && (ok = step())) {
                 now = ahead;
-#pragma unroll
-                for (int e = 0; e < kTurns; ++e) fetch(e, a.c.k + ch * 16, now, whole_of(now));
+                fetch(now, false);
             }
-            while (ok && any) {
-                ok = put(now, false, now, true);
-                any = have;
-                if (ok && any) ok = step();
-                ok = ok && put(now, true, ahead, any);
-                now = ahead;
+            // (one copy for keys and values)
+#pragma unroll 1
+            for (bool value = false; ok && any; value = !value) {
+                if (value) {
+                    any = have;
+                    if (any) ok = step();
+                }
+                ok = ok && put(now, value);
+                if (!ok) break;
+                if (value) now = ahead;
+                if (!value || any) fetch(now, !value);  // (a tile's pages are read before its first half is reported)
+                done();
             }
             if (!ok) *dead = 1u;
         }
         __syncwarp();
-    } else if (kSplit && w >= 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_IDLE));
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    } else if (!kSplit || w < 4) {
         // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
         const int hf = w >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
@@ -667,41 +681,46 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][2 * c]);
                         return f2(x.x * cs, x.y * cs);
                     };
-                    // f(chunk, its number) over the four chunks of 32 keys, where keys are hidden or scales or scores are out of the
-                    // ordinary: one copy, read chunk by chunk
+                    // f(chunk, its number) over the four chunks of 32 keys, the next one's load in flight.  (Loops, and one copy of what is
+                    // out of the ordinary: the roles' code shares a small instruction cache.)
+                    uint32_t z[2][32];
                     auto chunks = [&](auto f) {
+                        tmem_ld32(zt, z[0]);
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(zt + 32 * c, x);
+                        for (int c = 0; c < 4; c += 2) {
                             tc::tmem_wait_ld();
-                            f(x, c);
+                            tmem_ld32(zt + 32 * c + 32, z[1]);
+                            f(z[0], c);
+                            tc::tmem_wait_ld();
+                            if (c == 0) tmem_ld32(zt + 64, z[0]);
+                            f(z[1], c + 1);
                         }
                     };
-                    // (Z is read whole for the maximum; its second half is read again for the weights, which leaves registers for them)
-                    uint32_t z[128];
+                    auto chunks_one_by_one = [&](auto f) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld32(zt + 32 * c, z[0]);
+                            tc::tmem_wait_ld();
+                            f(z[0], c);
+                        }
+                    };
                     float top = -INFINITY;
                     if (!odd && !edge) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(zt + 32 * c, z + 32 * c);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        chunks([&](const uint32_t (&x)[32], int c) {
                             const float2 kg = k_of(c);
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const uint32_t* x = z + 32 * c + 16 * g;
-                                float m0 = fmaxf(f_of(x[0]), f_of(x[1])), m1 = fmaxf(f_of(x[2]), f_of(x[3]));
+                                float m0 = fmaxf(f_of(x[16 * g]), f_of(x[16 * g + 1])), m1 = fmaxf(f_of(x[16 * g + 2]), f_of(x[16 * g + 3]));
 #pragma unroll
                                 for (int i = 4; i < 16; i += 4) {
-                                    m0 = max3(m0, f_of(x[i]), f_of(x[i + 1]));
-                                    m1 = max3(m1, f_of(x[i + 2]), f_of(x[i + 3]));
+                                    m0 = max3(m0, f_of(x[16 * g + i]), f_of(x[16 * g + i + 1]));
+                                    m1 = max3(m1, f_of(x[16 * g + i + 2]), f_of(x[16 * g + i + 3]));
                                 }
                                 top = fmaxf(top, fmaxf(m0, m1) * (g ? kg.y : kg.x));
                             }
-                        }
+                        });
                     } else {
-                        chunks([&](uint32_t (&x)[32], int c) {
+                        chunks_one_by_one([&](const uint32_t (&x)[32], int c) {
                             const float2 kg = k_of(c);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
@@ -762,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                         }
                     };
                     if (!slow && !edge) {
-                        auto weigh = [&](const uint32_t* x, int c) {
+                        chunks([&](const uint32_t (&x)[32], int c) {
                             uint32_t p[16], p1[kSplit ? 16 : 1];
                             const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][2 * c]), ips = *reinterpret_cast<const float2*>(&sh.ip[slot][2 * c]);
 #pragma unroll
@@ -781,16 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                                 l = fmaf(sum.x + sum.y, ip, l);
                             }
                             store(p, p1, c);
-                        };
-                        tmem_ld32(zt + 64, z + 64);
-                        weigh(z, 0);
-                        tmem_ld32(zt + 96, z + 96);
-                        weigh(z + 32, 1);
-                        tc::tmem_wait_ld();
-                        weigh(z + 64, 2);
-                        weigh(z + 96, 3);
+                        });
                     } else {
-                        chunks([&](uint32_t (&x)[32], int c) {
+                        chunks_one_by_one([&](const uint32_t (&x)[32], int c) {
                             uint32_t p[16], p1[kSplit ? 16 : 1];
                             const float2 kg = k_of(c);
 #pragma unroll
