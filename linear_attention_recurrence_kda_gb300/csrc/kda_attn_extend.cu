@@ -40,11 +40,13 @@ using namespace attn;
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;
 constexpr int kConvert = 192;
 constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
 constexpr int kGroups = kKeys / 16;
 constexpr int kGap = 256;      // what a unit's start and end cost, in keys
+constexpr float kUnset = -FLT_MAX;  // the reference of a row that has met no score above -inf
+constexpr float kFar = 1048576.f;   // 2^20: references beyond it have their scores rounded first
+constexpr uint32_t kHidden = 0xff800000u;
 constexpr uint32_t kOdd = 256u;  // some scale of the tile is not a positive finite number
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRestUp = 2048.f;  // what a weight's second part is multiplied by (see kda_attn_decode.cu)
@@ -57,6 +59,11 @@ template <int D, bool kSplit> struct Cfg {
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
     static constexpr int HALVES = kSplit ? 1 : 2;
+    static constexpr int WARPS = 8 * HALVES;              // of the softmax: a row has two threads, one for each half of a tile's keys
+    static constexpr int THREADS = 32 * (WARPS + 8);      // products, pages, six of conversion
+    // warpgroups' registers after the split, of what the launch holds
+    static constexpr int REGS = kSplit ? 128 : 80, REGS_SOFTMAX = kSplit ? 152 : 88, REGS_OTHER = kSplit ? 104 : 64;
+    static_assert(32 * WARPS * REGS_SOFTMAX + 256 * REGS_OTHER <= THREADS * REGS, "register split");
     // tensor memory, columns: where the outputs of the halves (or of P's parts) are, and the sum over tiles (kSplit)
     static constexpr int O = kSplit ? 128 : 256, ACC = 384;
 };
@@ -151,16 +158,17 @@ struct Shared {
     uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], drained;
     uint32_t tmem, dead, flag;
     uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; kOdd: see there
-    int64_t off[kInfo][kGroups];                            // where its first row is in the cache
+    uint32_t at[kInfo][kGroups];                            // where it is in the cache, in groups of 16 rows (2^32 of them are terabytes)
     // a tile's scales of K; V's in the unit of O (pv), their logarithm and their reciprocal; the unit, and the last one over it
     alignas(16) float ks[kInfo][kGroups], pv[kInfo][kGroups], lg[kInfo][kGroups], ip[kInfo][kGroups];
     float2 unit[kInfo];
     uint32_t dirty[kInfo];           // by the segment's turn: turn + 1 where something is noted in odd[]
     unsigned long long odd[kInfo][128];  // by the segment's turn: the first key with a NaN in a channel
-    Walk begin;                // this CTA's first tile
-    Walk walk[kThreads / 32];  // by warp: where it is, and its segment (registers are short)
-    Segment seg[kThreads / 32];
-    uint32_t more[kThreads / 32];
+    Walk begin;     // this CTA's first tile
+    Walk walk[24];  // by warp: where it is, and its segment (registers are short)
+    Segment seg[24];
+    uint32_t more[24];
+    float top[2][2][2][128], sum[2][2][2][128];  // in turn: what a row's two threads tell each other, by half and part
 };
 
 // What is noted in odd[]: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers them), the
@@ -171,6 +179,17 @@ __device__ __forceinline__ unsigned long long odd_note(uint32_t turn, int key)
     return ((unsigned long long)(0xfffffffeu - turn) << 32) | (uint32_t)key;
 }
 
+// Or over the two warps (64 threads) that share rows; they meet here.
+__device__ __forceinline__ bool pair_any(int id, bool x)
+{
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y)
+                 : "r"((uint32_t)x), "r"(id)
+                 : "memory");
+    return y != 0u;
+}
+
 __device__ __forceinline__ float2 f2(float x, float y) { return make_float2(x, y); }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) { KDA_TMEM_LD16(taddr, v); }
@@ -179,11 +198,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) { K
 }  // namespace
 
 template <typename TIO, int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const AttnExtendArgs a, const int rows_max)
+__global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_attn_extend_kernel(const AttnExtendArgs a, const int rows_max)
 {
     constexpr bool kSplit = sizeof(TIO) == 4;
     using C = Cfg<D, kSplit>;
-    constexpr int S = C::STAGES;
+    constexpr int S = C::STAGES, kThreads = C::THREADS, kSoft = C::WARPS;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Shared sh;
     unsigned char* sq = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -198,9 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     griddep_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.q_full[i], 4);
+            tc::mbar_init(&sh.q_full[i], 8);
             tc::mbar_init(&sh.z_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.p_full[i], 8);
             tc::mbar_init(&sh.o_full[i], 1);
         }
         for (int i = 0; i < S; ++i) {
@@ -209,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         }
         for (int i = 0; i < kInfo; ++i) {
             tc::mbar_init(&sh.info_full[i], 1);
-            tc::mbar_init(&sh.info_free[i], 4 * C::HALVES);
+            tc::mbar_init(&sh.info_free[i], kSoft);
         }
         tc::mbar_init(&sh.drained, 1);
         sh.dead = 0u;
@@ -218,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     }
     for (int i = tid; i < kInfo * 128; i += kThreads) (&sh.odd[0][0])[i] = ~0ull;
     if (tid < kInfo) sh.dirty[tid] = 0u;
-    if (w == 8) tc::tmem_alloc(&sh.tmem, 512);
+    if (w == kSoft) tc::tmem_alloc(&sh.tmem, 512);
     // places before every run of `chunk` sequences
     const int chunk = (a.N + kThreads - 1) / kThreads;
     {
@@ -317,8 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
         return min(max(tiles - g.i0, 0), g.count);
     };
 
-    if (w >= 8) {
-        if (w == 9) {
+    if (w >= kSoft) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+        if (w == kSoft + 1) {
             // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
             const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
             uint32_t t = 0;
@@ -373,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                     if (!ok) break;
                     if (lane < 8) {
                         sh.ks[slot][grp] = scale;
-                        sh.off[slot][grp] = page >= 0 ? (((int64_t)page * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D : 0;
+                        sh.at[slot][grp] = page >= 0 ? (uint32_t)(((int64_t)page * a.Hkv + s.h) * (a.c.page / 16) + ((i * 8 + grp) & (a.c.page / 16 - 1))) : 0u;
                     } else if (lane < 16) {
                         sh.pv[slot][grp] = pv;
                         sh.lg[slot][grp] = lg;
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 }
             }
             if (!ok) *dead = 1u;
-        } else if (w == 8) {
+        } else if (w == kSoft) {
             // ---- products: Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ...
             const uint32_t f16 = ~((1u << 7) | (1u << 10));
             const uint32_t id_z = tc::idesc_bf16(128, kKeys) & f16, id_o = (tc::idesc_bf16(128, C::DP) & f16) | (1u << 16);
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 for (int p = 0; p < (kSplit ? 2 : 1); ++p)
 #pragma unroll
                     for (int e = 0; e < kKeys / 16; ++e)
-                        mma_ts(tm + C::O + C::DP * (kSplit ? p : hf), tm + 128 * hf + (kSplit ? 32 * (e >> 1) + 16 * p + 8 * (e & 1) : 8 * e), desc_v(v + e * 2048, D == 128 ? C::BLK : 1024u),
+                        mma_ts(tm + C::O + C::DP * (kSplit ? p : hf), tm + 128 * hf + (kSplit ? 32 * (e >> 1) + 16 * p + 8 * (e & 1) : 64 * (e >> 2) + 8 * (e & 3)), desc_v(v + e * 2048, D == 128 ? C::BLK : 1024u),
                                id_o, (!kSplit && !first) || e > 0);
             };
             // a slot is given back only after it was seen full, also by a half that has no use for it
@@ -462,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             // converted takes the next item's codes, which are on their way until that item's turn
             constexpr int RC = D / 16;  // 16-code pieces of a row
             constexpr int kTurns = (kKeys * RC + kConvert - 1) / kConvert;
-            const int me = tid - 10 * 32;
+            const int me = tid - 32 * (kSoft + 2);
             // 128 channels: sixteen lanes take two rows, eight of them half of each, so that their 16-byte stores, which the
             // layout puts at even places of one row and odd places of the other, fill the banks once
             constexpr int kStep = kConvert / RC;  // rows from a thread's piece to its next: multiples of 8
@@ -480,16 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             uint32_t t = 0, it = 0, turn = 0;  // tile, item (K or V of a tile), segment
             int i = 0;
             bool ok = true, have = next_segment();
-            // (volatile: on its way from here on, not from where it is used)
-            auto load = [&](int e, const uint8_t* base, uint32_t slot) {
-                const int row = row0 + kStep * e;
-                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w)
-                             : "l"(base + sh.off[slot][row >> 4] + (row & 15) * D));
+            // a thread's rows lie at one or two places of their groups of 16 (kStep is 24, 48 or 96)
+            const int64_t in0 = (int64_t)(row0 & 15) * D + ch * 16, in1 = (int64_t)((row0 + kStep) & 15) * D + ch * 16;
+            auto load = [&](int e, const uint8_t* base, uint32_t slot) {  // (volatile: on its way from here on, not from where it is used)
+                const uint8_t* from = base + (e & 1 ? in1 : in0) + (uint64_t)sh.at[slot][(row0 + kStep * e) >> 4] * (16u * D);
+                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w) : "l"(from));
             };
             auto inside = [&](int e) { return (e + 1) * kStep <= kKeys || row0 + kStep * e < kKeys; };
             auto fetch = [&](const Tile& x, bool value) {
-                const uint8_t* base = (value ? a.c.v : a.c.k) + ch * 16;
+                const uint8_t* base = value ? a.c.v : a.c.k;
                 if ((x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys) {
 #pragma unroll
                     for (int e = 0; e < kTurns; ++e)
@@ -584,68 +603,77 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             if (!ok) *dead = 1u;
         }
         __syncwarp();
-    } else if (!kSplit || w < 4) {
-        // ---- softmax: warpgroup hf owns half hf, a thread the row of its tensor-memory lane
-        const int hf = w >> 2, r = tid & 127;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+        // ---- softmax: two warpgroups have half hf, a row (of a tensor-memory lane) two threads: `part` 0 has keys 0-63 of a tile and the
+        // first half of the channels, 1 the others
+        const int hf = w >> 3, part = (w >> 2) & 1, r = tid & 127;
+        const int pair = 1 + 4 * hf + (w & 3);           // their warps' barrier
         const uint32_t lanes = (uint32_t)(w & 3) << 21;  // lane offset 32 (w % 4) in the address' upper half
-        const uint32_t zt = tm + 128 * hf + lanes, ot = tm + C::O + C::DP * hf + lanes, at = tm + C::ACC + lanes;
+        const uint32_t zt = tm + 128 * hf + 64 * part + lanes, ot = tm + C::O + C::DP * hf + D / 2 * part + lanes;
+        const uint32_t at = tm + C::ACC + D / 2 * part + lanes;
         const int rt = r / a.group, rh = r - rt * a.group;
-        uint32_t zc = 0, oc = 0, t = 0, turn = 0;
-        float2* ml = reinterpret_cast<float2*>(a.ws + L.ml);
-        float* po = reinterpret_cast<float*>(a.ws + L.o);
+        uint32_t zc = 0, oc = 0, t = 0, turn = 0, told = 0;
         bool gone = false;
         for (; !gone && next_segment(); ++turn) {
             const int nh = tiles_of_half(s, hf);
             const int tok = s.first + hf * tpt + rt;
             const bool on = rt < tpt && tok < s.last;
-            const TIO* q = static_cast<const TIO*>(a.q) + (s.start + tok) * a.qs + (int64_t)(s.h * a.group + rh) * D;
             float cs = 0.f;
             if (nh > 0) {
-                // the row of q, scaled by a power of two, into the products' layout (the half's last products have ended)
-                // twice, the second time from L1: a row held between would take the scores' registers
-                auto load8 = [&](int c, float (&x)[8]) {
-                    if constexpr (kSplit) {
-                        const float4 y = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        const float4 v = on ? __ldg(reinterpret_cast<const float4*>(q) + 2 * c + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-                        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-                    } else {
-                        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[2 * e] = __uint_as_float(y[e] << 16);
-                            x[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
-                        }
-                    }
-                };
-                constexpr int kBatch = kSplit ? 4 : D >= 64 ? 8 : 4;
+                // the row of q, scaled by a power of two, into the products' layout (the half's last products have ended); each thread
+                // half of the channels
+                const TIO* q = static_cast<const TIO*>(a.q) + (s.start + tok) * a.qs + (int64_t)(s.h * a.group + rh) * D + D / 2 * part;
+                constexpr int kWords = D / 2 * (int)sizeof(TIO) / 16, kBatch = kWords < 8 ? kWords : 8;
                 float mx = 0.f;
 #pragma unroll 1
-                for (int c4 = 0; c4 < D / 8; c4 += kBatch) {
-                    float x[kBatch][8];
+                for (int c = 0; c < kWords; c += kBatch) {
+                    uint4 u[kBatch];
 #pragma unroll
-                    for (int c = 0; c < kBatch; ++c) load8(c4 + c, x[c]);
+                    for (int i = 0; i < kBatch; ++i) u[i] = on ? __ldg(reinterpret_cast<const uint4*>(q) + c + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int c = 0; c < kBatch; ++c)
+                    for (int i = 0; i < kBatch; ++i) {
+                        const uint32_t y[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[c][e]));
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (kSplit) mx = fmaxf(mx, fabsf(f_of(y[e])));
+                            else mx = max3(mx, fabsf(f_of(y[e] << 16)), fabsf(f_of(y[e] & 0xffff0000u)));
+                        }
+                    }
                 }
+                told ^= 1u;
+                sh.top[told][hf][part][r] = mx;
+                (void)pair_any(pair, false);
+                mx = fmaxf(mx, sh.top[told][hf][part ^ 1][r]);
                 const int e = min(max((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127, -100), 127);
                 const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
                 cs = __uint_as_float((uint32_t)(127 + e - 14) << 23) * a.scale * kLog2e;
 #pragma unroll 2
-                for (int c = 0; c < C::DP / 8; ++c) {
+                for (int i = 0; i < C::DP / 16; ++i) {  // (again, from L1)
+                    // 8 channels; those past D are zeros
+                    const int c = i < D / 16 ? D / 16 * part + i : D / 8 + (C::DP - D) / 16 * part + i - D / 16;
                     uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-                    if (c < D / 8) {
+                    if (on && i < D / 16) {
                         float x[8];
-                        load8(c, x);
+                        if constexpr (kSplit) {
+                            const float4 y = __ldg(reinterpret_cast<const float4*>(q) + 2 * i), v = __ldg(reinterpret_cast<const float4*>(q) + 2 * i + 1);
+                            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w; x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                        } else {
+                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
+                            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
-                            hi[i] = pack_f16(x0, x1);
+                            for (int b = 0; b < 4; ++b) {
+                                x[2 * b] = f_of(y[b] << 16);
+                                x[2 * b + 1] = f_of(y[b] & 0xffff0000u);
+                            }
+                        }
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float x0 = x[2 * b] * up, x1 = x[2 * b + 1] * up;
+                            hi[b] = pack_f16(x0, x1);
                             if constexpr (kSplit) {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-                                lo[i] = pack_f16(x0 - f.x, x1 - f.y);
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[b]));
+                                lo[b] = pack_f16(x0 - f.x, x1 - f.y);
                             }
                         }
                     }
@@ -660,85 +688,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
             }
             const int seen = on ? s.ctx + tok + 1 : INT32_MAX;  // keys that the row sees
             const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
-            float m = -FLT_MAX, vu = 0.f;  // finite: a score of -inf then weighs nothing
-            float l = 0.f;
-            for (int j = 0; j < s.count; ++j, ++t) {
+            float m = kUnset, vu = 0.f, l = 0.f;  // m: finite, so that a score of -inf weighs nothing
+            const int count = s.count, i0 = s.i0;
+            bool late = false, left = false;  // a wait gave up, here or with the row's other thread: they leave together
+            for (int j = 0; j < count; ++j, ++t) {
                 const int slot = t % kInfo;
                 if (j < nh) {
-                    gone = !warp_wait(&sh.z_full[hf], zc++ & 1u);
-                    if (gone) break;
+                    late = !warp_wait(&sh.z_full[hf], zc++ & 1u);
                     tc::fence_after_sync();
-                    const uint32_t there = sh.there[slot];
-                    const float2 unit = sh.unit[slot];
-                    const float ratio = unit.y;
-                    vu = unit.x;
-                    const int key0 = (s.i0 + j) * kKeys, mine = seen - key0;
-                    const bool edge = key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu;
-                    const bool odd = (there & kOdd) != 0u;
-                    // a key of the tile (general form): is it seen by this row, and its score in base 2
-                    auto shown = [&](int i) { return i < mine && ((there >> (i >> 4)) & 1u) != 0u; };
-                    auto k_of = [&](int c) {
-                        const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][2 * c]);
-                        return f2(x.x * cs, x.y * cs);
-                    };
-                    // f(chunk, its number) over the four chunks of 32 keys, the next one's load in flight.  (Loops, and one copy of what is
-                    // out of the ordinary: the roles' code shares a small instruction cache.)
-                    uint32_t z[2][32];
-                    auto chunks = [&](auto f) {
-                        tmem_ld32(zt, z[0]);
-#pragma unroll 1
-                        for (int c = 0; c < 4; c += 2) {
-                            tc::tmem_wait_ld();
-                            tmem_ld32(zt + 32 * c + 32, z[1]);
-                            f(z[0], c);
-                            tc::tmem_wait_ld();
-                            if (c == 0) tmem_ld32(zt + 64, z[0]);
-                            f(z[1], c + 1);
-                        }
-                    };
-                    auto chunks_one_by_one = [&](auto f) {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld32(zt + 32 * c, z[0]);
-                            tc::tmem_wait_ld();
-                            f(z[0], c);
-                        }
-                    };
-                    float top = -INFINITY;
-                    if (!odd && !edge) {
-                        chunks([&](const uint32_t (&x)[32], int c) {
-                            const float2 kg = k_of(c);
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                float m0 = fmaxf(f_of(x[16 * g]), f_of(x[16 * g + 1])), m1 = fmaxf(f_of(x[16 * g + 2]), f_of(x[16 * g + 3]));
-#pragma unroll
-                                for (int i = 4; i < 16; i += 4) {
-                                    m0 = max3(m0, f_of(x[16 * g + i]), f_of(x[16 * g + i + 1]));
-                                    m1 = max3(m1, f_of(x[16 * g + i + 2]), f_of(x[16 * g + i + 3]));
-                                }
-                                top = fmaxf(top, fmaxf(m0, m1) * (g ? kg.y : kg.x));
-                            }
-                        });
-                    } else {
-                        chunks_one_by_one([&](const uint32_t (&x)[32], int c) {
-                            const float2 kg = k_of(c);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float y = __fmul_rn(f_of(x[i]), i < 16 ? kg.x : kg.y);
-                                if (shown(32 * c + i)) top = fmaxf(top, y);
-                            }
-                        });
-                    }
-                    const float ref = top - m > 15.f ? top - 7.f : m;
-                    const float alpha = ex2(m - ref);
-                    m = ref;
-                    l *= alpha;
-                    // (the products into O up to here ended with the scores that were waited for)
                     if constexpr (kSplit) {
+                        // the last tile's outputs, both parts, to the sum of those before it (their products ended with the scores)
                         if (j > 0) {
-                            const float f = alpha * ratio;
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
+                            for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o0[16], o1[16], ac[16];
                                 tmem_ld16(ot + 16 * c, o0);
                                 tmem_ld16(ot + C::DP + 16 * c, o1);
@@ -747,28 +709,21 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
                                     const float x = fmaf(f_of(o1[i]), 1.f / kRestUp, f_of(o0[i]));
-                                    ac[i] = __float_as_uint((j > 1 ? f_of(ac[i]) + x : x) * f);
+                                    ac[i] = __float_as_uint(j > 1 ? f_of(ac[i]) + x : x);
                                 }
                                 tmem_st16(at + 16 * c, ac);
                             }
                             tc::tmem_wait_st();
                         }
-                    } else if (j > 0 && __any_sync(0xffffffffu, alpha * ratio != 1.f)) {
-                        const float f = alpha * ratio;
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(ot + 16 * c, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f_of(o[i]) * f);
-                            tmem_st16(ot + 16 * c, o);
-                        }
                     }
-                    // Weights times their value's scale: the scale goes into the exponent and comes off the sums, group by group.
-                    // Not where a scale is none, and not beyond 2^20, where a score is rounded, as the reference was,
-                    // before the reference comes off, so that none passes the largest however large they are.
-                    const bool slow = odd || __any_sync(0xffffffffu, fabsf(m) > 1048576.f);
+                    const uint32_t there = sh.there[slot];
+                    const float2 unit = sh.unit[slot];
+                    vu = unit.x;
+                    const int key0 = (i0 + j) * kKeys;
+                    auto k_of = [&](int c) {  // at least FLT_MIN where all scales are positive numbers: -inf times it stays that
+                        const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][4 * part + 2 * c]);
+                        return (there & kOdd) != 0u ? f2(x.x * cs, x.y * cs) : f2(fmaxf(x.x * cs, FLT_MIN), fmaxf(x.y * cs, FLT_MIN));
+                    };
                     auto store = [&](const uint32_t (&p)[16], const uint32_t (&p1)[kSplit ? 16 : 1], int c) {
                         tmem_st16(zt + (kSplit ? 32 : 16) * c, p);
                         if constexpr (kSplit) tmem_st16(zt + 32 * c + 16, p1);
@@ -780,81 +735,196 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                             lo = pack_f16((y.x - f.x) * kRestUp, (y.y - f.y) * kRestUp);
                         }
                     };
-                    if (!slow && !edge) {
-                        chunks([&](const uint32_t (&x)[32], int c) {
-                            uint32_t p[16], p1[kSplit ? 16 : 1];
-                            const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][2 * c]), ips = *reinterpret_cast<const float2*>(&sh.ip[slot][2 * c]);
+                    // A weight has its value's scale in the exponent (2^(score + log2 pv - m), it comes off the sums group by group).
+                    // In an ordinary tile none passes 2^15, which is found out on the way; P, which goes over Z, waits for that.  (What
+                    // decides is the same for both threads of a row.)
+                    bool ordinary = j > 0 && there == 0xffu && key0 <= warp_seen - kKeys && unit.y == 1.f && !__any_sync(0xffffffffu, fabsf(m) > kFar);
+                    if (ordinary) {
+                        uint32_t z[32], p[2][16], p1[2][kSplit ? 16 : 1];
+                        float over = -INFINITY, sums = 0.f;
+                        tmem_ld32(zt, z);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const float off = (g ? lg.y : lg.x) - m, ip = g ? ips.y : ips.x;
-                                const float2 k2 = g ? f2(kg.y, kg.y) : f2(kg.x, kg.x), o2 = f2(off, off);
-                                float2 sum = f2(0.f, 0.f);
+                        for (int c = 0; c < 2; ++c) {
+                            const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][4 * part + 2 * c]);
+                            const float2 ip = *reinterpret_cast<const float2*>(&sh.ip[slot][4 * part + 2 * c]);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int e = 16 * g + 2 * i;
-                                    float2 y = __ffma2_rn(f2(f_of(x[e]), f_of(x[e + 1])), k2, o2);
-                                    y = f2(ex2(y.x), ex2(y.y));
-                                    sum = __fadd2_rn(sum, y);
-                                    pack(y, p[8 * g + i], p1[kSplit ? 8 * g + i : 0]);
-                                }
-                                l = fmaf(sum.x + sum.y, ip, l);
+                            for (int i = 0; i < 16; ++i) {
+                                const float k = i < 8 ? kg.x : kg.y, off = (i < 8 ? lg.x : lg.y) - m;
+                                const float2 x = __ffma2_rn(f2(f_of(z[2 * i]), f_of(z[2 * i + 1])), f2(k, k), f2(off, off));
+                                z[2 * i] = __float_as_uint(x.x);
+                                z[2 * i + 1] = __float_as_uint(x.y);
+                                over = max3(over, x.x, x.y);
                             }
-                            store(p, p1, c);
-                        });
-                    } else {
-                        chunks_one_by_one([&](const uint32_t (&x)[32], int c) {
-                            uint32_t p[16], p1[kSplit ? 16 : 1];
-                            const float2 kg = k_of(c);
+                            float2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                const float pv = sh.pv[slot][2 * c + g], k = g ? kg.y : kg.x;
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 y = f2(ex2(f_of(z[2 * i])), ex2(f_of(z[2 * i + 1])));
+                                sum[i >> 3] = __fadd2_rn(sum[i >> 3], y);
+                                pack(y, p[c][i], p1[c][kSplit ? i : 0]);
+                            }
+                            if (c == 0) tmem_ld32(zt + 32, z);
+                            sums = fmaf(sum[0].x + sum[0].y, ip.x, sums);
+                            sums = fmaf(sum[1].x + sum[1].y, ip.y, sums);
+                            if (c == 0) tc::tmem_wait_ld();
+                        }
+                        ordinary = !pair_any(pair, over > 15.f || late);
+                        if (ordinary) {
+                            l += sums;
+                            store(p[0], p1[0], 0);
+                            store(p[1], p1[1], 1);
+                        }
+                    }
+                    if (!ordinary) {
+                        // Any tile: hidden scores leave Z, the largest weight, where it passes 2^15 the reference moves to 2^7 below it, the
+                        // weights.  A row beyond 2^20, where a score's rounding would show (and all rows where a scale is no positive
+                        // number) has its scores rounded, as the reference is, before it comes off, so that none passes the largest
+                        // however large they are, and the value's scale is multiplied with.
+                        if (key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu) {
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t z[32];
+                                const int n = seen - key0 - 64 * part - 32 * c;
+                                const uint32_t first = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u, g = there >> (4 * part + 2 * c);
+                                const uint32_t see = first & ((g & 1u ? 0xffffu : 0u) | (g & 2u ? 0xffff0000u : 0u));
+                                tmem_ld32(zt + 32 * c, z);
+                                tc::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int e = 16 * g + 2 * i, key = 32 * c + e;
-                                    // (rounded apart: the packed forms fuse)
-                                    float2 y = f2(__fsub_rn(__fmul_rn(f_of(x[e]), k), m), __fsub_rn(__fmul_rn(f_of(x[e + 1]), k), m));
-                                    y = f2(shown(key) ? ex2(y.x) : 0.f, shown(key + 1) ? ex2(y.y) : 0.f);
-                                    l += y.x + y.y;
-                                    // (a hidden key's scale may be no number)
-                                    pack(f2(y.x == 0.f ? 0.f : y.x * pv, y.y == 0.f ? 0.f : y.y * pv), p[8 * g + i], p1[kSplit ? 8 * g + i : 0]);
+                                for (int i = 0; i < 32; ++i)
+                                    if ((see & (1u << i)) == 0u) z[i] = kHidden;
+                                tmem_st32(zt + 32 * c, z);
+                            }
+                            tc::tmem_wait_st();
+                        }
+                        bool own = (there & kOdd) != 0u, some = own;
+                        float now = m;
+                        for (int round = some ? 1 : 0;; ++round) {
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t z[32];
+                                tmem_ld32(zt + 32 * c, z);
+                                const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][4 * part + 2 * c]);
+                                tc::tmem_wait_ld();
+                                if (round == 0) {
+#pragma unroll
+                                    for (int g = 0; g < 2; ++g) {
+                                        const uint32_t* x = z + 16 * g;
+                                        float m0 = fmaxf(f_of(x[0]), f_of(x[1])), m1 = fmaxf(f_of(x[2]), f_of(x[3]));
+#pragma unroll
+                                        for (int i = 4; i < 16; i += 4) {
+                                            m0 = max3(m0, f_of(x[i]), f_of(x[i + 1]));
+                                            m1 = max3(m1, f_of(x[i + 2]), f_of(x[i + 3]));
+                                        }
+                                        top = fmaxf(top, fmaf(fmaxf(m0, m1), g ? kg.y : kg.x, g ? lg.y : lg.x));
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) {
+                                        const float y = __fmul_rn(f_of(z[i]), i < 16 ? kg.x : kg.y);
+                                        if (z[i] != kHidden) top = fmaxf(top, y);
+                                    }
                                 }
                             }
+                            told ^= 1u;
+                            sh.top[told][hf][part][r] = top;
+                            left = pair_any(pair, late);
+                            if (left) break;
+                            top = fmaxf(top, sh.top[told][hf][part ^ 1][r]);
+                            if (round == 0 || own) now = (m == kUnset && top > -INFINITY) || top - m > 15.f ? top - 7.f : m;
+                            if (round == 1) break;
+                            own = (fabsf(m) > kFar && m != kUnset) || (fabsf(now) > kFar && now != kUnset);
+                            some = __any_sync(0xffffffffu, own);
+                            if (!some) break;
+                        }
+                        if (left) break;
+                        const float alpha = now == m ? 1.f : ex2(m - now), f = alpha * unit.y;  // O's unit may have changed, too
+                        m = now;
+                        l *= alpha;
+                        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                const uint32_t to = (kSplit ? at : ot) + 16 * c;
+                                uint32_t o[16];
+                                tmem_ld16(to, o);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f_of(o[i]) * f);
+                                tmem_st16(to, o);
+                            }
+                        }
+                        const float ref = m == kUnset ? 0.f : m;
+                        float sums = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t z[32], p[16], p1[kSplit ? 16 : 1];
+                            tmem_ld32(zt + 32 * c, z);
+                            const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][4 * part + 2 * c]);
+                            const float2 ip = *reinterpret_cast<const float2*>(&sh.ip[slot][4 * part + 2 * c]);
+                            tc::tmem_wait_ld();
+                            if (some) {
+                                // this row's own scores less the reference; the others' scores as they are
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const float y = __fsub_rn(__fmul_rn(f_of(z[i]), i < 16 ? kg.x : kg.y), ref);
+                                    if (own) z[i] = z[i] == kHidden ? kHidden : __float_as_uint(y);
+                                }
+                            }
+                            float2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                            const float2 pv = *reinterpret_cast<const float2*>(&sh.pv[slot][4 * part + 2 * c]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float k = own ? 1.f : i < 8 ? kg.x : kg.y, off = own ? 0.f : (i < 8 ? lg.x : lg.y) - ref;
+                                float2 y = __ffma2_rn(f2(f_of(z[2 * i]), f_of(z[2 * i + 1])), f2(k, k), f2(off, off));
+                                y = f2(ex2(y.x), ex2(y.y));
+                                sum[i >> 3] = __fadd2_rn(sum[i >> 3], y);
+                                if (some && own) {  // (a hidden key's scale may be no number)
+                                    const float v = i < 8 ? pv.x : pv.y;
+                                    y = f2(y.x == 0.f ? 0.f : y.x * v, y.y == 0.f ? 0.f : y.y * v);
+                                }
+                                pack(y, p[i], p1[kSplit ? i : 0]);
+                            }
+                            sums = fmaf(sum[0].x + sum[0].y, own ? 1.f : ip.x, sums);
+                            sums = fmaf(sum[1].x + sum[1].y, own ? 1.f : ip.y, sums);
                             store(p, p1, c);
-                        });
+                        }
+                        l += sums;
                     }
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sh.p_full[hf]);
-                }
-                if (j >= nh) {  // (not before the tile is known: the barrier still counts the slot's last one)
-                    gone = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u);
-                    if (gone) break;
+                } else {
+                    // (not before the tile is known: the barrier still counts the slot's last one)
+                    late = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u) || late;
                 }
                 // the last tile's when the segment is over: conversion then is less than kInfo segments ahead (see odd_note)
                 __syncwarp();
-                if (lane == 0 && j + 1 < s.count) tc::mbar_arrive(&sh.info_free[slot]);
+                if (lane == 0 && j + 1 < count) tc::mbar_arrive(&sh.info_free[slot]);
             }
+            if (!left) {
+                if (nh > 0 && !late) late = !warp_wait(&sh.o_full[hf], oc++ & 1u);
+                sh.sum[turn & 1][hf][part][r] = l;
+                left = pair_any(pair, late || *dead != 0u);
+            }
+            gone = left;
             if (gone) break;
-            if (nh > 0) {
-                gone = !warp_wait(&sh.o_full[hf], oc++ & 1u);
-                gone = __any_sync(0xffffffffu, gone || *dead != 0u);
-                if (gone) break;
-                tc::fence_after_sync();
-            }
+            tc::fence_after_sync();
+            l += sh.sum[turn & 1][hf][part ^ 1][r];
             const bool whole = s.begun() && s.ended();
             const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
             const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
-            TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D;
-            if (on && !whole) ml[place] = make_float2(m, l);
+            TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D + D / 2 * part;
+            float* po = reinterpret_cast<float*>(a.ws + L.o) + place * D + D / 2 * part;
+            if (on && !whole && part == 0) reinterpret_cast<float2*>(a.ws + L.ml)[place] = make_float2(m, l);
             const bool dirty = kE4m3 && *(volatile uint32_t*)&sh.dirty[turn % kInfo] == turn + 1u;
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[16];
                 if (nh > 0) {
+                    tmem_ld16(ot + 16 * c, o);
                     if constexpr (kSplit) {
                         uint32_t o1[16], ac[16];
-                        tmem_ld16(ot + 16 * c, o);
                         tmem_ld16(ot + C::DP + 16 * c, o1);
                         if (nh > 1) tmem_ld16(at + 16 * c, ac);
                         tc::tmem_wait_ld();
@@ -864,7 +934,6 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                             o[i] = __float_as_uint(nh > 1 ? f_of(ac[i]) + x : x);
                         }
                     } else {
-                        tmem_ld16(ot + 16 * c, o);
                         tc::tmem_wait_ld();
                     }
                 } else {
@@ -878,13 +947,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
                 if (dirty) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const unsigned long long od = sh.odd[turn % kInfo][16 * c + i];
+                        const unsigned long long od = sh.odd[turn % kInfo][D / 2 * part + 16 * c + i];
                         if ((uint32_t)(od >> 32) == 0xfffffffeu - turn && (int)(uint32_t)od < seen) y[i] = NAN;
                     }
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(po + place * D + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(po + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
                 } else if constexpr (kSplit) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(out + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
@@ -904,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_extend_kernel(const Attn
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (w == 8) tc::tmem_dealloc(tm, 512);
+    if (w == kSoft) tc::tmem_dealloc(tm, 512);
     if (tid == 0) {
         // what this CTA leaves to be joined: the unit that it began and did not end
         Record rec{-1, 0, 0, 0, 0};
@@ -1021,7 +1090,7 @@ cudaError_t launch_extend(const AttnExtendArgs& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int ctas = sm_count_of_current_device();
     const int rows = piece_rows(a.T, a.group, kSplit ? KDA_F32 : KDA_BF16);
-    kern<<<ctas, kThreads, C::SMEM, s>>>(a, rows);
+    kern<<<ctas, C::THREADS, C::SMEM, s>>>(a, rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // about ctas / units pieces a unit: four or more a warp
