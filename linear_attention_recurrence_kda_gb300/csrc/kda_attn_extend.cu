@@ -689,6 +689,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             const int seen = on ? s.ctx + tok + 1 : INT32_MAX;  // keys that the row sees
             const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
             float m = kUnset, vu = 0.f, l = 0.f;  // m: finite, so that a score of -inf weighs nothing
+            float peak = -INFINITY;               // the largest weight's exponent among ordinary tiles since m was set (this thread's)
             const int count = s.count, i0 = s.i0;
             bool late = false, left = false;  // a wait gave up, here or with the row's other thread: they leave together
             for (int j = 0; j < count; ++j, ++t) {
@@ -771,13 +772,15 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         ordinary = !pair_any(pair, over > 15.f || late);
                         if (ordinary) {
                             l += sums;
+                            peak = fmaxf(peak, over);
                             store(p[0], p1[0], 0);
                             store(p[1], p1[1], 1);
                         }
                     }
                     if (!ordinary) {
-                        // Any tile: hidden scores leave Z, the largest weight, where it passes 2^15 the reference moves to 2^7 below it, the
-                        // weights.  A row beyond 2^20, where a score's rounding would show (and all rows where a scale is no positive
+                        // Any tile: hidden scores leave Z, the largest weight, the weights.  References move to 2^7 below the largest weight here, not
+                        // only where it has passed 2^15 but wherever it has grown by more than 2^2: what one row makes necessary then
+                        // serves its warp's others, whose turn would come one by one.  A row beyond 2^20, where a score's rounding would show (and all rows where a scale is no positive
                         // number) has its scores rounded, as the reference is, before it comes off, so that none passes the largest
                         // however large they are, and the value's scale is multiplied with.
                         if (key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu) {
@@ -827,11 +830,11 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                                 }
                             }
                             told ^= 1u;
-                            sh.top[told][hf][part][r] = top;
+                            sh.top[told][hf][part][r] = round == 0 ? fmaxf(top, m + peak) : top;
                             left = pair_any(pair, late);
                             if (left) break;
-                            top = fmaxf(top, sh.top[told][hf][part ^ 1][r]);
-                            if (round == 0 || own) now = (m == kUnset && top > -INFINITY) || top - m > 15.f ? top - 7.f : m;
+                            top = fmaxf(sh.top[told][hf][0][r], sh.top[told][hf][1][r]);
+                            if (round == 0 || own) now = (m == kUnset && top > -INFINITY) || top - m > (own ? 15.f : 9.f) ? top - 7.f : m;
                             if (round == 1) break;
                             own = (fabsf(m) > kFar && m != kUnset) || (fabsf(now) > kFar && now != kUnset);
                             some = __any_sync(0xffffffffu, own);
@@ -839,6 +842,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         }
                         if (left) break;
                         const float alpha = now == m ? 1.f : ex2(m - now), f = alpha * unit.y;  // O's unit may have changed, too
+                        peak -= now - m;
                         m = now;
                         l *= alpha;
                         if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
