@@ -228,7 +228,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
         }
         for (int i = 0; i < kInfo; ++i) {
             tc::mbar_init(&sh.info_full[i], 1);
-            tc::mbar_init(&sh.info_free[i], kSoft);
+            tc::mbar_init(&sh.info_free[i], kSoft + kConvert / 32);
         }
         tc::mbar_init(&sh.drained, 1);
         sh.dead = 0u;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                 for (int j = -1; j < count && ok; ++j) {
                     const uint32_t iv = it + 2 * j + 1;
                     const bool more = j + 1 < count;
-                    ok = !__any_sync(0xffffffffu, *dead != 0u) && (!more || full(iv + 1)) && (j < 0 || full(iv));
+                    ok = full(more ? iv + 1 : iv);
 #pragma unroll 1
                     for (int hf = 0; hf < C::HALVES; ++hf) {
                         const int nh = hf ? n1 : n0;
@@ -597,8 +597,12 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                 ok = ok && put(now, value);
                 if (!ok) break;
                 if (value) now = ahead;
-                if (!value || any) fetch(now, !value);  // (a tile's pages are read before its first half is reported)
                 done();
+                if (!value || any) fetch(now, !value);
+                if (!value) {  // the tile's pages are read
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sh.info_free[now.slot]);
+                }
             }
             if (!ok) *dead = 1u;
         }
@@ -744,11 +748,12 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         uint32_t z[32], p[2][16], p1[2][kSplit ? 16 : 1];
                         float over = -INFINITY, sums = 0.f;
                         tmem_ld32(zt, z);
+                        const float2 kgs[2] = {k_of(0), k_of(1)};
+                        const float4 lgs = *reinterpret_cast<const float4*>(&sh.lg[slot][4 * part]), ips = *reinterpret_cast<const float4*>(&sh.ip[slot][4 * part]);
                         tc::tmem_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float2 kg = k_of(c), lg = *reinterpret_cast<const float2*>(&sh.lg[slot][4 * part + 2 * c]);
-                            const float2 ip = *reinterpret_cast<const float2*>(&sh.ip[slot][4 * part + 2 * c]);
+                            const float2 kg = kgs[c], lg = c ? f2(lgs.z, lgs.w) : f2(lgs.x, lgs.y), ip = c ? f2(ips.z, ips.w) : f2(ips.x, ips.y);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const float k = i < 8 ? kg.x : kg.y, off = (i < 8 ? lg.x : lg.y) - m;
