@@ -27,7 +27,6 @@
 // Hidden keys: scores are replaced by -inf.  A NaN code in a value would spread over 0 x NaN, so a tile that some row does not see
 // whole is cleaned of them (noted by channel and key), and the rows that see them get them at the end.
 #include <cfloat>
-#include <type_traits>
 
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
@@ -56,8 +55,10 @@ template <int D, bool kSplit> struct Cfg {
     static constexpr int NB = DP / 64;                // 64-channel blocks of a row
     static constexpr uint32_t BLK = 128 * 128;        // bytes of a block: 128 rows of 128 bytes
     static constexpr uint32_t TILE = NB * BLK;
-    static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + 1024;
+    static constexpr int STAGES = D == 128 ? 3 : 6;   // K and V tiles in f16, in turn
+    static constexpr int RAWS = D == 128 ? 2 : 4;     // and as codes, on their way or waiting
+    static constexpr uint32_t RAW = 128 * D;
+    static constexpr uint32_t SMEM = 2 * TILE + STAGES * TILE + RAWS * RAW + 1024;
     static constexpr int HALVES = kSplit ? 1 : 2;
     static constexpr int WARPS = 8 * HALVES;              // of the softmax: a row has two threads, one for each half of a tile's keys
     static constexpr int THREADS = 32 * (WARPS + 8);      // products, pages, six of conversion
@@ -155,10 +156,9 @@ struct Walk {
 };
 
 struct Shared {
-    uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], drained;
+    uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], raw_full[4], raw_free[4], drained;
     uint32_t tmem, dead, flag;
     uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; kOdd: see there
-    uint32_t at[kInfo][kGroups];                            // where it is in the cache, in groups of 16 rows (2^32 of them are terabytes)
     // a tile's scales of K; V's in the unit of O (pv), their logarithm and their reciprocal; the unit, and the last one over it
     alignas(16) float ks[kInfo][kGroups], pv[kInfo][kGroups], lg[kInfo][kGroups], ip[kInfo][kGroups];
     float2 unit[kInfo];
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
     __shared__ Shared sh;
     unsigned char* sq = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* ring = sq + 2 * C::TILE;
+    unsigned char* raw = ring + S * C::TILE;
     int64_t* prefix = reinterpret_cast<int64_t*>(sq);  // until the work begins
     const int tid = threadIdx.x, lane = tid & 31;
     const int w = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
@@ -225,6 +226,10 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
         for (int i = 0; i < S; ++i) {
             tc::mbar_init(&sh.kv_full[i], kConvert / 32);
             tc::mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int i = 0; i < C::RAWS; ++i) {
+            tc::mbar_init(&sh.raw_full[i], 1);
+            tc::mbar_init(&sh.raw_free[i], kConvert / 32);
         }
         for (int i = 0; i < kInfo; ++i) {
             tc::mbar_init(&sh.info_full[i], 1);
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
         if (w == kSoft + 1) {
             // ---- pages and scales of a tile's groups of 16 keys (lanes 0-7 K's scales, 8-15 V's)
             const int page_shift = 31 - __clz(a.c.page), grp = lane & 7;
-            uint32_t t = 0;
+            uint32_t t = 0, it = 0;
             bool ok = true;
             while (ok && next_segment()) {
                 const int keys = s.ctx + s.last;
@@ -351,49 +356,40 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     const int p = __ldg(a.c.table + (int64_t)s.n * a.c.max_pages + (key >> page_shift));
                     return p >= 0 && p < a.c.num_pages ? p : -2;
                 };
-                // a page's piece of the tile on its way to L2, for k and v: the lane of its first group
-                const int box = min(kKeys, a.c.page), gpp = box / 16;
-                auto to_l2 = [&](int p, int i) {
-                    if (p < 0 || lane >= 16 || grp % gpp != 0) return;
-                    const uint8_t* at = (lane < 8 ? a.c.k : a.c.v) + (((int64_t)p * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D;
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(box * D) : "memory");
-                };
+                const int box = min(kKeys, a.c.page), gpp = box / 16;  // a page's part of a tile, and its groups
                 auto scale_of = [&](int p) {
                     return p >= 0 && lane < 16 ? __ldg((lane < 8 ? a.c.k_scale : a.c.v_scale) + (int64_t)p * a.Hkv + s.h) : 0.f;
                 };
                 // a tile's pages are asked for two tiles ahead, its scales one
                 int page = page_of(s.i0), page1 = page_of(s.i0 + 1);
-                float vu = 0.f, vtop = 0.f;
+                float vu = 0.f, vtop = 0.f, inv = 0.f;
                 float scale = scale_of(page);
-                to_l2(page, s.i0);
                 for (int i = s.i0; i < s.i0 + s.count && ok; ++i, ++t) {
                     const int page2 = page_of(i + 2);
                     const float scale1 = scale_of(page1);
-                    to_l2(page1, i + 1);
                     uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
                     if (__any_sync(0xffffffffu, page >= 0 && lane < 16 && !(scale > 0.f && scale < INFINITY))) there |= kOdd;
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
                     // The unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the
                     // largest met (what is in O would grow past fp32).  Lanes 8-15 have the scales.
-                    float big = page >= 0 && fabsf(scale) < INFINITY ? fabsf(scale) : 0.f;
-#pragma unroll
-                    for (int off = 4; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                    big = __shfl_sync(0xffffffffu, big, 8);
+                    const uint32_t mag = page >= 0 && lane >= 8 && lane < 16 && fabsf(scale) < INFINITY ? __float_as_uint(fabsf(scale)) : 0u;
+                    const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, mag));  // (magnitudes compare as integers)
                     float ratio = 1.f;
                     if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
                         vtop = fmaxf(vtop, big);
                         const float nu = fmaxf(big, vtop * 0x1p-40f);
                         ratio = vu == 0.f ? 0.f : vu / nu;
                         vu = nu;
+                        inv = 1.f / vu;
                     }
-                    const float pv = page < 0 ? 1.f : vu == 0.f ? (scale == scale ? 0.f : scale) : scale / vu;
-                    const float lg = log2f(pv), ip = 1.f / pv;
+                    // (a scale's logarithm and reciprocal are those of a power of two, or off by some 2^-22)
+                    const float pv = page < 0 ? 1.f : vu == 0.f ? (scale == scale ? 0.f : scale) : scale * inv;
+                    const float lg = __log2f(pv), ip = __frcp_rn(pv);
                     const uint32_t slot = t % kInfo;
                     ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
                     if (lane < 8) {
                         sh.ks[slot][grp] = scale;
-                        sh.at[slot][grp] = page >= 0 ? (uint32_t)(((int64_t)page * a.Hkv + s.h) * (a.c.page / 16) + ((i * 8 + grp) & (a.c.page / 16 - 1))) : 0u;
                     } else if (lane < 16) {
                         sh.pv[slot][grp] = pv;
                         sh.lg[slot][grp] = lg;
@@ -404,12 +400,29 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&sh.info_full[slot]);
+                    // the codes: a page of a head is contiguous, the lane of its first group copies it
+                    const int pieces = (__popc(there & 0xffu) + gpp - 1) / gpp;
+#pragma unroll 1
+                    for (int x = 0; x < 2 && ok; ++x, ++it) {
+                        const uint32_t st = it % C::RAWS;
+                        ok = warp_wait(&sh.raw_free[st], ((it / C::RAWS) & 1u) ^ 1u);
+                        if (!ok) break;
+                        if (lane == 0) tc::mbar_arrive_expect_tx(&sh.raw_full[st], (uint32_t)pieces * box * D);
+                        __syncwarp();
+                        if (lane < 8 && page >= 0 && grp % gpp == 0) {
+                            const uint8_t* src = (x ? a.c.v : a.c.k) + (((int64_t)page * a.Hkv + s.h) * a.c.page + ((i * kKeys + grp * 16) & (a.c.page - 1))) * D;
+                            tc::bulk_load(raw + st * C::RAW + grp * 16 * D, src, (uint32_t)box * D, &sh.raw_full[st]);
+                        }
+                    }
                     page = page1;
                     page1 = page2;
                     scale = scale1;
                 }
             }
             if (!ok) *dead = 1u;
+            // what was issued lands before the CTA ends, also where another role's wait gave up
+            if (lane == 0)
+                for (uint32_t i = it > (uint32_t)C::RAWS ? it - C::RAWS : 0; i < it; ++i) (void)tc::mbar_wait(&sh.raw_full[i % C::RAWS], (i / C::RAWS) & 1u, kTries);
         } else if (w == kSoft) {
             // ---- products: Z0(0) Z1(0) | O0(0) Z0(1) O1(0) Z1(1) | ...
             const uint32_t f16 = ~((1u << 7) | (1u << 10));
@@ -451,25 +464,29 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             while (ok && next_segment()) {
                 const int n0 = tiles_of_half(s, 0), n1 = C::HALVES == 2 ? tiles_of_half(s, 1) : 0, count = s.count;
                 // iteration j: the halves' O of tile j, each followed by its Z of tile j + 1 (one copy of either: the roles' code
-                // shares a small instruction cache)
+                // shares a small instruction cache).  V is given back before the last Z, so that the next K has its place early.
 #pragma unroll 1
                 for (int j = -1; j < count && ok; ++j) {
                     const uint32_t iv = it + 2 * j + 1;
                     const bool more = j + 1 < count;
-                    ok = full(more ? iv + 1 : iv);
+                    if (j >= 0) ok = full(iv);
 #pragma unroll 1
-                    for (int hf = 0; hf < C::HALVES; ++hf) {
+                    for (int hf = 0; hf < C::HALVES && ok; ++hf) {
                         const int nh = hf ? n1 : n0;
-                        if (!ok || j >= nh || nh == 0) continue;
-                        ok = j < 0 ? flip(&sh.q_full[hf], hf) : flip(&sh.p_full[hf], 2 + hf);
-                        if (!ok) continue;
-                        tc::fence_after_sync();
-                        if (j >= 0) issue_o(hf, iv, j == 0);
+                        const bool on = j < nh && nh > 0;
+                        if (on) {
+                            ok = j < 0 ? flip(&sh.q_full[hf], hf) : flip(&sh.p_full[hf], 2 + hf);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            if (j >= 0) issue_o(hf, iv, j == 0);
+                        }
+                        if (j >= 0 && hf == C::HALVES - 1) release(iv);
+                        if (more && hf == 0) ok = full(iv + 1);
+                        if (!ok || !on) continue;
                         if (j + 1 < nh) issue_z(hf, iv + 1);  // its commit also covers O's product
                         else commit(&sh.o_full[hf]);
                     }
                     if (!ok) break;
-                    if (j >= 0) release(iv);
                     if (more) release(iv + 1);
                 }
                 it += 2 * count;
@@ -478,8 +495,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             commit(&sh.drained);  // products in flight end before tensor memory is given back
             (void)warp_wait(&sh.drained, 0);
         } else {
-            // ---- conversion: 16 codes a thread at a time, from global memory into the products' layout; a register that has been
-            // converted takes the next item's codes, which are on their way until that item's turn
+            // ---- conversion: 16 codes a thread at a time, into the products' layout
             constexpr int RC = D / 16;  // 16-code pieces of a row
             constexpr int kTurns = (kKeys * RC + kConvert - 1) / kConvert;
             const int me = tid - 32 * (kSoft + 2);
@@ -491,117 +507,73 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             static_assert(kConvert % RC == 0 && kStep % 8 == 0, "a thread's pieces lie in one column of the layout");
             unsigned char* const to = ring + (ch >> 2) * C::BLK + row0 * 128;
             const int c0 = ((2 * ch) & 7) ^ (row0 & 7), c1 = c0 ^ 1;
-            struct Tile {
-                uint32_t there, turn, slot;
-                int key0, keys, hidden;  // hidden: the first key that some row does not see
-            };
-            uint4 u[kTurns];
-            Tile now{}, ahead{};
+            const uint32_t from = row0 * D + ch * 16;
             uint32_t t = 0, it = 0, turn = 0;  // tile, item (K or V of a tile), segment
-            int i = 0;
-            bool ok = true, have = next_segment();
-            // a thread's rows lie at one or two places of their groups of 16 (kStep is 24, 48 or 96)
-            const int64_t in0 = (int64_t)(row0 & 15) * D + ch * 16, in1 = (int64_t)((row0 + kStep) & 15) * D + ch * 16;
-            auto load = [&](int e, const uint8_t* base, uint32_t slot) {  // (volatile: on its way from here on, not from where it is used)
-                const uint8_t* from = base + (e & 1 ? in1 : in0) + (uint64_t)sh.at[slot][(row0 + kStep * e) >> 4] * (16u * D);
-                asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u[e].x), "=r"(u[e].y), "=r"(u[e].z), "=r"(u[e].w) : "l"(from));
-            };
+            bool ok = true;
             auto inside = [&](int e) { return (e + 1) * kStep <= kKeys || row0 + kStep * e < kKeys; };
-            auto fetch = [&](const Tile& x, bool value) {
-                const uint8_t* base = value ? a.c.v : a.c.k;
-                if ((x.there & 0xffu) == 0xffu && x.key0 <= x.keys - kKeys) {
-#pragma unroll
-                    for (int e = 0; e < kTurns; ++e)
-                        if (inside(e)) load(e, base, x.slot);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kTurns; ++e) {
-                        const int row = row0 + kStep * e;
-                        u[e] = make_uint4(0u, 0u, 0u, 0u);
-                        if (inside(e) && x.key0 + row < x.keys && ((x.there >> (row >> 4)) & 1u) != 0u) load(e, base, x.slot);
-                    }
-                }
-            };
-            // the next tile, once its pages are known
-            auto step = [&]() {
-                if (!warp_wait(&sh.info_full[t % kInfo], (t / kInfo) & 1u) || __any_sync(0xffffffffu, *dead != 0u)) return false;
-                ahead.slot = t % kInfo;
-                ahead.there = sh.there[ahead.slot];
-                ahead.turn = turn;
-                ahead.key0 = (s.i0 + i) * kKeys;
-                ahead.keys = s.ctx + s.last;
-                ahead.hidden = s.ctx + s.first + 1;
-                ++t;
-                if (++i == s.count) {
-                    have = next_segment();
-                    i = 0;
-                    ++turn;
-                }
-                return true;
-            };
-            // item x into its place
-            auto put = [&](const Tile& x, bool value) {
-                const uint32_t st = it % S;
-                if (!warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u)) return false;
-                unsigned char* dst = to + st * C::TILE;
-                if (kE4m3 && value && x.key0 > x.hidden - kKeys) {
-                    // NaN that not every row may see leave the tile
-#pragma unroll
-                    for (int e = 0; e < kTurns; ++e) {
-                        uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t nan = inside(e) ? __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
-                            if (nan == 0u) continue;
+            for (; ok && next_segment(); ++turn) {
+                const int keys = s.ctx + s.last, hidden = s.ctx + s.first + 1, end = s.i0 + s.count;  // hidden: the first key that some row does not see
 #pragma unroll 1
-                            for (int b = 0; b < 4; ++b)
-                                if ((nan >> (8 * b)) & 1u)
-                                    atomicMin(&sh.odd[x.turn % kInfo][ch * 16 + q * 4 + b], odd_note(x.turn, x.key0 + row0 + kStep * e));
-                            sh.dirty[x.turn % kInfo] = x.turn + 1u;
-                            c[q] &= ~nan;
+                for (int i = s.i0; i < end && ok; ++i, ++t) {
+                    const int key0 = i * kKeys;
+                    uint32_t there = 0u;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x, ++it) {
+                        const uint32_t rs = it % C::RAWS, st = it % S;
+                        ok = warp_wait(&sh.raw_full[rs], (it / C::RAWS) & 1u);
+                        if (!ok) break;
+                        if (x == 0) there = sh.there[t % kInfo] & 0xffu;
+                        uint4 u[kTurns];
+#pragma unroll
+                        for (int e = 0; e < kTurns; ++e)
+                            if (inside(e)) u[e] = *reinterpret_cast<const uint4*>(raw + rs * C::RAW + from + e * kStep * D);
+                        if (there != 0xffu || key0 > keys - kKeys) {  // keys that are not there
+#pragma unroll
+                            for (int e = 0; e < kTurns; ++e) {
+                                const int row = row0 + kStep * e;
+                                if (key0 + row >= keys || ((there >> (row >> 4)) & 1u) == 0u) u[e] = make_uint4(0u, 0u, 0u, 0u);
+                            }
                         }
-                        u[e] = make_uint4(c[0], c[1], c[2], c[3]);
-                    }
-                }
+                        if (kE4m3 && x && key0 > hidden - kKeys) {  // NaN that not every row may see leave the tile
 #pragma unroll
-                for (int e = 0; e < kTurns; ++e) {
-                    if (!inside(e)) continue;
-                    uint32_t h[8];
-                    widen<kE4m3>(u[e].x, h[0], h[1]);
-                    widen<kE4m3>(u[e].y, h[2], h[3]);
-                    widen<kE4m3>(u[e].z, h[4], h[5]);
-                    widen<kE4m3>(u[e].w, h[6], h[7]);
-                    *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c0 * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c1 * 16) = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-                return true;
-            };
-            auto done = [&]() {
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.kv_full[it % S]);
-                ++it;
-            };
-            bool any = have;
-            if (any && (ok = step())) {
-                now = ahead;
-                fetch(now, false);
-            }
-            // (one copy for keys and values)
+                            for (int e = 0; e < kTurns; ++e) {
+                                uint32_t c[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint32_t nan = inside(e) ? __vcmpeq4(c[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+                                    if (nan == 0u) continue;
 #pragma unroll 1
-            for (bool value = false; ok && any; value = !value) {
-                if (value) {
-                    any = have;
-                    if (any) ok = step();
-                }
-                ok = ok && put(now, value);
-                if (!ok) break;
-                if (value) now = ahead;
-                done();
-                if (!value || any) fetch(now, !value);
-                if (!value) {  // the tile's pages are read
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&sh.info_free[now.slot]);
+                                    for (int b = 0; b < 4; ++b)
+                                        if ((nan >> (8 * b)) & 1u)
+                                            atomicMin(&sh.odd[turn % kInfo][ch * 16 + q * 4 + b], odd_note(turn, key0 + row0 + kStep * e));
+                                    sh.dirty[turn % kInfo] = turn + 1u;
+                                    c[q] &= ~nan;
+                                }
+                                u[e] = make_uint4(c[0], c[1], c[2], c[3]);
+                            }
+                        }
+                        ok = warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u);
+                        if (!ok) break;
+                        unsigned char* dst = to + st * C::TILE;
+#pragma unroll
+                        for (int e = 0; e < kTurns; ++e) {
+                            if (!inside(e)) continue;
+                            uint32_t h[8];
+                            widen<kE4m3>(u[e].x, h[0], h[1]);
+                            widen<kE4m3>(u[e].y, h[2], h[3]);
+                            widen<kE4m3>(u[e].z, h[4], h[5]);
+                            widen<kE4m3>(u[e].w, h[6], h[7]);
+                            *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c0 * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(dst + e * kStep * 128 + c1 * 16) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
+                        tc::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tc::mbar_arrive(&sh.kv_full[st]);
+                            tc::mbar_arrive(&sh.raw_free[rs]);
+                            if (x == 0) tc::mbar_arrive(&sh.info_free[t % kInfo]);
+                        }
+                    }
                 }
             }
             if (!ok) *dead = 1u;
