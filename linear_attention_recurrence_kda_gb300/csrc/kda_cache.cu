@@ -18,8 +18,13 @@
 //
 // Keys that turn: the sines and cosines of the page's tokens are formed once into a table in shared memory and serve the
 // CTA's heads; a row's other channel of each pair lies with a neighbour in the same warp.  The turned values stay in
-// registers, in fp32, between the maximum and the rounding.  Warps past the pages' CTAs turn q.
+// registers, in fp32, between the maximum and the rounding.  Warps past the pages' CTAs turn q.  The same 69,632 tokens
+// with 32 heads of q: 296 us for 231 us of bytes (5.3 TB/s), the pages alone 146; they are bound by issue and by their 96 KB
+// a CTA, two to an SM.  Measured against (366 us when begun): the table read 8 bytes at a time, with its bank conflicts, 329;
+// registers for three CTAs an SM, which spill, 330; q in a launch of its own 364.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "kda_attn.cuh"
 #include "kda_rotary.cuh"
@@ -32,14 +37,15 @@ constexpr int kVec = 8;        // values a thread holds of a row
 constexpr int kMaxThreads = 256;
 constexpr int kMaxStages = 4;   // units whose rows are on their way or held
 constexpr int kMinExp = -60;
-constexpr int kMaxRows = 8;    // rows of a page that a thread may hold: 128 of 16 threads each by 256 threads
 
 // What a call does to its keys and queries on the way: nothing, or a turn.
 struct AsTheyAre {
     static constexpr bool kTurns = false;
+    static constexpr int kRows = 1;
 };
-struct Turned {
+template <int R> struct Turned {  // R: rows that a thread holds at most
     static constexpr bool kTurns = true;
+    static constexpr int kRows = R;
     TurnArgs t;
     TurnRows q;
     int64_t tasks;  // warps of q
@@ -224,16 +230,16 @@ __global__ void __launch_bounds__(kMaxThreads)
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if constexpr (How::kTurns) {
-        // [rows][pairs] of (cos, sin); the first unit's barrier comes before anything is read, see below
+        // (cos, sin) of [rows][pairs], a thread's pairs two by two, so that neighbours read 16 bytes side by side
         float2* table = reinterpret_cast<float2*>(ring + how.table);
-        const int pairs = how.t.rot >> 1;
+        const int pairs = how.t.rot >> 1, own = how.t.adjacent ? 2 : 3, parts = pairs >> own;  // 2^own pairs are a thread's
         for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
             const int r = i / pairs, pair = i - r * pairs;
             const int64_t token = t0 + (p0 - first) + r;
             const int position = how.t.positions != nullptr ? how.t.positions[(int64_t)how.t.axis[pair] * a.T + token] : (int)(p0 + r);
             float s, c;
             sincos_of(how.t, pair, position, s, c);
-            table[i] = make_float2(c, s);
+            table[r * pairs + 2 * (((pair & ((1 << own) - 1)) >> 1) * parts + (pair >> own)) + (pair & 1)] = make_float2(c, s);
         }
     }
     // A thread's eight channels of its row i, turned: the other channels of their pairs lie in the same row, eight
@@ -244,23 +250,28 @@ __global__ void __launch_bounds__(kMaxThreads)
             get8<TIO>(at, x);
             const int rot = how.t.rot, half = rot >> 1;
             if (c0 >= rot) return;
-            const float2* row = reinterpret_cast<const float2*>(ring + how.table) + (r0 + i * rstep) * half;
+            const float4* row = reinterpret_cast<const float4*>(ring + how.table) + (r0 + i * rstep) * (half >> 1);
             if (how.t.adjacent) {
+                row += c0 >> 3;
 #pragma unroll
-                for (int e = 0; e < kVec / 2; ++e) {
-                    const float2 cs = row[(c0 >> 1) + e];
-                    const float p = x[2 * e], q = x[2 * e + 1];
-                    x[2 * e] = fmaf(p, cs.x, -q * cs.y);
-                    x[2 * e + 1] = fmaf(q, cs.x, p * cs.y);
+                for (int e = 0; e < kVec / 4; ++e) {
+                    const float4 cs = row[e * (half >> 2)];
+                    const float p = x[4 * e], q = x[4 * e + 2];
+                    x[4 * e] = fmaf(p, cs.x, -x[4 * e + 1] * cs.y);
+                    x[4 * e + 1] = fmaf(x[4 * e + 1], cs.x, p * cs.y);
+                    x[4 * e + 2] = fmaf(q, cs.z, -x[4 * e + 3] * cs.w);
+                    x[4 * e + 3] = fmaf(x[4 * e + 3], cs.z, q * cs.w);
                 }
             } else {
                 const bool up = c0 >= half;
                 float y[kVec];
                 get8<TIO>(at + (up ? -half : half) * (int)sizeof(TIO), y);
+                row += (up ? c0 - half : c0) >> 3;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float2 cs = row[(up ? c0 - half : c0) + e];
-                    x[e] = up ? fmaf(x[e], cs.x, y[e] * cs.y) : fmaf(x[e], cs.x, -y[e] * cs.y);
+                for (int e = 0; e < kVec / 2; ++e) {
+                    const float4 cs = row[e * (half >> 3)];
+                    x[2 * e] = fmaf(x[2 * e], cs.x, y[2 * e] * (up ? cs.y : -cs.y));
+                    x[2 * e + 1] = fmaf(x[2 * e + 1], cs.z, y[2 * e + 1] * (up ? cs.w : -cs.w));
                 }
             }
         }
@@ -274,19 +285,31 @@ __global__ void __launch_bounds__(kMaxThreads)
         // magnitudes compare as integers; where the largest is an infinity or NaN, which set no scale,
         // the rows are looked through again for the largest that is neither
         uint32_t top = 0u;
-        float turned[How::kTurns ? kMaxRows : 1][kVec];
+        float turned[How::kRows][kVec];
         const bool turn = How::kTurns && (u & 1) == 0;
         float amax = 0.f;
         if (turn) {
             __syncwarp();  // the neighbours' copies have landed, too
 #pragma unroll
-            for (int i = 0; i < kMaxRows; ++i) {
+            for (int i = 0; i < How::kRows; ++i) {
                 if (i >= mine_rows) continue;
                 turned8(held, i, turned[How::kTurns ? i : 0]);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e) {
-                    const float m = fabsf(turned[How::kTurns ? i : 0][e]);
-                    amax = m < INFINITY ? fmaxf(amax, m) : amax;
+                    top = max(top, __float_as_uint(turned[How::kTurns ? i : 0][e]) & 0x7fffffffu);
+                }
+            }
+            amax = __uint_as_float(top);
+            if (!(amax < INFINITY)) {
+                amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < How::kRows; ++i) {
+                    if (i >= mine_rows) continue;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        const float m = fabsf(turned[How::kTurns ? i : 0][e]);
+                        amax = m < INFINITY ? fmaxf(amax, m) : amax;
+                    }
                 }
             }
         } else {
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         uint8_t* dst = codes + (slot0 + r0) * a.d + c0;
         if (turn) {
 #pragma unroll
-            for (int i = 0; i < kMaxRows; ++i)
+            for (int i = 0; i < How::kRows; ++i)
                 if (i < mine_rows) *reinterpret_cast<uint2*>(dst + i * rstep * a.d) = encode8<kE4m3>(turned[How::kTurns ? i : 0], inv);
             return;
         }
@@ -375,18 +398,23 @@ cudaError_t launch(const AppendArgs& a, How how, kda_dtype_t dt, cudaStream_t s)
     const int64_t rows = c < a.c.page ? c : a.c.page;
     int threads = (int)((rows * (a.d / kVec) + 31) / 32 * 32);
     if (threads > kMaxThreads) threads = kMaxThreads;
-    // several heads a CTA while about eight CTAs an SM remain
-    int heads = 1;
-    while (2 * heads <= a.Hkv && slots * ((a.Hkv + 2 * heads - 1) / (2 * heads)) >= 8LL * sm_count_of_current_device()) heads *= 2;
-    dim3 grid((unsigned)slots, (unsigned)((a.Hkv + heads - 1) / heads));
     const int stage_bytes = (int)rows * a.d * (dt == KDA_BF16 ? 2 : 4);  // at most 64 KB
     int stages = 65536 / stage_bytes;
     stages = stages > kMaxStages ? kMaxStages : stages < 2 ? 2 : stages;
-    int smem = stages * stage_bytes;
+    int smem = stages * stage_bytes, resident = 8;
     if constexpr (How::kTurns) {
         how.slots = (int)slots;
         how.table = smem;
         smem += (int)rows * how.t.rot / 2 * (int)sizeof(float2);  // at most 64 KB
+        resident = std::min(resident, 229376 / smem);
+    }
+    // Several heads a CTA while about eight CTAs an SM remain, or as many as it holds: where the table leaves room for two,
+    // more CTAs only read, look up and form again what one does for all heads (256 single tokens of 8 and 32 heads:
+    // 31.5 us with the eight, 21 with the two; 69,632 tokens: 366 and 329).
+    int heads = 1;
+    while (2 * heads <= a.Hkv && slots * ((a.Hkv + 2 * heads - 1) / (2 * heads)) >= (int64_t)resident * sm_count_of_current_device()) heads *= 2;
+    dim3 grid((unsigned)slots, (unsigned)((a.Hkv + heads - 1) / heads));
+    if constexpr (How::kTurns) {
         if (how.q.heads[0] > 0) how.tasks = turn_tasks(how.t, how.q, &how.groups);
         const int64_t per = (int64_t)grid.y * (threads / 32);  // of q's warps that a place of x holds
         const int64_t x = slots + (how.tasks + per - 1) / per;
@@ -414,10 +442,13 @@ cudaError_t launch_cache_append(const AppendArgs& a, kda_dtype_t dt, cudaStream_
 
 cudaError_t launch_rotary_append(const AppendArgs& a, const TurnArgs& t, const TurnRows& q, kda_dtype_t dt, cudaStream_t s)
 {
-    Turned how{};
-    how.t = t;
-    how.q = q;
-    return launch(a, how, dt, s);
+    auto go = [&](auto how) {
+        how.t = t;
+        how.q = q;
+        return launch(a, how, dt, s);
+    };
+    // (four rows a thread where they do: 294 us for the 69,632 tokens, 305 with eight's registers)
+    return a.c.page * (a.d / kVec) <= 4 * kMaxThreads ? go(Turned<4>{}) : go(Turned<8>{});
 }
 
 }  // namespace kda
