@@ -4,16 +4,17 @@
 //   Z = scale ks (Q K^T),  P = 2^(Z log2 e - m),  O = sum P (vs V),  o = O / l        per row, keys in tiles of 128
 //
 // A unit is one sequence, one key head and up to 256 rows (a group's query heads times 256 / group tokens), in two halves of
-// 128; a CTA walks the unit's keys for both.  Codes are converted to f16 once a tile, exactly (e4m3 and int8 are
-// subsets of f16), by warps that do nothing else, straight from global memory into the products' layout.  The products are
-// tcgen05.mma with M = 128: Z from Q and K in shared memory, O += P V with P read from tensor memory and V token-major as it
-// lies.  Tensor memory: Z0 | Z1 | O0 | O1, P as packed f16 over its Z.  A thread of the softmax owns a row.
+// 128; a CTA walks the unit's keys for both.  Codes arrive by bulk copies, a page of a head each, and are converted to f16
+// once a tile, exactly (e4m3 and int8 are subsets of f16), by warps that do nothing else.  The products are tcgen05.mma with
+// M = 128: Z from Q and K in shared memory, O += P V with P read from tensor memory and V token-major as it lies.  Tensor
+// memory: Z0 | Z1 | O0 | O1, P as packed f16 over its Z.  Two threads of the softmax own a row, half of a tile's keys each.
 //
 // All units' keys, with a gap before each unit for what its start costs, form one line that is cut evenly among the CTAs,
 // whatever the lengths are; pieces of a unit are joined by a second kernel in a fixed order.  A unit's key tiles grow with
 // its rows' places (causality), so the line is counted in keys, in closed form.
 //
-// Warps 0-3 and 4-7: softmax of the halves, 8: products, 9: pages and scales, 10-15: conversion.  They meet at mbarriers.
+// Warps 0-7 and 8-15: softmax of the halves, 16: products, 17: pages and scales, 18-23: conversion (fp32: eight fewer).  They
+// meet at mbarriers, each with a limit to its wait.
 //
 // A row of q enters as f16 times a power of two that brings its largest value to [2^14, 2^15): bf16's eight bits are
 // exact down to 2^-31 of it.  Weights are held against a reference 2^7 below the row's largest score, which moves only when the
@@ -26,6 +27,16 @@
 //
 // Hidden keys: scores are replaced by -inf.  A NaN code in a value would spread over 0 x NaN, so a tile that some row does not see
 // whole is cleaned of them (noted by channel and key), and the rows that see them get them at the end.
+//
+// 2048 tokens behind 30,720 keys, 32 heads of 128 channels over 8: 797 us, 1.34 PFLOP/s (int8 763 us, 1.40), 68 % of the library's
+// bf16 products; 256 tokens behind 1,048,320: 3136 us, 1.40 PFLOP/s.  The products alone would take 60 % of a tile's 3400 cycles;
+// the rest is the way of a half's tile from scores to weights, which the other half's products do not cover.  What counted
+// (the first form took 1813 us): one copy of each role's code, which has to fit a small instruction cache, 1134 -> 943;
+// two threads a row, ordinary tiles in one pass over tensor memory, 890; a tile's scales read before its scores arrive; codes by bulk
+// copies and not loaded by the converting warps, without a prefetch into L2, 883 -> 797 (with it 909).  Eight warps of
+// conversion 919; scores held in registers by one thread a row 950 to 1000.  Few rows: 64 sequences of 4096 keys and one
+// token each take 236 us, 2.3 TB/s, bound by conversion and half-empty products (the decode kernel is the one for these).
+#include <algorithm>
 #include <cfloat>
 
 #include "kda_attn.cuh"
@@ -42,7 +53,7 @@ constexpr int kKeys = 128;
 constexpr int kConvert = 192;
 constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
 constexpr int kGroups = kKeys / 16;
-constexpr int kGap = 256;      // what a unit's start and end cost, in keys
+constexpr int kGap = 256;      // what a unit's start and end cost, in keys (128 and 512: within 1 % on long and on many short units, 10 % worse with 128 on fp32)
 constexpr float kUnset = -FLT_MAX;  // the reference of a row that has met no score above -inf
 constexpr float kFar = 1048576.f;   // 2^20: references beyond it have their scores rounded first
 constexpr uint32_t kHidden = 0xff800000u;
@@ -972,19 +983,38 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
 }
 
 // Joins a unit's pieces: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the CTAs that hold one, in an order
-// that the pieces' number fixes.  Block x looks after the unit that CTA x began; `wpr` warps take a row's pieces in turn.
+// that the pieces' number fixes.  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit at a
+// time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
 constexpr int kJoinWarps = 8;
+constexpr int kMaxWorkers = 512;
 
-template <typename TIO, int D>
+template <typename TIO, int D, bool kFew>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     kda_attn_extend_join_kernel(const AttnExtendArgs a, const int rows_max, const int workers, const int tpu, const int half_tokens, const int wpr)
 {
     constexpr int V = D / 32;
     __shared__ float part[kJoinWarps][D + 1];
+    __shared__ int units[kFew ? kMaxWorkers : 1];  // the CTAs that began a unit which they did not end, in order
+    __shared__ int counts[kJoinWarps];
     __shared__ uint32_t word;
     const DecodeLayout L = decode_layout(workers, workers, rows_max, D);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     griddep_wait();
+    const Record* records = reinterpret_cast<const Record*>(a.ws + L.records);
+    int count = 0;
+    for (int base = 0; kFew && base < workers; base += kJoinWarps * 32) {
+        const int i = base + threadIdx.x;
+        const uint32_t yes = __ballot_sync(0xffffffffu, i < workers && records[i].n >= 0);
+        if (lane == 0) counts[w] = __popc(yes);
+        __syncthreads();
+        int before = count;
+        for (int x = 0; x < kJoinWarps; ++x) {
+            before += x < w ? counts[x] : 0;
+            count += counts[x];
+        }
+        if ((yes >> lane) & 1u) units[before + __popc(yes & ((1u << lane) - 1u))] = i;
+        __syncthreads();
+    }
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         // the call's check word: every CTA's flags, so that nothing has to be cleared before the call
         if (threadIdx.x == 0) word = 0u;
@@ -996,61 +1026,70 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         __syncthreads();
         if (threadIdx.x == 0) *reinterpret_cast<uint32_t*>(a.ws) = word;
     }
-    const Record rec = reinterpret_cast<const Record*>(a.ws + L.records)[blockIdx.x];
-    if (rec.n < 0) return;
-    const Seq s = seq_of(a, rec.n);
-    const int r = blockIdx.y * (kJoinWarps / wpr) + w / wpr;  // row of the unit: 128 a half
-    const int in_half = r & 127, tok = rec.rt * tpu + (r >> 7) * half_tokens + in_half / a.group;
-    const bool on = r < rows_max && in_half < half_tokens * a.group && tok < min((rec.rt + 1) * tpu, s.rows);
-    const float2* ml = reinterpret_cast<const float2*>(a.ws + L.ml);
-    const float* po = reinterpret_cast<const float*>(a.ws + L.o);
-    const int pieces = rec.last - rec.first + 1;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * rec.first + 1 : 2 * (rec.first + i)); };
-    float l = 0.f, o[V];
+    const int rows = kJoinWarps / wpr, turns = (rows_max + rows - 1) / rows;  // rows at a time, times for a unit
+    for (int item = blockIdx.x; !kFew || item < count * turns; item += gridDim.x) {
+        const Record rec = records[kFew ? units[item / turns] : blockIdx.x];
+        if (!kFew && rec.n < 0) return;
+        const Seq s = seq_of(a, rec.n);
+        const int r = (kFew ? item % turns : blockIdx.y) * rows + w / wpr;  // row of the unit: 128 a half
+        const int in_half = r & 127, tok = rec.rt * tpu + (r >> 7) * half_tokens + in_half / a.group;
+        const bool on = r < rows_max && in_half < half_tokens * a.group && tok < min((rec.rt + 1) * tpu, s.rows);
+        const float2* ml = reinterpret_cast<const float2*>(a.ws + L.ml);
+        const float* po = reinterpret_cast<const float*>(a.ws + L.o);
+        const int pieces = rec.last - rec.first + 1;
+        auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * rec.first + 1 : 2 * (rec.first + i)); };
+        float l = 0.f, o[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = 0.f;
-    if (on) {
-        float m = -FLT_MAX;
-        for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
+        for (int v = 0; v < V; ++v) o[v] = 0.f;
+        if (on) {
+            float m = -FLT_MAX;
+            for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 #pragma unroll 4
-        for (int i = w % wpr; i < pieces; i += wpr) {
-            const float2 x = ml[slot(i) * rows_max + r];
-            const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
-            const float f = ex2(x.x - m);
-            l += x.y * f;
-            if constexpr (V == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(p);
-                o[0] += y.x * f; o[1] += y.y * f; o[2] += y.z * f; o[3] += y.w * f;
-            } else if constexpr (V == 2) {
-                const float2 y = *reinterpret_cast<const float2*>(p);
-                o[0] += y.x * f; o[1] += y.y * f;
-            } else {
-                o[0] += *p * f;
+            for (int i = w % wpr; i < pieces; i += wpr) {
+                const float2 x = ml[slot(i) * rows_max + r];
+                const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
+                const float f = ex2(x.x - m);
+                l += x.y * f;
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(p);
+                    o[0] += y.x * f; o[1] += y.y * f; o[2] += y.z * f; o[3] += y.w * f;
+                } else if constexpr (V == 2) {
+                    const float2 y = *reinterpret_cast<const float2*>(p);
+                    o[0] += y.x * f; o[1] += y.y * f;
+                } else {
+                    o[0] += *p * f;
+                }
             }
         }
-    }
-    if (wpr > 1) {
+        if (wpr > 1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) part[w][lane * V + v] = o[v];
-        if (lane == 0) part[w][D] = l;
-        __syncthreads();
-        if (w % wpr != 0) return;
-        for (int i = 1; i < wpr; ++i) {
+            for (int v = 0; v < V; ++v) part[w][lane * V + v] = o[v];
+            if (lane == 0) part[w][D] = l;
+            __syncthreads();
+            for (int i = 1; i < wpr && w % wpr == 0; ++i) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += part[w + i][lane * V + v];
-            l += part[w + i][D];
+                for (int v = 0; v < V; ++v) o[v] += part[w + i][lane * V + v];
+                l += part[w + i][D];
+            }
+            if (kFew) __syncthreads();  // (read before the next rows' replace it)
         }
-    }
-    if (!on) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    TIO* od = static_cast<TIO*>(a.out) + ((s.start + tok) * a.Hq + rec.h * a.group + in_half % a.group) * D + lane * V;
+        if (!on || w % wpr != 0) {
+            if constexpr (kFew) continue;
+            else return;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        TIO* od = static_cast<TIO*>(a.out) + ((s.start + tok) * a.Hq + rec.h * a.group + in_half % a.group) * D + lane * V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
+        for (int v = 0; v < V; ++v) st_io(od, v, o[v] * inv);
+        if (!kFew) return;
+    }
 }
 
 namespace {
+
+int extend_ctas() { return std::min(sm_count_of_current_device(), kMaxWorkers); }
 
 // Rows of a piece: a unit's, or fewer where the call has no more in one half.
 int piece_rows(int64_t tokens, int group, kda_dtype_t dt)
@@ -1069,17 +1108,23 @@ cudaError_t launch_extend(const AttnExtendArgs& a, cudaStream_t s)
     static SmemLimit limit;
     cudaError_t e = limit.raise(kern, (int)C::SMEM);
     if (e != cudaSuccess) return e;
-    const int ctas = sm_count_of_current_device();
+    const int ctas = extend_ctas();
     const int rows = piece_rows(a.T, a.group, kSplit ? KDA_F32 : KDA_BF16);
     kern<<<ctas, C::THREADS, C::SMEM, s>>>(a, rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // about ctas / units pieces a unit: four or more a warp
+    // About ctas / units pieces a unit: four or more a warp.  Where a quarter of the CTAs at most can have begun a unit (one for
+    // every token tile and sequence), no more blocks than their rows need or an SM holds: 4 units in 32 pieces take 24.6 us with
+    // these and 38.5 with blocks for every CTA's every row; 150 units 806 with these and 800 with all.
     const int half_tokens = 128 / a.group, tpu = C::HALVES * half_tokens;
     const int64_t units = (a.T + tpu - 1) / tpu * a.Hkv, pieces = ctas / units;
     const int wpr = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
-    const dim3 grid((unsigned)ctas, (unsigned)((rows * wpr + kJoinWarps - 1) / kJoinWarps));
-    return launch_dependent(kda_attn_extend_join_kernel<TIO, D>, grid, dim3(kJoinWarps * 32), 0, s, a, rows, ctas, tpu, half_tokens, wpr);
+    const int64_t most = (a.T / tpu + std::min<int64_t>(a.T, a.N)) * a.Hkv, turns = (rows * wpr + kJoinWarps - 1) / kJoinWarps;
+    if (most <= ctas / 4) {
+        const int64_t blocks = std::min<int64_t>(most * turns, 8LL * ctas);
+        return launch_dependent(kda_attn_extend_join_kernel<TIO, D, true>, dim3((unsigned)blocks), dim3(kJoinWarps * 32), 0, s, a, rows, ctas, tpu, half_tokens, wpr);
+    }
+    return launch_dependent(kda_attn_extend_join_kernel<TIO, D, false>, dim3((unsigned)ctas, (unsigned)turns), dim3(kJoinWarps * 32), 0, s, a, rows, ctas, tpu, half_tokens, wpr);
 }
 
 template <typename TIO, int D>
@@ -1098,7 +1143,7 @@ cudaError_t launch_d(const AttnExtendArgs& a, cudaStream_t s)
 
 size_t attn_extend_workspace_bytes(int64_t tokens, int group, int d, kda_dtype_t dt)
 {
-    const int ctas = sm_count_of_current_device();
+    const int ctas = extend_ctas();
     return decode_layout(ctas, ctas, piece_rows(tokens, group, dt), d).total;
 }
 
