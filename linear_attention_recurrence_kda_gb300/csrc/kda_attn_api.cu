@@ -101,6 +101,15 @@ kda::CacheArgs cache_args(const kda_cache_t& c)
     return a;
 }
 
+// The descriptor of a call that turns, which uses no scale.
+kda_status_t check_turn_problem(const kda_attention_t* problem, bool has_q, kda_attention_t* p)
+{
+    if (problem == nullptr) return KDA_ERR_INVALID_ARG;
+    *p = *problem;
+    p->scale = 1.f;
+    return check_attention(p, has_q);
+}
+
 // The rotary descriptor, and its frequencies as fractions of a turn.
 kda_status_t check_rotary(const kda_rotary_t* r, const kda_attention_t& p, bool inverse, kda::TurnArgs* out)
 {
@@ -288,9 +297,9 @@ kda_status_t kda_rotary_append(const void* q, const void* k, const void* v, cons
                                const int32_t* positions, void* q_out, const kda_cache_t* cache, const kda_attention_t* problem,
                                const kda_rotary_t* rotary, uint32_t* check, void* stream)
 {
-    kda_status_t st = check_attention(problem, q != nullptr);
+    kda_attention_t p;
+    kda_status_t st = check_turn_problem(problem, q != nullptr, &p);
     if (st != KDA_OK) return st;
-    const kda_attention_t& p = *problem;
     kda::TurnArgs t{};
     kda::TurnRows r{};
     if ((st = check_rotary(rotary, p, false, &t)) != KDA_OK) return st;
@@ -333,9 +342,9 @@ kda_status_t kda_rotary(const void* q, const void* k, const int32_t* cu_seqlens,
                         const int32_t* positions, void* q_out, void* k_out, const kda_attention_t* problem,
                         const kda_rotary_t* rotary, int32_t inverse, void* stream)
 {
-    kda_status_t st = check_attention(problem, q != nullptr);
+    kda_attention_t p;
+    kda_status_t st = check_turn_problem(problem, q != nullptr, &p);
     if (st != KDA_OK) return st;
-    const kda_attention_t& p = *problem;
     if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
     if (inverse != 0 && inverse != 1) return KDA_ERR_INVALID_ARG;
     kda::TurnArgs t{};

@@ -65,6 +65,14 @@ def test_null_descriptors(L):  # noqa: F811
     assert rotary(L, attention(num_seqs=3), descriptor()) == append(L, attention(num_seqs=3), cache(), descriptor()) == B.KDA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("scale", [0.0, -1.0, math.nan])
+def test_scale_is_not_used(L, scale):  # noqa: F811
+    good = rotary(L, attention(), descriptor())
+    assert good != B.KDA_ERR_INVALID_ARG and rotary(L, attention(scale=scale), descriptor()) == good
+    good = append(L, attention(), cache(), descriptor())
+    assert good != B.KDA_ERR_INVALID_ARG and append(L, attention(scale=scale), cache(), descriptor()) == good
+
+
 def test_pointers_and_overlap(L):  # noqa: F811
     p, r, c = attention(), descriptor(), cache()
     for name in ("q", "k", "q_out", "k_out"):  # a tensor and its output come together, on 16 bytes
