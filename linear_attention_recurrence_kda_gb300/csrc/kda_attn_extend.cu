@@ -53,7 +53,9 @@ constexpr int kKeys = 128;
 constexpr int kConvert = 192;
 constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
 constexpr int kGroups = kKeys / 16;
-constexpr int kGap = 256;      // what a unit's start and end cost, in keys (128 and 512: within 1 % on long and on many short units, 10 % worse with 128 on fp32)
+// What a unit's start and end cost, in keys.  With 128 and 512 long units and many short ones take the same within 1 %, fp32 chunks
+// of 333 tokens 43 us with 128 (39 with 256 and 512).
+constexpr int kGap = 256;
 constexpr float kUnset = -FLT_MAX;  // the reference of a row that has met no score above -inf
 constexpr float kFar = 1048576.f;   // 2^20: references beyond it have their scores rounded first
 constexpr uint32_t kHidden = 0xff800000u;
@@ -766,11 +768,12 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         }
                     }
                     if (!ordinary) {
-                        // Any tile: hidden scores leave Z, the largest weight, the weights.  References move to 2^7 below the largest weight here, not
-                        // only where it has passed 2^15 but wherever it has grown by more than 2^2: what one row makes necessary then
-                        // serves its warp's others, whose turn would come one by one.  A row beyond 2^20, where a score's rounding would show (and all rows where a scale is no positive
-                        // number) has its scores rounded, as the reference is, before it comes off, so that none passes the largest
-                        // however large they are, and the value's scale is multiplied with.
+                        // Any tile: hidden scores leave Z, the largest weight, the weights.  References move to 2^7 below the largest
+                        // weight here, not only where it has passed 2^15 but wherever it has grown by more than 2^2: what one row
+                        // makes necessary then serves its warp's others, whose turn would come one by one.  A row beyond 2^20, where a
+                        // score's rounding would show (and all rows where a scale is no positive number), has its scores rounded, as
+                        // the reference is, before it comes off, so that none passes the largest however large they are, and the
+                        // value's scale is multiplied with.
                         if (key0 > warp_seen - kKeys || (there & 0xffu) != 0xffu) {
 #pragma unroll 1
                             for (int c = 0; c < 2; ++c) {
