@@ -14,7 +14,8 @@
 // its rows' places (causality), so the line is counted in keys, in closed form.
 //
 // Warps 0-7 and 8-15: softmax of the halves, 16: products, 17: pages and scales, 18-23: conversion (fp32: eight fewer).  They
-// meet at mbarriers, each with a limit to its wait.
+// meet at mbarriers, each with a limit to its wait: who gives up stops, and with it whoever waits for it, then what is in flight
+// is waited for (always with the full limit) and the call's check word tells.
 //
 // A row of q enters as f16 times a power of two that brings its largest value to [2^14, 2^15): bf16's eight bits are
 // exact down to 2^-31 of it.  Weights are held against a reference 2^7 below the row's largest score, which moves only when the
@@ -42,6 +43,7 @@
 #include "kda_attn.cuh"
 #include "kda_attn_decode.cuh"
 #include "kda_attn_tc.cuh"
+#include "kda_checks.cuh"
 
 namespace kda {
 
@@ -211,7 +213,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) { K
 }  // namespace
 
 template <typename TIO, int D, bool kE4m3>
-__global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_attn_extend_kernel(const AttnExtendArgs a, const int rows_max)
+__global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_attn_extend_kernel(const AttnExtendArgs a, const int rows_max, const uint32_t tries)
 {
     constexpr bool kSplit = sizeof(TIO) == 4;
     using C = Cfg<D, kSplit>;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     const float pv = page < 0 ? 1.f : vu == 0.f ? (scale == scale ? 0.f : scale) : scale * inv;
                     const float lg = __log2f(pv), ip = __frcp_rn(pv);
                     const uint32_t slot = t % kInfo;
-                    ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u) && !__any_sync(0xffffffffu, *dead != 0u);
+                    ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u, tries) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
                     if (lane < 8) {
                         sh.ks[slot][grp] = scale;
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
 #pragma unroll 1
                     for (int x = 0; x < 2 && ok; ++x, ++it) {
                         const uint32_t st = it % C::RAWS;
-                        ok = warp_wait(&sh.raw_free[st], ((it / C::RAWS) & 1u) ^ 1u);
+                        ok = warp_wait(&sh.raw_free[st], ((it / C::RAWS) & 1u) ^ 1u, tries);
                         if (!ok) break;
                         if (lane == 0) tc::mbar_arrive_expect_tx(&sh.raw_full[st], (uint32_t)pieces * box * D);
                         __syncwarp();
@@ -443,9 +445,9 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
             uint32_t it = 0, phase = 0;  // phase: bits 0, 1 of q, 2, 3 of P
             bool ok = true;
-            auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u); };
+            auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u, tries); };
             auto flip = [&](uint64_t* bar, uint32_t bit) {
-                const bool got = warp_wait(bar, (phase >> bit) & 1u);
+                const bool got = warp_wait(bar, (phase >> bit) & 1u, tries);
                 phase ^= 1u << bit;
                 return got;
             };
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
 #pragma unroll 1
                     for (int x = 0; x < 2; ++x, ++it) {
                         const uint32_t rs = it % C::RAWS, st = it % S;
-                        ok = warp_wait(&sh.raw_full[rs], (it / C::RAWS) & 1u);
+                        ok = warp_wait(&sh.raw_full[rs], (it / C::RAWS) & 1u, tries);
                         if (!ok) break;
                         if (x == 0) there = sh.there[t % kInfo] & 0xffu;
                         uint4 u[kTurns];
@@ -565,7 +567,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                                 u[e] = make_uint4(c[0], c[1], c[2], c[3]);
                             }
                         }
-                        ok = warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u);
+                        ok = warp_wait(&sh.kv_empty[st], ((it / S) & 1u) ^ 1u, tries);
                         if (!ok) break;
                         unsigned char* dst = to + st * C::TILE;
 #pragma unroll
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             for (int j = 0; j < count; ++j, ++t) {
                 const int slot = t % kInfo;
                 if (j < nh) {
-                    late = !warp_wait(&sh.z_full[hf], zc++ & 1u);
+                    late = !warp_wait(&sh.z_full[hf], zc++ & 1u, tries);
                     tc::fence_after_sync();
                     if constexpr (kSplit) {
                         // the last tile's outputs, both parts, to the sum of those before it (their products ended with the scores)
@@ -891,14 +893,18 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     if (lane == 0) tc::mbar_arrive(&sh.p_full[hf]);
                 } else {
                     // (not before the tile is known: the barrier still counts the slot's last one)
-                    late = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u) || late;
+                    late = !warp_wait(&sh.info_full[slot], (t / kInfo) & 1u, tries) || __any_sync(0xffffffffu, *dead != 0u);
+                    if (late) {  // once for all of the segment's tiles; the row's threads meet below
+                        *dead = 1u;
+                        break;
+                    }
                 }
                 // the last tile's when the segment is over: conversion then is less than kInfo segments ahead (see odd_note)
                 __syncwarp();
                 if (lane == 0 && j + 1 < count) tc::mbar_arrive(&sh.info_free[slot]);
             }
             if (!left) {
-                if (nh > 0 && !late) late = !warp_wait(&sh.o_full[hf], oc++ & 1u);
+                if (nh > 0 && !late) late = !warp_wait(&sh.o_full[hf], oc++ & 1u, tries);
                 sh.sum[turn & 1][hf][part][r] = l;
                 left = pair_any(pair, late || *dead != 0u);
             }
@@ -1113,7 +1119,7 @@ cudaError_t launch_extend(const AttnExtendArgs& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int ctas = extend_ctas();
     const int rows = piece_rows(a.T, a.group, kSplit ? KDA_F32 : KDA_BF16);
-    kern<<<ctas, C::THREADS, C::SMEM, s>>>(a, rows);
+    kern<<<ctas, C::THREADS, C::SMEM, s>>>(a, rows, checks::handoff_tries(kTries));
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // About ctas / units pieces a unit: four or more a warp.  Where a quarter of the CTAs at most can have begun a unit (one for
