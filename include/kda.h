@@ -430,8 +430,8 @@ typedef struct {
  *   positions : [axes, T_tot] int32 on the device, any values; or NULL: a token's place in its sequence, from 0, on every axis.
  *   q_out, k_out : packed outputs like q and k, or q and k themselves (in place, strides and all); no other overlap.
  *   problem : num_seqs, total_tokens, num_heads, num_kv_heads, head_dim, io_dtype, q_stride, k_stride (the rest unused).
- * Angles are reduced exactly (a position times freq as a 64-bit fraction of a turn), so that far positions lose nothing
- * to fp32; arithmetic is fp32, rounded to the io dtype once.
+ * freq / (2 pi) is kept as a fraction of a turn to within 2^-64 and multiplied with the position exactly, so that an angle is
+ * off by less than 2^-31 of a turn at any position and frequency; arithmetic is fp32, rounded to the io dtype once.
  */
 kda_status_t kda_rotary(const void* q, const void* k, const int32_t* cu_seqlens, const int32_t* lengths,
                         const int32_t* positions, void* q_out, void* k_out, const kda_attention_t* problem,

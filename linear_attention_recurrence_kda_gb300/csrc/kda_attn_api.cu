@@ -110,6 +110,13 @@ kda_status_t check_turn_problem(const kda_attention_t* problem, bool has_q, kda_
     return check_attention(p, has_q);
 }
 
+// A part of a turn (at most a half), to the nearest multiple of 2^-64, mod 1.
+uint64_t turn64(double part)
+{
+    const uint64_t mag = (uint64_t)std::nearbyint(std::ldexp(std::fabs(part), 64));
+    return part < 0.0 ? 0 - mag : mag;
+}
+
 // The rotary descriptor, and its frequencies as fractions of a turn.
 kda_status_t check_rotary(const kda_rotary_t* r, const kda_attention_t& p, bool inverse, kda::TurnArgs* out)
 {
@@ -123,10 +130,11 @@ kda_status_t check_rotary(const kda_rotary_t* r, const kda_attention_t& p, bool 
     out->d = p.head_dim;
     for (int i = 0; i < r->rot_dim / 2; ++i) {
         if (r->axis[i] >= r->axes || !(std::fabs(r->freq[i]) <= 65536.0)) return KDA_ERR_INVALID_ARG;
-        const double turns = r->freq[i] * 0.15915494309189535;  // 1 / (2 pi)
-        const double part = turns - std::nearbyint(turns);      // exact, within a half
-        const uint64_t mag = (uint64_t)std::ldexp(std::fabs(part), 64);
-        out->turn[i] = (part < 0.0) != inverse ? 0 - mag : mag;
+        // freq / (2 pi), with 1 / (2 pi) and the product each in two doubles: what one leaves out is taken position times
+        constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+        const double hi = r->freq[i] * kHi, lo = std::fma(r->freq[i], kHi, -hi) + r->freq[i] * kLo;
+        const uint64_t turn = turn64(hi - std::nearbyint(hi)) + turn64(lo);
+        out->turn[i] = inverse ? 0 - turn : turn;
         out->axis[i] = r->axis[i];
     }
     return KDA_OK;

@@ -2,8 +2,8 @@
 // heads (kda_rotary.cu; kda_cache.cu turns keys on their way into the cache).
 //
 // A position p times a frequency f is an angle of p f / (2 pi) turns, of which only the fraction counts.  f / (2 pi) mod 1 is kept
-// as a 64-bit fraction F, so that the integer product p F mod 2^64 is the fraction exactly, however far p is;
-// its upper 32 bits leave 2^-32 of a turn.
+// as a 64-bit fraction F, off by at most 2^-64, and the integer product p F mod 2^64 is exact: p takes that to 2^-33 of a turn at
+// most, and of the product the upper 32 bits, which leave 2^-32, go on.
 #pragma once
 
 #include "kda_attn.cuh"
