@@ -170,9 +170,11 @@ bool interleaved(const void* a, size_t row_a, int64_t stride_a, const void* b, s
     return x < y ? off >= row_a && off + row_b <= gap : off >= row_b && off + row_a <= gap;
 }
 
-// The arguments of an append, past its descriptor.  `out`: what the call writes beside the cache (turned queries).
+// The arguments of an append, past its descriptor.  `out`: what the call writes beside the cache (turned queries), `among`: whose
+// rows lie between those of k and v without touching them.
 kda_status_t check_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,
-                          const kda_attention_t& p, uint32_t* check, const Range* more_in, int more, Range out, kda::AppendArgs& a)
+                          const kda_attention_t& p, uint32_t* check, const Range* more_in, int more, Range out, bool among,
+                          kda::AppendArgs& a)
 {
     kda_status_t st;
     if (cu_seqlens == nullptr && p.total_tokens % p.num_seqs != 0) return KDA_ERR_INVALID_ARG;
@@ -203,8 +205,8 @@ kda_status_t check_append(const void* k, const void* v, const int32_t* cu_seqlen
         }
         if (overlaps(rk, rc.r[i]) || overlaps(out, rc.r[i])) return KDA_ERR_INVALID_ARG;
     }
-    for (const Range& r : in) {
-        if (overlaps(rk, r) || overlaps(out, r)) return KDA_ERR_INVALID_ARG;
+    for (int i = 0; i < 5; ++i) {
+        if (overlaps(rk, in[i]) || (!(among && i < 2) && overlaps(out, in[i]))) return KDA_ERR_INVALID_ARG;
     }
     for (int j = 0; j < more; ++j) {
         if (overlaps(rk, more_in[j])) return KDA_ERR_INVALID_ARG;
@@ -292,7 +294,7 @@ kda_status_t kda_cache_append(const void* k, const void* v, const int32_t* cu_se
     if (st != KDA_OK) return st;
     const kda_attention_t& p = *problem;
     kda::AppendArgs a{};
-    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, nullptr, 0, Range{0, 0}, a)) != KDA_OK) return st;
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, nullptr, 0, Range{0, 0}, false, a)) != KDA_OK) return st;
     if (p.total_tokens == 0) return KDA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     kda::prof_start("kda_cache_append", s);
@@ -326,14 +328,7 @@ kda_status_t kda_rotary_append(const void* q, const void* k, const void* v, cons
     const size_t io = io_size(p.io_dtype), row = (size_t)p.num_heads * p.head_dim * io, krow = (size_t)p.num_kv_heads * p.head_dim * io;
     const bool among = q != nullptr && q == q_out && k != nullptr && v != nullptr && interleaved(q, row, qs, k, krow, ks, io) &&
                        interleaved(q, row, qs, v, krow, vs, io);
-    if (among) {
-        for (const Range& x : {range_of(cu_seqlens, cu_seqlens ? ((size_t)p.num_seqs + 1) * 4 : 0),
-                               range_of(lengths, lengths ? (size_t)p.num_seqs * 4 : 0)}) {
-            if (overlaps(out, x)) return KDA_ERR_INVALID_ARG;
-        }
-    }
-    const Range apart = among ? Range{0, 0} : out;
-    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, more, 2, apart, a)) != KDA_OK) return st;
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, more, 2, out, among, a)) != KDA_OK) return st;
     for (const void* ptr : {q, (const void*)positions, (const void*)q_out}) {
         if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
     }
