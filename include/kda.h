@@ -428,7 +428,8 @@ typedef struct {
  *   lengths : [N] int32 on the device, tokens of each sequence INCLUDING the T_tot new ones as for kda_cache_append,
  *       or NULL where the sequences begin with them.  Not read where positions are given.
  *   positions : [axes, T_tot] int32 on the device, any values; or NULL: a token's place in its sequence, from 0, on every axis.
- *   q_out, k_out : packed outputs like q and k, or q and k themselves (in place, strides and all); no other overlap.
+ *   q_out, k_out : packed outputs like q and k, or q and k themselves (in place, strides and all; q and k that are views of
+ *       one projection then both); no other overlap.
  *   problem : num_seqs, total_tokens, num_heads, num_kv_heads, head_dim, io_dtype, q_stride, k_stride (the rest unused).
  * freq / (2 pi) is kept as a fraction of a turn to within 2^-64 and multiplied with the position exactly, so that an angle is
  * off by less than 2^-31 of a turn at any position and frequency; arithmetic is fp32, rounded to the io dtype once.
@@ -441,7 +442,8 @@ kda_status_t kda_rotary(const void* q, const void* k, const int32_t* cu_seqlens,
  * kda_cache_append of keys turned by their positions, in one launch: k is turned in fp32 and rounded once, to the codes
  * (its scale follows the turned values); v enters as it is.  q, where given, is turned in the same call.
  *
- *   q : [T_tot, num_heads, head_dim] io dtype (q_stride), or NULL;  q_out : as for kda_rotary.
+ *   q : [T_tot, num_heads, head_dim] io dtype (q_stride), or NULL;  q_out : packed, or q itself, also where q is a view of one
+ *       projection with k, v or both.
  *   positions : as for kda_rotary; NULL: a token's place in its sequence, lengths[n] - (new tokens) + i.
  *   rows of q past the last sequence's are left as they were; a sequence that is skipped (see kda_cache_append) has its
  *   queries turned all the same.

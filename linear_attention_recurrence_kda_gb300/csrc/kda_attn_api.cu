@@ -170,10 +170,10 @@ bool interleaved(const void* a, size_t row_a, int64_t stride_a, const void* b, s
     return x < y ? off >= row_a && off + row_b <= gap : off >= row_b && off + row_a <= gap;
 }
 
-// The arguments of an append, past its descriptor.  `out`: what the call writes beside the cache (turned queries), `among`: whose
-// rows lie between those of k and v without touching them.
+// The arguments of an append, past its descriptor.  `out`: what the call writes beside the cache (turned queries), `beside_k`, `beside_v`:
+// its rows lie between those of k, of v, without touching them.
 kda_status_t check_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,
-                          const kda_attention_t& p, uint32_t* check, const Range* more_in, int more, Range out, bool among,
+                          const kda_attention_t& p, uint32_t* check, const Range* more_in, int more, Range out, bool beside_k, bool beside_v,
                           kda::AppendArgs& a)
 {
     kda_status_t st;
@@ -206,7 +206,8 @@ kda_status_t check_append(const void* k, const void* v, const int32_t* cu_seqlen
         if (overlaps(rk, rc.r[i]) || overlaps(out, rc.r[i])) return KDA_ERR_INVALID_ARG;
     }
     for (int i = 0; i < 5; ++i) {
-        if (overlaps(rk, in[i]) || (!(among && i < 2) && overlaps(out, in[i]))) return KDA_ERR_INVALID_ARG;
+        const bool beside = i == 0 ? beside_k : i == 1 && beside_v;
+        if (overlaps(rk, in[i]) || (!beside && overlaps(out, in[i]))) return KDA_ERR_INVALID_ARG;
     }
     for (int j = 0; j < more; ++j) {
         if (overlaps(rk, more_in[j])) return KDA_ERR_INVALID_ARG;
@@ -294,7 +295,7 @@ kda_status_t kda_cache_append(const void* k, const void* v, const int32_t* cu_se
     if (st != KDA_OK) return st;
     const kda_attention_t& p = *problem;
     kda::AppendArgs a{};
-    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, nullptr, 0, Range{0, 0}, false, a)) != KDA_OK) return st;
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, nullptr, 0, Range{0, 0}, false, false, a)) != KDA_OK) return st;
     if (p.total_tokens == 0) return KDA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     kda::prof_start("kda_cache_append", s);
@@ -321,14 +322,15 @@ kda_status_t kda_rotary_append(const void* q, const void* k, const void* v, cons
     more[1] = range_of(positions, positions ? (size_t)p.total_tokens * t.axes * 4 : 0);
     if (overlaps(out, more[1])) return KDA_ERR_INVALID_ARG;
     kda::AppendArgs a{};
-    // queries turned in place among the keys and values of one projection share their range, not their rows
+    // queries turned in place among the keys or values of one projection share their range, not their rows
     int64_t ks = 0, vs = 0;
     if ((st = token_stride(p.k_stride, p.num_kv_heads, p, &ks)) != KDA_OK) return st;
     if ((st = token_stride(p.v_stride, p.num_kv_heads, p, &vs)) != KDA_OK) return st;
     const size_t io = io_size(p.io_dtype), row = (size_t)p.num_heads * p.head_dim * io, krow = (size_t)p.num_kv_heads * p.head_dim * io;
-    const bool among = q != nullptr && q == q_out && k != nullptr && v != nullptr && interleaved(q, row, qs, k, krow, ks, io) &&
-                       interleaved(q, row, qs, v, krow, vs, io);
-    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, more, 2, out, among, a)) != KDA_OK) return st;
+    const bool place = q != nullptr && q == q_out;
+    const bool beside_k = place && k != nullptr && interleaved(q, row, qs, k, krow, ks, io);
+    const bool beside_v = place && v != nullptr && interleaved(q, row, qs, v, krow, vs, io);
+    if ((st = check_append(k, v, cu_seqlens, lengths, cache, p, check, more, 2, out, beside_k, beside_v, a)) != KDA_OK) return st;
     for (const void* ptr : {q, (const void*)positions, (const void*)q_out}) {
         if ((st = check_device_pointer(ptr)) != KDA_OK) return st;
     }

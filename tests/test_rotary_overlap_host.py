@@ -21,3 +21,16 @@ def test_nothing_else_lies_inside(L):  # noqa: F811
         assert append(L, p, c, r, **views(**{name: at})) == B.KDA_ERR_INVALID_ARG, name
     for name in ("block_table", "k", "v", "k_scale", "v_scale"):
         assert append(L, p, cache(**{name: INSIDE}), r, **views()) == B.KDA_ERR_INVALID_ARG, name
+
+
+def test_a_projection_of_two(L):  # noqa: F811
+    """q with k or with v; the third lies elsewhere, packed.  Rows that touch are refused."""
+    c, r = cache(), descriptor()
+    ok = append(L, attention(**WIDE), c, r, **views())
+    assert ok != B.KDA_ERR_INVALID_ARG
+    assert append(L, attention(q_stride=512, k_stride=512), c, r, k=_addr(0) + 512, q_out=_addr(0)) == ok
+    assert append(L, attention(q_stride=512, v_stride=512), c, r, v=_addr(0) + 512, q_out=_addr(0)) == ok
+    assert append(L, attention(q_stride=512, k_stride=512), c, r, k=_addr(0) + 256, q_out=_addr(0)) == B.KDA_ERR_INVALID_ARG
+    assert append(L, attention(q_stride=512, v_stride=512), c, r, v=_addr(0) + 896, q_out=_addr(0)) == B.KDA_ERR_INVALID_ARG
+    assert append(L, attention(q_stride=512, k_stride=256), c, r, k=_addr(0) + 512, q_out=_addr(0)) == B.KDA_ERR_INVALID_ARG
+    assert append(L, attention(q_stride=512, k_stride=512), c, r, k=_addr(0) + 512) == ok  # out of place: no question
