@@ -914,7 +914,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             l += sh.sum[turn & 1][hf][part ^ 1][r];
             const bool whole = s.begun() && s.ended();
             const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
-            const float mul = whole ? (l == 0.f ? 0.f : vu / l) : vu;
+            const float mul = l == 0.f ? 0.f : vu / l;  // a piece is a mean, too: sums of large values would pass fp32's range
             TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D + D / 2 * part;
             float* po = reinterpret_cast<float*>(a.ws + L.o) + place * D + D / 2 * part;
             if (on && !whole && part == 0) reinterpret_cast<float2*>(a.ws + L.ml)[place] = make_float2(m, l);
@@ -991,9 +991,10 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
     }
 }
 
-// Joins a unit's pieces: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the CTAs that hold one, in an order
-// that the pieces' number fixes.  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit at a
-// time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
+// Joins a unit's pieces: o = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - m) l_i 2^-48, over the CTAs that hold one, in an order
+// that the pieces' number fixes.  (A piece's sums, with at most 2^15 for each of 2^31 keys, are below 2^46 times its largest
+// value: none passes fp32's range here.)  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit
+// at a time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
 constexpr int kJoinWarps = 8;
 constexpr int kMaxWorkers = 512;
 
@@ -1059,8 +1060,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             for (int i = w % wpr; i < pieces; i += wpr) {
                 const float2 x = ml[slot(i) * rows_max + r];
                 const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
-                const float f = ex2(x.x - m);
-                l += x.y * f;
+                const float f = x.y * ex2(x.x - m) * 0x1p-48f;
+                l += f;
                 if constexpr (V == 4) {
                     const float4 y = *reinterpret_cast<const float4*>(p);
                     o[0] += y.x * f; o[1] += y.y * f; o[2] += y.z * f; o[3] += y.w * f;

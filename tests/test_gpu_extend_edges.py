@@ -1,5 +1,5 @@
-"""Chunks over the 8-bit cache where they can go wrong: odd page scales, scales and scores far apart, a graph's other
-lengths.
+"""Chunks over the 8-bit cache where they can go wrong: odd page scales, scales and scores far apart, the largest values,
+a graph's other lengths.
 
 Tolerances are those of test_gpu_extend.py, whose head derives them; what differs is derived beside the test."""
 import math
@@ -192,6 +192,18 @@ def test_scores_of_minus_infinity_alone(io=torch.bfloat16):
     want = clean.clone()
     want[9, 2] = 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("io", IO, **IDS)
+@pytest.mark.parametrize("keys,many", [(300, 200), (300, 1), (20011, 1)], ids=["whole", "few_pieces", "many_pieces"])
+def test_values_near_the_largest(keys, many, io):
+    """Values up to 2^127, in units that one CTA holds and in units that many share: their means are finite."""
+    q, c, table, lengths = case([keys] * many, [2] * many, 4, 2, 64, 64, torch.int8, io, seed=31)
+    c = B.KvCache(c.k, (c.v.float().abs() + 1).clamp(max=127).to(torch.int8), c.k_scale, torch.full_like(c.v_scale, 2.0 ** 120))
+    out = B.kda_attention_extend(q, c, table, lengths).double().cpu() * 2.0 ** -120
+    small = with_scales(c, vs=torch.ones_like(c.v_scale))
+    want = want_of(q, small, table, [keys] * many, [2] * many)
+    close(out.float() if io == torch.float32 else out.bfloat16(), want, small, keys)
 
 
 def test_other_lengths_through_the_same_graph():
