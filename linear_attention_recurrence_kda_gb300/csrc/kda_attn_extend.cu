@@ -398,7 +398,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         inv = 1.f / vu;
                     }
                     // (a scale's logarithm and reciprocal are those of a power of two, or off by some 2^-22)
-                    const float pv = page < 0 ? 1.f : vu == 0.f ? (scale == scale ? 0.f : scale) : scale * inv;
+                    const float pv = page < 0 ? 1.f : vu == 0.f ? (fabsf(scale) < INFINITY ? 0.f : scale) : scale * inv;
                     const float lg = __log2f(pv), ip = __frcp_rn(pv);
                     const uint32_t slot = t % kInfo;
                     ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u, tries) && !__any_sync(0xffffffffu, *dead != 0u);

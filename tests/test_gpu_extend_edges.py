@@ -76,6 +76,15 @@ def test_scales_that_are_no_number(of, bad, io):
 
 
 @pytest.mark.parametrize("io", IO, **IDS)
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_a_scale_that_is_no_number_alone(bad, io):
+    """No other page gives the outputs a unit."""
+    q, c, table, lengths = case([16], [3], 4, 2, 64, 16, torch.int8, io, seed=25)
+    out = B.kda_attention_extend(q, with_scales(c, vs=torch.full_like(c.v_scale, bad)), table, lengths)
+    assert not bool(torch.isfinite(out).any())
+
+
+@pytest.mark.parametrize("io", IO, **IDS)
 @pytest.mark.parametrize("low,high", [(-50, 1)])
 def test_value_scales_far_apart(low, high, io):
     """Pages side by side whose value scales differ by up to 2^51, zeros among them."""
