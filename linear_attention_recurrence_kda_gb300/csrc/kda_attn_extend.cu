@@ -61,7 +61,7 @@ constexpr int kGap = 256;
 constexpr float kUnset = -FLT_MAX;  // the reference of a row that has met no score above -inf
 constexpr float kFar = 1048576.f;   // 2^20: references beyond it have their scores rounded first
 constexpr uint32_t kHidden = 0xff800000u;
-constexpr uint32_t kOdd = 256u;  // some scale of the tile is not a positive finite number
+constexpr uint32_t kOdd = 256u;  // some scale of the tile is not a positive finite number, or V's is far below the unit of O
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRestUp = 2048.f;  // what a weight's second part is multiplied by (see kda_attn_decode.cu)
 
@@ -173,7 +173,7 @@ struct Walk {
 struct Shared {
     uint64_t q_full[2], z_full[2], p_full[2], o_full[2], kv_full[8], kv_empty[8], info_full[kInfo], info_free[kInfo], raw_full[4], raw_free[4], drained;
     uint32_t tmem, dead, flag;
-    uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; kOdd: see there
+    uint32_t there[kInfo];                                  // bit g: group g of 16 keys is there; and kOdd
     // a tile's scales of K; V's in the unit of O (pv), their logarithm and their reciprocal; the unit, and the last one over it
     alignas(16) float ks[kInfo][kGroups], pv[kInfo][kGroups], lg[kInfo][kGroups], ip[kInfo][kGroups];
     float2 unit[kInfo];
@@ -386,13 +386,13 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     if (__any_sync(0xffffffffu, page >= 0 && lane < 16 && !(scale > 0.f && scale < INFINITY))) there |= kOdd;
                     if (page == -2) atomicOr(&sh.flag, kCheckBadSeqlens);
                     // The unit of O follows V's scales, from the tile's largest to 64 times it, but never falls under 2^-40 of the
-                    // largest met (what is in O would grow past fp32).  Lanes 8-15 have the scales.
+                    // largest met (what is in O would grow past fp32), nor under the smallest with a reciprocal.  Lanes 8-15 have the scales.
                     const uint32_t mag = page >= 0 && lane >= 8 && lane < 16 && fabsf(scale) < INFINITY ? __float_as_uint(fabsf(scale)) : 0u;
                     const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, mag));  // (magnitudes compare as integers)
                     float ratio = 1.f;
                     if (!(big <= vu && big * 64.f >= vu) && big > 0.f) {
                         vtop = fmaxf(vtop, big);
-                        const float nu = fmaxf(big, vtop * 0x1p-40f);
+                        const float nu = fmaxf(fmaxf(big, FLT_MIN), vtop * 0x1p-40f);
                         ratio = vu == 0.f ? 0.f : vu / nu;
                         vu = nu;
                         inv = 1.f / vu;
@@ -400,6 +400,9 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     // (a scale's logarithm and reciprocal are those of a power of two, or off by some 2^-22)
                     const float pv = page < 0 ? 1.f : vu == 0.f ? (fabsf(scale) < INFINITY ? 0.f : scale) : scale * inv;
                     const float lg = __log2f(pv), ip = __frcp_rn(pv);
+                    // Below 2^-64 weights in the unit of O leave fp32's range, and what their sum gets back from them is not what
+                    // went in: such a tile's weights are formed without V's scales, as for scales that have no logarithm.
+                    if (__any_sync(0xffffffffu, page >= 0 && lane >= 8 && lane < 16 && fabsf(pv) < 0x1p-64f)) there |= kOdd;
                     const uint32_t slot = t % kInfo;
                     ok = warp_wait(&sh.info_free[slot], ((t / kInfo) & 1u) ^ 1u, tries) && !__any_sync(0xffffffffu, *dead != 0u);
                     if (!ok) break;
@@ -914,7 +917,8 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             l += sh.sum[turn & 1][hf][part ^ 1][r];
             const bool whole = s.begun() && s.ended();
             const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
-            const float mul = l == 0.f ? 0.f : vu / l;  // a piece is a mean, too: sums of large values would pass fp32's range
+            // a piece is a mean, too: sums of large values would pass fp32's range (and vu / l could fall under it)
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D + D / 2 * part;
             float* po = reinterpret_cast<float*>(a.ws + L.o) + place * D + D / 2 * part;
             if (on && !whole && part == 0) reinterpret_cast<float2*>(a.ws + L.ml)[place] = make_float2(m, l);
@@ -944,7 +948,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                 if (!on) continue;
                 float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = f_of(o[i]) * mul;
+                for (int i = 0; i < 16; ++i) y[i] = f_of(o[i]) * inv * vu;
                 if (dirty) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -991,10 +995,10 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
     }
 }
 
-// Joins a unit's pieces: o = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - m) l_i 2^-48, over the CTAs that hold one, in an order
-// that the pieces' number fixes.  (A piece's sums, with at most 2^15 for each of 2^31 keys, are below 2^46 times its largest
-// value: none passes fp32's range here.)  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit
-// at a time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
+// Joins a unit's pieces: o = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - m) l_i, over the CTAs that hold one, in an order that the
+// pieces' number fixes.  m: the largest m_i + floor(log2 l_i) and 10 more, so that no weight passes 2^-9, nor 512 pieces' sum the
+// largest value.  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit at a
+// time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
 constexpr int kJoinWarps = 8;
 constexpr int kMaxWorkers = 512;
 
@@ -1053,14 +1057,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         for (int v = 0; v < V; ++v) o[v] = 0.f;
         if (on) {
             float m = -FLT_MAX;
-            for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[slot(i) * rows_max + r].x);
+            for (int i = lane; i < pieces; i += 32) {
+                const float2 x = ml[slot(i) * rows_max + r];
+                m = fmaxf(m, x.x + (float)((int)(__float_as_uint(x.y) >> 23) - 117));
+            }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
 #pragma unroll 4
             for (int i = w % wpr; i < pieces; i += wpr) {
                 const float2 x = ml[slot(i) * rows_max + r];
                 const float* p = po + (slot(i) * rows_max + r) * D + lane * V;
-                const float f = x.y * ex2(x.x - m) * 0x1p-48f;
+                const float f = x.y * ex2(x.x - m);
                 l += f;
                 if constexpr (V == 4) {
                     const float4 y = *reinterpret_cast<const float4*>(p);

@@ -85,9 +85,9 @@ def test_a_scale_that_is_no_number_alone(bad, io):
 
 
 @pytest.mark.parametrize("io", IO, **IDS)
-@pytest.mark.parametrize("low,high", [(-50, 1)])
+@pytest.mark.parametrize("low,high", [(-50, 1), (-60, 70), (-126, 0), (-60, 118), (-140, -100)])
 def test_value_scales_far_apart(low, high, io):
-    """Pages side by side whose value scales differ by up to 2^51, zeros among them."""
+    """Pages side by side whose value scales differ by up to 2^178, zeros among them."""
     q, c, table, lengths = case(LENS, NEW, 4, 2, 64, 16, torch.int8, io, seed=26)
     g = torch.Generator().manual_seed(27)
     vs = torch.exp2(torch.randint(low, high + 1, c.v_scale.shape, generator=g).float())
