@@ -667,7 +667,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                             hi[b] = pack_f16(x0, x1);
                             if constexpr (kSplit) {
                                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[b]));
-                                lo[b] = pack_f16(x0 - f.x, x1 - f.y);
+                                lo[b] = pack_f16(x0 == f.x ? 0.f : x0 - f.x, x1 == f.y ? 0.f : x1 - f.y);  // (an infinity has no rest)
                             }
                         }
                     }

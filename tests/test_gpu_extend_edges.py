@@ -187,7 +187,8 @@ def test_one_key_before_a_long_flat_tail(io, at, high, first, code):
     assert float(err.max()) <= tol * float(v.max() * 2.0 ** -6)
 
 
-def test_scores_of_minus_infinity_alone(io=torch.bfloat16):
+@pytest.mark.parametrize("io", IO, **IDS)
+def test_scores_of_minus_infinity_alone(io):
     """A row whose every score is -inf has no weight: zeros, and the other rows as they were."""
     lens, new = [150, 300], [7, 130]
     q, c, table, lengths = case(lens, new, 4, 1, 128, 16, torch.int8, io, seed=30)
