@@ -58,6 +58,11 @@ constexpr int kGroups = kKeys / 16;
 // What a unit's start and end cost, in keys.  With 128 and 512 long units and many short ones take the same within 1 %, fp32 chunks
 // of 333 tokens 43 us with 128 (39 with 256 and 512).
 constexpr int kGap = 256;
+// Key tiles of a unit that the products add up by themselves.  Their sums are cut off, not rounded, which lowers values of one
+// sign: 25,000 steps of 16 keys came out 2.4e-3 low, 2^-23.3 a step.  So what a CTA holds of a unit is a run after the other,
+// joined by ordinary additions: of 2^12 steps, 2^-11 of the sum, where half a step of bf16 is 2^-8.  A run's start costs as a unit's
+// does, some 25 us: 256 tokens behind 1,048,320 keys take 5 % more with runs of 256 tiles, 2 % with 512.
+constexpr int kRun = 512;
 constexpr float kUnset = -FLT_MAX;  // the reference of a row that has met no score above -inf
 constexpr float kFar = 1048576.f;   // 2^20: references beyond it have their scores rounded first
 constexpr uint32_t kHidden = 0xff800000u;
@@ -127,19 +132,21 @@ __device__ __forceinline__ int64_t places_of(const Seq& s, int tpu)
     return k == 0 ? 0 : places_before(s, tpu, k - 1) + kGap + s.ctx + s.rows;
 }
 
-// A run of a unit's key tiles.
+// A run of a unit's key tiles: of those that the CTA holds, which begin with the tile `from`.
 struct Segment {
-    int n, h, rt, i0, count, tiles;
+    int n, h, rt, from, i0, count, tiles;
     int first, last, ctx;   // the unit's tokens [first, last) of its sequence's, and the keys before the sequence's first
     int64_t start, place;   // token of q of the sequence's first; where the unit's keys begin in the line
-    __device__ __forceinline__ bool begun() const { return i0 == 0; }
+    bool paused;            // the CTA's next run goes on with the unit
+    __device__ __forceinline__ bool begun() const { return from == 0; }
+    __device__ __forceinline__ bool resumed() const { return i0 > from; }
     __device__ __forceinline__ bool ended() const { return i0 + count == tiles; }
 };
 
 // The segments of a CTA, one after the other: the tiles whose first key has its place in [., end).
 struct Walk {
     Seq s;
-    int n, h, rt, i, units;
+    int n, h, rt, i, from, units;  // from: the unit's first tile here
     int64_t at, end;  // place of the unit's gap
     __device__ __forceinline__ bool next(const AttnExtendArgs& a, int tpu, Segment& g)
     {
@@ -149,14 +156,16 @@ struct Walk {
             const int64_t room = end - (at + kGap + (int64_t)kKeys * i);
             if (i < tiles) {
                 if (room <= 0) return false;
-                g.n = n; g.h = h; g.rt = rt; g.i0 = i; g.tiles = tiles;
-                g.count = (int)min((int64_t)(tiles - i), (room + kKeys - 1) / kKeys);
+                const int left = (int)min((int64_t)(tiles - i), (room + kKeys - 1) / kKeys);
+                g.n = n; g.h = h; g.rt = rt; g.from = from; g.i0 = i; g.tiles = tiles;
+                g.count = min(left, kRun);
+                g.paused = left > kRun;
                 g.first = rt * tpu; g.last = last; g.ctx = s.ctx; g.start = s.start; g.place = at + kGap;
                 i += g.count;
                 return true;
             }
             at += kGap + keys;
-            i = 0;
+            i = from = 0;
             if (++rt < units) continue;
             rt = 0;
             if (++h < a.Hkv) continue;
@@ -184,6 +193,7 @@ struct Shared {
     Segment seg[24];
     uint32_t more[24];
     float top[2][2][2][128], sum[2][2][2][128];  // in turn: what a row's two threads tell each other, by half and part
+    float2 was[2][2][128];                       // in turn: a row's reference and sum where its unit pauses, by half
 };
 
 // What is noted in odd[]: the segment's turn in the upper half (later turns are smaller, so that atomicMin prefers them), the
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
         }
         walk.rt = lo;
         walk.at = at + places_before(walk.s, tpu, lo);
-        walk.i = (int)max((int64_t)0, (b0 - walk.at - kGap + kKeys - 1) / kKeys);
+        walk.i = walk.from = (int)max((int64_t)0, (b0 - walk.at - kGap + kKeys - 1) / kKeys);
     }
     if (tid == 0) sh.begin = walk;
     __syncthreads();  // the prefix is read
@@ -919,6 +929,18 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             const int64_t place = (2 * (int64_t)blockIdx.x + (s.begun() ? 1 : 0)) * rows_max + hf * 128 + r;
             // a piece is a mean, too: sums of large values would pass fp32's range (and vu / l could fall under it)
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            // What the unit's earlier runs left here, and the weights of this one and of those in what both give.
+            const bool resumed = s.resumed();
+            float now = 1.f, then = 0.f;
+            if (resumed) {
+                const float2 was = sh.was[(turn & 1) ^ 1][hf][r];
+                const float both = fmaxf(m, was.x), l1 = l * ex2(m - both), l0 = was.y * ex2(was.x - both);
+                m = both;
+                l = l1 + l0;
+                now = l == 0.f ? 0.f : l1 / l;
+                then = l == 0.f ? 0.f : l0 / l;
+            }
+            if (s.paused && part == 0) sh.was[turn & 1][hf][r] = f2(m, l);
             TIO* out = static_cast<TIO*>(a.out) + (s.start + tok) * tokrow + (int64_t)(s.h * a.group + rh) * D + D / 2 * part;
             float* po = reinterpret_cast<float*>(a.ws + L.o) + place * D + D / 2 * part;
             if (on && !whole && part == 0) reinterpret_cast<float2*>(a.ws + L.ml)[place] = make_float2(m, l);
@@ -956,6 +978,16 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                         if ((uint32_t)(od >> 32) == 0xfffffffeu - turn && (int)(uint32_t)od < seen) y[i] = NAN;
                     }
                 }
+                if (resumed) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 x = *reinterpret_cast<const float4*>(po + 16 * c + 4 * i);
+                        y[4 * i] = fmaf(y[4 * i], now, x.x * then);
+                        y[4 * i + 1] = fmaf(y[4 * i + 1], now, x.y * then);
+                        y[4 * i + 2] = fmaf(y[4 * i + 2], now, x.z * then);
+                        y[4 * i + 3] = fmaf(y[4 * i + 3], now, x.w * then);
+                    }
+                }
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(po + 16 * c + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
@@ -986,7 +1018,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
         Walk walk = sh.begin;
         Segment s;
         while (walk.next(a, tpu, s)) {
-            if (failed || !s.begun() || s.ended()) continue;
+            if (failed || s.paused || !s.begun() || s.ended()) continue;
             const int64_t e = s.place + (int64_t)kKeys * (s.tiles - 1);  // the last tile's place
             rec = Record{s.n, s.h, s.rt, (int32_t)blockIdx.x, (int32_t)(((e + 1) * W - 1) / total)};
         }

@@ -1,5 +1,5 @@
 """Chunks over the 8-bit cache where they can go wrong: odd page scales, scales and scores far apart, the largest values,
-a graph's other lengths.
+long sums of one sign, a graph's other lengths.
 
 Tolerances are those of test_gpu_extend.py, whose head derives them; what differs is derived beside the test."""
 import math
@@ -214,6 +214,42 @@ def test_values_near_the_largest(keys, many, io):
     small = with_scales(c, vs=torch.ones_like(c.v_scale))
     want = want_of(q, small, table, [keys] * many, [2] * many)
     close(out.float() if io == torch.float32 else out.bfloat16(), want, small, keys)
+
+
+@pytest.mark.parametrize("io", IO, **IDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sums_of_one_sign(d, io):
+    """Units enough to fill the SMs, 400,000 keys each, which a CTA adds up by itself; every value of some channels is 1, of others
+    positive.  The tolerance does not grow with the length."""
+    keys, page, hkv, many = 400_000, 128, 8, 40
+    pages = 64
+    g = torch.Generator().manual_seed(32)
+    k = torch.randn(pages, hkv, page, d, generator=g).mul(30).round().clamp(-127, 127)
+    v = torch.randint(1, 128, (pages, hkv, page, d), generator=g).float()
+    v[..., ::3] = 127
+    c = B.KvCache(k.to(torch.int8).to(DEV), v.to(torch.int8).to(DEV), torch.full((pages, hkv), 2.0 ** -6).to(DEV), torch.full((pages, hkv), 2.0 ** -7).to(DEV))
+    cols = keys // page
+    table = (torch.arange(cols, dtype=torch.int32) % pages).repeat(many, 1).to(DEV)
+    q = torch.randn(many, hkv, d, generator=g).to(io).to(DEV)
+    q[::2] *= 0.01  # weights nearly alike
+    out = B.kda_attention_extend(q, c, table, i32([cols * page] * many))
+    # the pages repeat: their keys' weights are counted as often as they stand in the table
+    often = torch.bincount(table[0].long().cpu(), minlength=pages).double().repeat_interleave(page)
+    want = torch.zeros(out.shape, dtype=torch.float64)
+    kd, vd = ref.dequant(c.k, c.k_scale), ref.dequant(c.v, c.v_scale)
+    for h in range(hkv):
+        kk, vv = kd[:, h].reshape(-1, d), vd[:, h].reshape(-1, d)
+        z = q[:, h].double().cpu() @ kk.T * d ** -0.5
+        p = torch.exp(z - z.amax(1, keepdim=True)) * often
+        want[:, h] = (p / p.sum(1, keepdim=True)) @ vv
+    worst = ((out.double().cpu() - want).abs() / want.abs()).max()
+    print(f"largest relative distance {float(worst):.2e}, mean {float(((out.double().cpu() - want) / want).mean()):.2e}")
+    # as for few keys: weights in f16 (2^-11, of either sign), sums cut off for 2^12 steps at most, by 2^-23 each, the output's half a
+    # step; fp32: 2^-15 as for scores of signs
+    assert float(worst) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11 if io == torch.bfloat16 else 2.0 ** -15)
+    # and on the whole no more bias than those steps': f16's and bf16's roundings are of either sign, what is cut off is not
+    bias = float(((out.double().cpu() - want) / want).mean())
+    assert abs(bias) <= (2.0 ** -11 if io == torch.bfloat16 else 2.0 ** -17)
 
 
 def test_other_lengths_through_the_same_graph():
