@@ -124,7 +124,7 @@ __device__ __forceinline__ Seq seq_of(const AttnExtendArgs& a, int n, bool* bad 
 __device__ __forceinline__ int units_of(const Seq& s, int tpu) { return (s.rows + tpu - 1) / tpu; }
 __device__ __forceinline__ int64_t places_before(const Seq& s, int tpu, int64_t k)  // of the units before the k-th
 {
-    return k * (kGap + s.ctx) + (int64_t)tpu * (k * (k + 1) / 2);
+    return k * ((int64_t)kGap + s.ctx) + (int64_t)tpu * (k * (k + 1) / 2);
 }
 __device__ __forceinline__ int64_t places_of(const Seq& s, int tpu)
 {
@@ -164,7 +164,7 @@ struct Walk {
                 i += g.count;
                 return true;
             }
-            at += kGap + keys;
+            at += (int64_t)kGap + keys;
             i = from = 0;
             if (++rt < units) continue;
             rt = 0;
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             while (ok && next_segment()) {
                 const int keys = s.ctx + s.last;
                 auto page_of = [&](int i) -> int {
+                    if (i >= s.i0 + s.count || i * kKeys + grp * 16 >= keys) return -1;
                     const int key = i * kKeys + grp * 16;
-                    if (i >= s.i0 + s.count || key >= keys) return -1;
                     const int p = __ldg(a.c.table + (int64_t)s.n * a.c.max_pages + (key >> page_shift));
                     return p >= 0 && p < a.c.num_pages ? p : -2;
                 };

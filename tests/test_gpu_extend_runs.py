@@ -83,3 +83,16 @@ def test_nans_in_any_run():
         want[:, max(0, at - (keys - new)):, 2:, 9] = float("nan")
         same = (out == want) | (out.isnan() & want.isnan())
         assert bool(same.all()), (at, [tuple(i) for i in (~same).nonzero()[:4].tolist()])
+
+
+@pytest.mark.parametrize("io", IO, ids=["bf16", "f32"])
+def test_the_longest_table(io):
+    """A sequence of 2^31 - 128 keys, as many as the largest table of its pages holds: places of its units pass 32 bits."""
+    keys, new = 2 ** 31 - 128, 2
+    c, table = repeated(keys, seed=5, d=32)
+    assert table.numel() == 2 ** 24 - 1
+    q = torch.randn(new, 4, 32, generator=torch.Generator().manual_seed(3)).to(io).to(DEV)
+    ws = torch.zeros(B.kda_attention_extend_workspace_bytes(B.KdaAttention(1, new, 4, 2, 32, B._IO[io], 1.0, 0, 0, 0)), dtype=torch.uint8, device=DEV)
+    out = B.kda_attention_extend(q, c, table[None], torch.tensor([keys], dtype=torch.int32, device=DEV), workspace=ws)
+    assert B.kda_workspace_status(ws) == B.KDA_OK
+    close(out, want_of(q, c, table, keys, new), c, 1 << 16)
