@@ -73,7 +73,7 @@ class HybridStack:
         return kda.kda_rotary_append(self.rotary, k, v, memory, self.table, lengths, q=q, cu_seqlens=cu)
 
     def _add(self, x, o, w):
-        return x + o.reshape(o.shape[0], -1) @ w["out"]
+        return x + o.flatten(1) @ w["out"]
 
     def prompt(self, x, lens):
         """The packed prompts x [sum(lens), width]; returns the stack's output for every token.  The attention layers'
