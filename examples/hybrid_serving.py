@@ -66,7 +66,7 @@ class HybridStack:
         return y[:, :self.heads], y[:, self.heads:self.heads + self.kv_heads], y[:, self.heads + self.kv_heads:]
 
     def _remember(self, q, k, v, memory, lengths, cu=None):
-        """The tokens' keys and values into the cache, and their queries, both turned where the layers have positions."""
+        """The tokens' keys and values into the cache, and their queries (if any), both turned where the layers have positions."""
         if self.rotary is None:
             kda.kda_cache_append(k, v, memory, self.table, lengths, cu_seqlens=cu)
             return q
@@ -89,10 +89,11 @@ class HybridStack:
                                        cu_seqlens=cu, max_seqlen=max(lens))
             else:
                 q, k, v = self._attention_inputs(x, w)
-                if self.rotary is not None:
-                    q, k = kda.kda_rotary(self.rotary, q, k, cu_seqlens=cu)
-                o = kda.kda_attention_prefill(q, k, v, cu_seqlens=cu)
-                kda.kda_cache_append(k, v, self.memory[i], self.table, self.lengths, cu_seqlens=cu)
+                # (turned keys are rounded once on their way into the cache, as more() and step() have it, so that a prompt's
+                # codes are those of its pieces)
+                turned = (q, k) if self.rotary is None else kda.kda_rotary(self.rotary, q, k, cu_seqlens=cu)
+                o = kda.kda_attention_prefill(*turned, v, cu_seqlens=cu)
+                self._remember(None, k, v, self.memory[i], self.lengths, cu)
             x = self._add(x, o, w)
         return x
 

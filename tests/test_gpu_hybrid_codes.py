@@ -25,7 +25,7 @@ def served(rotary, lens, piece):
     return s
 
 
-@pytest.mark.parametrize("rotary", [False])
+@pytest.mark.parametrize("rotary", [False, True])
 def test_codes_of_whole_prompts_and_of_pieces(rotary):
     """Pieces of whole pages, so that no page's scale grows between them (rounded keys would be rounded again)."""
     lens = [300, 64, 129]
