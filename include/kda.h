@@ -497,7 +497,7 @@ size_t kda_attention_extend_workspace_bytes(const kda_attention_t* problem);
  *       running call.
  * Lengths, pages and the check word (kda_workspace_status(workspace, ...)) as for kda_attention_decode, and so are the
  * products' operands: codes exactly, q and the weights as f16 (fp32 io: as sums of two f16 parts).  A bounded wait inside the
- * kernel that gives up (after ~2.6 s, sooner where KDA_DEBUG_HANDOFF_TRIES is set, see kda_forward) ends the call early: the
+ * kernel that gives up (after 1.3 to 2.6 s, most of them sooner where KDA_DEBUG_HANDOFF_TRIES is set, see kda_forward) ends the call: the
  * check word then reports KDA_ERR_TIMEOUT and the outputs are unspecified.
  */
 kda_status_t kda_attention_extend(const void* q, const int32_t* cu_seqlens, const int32_t* lengths, const kda_cache_t* cache,

@@ -54,6 +54,9 @@ namespace {
 constexpr int kKeys = 128;
 constexpr int kConvert = 192;
 constexpr int kInfo = 8;       // tiles whose pages and scales are known ahead
+// The products' warp has a limit of its own, fixed so that it costs nothing: with one from the launch, as the others have, 2048 tokens
+// behind 30,720 keys take 2 to 3 % more.
+constexpr uint32_t kProductTries = 1u << 16;  // of up to 20 us each
 constexpr int kGroups = kKeys / 16;
 // What a unit's start and end cost, in keys.  With 128 and 512 long units and many short ones take the same within 1 %, fp32 chunks
 // of 333 tokens 43 us with 128 (39 with 256 and 512).
@@ -458,9 +461,9 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             const uint32_t qa = tc::smem_u32(sq), ra = tc::smem_u32(ring);
             uint32_t it = 0, phase = 0;  // phase: bits 0, 1 of q, 2, 3 of P
             bool ok = true;
-            auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u, tries); };
+            auto full = [&](uint32_t x) { return warp_wait(&sh.kv_full[x % S], (x / S) & 1u, kProductTries); };
             auto flip = [&](uint64_t* bar, uint32_t bit) {
-                const bool got = warp_wait(bar, (phase >> bit) & 1u, tries);
+                const bool got = warp_wait(bar, (phase >> bit) & 1u, kProductTries);
                 phase ^= 1u << bit;
                 return got;
             };
@@ -694,9 +697,9 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
             const int warp_seen = __reduce_min_sync(0xffffffffu, seen);
             float m = kUnset, vu = 0.f, l = 0.f;  // m: finite, so that a score of -inf weighs nothing
             float peak = -INFINITY;               // the largest weight's exponent among ordinary tiles since m was set (this thread's)
-            const volatile Segment& seg = sh.seg[w];  // (read again at every tile: registers are short)
+            const int count = s.count, i0 = s.i0;
             bool late = false, left = false;  // a wait gave up, here or with the row's other thread: they leave together
-            for (int j = 0; j < seg.count; ++j, ++t) {
+            for (int j = 0; j < count; ++j, ++t) {
                 const int slot = t % kInfo;
                 if (j < nh) {
                     late = !warp_wait(&sh.z_full[hf], zc++ & 1u, tries);
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                     const uint32_t there = sh.there[slot];
                     const float2 unit = sh.unit[slot];
                     vu = unit.x;
-                    const int key0 = (seg.i0 + j) * kKeys;
+                    const int key0 = (i0 + j) * kKeys;
                     auto k_of = [&](int c) {  // at least FLT_MIN where all scales are positive numbers: -inf times it stays that
                         const float2 x = *reinterpret_cast<const float2*>(&sh.ks[slot][4 * part + 2 * c]);
                         return (there & kOdd) != 0u ? f2(x.x * cs, x.y * cs) : f2(fmaxf(x.x * cs, FLT_MIN), fmaxf(x.y * cs, FLT_MIN));
@@ -914,7 +917,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
                 }
                 // the last tile's when the segment is over: conversion then is less than kInfo segments ahead (see odd_note)
                 __syncwarp();
-                if (lane == 0 && j + 1 < seg.count) tc::mbar_arrive(&sh.info_free[slot]);
+                if (lane == 0 && j + 1 < count) tc::mbar_arrive(&sh.info_free[slot]);
             }
             if (!left) {
                 if (nh > 0 && !late) late = !warp_wait(&sh.o_full[hf], oc++ & 1u, tries);
