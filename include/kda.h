@@ -485,7 +485,8 @@ size_t kda_attention_extend_workspace_bytes(const kda_attention_t* problem);
  * A chunk of new tokens of every sequence, of any length each, attends to the paged 8-bit cache, which holds their keys
  * and values already (kda_cache_append, kda_rotary_append): a prompt that arrives in pieces, the next turn of a
  * conversation, or a serving step in which some sequences bring one token and others a piece of their prompt.
- * Token i of the L_n new ones of sequence n sees the first lengths[n] - L_n + i + 1 keys of its sequence.
+ * Token i of the L_n new ones of sequence n sees the first lengths[n] - L_n + i + 1 keys of its sequence.  Where every
+ * sequence brings one token, or as many as every other one and few, kda_attention_decode does the same in less than half the time.
  *
  *   q : [T_tot, num_heads, head_dim] io dtype, q_stride as for kda_attention_prefill.
  *   cu_seqlens : device [N+1] offsets of every sequence's new tokens, or NULL for T_tot / N each.  Offsets are not

@@ -29,14 +29,16 @@
 // Hidden keys: scores are replaced by -inf.  A NaN code in a value would spread over 0 x NaN, so a tile that some row does not see
 // whole is cleaned of them (noted by channel and key), and the rows that see them get them at the end.
 //
-// 2048 tokens behind 30,720 keys, 32 heads of 128 channels over 8: 797 us, 1.34 PFLOP/s (int8 763 us, 1.40), 68 % of the library's
-// bf16 products; 256 tokens behind 1,048,320: 3136 us, 1.40 PFLOP/s.  The products alone would take 60 % of a tile's 3400 cycles;
+// 2048 tokens behind 30,720 keys, 32 heads of 128 channels over 8: 803 us, 1.33 PFLOP/s (int8 782 us, 1.36), 67 % of the library's
+// bf16 products; 256 tokens behind 1,048,320: 3230 us, 1.36 PFLOP/s.  The products alone would take 60 % of a tile's 3400 cycles;
 // the rest is the way of a half's tile from scores to weights, which the other half's products do not cover.  What counted
 // (the first form took 1813 us): one copy of each role's code, which has to fit a small instruction cache, 1134 -> 943;
 // two threads a row, ordinary tiles in one pass over tensor memory, 890; a tile's scales read before its scores arrive; codes by bulk
 // copies and not loaded by the converting warps, without a prefetch into L2, 883 -> 797 (with it 909).  Eight warps of
 // conversion 919; scores held in registers by one thread a row 950 to 1000.  Few rows: 64 sequences of 4096 keys and one
-// token each take 236 us, 2.3 TB/s, bound by conversion and half-empty products (the decode kernel is the one for these).
+// token each take 242 us, 2.2 TB/s, bound by conversion and half-empty products (kda_attention_decode takes 100).
+// By fits over 8 to 64 tiles a unit: a tile costs an SM 1.6 to 1.9 us, whether 4 rows see it or 256, and a unit's start 3 to 5 us with 4
+// rows, 20 with 256.
 #include <algorithm>
 #include <cfloat>
 
