@@ -1034,7 +1034,7 @@ __global__ void __launch_bounds__((Cfg<D, sizeof(TIO) == 4>::THREADS), 1) kda_at
 
 // Joins a unit's pieces: o = sum_i w_i o_i / sum_i w_i, w_i = 2^(m_i - m) l_i, over the CTAs that hold one, in an order that the
 // pieces' number fixes.  m: the largest m_i + floor(log2 l_i) and 10 more, so that no weight passes 2^-9, nor 512 pieces' sum the
-// largest value.  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit at a
+// largest value (beyond scores of 2^24, which have no room for that logarithm, values have to stay below 2^70).  `wpr` warps take a row's pieces in turn; a block takes kJoinWarps / wpr rows of a unit at a
 // time: block (x, y) those of the unit that CTA x began or, where few CTAs have begun one (kFew), of the units in turn.
 constexpr int kJoinWarps = 8;
 constexpr int kMaxWorkers = 512;
